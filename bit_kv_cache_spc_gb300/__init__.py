@@ -22,7 +22,9 @@ __all__ = [
     "spc_topk_select_prev", "spc_merged_attn_fetch_prev", "spc_host_gather_prev", "spc_decode_step_prev",
     "spc_host_gather", "spc_merged_attn_noalloc", "spc_merged_attn_fetch", "spc_attn_kernel_count",
     "spc_decode_step_kernel_count", "spc_decode_step_on_chip", "spc_decode_step", "spc_step_workspace_bytes",
-    "spc_read_device_status", "spc_append_kv", "spc_offload_kv", "lib_path",
+    "spc_read_device_status", "spc_append_kv", "spc_offload_kv", "spc_rope_frequencies", "spc_rope",
+    "spc_prompt_attn", "spc_prompt_attn_workspace_bytes", "spc_prompt_attn_status", "spc_extend_kv",
+    "spc_dequantize_kv", "lib_path",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -67,8 +69,29 @@ def Dims(B, Hq, Hkv, N, R, bits, q_groups_cap=None, resid_cap=None, scale=None, 
     return spc_dims(B, Hq, Hkv, D, bits, group, N, R, q_groups_cap, resid_cap, scale)
 
 
+class spc_layout(C.Structure):
+    _fields_ = [("b", C.c_int64), ("t", C.c_int64), ("h", C.c_int64)]
+
+
+class spc_rope_scaling(C.Structure):
+    _fields_ = [("kind", C.c_int32), ("theta", C.c_double), ("factor", C.c_double), ("low", C.c_double),
+                ("high", C.c_double), ("context", C.c_double)]
+
+
+class spc_rope_dims(C.Structure):
+    _fields_ = [("B", C.c_int32), ("T", C.c_int32), ("Hq", C.c_int32), ("Hkv", C.c_int32), ("D", C.c_int32),
+                ("rot", C.c_int32), ("interleaved", C.c_int32), ("mscale", C.c_float)] + [
+                    (n, spc_layout) for n in ("q", "k", "v", "q_out", "k_out", "v_out")]
+
+
+class spc_prompt_dims(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("S", "Hq", "Hkv", "D", "q_tokens", "k_tokens", "q_max", "k_max")] + [
+        ("scale", C.c_float)] + [(n, spc_layout) for n in ("q", "k", "v", "o")]
+
+
 _P = C.c_void_p
 _D = C.POINTER(spc_dims)
+_L = C.POINTER(spc_layout)
 _sig = {
     "spc_abi_version": (C.c_int32, []),
     "spc_status_string": (C.c_char_p, [C.c_int]),
@@ -101,6 +124,13 @@ _sig = {
                                        _P, _P, C.c_size_t, _P, C.c_int64, _P, C.c_int32, _P, _P, _P, C.c_int32,
                                        _P]),
     "spc_read_device_status": (C.c_int, [_P, _D, _P]),
+    "spc_rope_frequencies": (C.c_int, [C.POINTER(spc_rope_scaling), C.c_int32, _P, C.POINTER(C.c_float)]),
+    "spc_rope": (C.c_int, [C.POINTER(spc_rope_dims), _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "spc_prompt_attn_workspace_bytes": (C.c_size_t, [C.POINTER(spc_prompt_dims)]),
+    "spc_prompt_attn": (C.c_int, [C.POINTER(spc_prompt_dims), _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, C.c_size_t, _P]),
+    "spc_prompt_attn_status": (C.c_int, [_P, _P]),
+    "spc_extend_kv": (C.c_int, [_D, C.c_int32, _P, _P, _L, _L, _P, _P, _P, C.c_int64, _P]),
+    "spc_dequantize_kv": (C.c_int, [_D, _P, _P, C.c_int32, C.c_int32, _P, _P, _L, _L, _P]),
 }
 for _name, (_res, _args) in _sig.items():
     _f = getattr(_lib, _name)
@@ -281,3 +311,191 @@ def spc_host_gather_prev(d, host_kv, n_cap, idx, k, staging, src, prev_staging, 
     _check("spc_host_gather_prev",
            _lib.spc_host_gather_prev(C.byref(d), _ptr(host_kv), int(n_cap), _ptr(idx), int(k), _ptr(staging),
                                      _ptr(src), _ptr(prev_staging), int(prev_k), int(max_ctas), _stream(stream)))
+
+
+# ------------------------------------------------------------------ the prompt path
+# These calls take tensors of any strides (views of a fused projection, of a
+# cache buffer), so they read shapes and strides from the tensors and check
+# what a pointer cannot say: rank, shapes, 16-bit elements, the last axis
+# contiguous, and that every tensor is on the current CUDA device.
+
+ROPE_KINDS = {"plain": 0, "linear": 1, "bands": 2, "ramp": 3}
+
+
+def _on_device(fn, name, t):
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{fn}: {name} must be on the current CUDA device")
+
+
+def _rows(fn, name, t, shape=None):
+    """(shape, layout) of a 16-bit [batch][token][head][D] tensor, or of packed [token][head][D]."""
+    if t.dim() not in (3, 4) or t.element_size() != 2:
+        raise ValueError(f"{fn}: {name} must be a 16-bit tensor [batch][token][head][D] (or packed, without the batch)")
+    _on_device(fn, name, t)
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{fn}: the last axis of {name} must be contiguous")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    n, st = tuple(t.shape), t.stride()
+    if t.dim() == 3:
+        n, st = (1,) + n, (0,) + tuple(st)
+    return n, spc_layout(st[0] if n[0] > 1 else 0, st[1] if n[1] > 1 else 0, st[2] if n[2] > 1 else 0)
+
+
+def _words(fn, name, t, dtype, n):
+    if t is None:
+        return None
+    _on_device(fn, name, t)
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor of {n} elements")
+    return t.data_ptr()
+
+
+def spc_rope_frequencies(rot=128, theta=10000.0, kind="plain", factor=1.0, low=1.0, high=4.0, context=8192.0):
+    """(turns, mscale) of a rotary rule: turns is an int64 CPU tensor (the bits
+    of rot/2 64-bit fractions of a turn per position; move it to the device
+    once), mscale the factor of the result.  kind: "plain", "linear",
+    "bands" or "ramp" (see spc_rope_kind in include/spc.h)."""
+    s = spc_rope_scaling(ROPE_KINDS[kind], theta, factor, low, high, context)
+    turns = torch.empty(max(int(rot), 0) // 2, dtype=torch.int64)
+    mscale = C.c_float()
+    buf = (C.c_uint64 * 64)()
+    _check("spc_rope_frequencies", _lib.spc_rope_frequencies(C.byref(s), int(rot), buf, C.byref(mscale)))
+    for i in range(turns.numel()):
+        turns[i] = buf[i]  # below 2^62: positive as int64 too
+    return turns, mscale.value
+
+
+def spc_rope(q, k, pos, turns, rot=128, interleaved=False, mscale=1.0, v=None, q_out=None, k_out=None, v_out=None,
+             stream=None):
+    """q [B][T][Hq][D], k (and v) [B][T][Hkv][D], q or k None; the outputs of q
+    and k default to in place (v is copied, so it needs v_out)."""
+    fn = "spc_rope"
+    if q is None and k is None:
+        raise ValueError(f"{fn}: neither q nor k")
+    d = spc_rope_dims(D=128, rot=int(rot), interleaved=int(bool(interleaved)), mscale=mscale)
+    ptr = {}
+    for name, x, out in (("q", q, q_out), ("k", k, k_out), ("v", v, v_out)):
+        if x is None:
+            if out is not None:
+                raise ValueError(f"{fn}: {name}_out without {name}")
+            ptr[name] = ptr[name + "_out"] = None
+            continue
+        if name == "v" and (out is None or k is None or x.shape != k.shape):
+            raise ValueError(f"{fn}: v has k's shape and needs v_out")
+        out = x if out is None else out
+        (B, T, H, D), lay = _rows(fn, name, x)
+        _, lay_out = _rows(fn, name + "_out", out, x.shape)
+        if d.B and (d.B, d.T) != (B, T):
+            raise ValueError(f"{fn}: q and k differ in batch or tokens")
+        d.B, d.T, d.D = B, T, D
+        setattr(d, name, lay)
+        setattr(d, name + "_out", lay_out)
+        if name != "v":
+            setattr(d, "Hq" if name == "q" else "Hkv", H)
+        ptr[name], ptr[name + "_out"] = x.data_ptr(), out.data_ptr()
+    pos = _words(fn, "pos", pos, torch.int32, d.B * d.T)
+    turns = _words(fn, "turns", turns, torch.int64, max(d.rot, 0) // 2)
+    if d.T == 0:
+        return
+    _check(fn, _lib.spc_rope(C.byref(d), pos, turns, ptr["q"], ptr["k"], ptr["v"], ptr["q_out"], ptr["k_out"],
+                             ptr["v_out"], _stream(stream)))
+
+
+def _prompt_dims(fn, q, k, v, o, S, q_max, k_max, scale):
+    (qs, qt, Hq, D), ql = _rows(fn, "q", q)
+    (ks, kt, Hkv, Dk), kl = _rows(fn, "k", k)
+    _, vl = _rows(fn, "v", v, k.shape)
+    _, ol = _rows(fn, "o", o, q.shape)
+    if Dk != D:
+        raise ValueError(f"{fn}: q has rows of {D} elements, k of {Dk}")
+    for name, t, n in (("q", q, qs), ("k", k, ks)):
+        if t.dim() == 4 and n != S:
+            raise ValueError(f"{fn}: {name} has a batch of {n}, and there are {S} sequences")
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    return spc_prompt_dims(S, Hq, Hkv, D, qt, kt, qt if q_max is None else int(q_max),
+                           kt if k_max is None else int(k_max), scale, ql, kl, vl, ol)
+
+
+def _sequences(q, k, *words):
+    for t in words:
+        if t is not None:
+            return t.numel()
+    return q.shape[0] if q.dim() == 4 else k.shape[0] if k.dim() == 4 else 1
+
+
+def spc_prompt_attn_workspace_bytes(q, k, v, o, S=None, q_max=None, k_max=None) -> int:
+    """Bytes of workspace of spc_prompt_attn over these tensors (S sequences; default: the batch)."""
+    d = _prompt_dims("spc_prompt_attn_workspace_bytes", q, k, v, o, _sequences(q, k) if S is None else int(S), q_max,
+                     k_max, None)
+    return int(_lib.spc_prompt_attn_workspace_bytes(C.byref(d)))
+
+
+def spc_prompt_attn(q, k, v, o, lse=None, q_begin=None, q_len=None, k_begin=None, k_len=None, q_max=None, k_max=None,
+                    scale=None, ws=None, ws_bytes=None, stream=None):
+    """q and o: [T][Hq][D] (packed sequences) or [S][T][Hq][D]; k and v
+    [T][Hkv][D] or [S][T][Hkv][D].  q_begin, q_len, k_begin, k_len: int32 [S]
+    on the device, or None.  q_max, k_max bound the lengths (default: the
+    token axis).  lse: fp32 of o's shape without D, contiguous.  Without ws a
+    workspace is taken from torch's allocator for the call, which needs the
+    call to be on the current stream."""
+    fn = "spc_prompt_attn"
+    S = _sequences(q, k, q_begin, q_len, k_begin, k_len)
+    d = _prompt_dims(fn, q, k, v, o, S, q_max, k_max, scale)
+    at = [_words(fn, n, t, torch.int32, S) for n, t in (("q_begin", q_begin), ("q_len", q_len), ("k_begin", k_begin),
+                                                       ("k_len", k_len))]
+    lse_ptr = _words(fn, "lse", lse, torch.float32, q.numel() // max(d.D, 1))
+    if ws is None:
+        if stream is not None and _stream(stream) != _stream(None):
+            raise ValueError(f"{fn}: a call on another stream than the current one needs ws")
+        need = int(_lib.spc_prompt_attn_workspace_bytes(C.byref(d)))
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    elif not isinstance(ws, int):
+        _on_device(fn, "ws", ws)
+    if ws_bytes is None:
+        ws_bytes = ws.numel() * ws.element_size()
+    _check(fn, _lib.spc_prompt_attn(C.byref(d), q.data_ptr(), k.data_ptr(), v.data_ptr(), *at, o.data_ptr(), lse_ptr,
+                                    _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def spc_prompt_attn_status(ws, stream=None) -> int:
+    """0, or SPC_ERR_TIMEOUT (6) if a bounded wait in spc_prompt_attn ran out (the word is cleared)."""
+    return int(_lib.spc_prompt_attn_status(_ptr(ws), _stream(stream)))
+
+
+def _cache_rows(fn, d, names, tensors, n):
+    got = []
+    for name, t in zip(names, tensors):
+        if t.dim() != 4:
+            raise ValueError(f"{fn}: {name} must be a 16-bit tensor [B][n][Hkv][D]")
+        got.append(_rows(fn, name, t, (d.B, n, d.Hkv, d.D))[1])
+    return got
+
+
+def _cache(fn, d, records, resid):
+    for name, t, need in (("records", records, spc_records_bytes(d)), ("resid", resid, spc_resid_bytes(d))):
+        if t is None or isinstance(t, int):
+            continue
+        _on_device(fn, name, t)
+        if not t.is_contiguous() or t.numel() * t.element_size() < need:
+            raise ValueError(f"{fn}: {name} must be contiguous and hold {need} bytes")
+
+
+def spc_extend_kv(d, k_new, v_new, records, resid, host_kv=None, n_cap=0, stream=None):
+    """k_new, v_new: 16-bit [B][n][Hkv][D] of any strides; the caller advances d.N by n."""
+    n = k_new.shape[1] if k_new.dim() == 4 else 0
+    lk, lv = _cache_rows("spc_extend_kv", d, ("k_new", "v_new"), (k_new, v_new), n)
+    _cache("spc_extend_kv", d, records, resid)
+    _check("spc_extend_kv", _lib.spc_extend_kv(C.byref(d), n, k_new.data_ptr(), v_new.data_ptr(), C.byref(lk),
+                                               C.byref(lv), _ptr(records), _ptr(resid), _ptr(host_kv), int(n_cap),
+                                               _stream(stream)))
+
+
+def spc_dequantize_kv(d, records, resid, first, k, v, stream=None):
+    """k, v: 16-bit [B][n][Hkv][D] of any strides, for the tokens first .. first+n-1."""
+    n = k.shape[1] if k.dim() == 4 else 0
+    lk, lv = _cache_rows("spc_dequantize_kv", d, ("k", "v"), (k, v), n)
+    _cache("spc_dequantize_kv", d, records, resid)
+    _check("spc_dequantize_kv", _lib.spc_dequantize_kv(C.byref(d), _ptr(records), _ptr(resid), int(first), n,
+                                                       k.data_ptr(), v.data_ptr(), C.byref(lk), C.byref(lv),
+                                                       _stream(stream)))

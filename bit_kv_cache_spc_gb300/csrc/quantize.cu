@@ -574,4 +574,154 @@ spc_status launch_append(const spc_dims* d, const uint16_t* k_new, const uint16_
   return SPC_OK;
 }
 
+// ------------------------------------------------------- a run of new tokens
+// n new tokens join the cache at once (a prompt, or a follow-up prompt), with
+// the result of n appends: the groups that complete are coded straight from
+// where their rows are (the window's old rows, then the new tokens' views),
+// then the window shifts and takes the rows that stay in 16 bits.
+struct ExtendArgs {
+  const uint16_t* k_new;  // views [B][n][Hkv][D]
+  const uint16_t* v_new;
+  spc_layout lk, lv;
+  uint8_t* records;
+  uint16_t* resid;
+  uint16_t* host;  // device address of [B][Hkv][n_cap][2][D], or null
+  int64_t n_cap, total_groups;
+  int32_t Hkv, N, n, nq, nq1, resid_cap, units_cap;
+  int32_t window_parts;  // CTAs per (b, hkv) that write the window
+};
+
+// 16-byte piece `q` (0-15 key, 16-31 value) of token t of (b, hkv).
+__device__ __forceinline__ const uint4* extend_source(const ExtendArgs& a, int64_t bh, int t, int q) {
+  if (t < a.N) return reinterpret_cast<const uint4*>(a.resid + (bh * a.resid_cap + (t - a.nq)) * 2 * kD) + q;
+  const int64_t b = bh / a.Hkv, h = bh % a.Hkv;
+  return q < 16 ? reinterpret_cast<const uint4*>(a.k_new + b * a.lk.b + (t - a.N) * a.lk.t + h * a.lk.h) + q
+                : reinterpret_cast<const uint4*>(a.v_new + b * a.lv.b + (t - a.N) * a.lv.t + h * a.lv.h) + (q - 16);
+}
+
+template <int BITS, int GROUP>
+__global__ void __launch_bounds__(128) extend_groups_kernel(const __grid_constant__ ExtendArgs a) {
+  extern __shared__ __align__(16) uint8_t qsmem[];
+  QuantSmem& sm = *reinterpret_cast<QuantSmem*>(qsmem);
+  const int tid = threadIdx.x;
+  const int per = (a.nq1 - a.nq) / GROUP;
+  for (int64_t gi = blockIdx.x; gi < a.total_groups; gi += gridDim.x) {
+    const int64_t bh = gi / per;
+    const int g = (int)(gi % per);
+    const int t0 = a.nq + g * GROUP;
+#pragma unroll
+    for (int half = 0; half < GROUP / 32; ++half)
+      for (int i = tid; i < 1024; i += 128) {
+        const int row = i >> 5, q = i & 31;
+        uint16_t* tile = sm.tile[half][q >> 4];
+        cp_async16(tile + row * kD + 8 * (q & 15), extend_source(a, bh, t0 + 32 * half + row, q));
+      }
+    cp_async_commit();
+    cp_async_wait<0>();
+    __syncthreads();
+    uint8_t* rec = a.records + (bh * a.units_cap + a.nq / GROUP + g) * record_bytes(BITS, GROUP);
+    code_group<BITS, GROUP>(sm, sm.tile[0][0], sm.tile[0][1], sm.tile[1][0], rec, 0);
+    if (GROUP == 64) code_group<BITS, GROUP>(sm, sm.tile[1][0], sm.tile[1][1], sm.tile[0][0], rec, 1);
+  }
+}
+
+// The window's rows (tokens nq1 .. N+n-1), and the new rows of the host cache.
+// Old rows that stay move down by nq1 - nq; a CTA that moves them owns the
+// window of its (b, hkv) (window_parts = 1) and moves 32 at a time, each chunk
+// read in full before it is written, before it writes the new rows.
+__global__ void __launch_bounds__(256) extend_window_kernel(const __grid_constant__ ExtendArgs a) {
+  const int64_t bh = blockIdx.x;
+  const int tid = threadIdx.x;
+  if ((int)blockIdx.y < a.window_parts) {
+    uint4* win = reinterpret_cast<uint4*>(a.resid + bh * a.resid_cap * 2 * kD);  // 32 pieces a row
+    const int shift = a.nq1 - a.nq, kept = max(a.N - a.nq1, 0);                   // old rows that stay
+    if (shift > 0) {
+      for (int c0 = 0; c0 < kept; c0 += 32) {
+        const int pieces = 32 * min(32, kept - c0);
+        uint4 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = tid + 256 * u;
+          if (i < pieces) v[u] = win[(int64_t)(shift + c0) * 32 + i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = tid + 256 * u;
+          if (i < pieces) win[(int64_t)c0 * 32 + i] = v[u];
+        }
+        __syncthreads();
+      }
+    }
+    const int first = max(a.N, a.nq1);  // the first new token that stays
+    const int64_t pieces = (int64_t)(a.N + a.n - first) * 32;
+    for (int64_t i = blockIdx.y * 256 + tid; i < pieces; i += 256 * a.window_parts) {
+      const int t = first + (int)(i >> 5);
+      win[(int64_t)(t - a.nq1) * 32 + (i & 31)] = *extend_source(a, bh, t, (int)(i & 31));
+    }
+  } else {
+    uint4* host = reinterpret_cast<uint4*>(a.host + (bh * a.n_cap + a.N) * 2 * kD);
+    const int64_t pieces = (int64_t)a.n * 32;
+    const int parts = gridDim.y - a.window_parts;
+    for (int64_t i = (blockIdx.y - a.window_parts) * 256 + tid; i < pieces; i += 256 * parts)
+      host[i] = *extend_source(a, bh, a.N + (int)(i >> 5), (int)(i & 31));
+  }
+}
+
+template <int BITS, int GROUP>
+static cudaError_t launch_extend_k(const ExtendArgs& a, cudaStream_t stream) {
+  const int smem = GROUP == 32 ? (int)offsetof(QuantSmem, tile[1]) : (int)sizeof(QuantSmem);
+  static unsigned long long configured = 0ull;
+  const cudaError_t e = spc_host::ensure_smem_limit(configured, extend_groups_kernel<BITS, GROUP>, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = std::min<int64_t>(a.total_groups, (int64_t)spc_host::sm_count() * 8);
+  extend_groups_kernel<BITS, GROUP><<<(unsigned)grid, 128, smem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+spc_status launch_extend(const spc_dims* d, int32_t n, const uint16_t* k_new, const uint16_t* v_new,
+                         const spc_layout* lk, const spc_layout* lv, void* records, uint16_t* resid,
+                         uint16_t* host_dev, int64_t n_cap, cudaStream_t stream) {
+  ExtendArgs a = {};
+  a.k_new = k_new;
+  a.v_new = v_new;
+  a.lk = *lk;
+  a.lv = *lv;
+  a.records = static_cast<uint8_t*>(records);
+  a.resid = resid;
+  a.host = host_dev;
+  a.n_cap = n_cap;
+  a.Hkv = d->Hkv;
+  a.N = d->N;
+  a.n = n;
+  a.nq = num_quantized(d->N, d->R, d->group);
+  a.nq1 = num_quantized(d->N + n, d->R, d->group);
+  a.resid_cap = d->resid_cap;
+  a.units_cap = records_cap(d->group, d->q_groups_cap);
+  const int64_t BH = (int64_t)d->B * d->Hkv;
+  a.total_groups = BH * ((a.nq1 - a.nq) / d->group);
+  cudaError_t e = cudaSuccess;
+  if (a.total_groups > 0) {
+    if (d->bits == 1)
+      e = d->group == 64 ? launch_extend_k<1, 64>(a, stream) : launch_extend_k<1, 32>(a, stream);
+    else
+      e = d->group == 64 ? launch_extend_k<2, 64>(a, stream) : launch_extend_k<2, 32>(a, stream);
+  }
+  if (e == cudaSuccess) {
+    const bool moves = a.nq1 > a.nq && a.N > a.nq1;
+    const int32_t rows = a.N + n - std::max(a.N, a.nq1);
+    a.window_parts = moves ? 1 : (int32_t)std::min<int64_t>(64, (rows + 31) / 32);
+    const int host_parts = host_dev != nullptr ? (int)std::min<int64_t>(64, (n + 31) / 32) : 0;
+    if (a.window_parts + host_parts > 0) {
+      extend_window_kernel<<<dim3((unsigned)BH, (unsigned)(a.window_parts + host_parts)), 256, 0, stream>>>(a);
+      e = cudaGetLastError();
+    }
+  }
+  if (e != cudaSuccess) {
+    spc_host::set_cuda_error(e);
+    return SPC_ERR_CUDA;
+  }
+  return SPC_OK;
+}
+
 }  // namespace spc

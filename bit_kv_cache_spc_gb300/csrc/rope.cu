@@ -1,0 +1,132 @@
+// Rotary positions of a run of tokens' query and key rows, and the copy of
+// their value rows, from the projection to where they are used.
+//
+// Pair i at position p is turned by p * turns[i] (mod 2^64, 64-bit fractions
+// of a turn): the integer product is exact, its top 32 bits give the angle in
+// [-1/2, 1/2) turns to 2^-32, and sincospi needs no range reduction.
+//
+// Eight lanes hold a head's row, 16 elements each: lane l < rot/16 the eight
+// pairs 8l .. 8l+7 (the half layout: elements 8l .. and rot/2 + 8l ..;
+// interleaved: 16l .. 16l+15), the other lanes the elements that stay as they
+// are.  So a lane needs eight angles of its token, computes them once and
+// walks over heads with them in registers.  Bound by HBM: every row is read
+// and written once.
+#include <algorithm>
+
+#include "common.cuh"
+
+namespace spc {
+namespace {
+
+struct RopeArgs {
+  const uint16_t *q, *k, *v;
+  uint16_t *q_out, *k_out, *v_out;
+  const int32_t* pos;
+  const uint64_t* turns;
+  spc_layout lq, lk, lv, oq, ok, ov;
+  int64_t tokens;                       // B * T
+  int32_t T, Hq, Hkv, heads, rot, per;  // heads of all three; heads a group of lanes walks over
+  int32_t slices;                       // groups of `per` heads
+  float mscale;
+};
+
+__device__ __forceinline__ uint32_t rope_pack(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <bool INTERLEAVED>
+__global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeArgs a) {
+  const int64_t g = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
+  const int l = threadIdx.x & 7;
+  const int64_t token = g / a.slices;
+  if (token >= a.tokens) return;
+  const int64_t b = token / a.T, t = token % a.T;
+  const int h0 = (int)(g % a.slices) * a.per, h1 = min(h0 + a.per, a.heads);
+  const bool turned = l < a.rot / 16;
+  float c[8], s[8];
+  if (turned && h0 < a.Hq + a.Hkv) {
+    const uint64_t p = (uint64_t)(int64_t)a.pos[token];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int32_t turn = (int32_t)((p * a.turns[8 * l + i]) >> 32);
+      sincospif((float)turn * 4.656612873077393e-10f, &s[i], &c[i]);  // 2^-31: half turns
+      s[i] *= a.mscale;
+      c[i] *= a.mscale;
+    }
+  }
+#pragma unroll 2
+  for (int h = h0; h < h1; ++h) {
+    const uint16_t* src;
+    uint16_t* dst;
+    bool rot = turned;
+    if (h < a.Hq) {
+      src = a.q + b * a.lq.b + t * a.lq.t + h * a.lq.h;
+      dst = a.q_out + b * a.oq.b + t * a.oq.t + h * a.oq.h;
+    } else if (h < a.Hq + a.Hkv) {
+      src = a.k + b * a.lk.b + t * a.lk.t + (h - a.Hq) * a.lk.h;
+      dst = a.k_out + b * a.ok.b + t * a.ok.t + (h - a.Hq) * a.ok.h;
+    } else {
+      src = a.v + b * a.lv.b + t * a.lv.t + (h - a.Hq - a.Hkv) * a.lv.h;
+      dst = a.v_out + b * a.ov.b + t * a.ov.t + (h - a.Hq - a.Hkv) * a.ov.h;
+      rot = false;
+    }
+    const int e0 = !INTERLEAVED && rot ? 8 * l : 16 * l;
+    const int e1 = !INTERLEAVED && rot ? 8 * l + a.rot / 2 : 16 * l + 8;
+    uint4 u = *reinterpret_cast<const uint4*>(src + e0), w = *reinterpret_cast<const uint4*>(src + e1);
+    if (rot) {
+      uint32_t x[4] = {u.x, u.y, u.z, u.w}, y[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float x0 = __uint_as_float(x[i] << 16), x1 = __uint_as_float(x[i] & 0xFFFF0000u);
+        const float y0 = __uint_as_float(y[i] << 16), y1 = __uint_as_float(y[i] & 0xFFFF0000u);
+        if (INTERLEAVED) {  // words of u: pairs 0 .. 3, of w: pairs 4 .. 7
+          x[i] = rope_pack(x0 * c[i] - x1 * s[i], x0 * s[i] + x1 * c[i]);
+          y[i] = rope_pack(y0 * c[4 + i] - y1 * s[4 + i], y0 * s[4 + i] + y1 * c[4 + i]);
+        } else {  // elements 2i, 2i+1 of u with those of w
+          x[i] = rope_pack(x0 * c[2 * i] - y0 * s[2 * i], x1 * c[2 * i + 1] - y1 * s[2 * i + 1]);
+          y[i] = rope_pack(x0 * s[2 * i] + y0 * c[2 * i], x1 * s[2 * i + 1] + y1 * c[2 * i + 1]);
+        }
+      }
+      u = make_uint4(x[0], x[1], x[2], x[3]);
+      w = make_uint4(y[0], y[1], y[2], y[3]);
+    }
+    *reinterpret_cast<uint4*>(dst + e0) = u;
+    *reinterpret_cast<uint4*>(dst + e1) = w;
+  }
+}
+
+}  // namespace
+
+spc_status launch_rope(const spc_rope_dims* d, const int32_t* pos, const uint64_t* turns, const uint16_t* q,
+                       const uint16_t* k, const uint16_t* v, uint16_t* q_out, uint16_t* k_out, uint16_t* v_out,
+                       cudaStream_t stream) {
+  RopeArgs a = {q, k, v, q_out, k_out, v_out, pos, turns, d->q, d->k, d->v, d->q_out, d->k_out, d->v_out};
+  a.tokens = (int64_t)d->B * d->T;
+  a.T = d->T;
+  a.Hq = d->Hq;
+  a.Hkv = d->Hkv;
+  a.heads = d->Hq + (v != nullptr ? 2 : 1) * d->Hkv;
+  a.rot = d->rot;
+  a.mscale = d->mscale;
+  // few tokens: a head per group of lanes, for latency; many: up to eight
+  // heads share a token's angles once the GPU is filled several times over
+  const int64_t rows = a.tokens * a.heads, fill = (int64_t)spc_host::sm_count() * 512;
+  a.per = (int32_t)std::max<int64_t>(1, std::min<int64_t>(8, rows / fill));
+  a.slices = (a.heads + a.per - 1) / a.per;
+  const int64_t blocks = (a.tokens * a.slices + 31) / 32;
+  if (blocks > 0x7FFFFFFF) return SPC_ERR_UNSUPPORTED;
+  if (d->interleaved)
+    rope_kernel<true><<<(unsigned)blocks, 256, 0, stream>>>(a);
+  else
+    rope_kernel<false><<<(unsigned)blocks, 256, 0, stream>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) {
+    spc_host::set_cuda_error(e);
+    return SPC_ERR_CUDA;
+  }
+  return SPC_OK;
+}
+
+}  // namespace spc

@@ -23,6 +23,16 @@ spc_status launch_host_gather(const spc_dims*, const uint16_t*, int64_t, const i
                               int32_t prev_k = 0);
 spc_status launch_append(const spc_dims*, const uint16_t*, const uint16_t*, void*, uint16_t*, uint16_t*, int64_t,
                          cudaStream_t);
+spc_status launch_rope(const spc_rope_dims*, const int32_t*, const uint64_t*, const uint16_t*, const uint16_t*,
+                       const uint16_t*, uint16_t*, uint16_t*, uint16_t*, cudaStream_t);
+size_t prompt_workspace_bytes(const spc_prompt_dims*);
+spc_status launch_prompt_attn(const spc_prompt_dims*, const uint16_t*, const uint16_t*, const uint16_t*,
+                              const int32_t*, const int32_t*, const int32_t*, const int32_t*, uint16_t*, float*,
+                              void*, cudaStream_t);
+spc_status launch_extend(const spc_dims*, int32_t, const uint16_t*, const uint16_t*, const spc_layout*,
+                         const spc_layout*, void*, uint16_t*, uint16_t*, int64_t, cudaStream_t);
+spc_status launch_dequantize(const spc_dims*, const void*, const uint16_t*, int32_t, int32_t, uint16_t*, uint16_t*,
+                             const spc_layout*, const spc_layout*, cudaStream_t);
 }  // namespace spc
 
 namespace spc_host {
@@ -527,6 +537,225 @@ spc_status spc_host_gather_prev(const spc_dims* d, const uint16_t* host_kv, int6
   return spc::launch_host_gather(d, static_cast<const uint16_t*>(dev), n_cap, idx, k, staging, max_ctas,
                                  reinterpret_cast<cudaStream_t>(stream), src,
                                  prev_k > 0 ? prev_staging : nullptr, prev_k);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- the prompt path
+namespace {
+
+// A view of [b][t][h][128] whose rows lie on 16-byte boundaries and apart from
+// one another: each stride, smallest first, clears what the smaller ones span
+// (an axis of one element is never stepped along).
+bool layout_ok(const spc_layout& l, int64_t nb, int64_t nt, int64_t nh) {
+  const int64_t lim = (int64_t)1 << 38;  // elements: 2^39 bytes, within a TMA stride's range
+  if (l.b % 8 != 0 || l.t % 8 != 0 || l.h % 8 != 0) return false;
+  if (l.b < 0 || l.t < 0 || l.h < 0 || l.b >= lim || l.t >= lim || l.h >= lim) return false;
+  int64_t st[3] = {l.b, l.t, l.h}, n[3] = {nb, nt, nh};
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2 - i; ++j)
+      if (st[j] > st[j + 1]) {
+        std::swap(st[j], st[j + 1]);
+        std::swap(n[j], n[j + 1]);
+      }
+  int64_t span = spc::kD;
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] <= 1) continue;
+    if (st[i] < span) return false;
+    span += st[i] * (n[i] - 1);  // below 2^38 * 2^31
+    if (span >= ((int64_t)1 << 60)) return false;
+  }
+  return true;
+}
+
+// Bytes from the view's first element to behind its last.
+size_t layout_bytes(const spc_layout& l, int64_t nb, int64_t nt, int64_t nh) {
+  if (nb <= 0 || nt <= 0 || nh <= 0) return 0;
+  return 2 * (size_t)((nb - 1) * l.b + (nt - 1) * l.t + (nh - 1) * l.h + spc::kD);
+}
+
+bool same_layout(const spc_layout& x, const spc_layout& y) { return x.b == y.b && x.t == y.t && x.h == y.h; }
+
+}  // namespace
+
+extern "C" {
+
+spc_status spc_rope_frequencies(const spc_rope_scaling* s, int32_t rot, uint64_t* turns, float* mscale) {
+  if (s == nullptr || turns == nullptr || mscale == nullptr) return SPC_ERR_INVALID;
+  if (rot < 16 || rot > spc::kD || rot % 16 != 0) return SPC_ERR_UNSUPPORTED;
+  if (s->kind < SPC_ROPE_PLAIN || s->kind > SPC_ROPE_RAMP) return SPC_ERR_INVALID;
+  if (!(std::isfinite(s->theta) && s->theta > 1.0)) return SPC_ERR_INVALID;
+  if (s->kind != SPC_ROPE_PLAIN && !(std::isfinite(s->factor) && s->factor >= 1.0)) return SPC_ERR_INVALID;
+  const bool by_turns = s->kind == SPC_ROPE_BANDS || s->kind == SPC_ROPE_RAMP;
+  if (by_turns && !(std::isfinite(s->high) && std::isfinite(s->context) && s->low > 0.0 && s->low < s->high &&
+                    s->context > 0.0))
+    return SPC_ERR_INVALID;
+  const double two_pi = 6.283185307179586476925286766559;
+  double from = 0.0, to = 0.0;  // RAMP: the pairs between which it falls
+  if (s->kind == SPC_ROPE_RAMP) {
+    const auto pair_of = [&](double n) { return rot * std::log(s->context / (n * two_pi)) / (2.0 * std::log(s->theta)); };
+    from = std::max(std::floor(pair_of(s->high)), 0.0);
+    to = std::min(std::ceil(pair_of(s->low)), (double)(rot - 1));
+  }
+  for (int32_t i = 0; i < rot / 2; ++i) {
+    double f = std::pow(s->theta, -2.0 * i / rot);
+    if (s->kind == SPC_ROPE_LINEAR) {
+      f /= s->factor;
+    } else if (s->kind == SPC_ROPE_BANDS) {
+      const double n = s->context * f / two_pi;
+      const double mix = std::min(1.0, std::max(0.0, (n - s->low) / (s->high - s->low)));
+      f = (1.0 - mix) * f / s->factor + mix * f;
+    } else if (s->kind == SPC_ROPE_RAMP) {
+      const double ramp = std::min(1.0, std::max(0.0, (i - from) / std::max(to - from, 0.001)));
+      f = f / s->factor * ramp + f * (1.0 - ramp);
+    }
+    turns[i] = (uint64_t)(f / two_pi * 18446744073709551616.0);  // f <= 1: below 2^62
+  }
+  *mscale = s->kind == SPC_ROPE_RAMP ? (float)(0.1 * std::log(s->factor) + 1.0) : 1.0f;
+  return SPC_OK;
+}
+
+spc_status spc_rope(const spc_rope_dims* d, const int32_t* pos, const uint64_t* turns, const uint16_t* q,
+                    const uint16_t* k, const uint16_t* v, uint16_t* q_out, uint16_t* k_out, uint16_t* v_out,
+                    spc_stream stream) {
+  if (d == nullptr || d->B <= 0 || d->T < 0 || d->Hq < 0 || d->Hkv < 0 || d->D <= 0) return SPC_ERR_INVALID;
+  if (d->Hq > (1 << 16) || d->Hkv > (1 << 16)) return SPC_ERR_INVALID;
+  if (d->interleaved != 0 && d->interleaved != 1) return SPC_ERR_INVALID;
+  if (!std::isfinite(d->mscale)) return SPC_ERR_INVALID;
+  if (d->D != spc::kD || d->rot < 16 || d->rot > spc::kD || d->rot % 16 != 0) return SPC_ERR_UNSUPPORTED;
+  if ((q == nullptr) != (q_out == nullptr) || (k == nullptr) != (k_out == nullptr) ||
+      (v == nullptr) != (v_out == nullptr))
+    return SPC_ERR_INVALID;
+  if (d->T == 0) return SPC_OK;
+  if ((q == nullptr) != (d->Hq == 0) || (k == nullptr) != (d->Hkv == 0) || (v != nullptr && d->Hkv == 0))
+    return SPC_ERR_INVALID;
+  if (q == nullptr && k == nullptr) return SPC_OK;
+  if (pos == nullptr || turns == nullptr || (reinterpret_cast<uintptr_t>(turns) & 7u) != 0) return SPC_ERR_INVALID;
+  const struct {
+    const uint16_t* in;
+    uint16_t* out;
+    const spc_layout *li, *lo;
+    int32_t heads;
+  } rows[3] = {{q, q_out, &d->q, &d->q_out, d->Hq},
+               {k, k_out, &d->k, &d->k_out, d->Hkv},
+               {v, v_out, &d->v, &d->v_out, d->Hkv}};
+  for (const auto& r : rows) {
+    if (r.in == nullptr) continue;
+    if (!aligned16(r.in) || !aligned16(r.out)) return SPC_ERR_INVALID;
+    if (!layout_ok(*r.li, d->B, d->T, r.heads) || !layout_ok(*r.lo, d->B, d->T, r.heads)) return SPC_ERR_INVALID;
+    // in place is the same view; any other output that reaches into its input would race with the reads
+    if (!(r.in == r.out && same_layout(*r.li, *r.lo)) &&
+        overlap(r.in, layout_bytes(*r.li, d->B, d->T, r.heads), r.out, layout_bytes(*r.lo, d->B, d->T, r.heads)))
+      return SPC_ERR_INVALID;
+  }
+  return spc::launch_rope(d, pos, turns, q, k, v, q_out, k_out, v_out, reinterpret_cast<cudaStream_t>(stream));
+}
+
+static spc_status check_prompt_dims(const spc_prompt_dims* d) {
+  if (d == nullptr || d->S <= 0 || d->Hq <= 0 || d->Hkv <= 0 || d->D <= 0 || d->q_tokens < 0 || d->k_tokens < 0 ||
+      d->q_max < 0 || d->k_max < 0 || d->q_max > d->q_tokens || d->k_max > d->k_tokens)
+    return SPC_ERR_INVALID;
+  if (d->Hq % d->Hkv != 0 || !(std::isfinite(d->scale) && d->scale > 0.f)) return SPC_ERR_INVALID;
+  if (d->D != spc::kD || d->Hq / d->Hkv > 128) return SPC_ERR_UNSUPPORTED;
+  if (d->q_tokens >= (1 << 30) || d->k_tokens >= (1 << 30)) return SPC_ERR_UNSUPPORTED;
+  if (d->S > 1 && ((d->q.b == 0) != (d->o.b == 0) || (d->k.b == 0) != (d->v.b == 0))) return SPC_ERR_INVALID;
+  const int64_t qb = d->q.b ? d->S : 1, kb = d->k.b ? d->S : 1;
+  if (!layout_ok(d->q, qb, d->q_tokens, d->Hq) || !layout_ok(d->o, qb, d->q_tokens, d->Hq) ||
+      !layout_ok(d->k, kb, d->k_tokens, d->Hkv) || !layout_ok(d->v, kb, d->k_tokens, d->Hkv))
+    return SPC_ERR_INVALID;
+  // the grid numbers pairs of query tiles, KV heads, sequences and splits
+  const int64_t pairs = (int64_t)d->q_max * (d->Hq / d->Hkv) / 128 + 2;
+  if ((int64_t)d->S * d->Hkv > (1 << 30) / pairs) return SPC_ERR_UNSUPPORTED;
+  return SPC_OK;
+}
+
+size_t spc_prompt_attn_workspace_bytes(const spc_prompt_dims* d) {
+  return check_prompt_dims(d) == SPC_OK ? spc::prompt_workspace_bytes(d) : 0;
+}
+
+spc_status spc_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                           const int32_t* q_begin, const int32_t* q_len, const int32_t* k_begin,
+                           const int32_t* k_len, uint16_t* o, float* lse, void* ws, size_t ws_bytes,
+                           spc_stream stream) {
+  spc_status st = check_prompt_dims(d);
+  if (st != SPC_OK) return st;
+  if (d->q_max == 0) return SPC_OK;
+  if (q == nullptr || o == nullptr || (d->k_max > 0 && (k == nullptr || v == nullptr))) return SPC_ERR_INVALID;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return SPC_ERR_INVALID;
+  if (ws == nullptr || !aligned16(ws)) return SPC_ERR_INVALID;
+  if (ws_bytes < spc::prompt_workspace_bytes(d)) return SPC_ERR_WORKSPACE;
+  return spc::launch_prompt_attn(d, q, k, v, q_begin, q_len, k_begin, k_len, o, lse, ws,
+                                 reinterpret_cast<cudaStream_t>(stream));
+}
+
+spc_status spc_prompt_attn_status(void* ws, spc_stream stream) {
+  if (ws == nullptr) return SPC_ERR_INVALID;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  uint32_t v = 0;
+  cudaError_t e = cudaMemcpyAsync(&v, ws, sizeof(v), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess && v != 0u) e = cudaMemsetAsync(ws, 0, sizeof(v), s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) {
+    spc_host::set_cuda_error(e);
+    return SPC_ERR_CUDA;
+  }
+  return v != 0u ? SPC_ERR_TIMEOUT : SPC_OK;
+}
+
+spc_status spc_extend_kv(const spc_dims* d, int32_t n, const uint16_t* k_new, const uint16_t* v_new,
+                         const spc_layout* k_layout, const spc_layout* v_layout, void* records, uint16_t* resid,
+                         uint16_t* host_kv, int64_t n_cap, spc_stream stream) {
+  spc_status st = check_dims(d);
+  if (st != SPC_OK) return st;
+  if (n < 0 || (int64_t)d->N + n > (1 << 30)) return SPC_ERR_INVALID;
+  if (n == 0) return SPC_OK;
+  spc_dims after = *d;
+  after.N += n;
+  st = check_dims(&after);  // the capacities hold the extended cache
+  if (st != SPC_OK) return st;
+  const int32_t nq = spc::num_quantized(d->N, d->R, d->group), nq1 = spc::num_quantized(after.N, d->R, d->group);
+  if (k_new == nullptr || v_new == nullptr || k_layout == nullptr || v_layout == nullptr) return SPC_ERR_INVALID;
+  if (nq1 > nq && records == nullptr) return SPC_ERR_INVALID;
+  if ((d->N > nq || after.N > nq1) && resid == nullptr) return SPC_ERR_INVALID;
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(records) || !aligned16(resid) || !aligned16(host_kv))
+    return SPC_ERR_INVALID;
+  if (!layout_ok(*k_layout, d->B, n, d->Hkv) || !layout_ok(*v_layout, d->B, n, d->Hkv)) return SPC_ERR_INVALID;
+  const size_t res = spc_resid_bytes(d), rec = spc_records_bytes(d);
+  const size_t kb = layout_bytes(*k_layout, d->B, n, d->Hkv), vb = layout_bytes(*v_layout, d->B, n, d->Hkv);
+  if (overlap(k_new, kb, resid, res) || overlap(v_new, vb, resid, res) || overlap(k_new, kb, records, rec) ||
+      overlap(v_new, vb, records, rec))
+    return SPC_ERR_INVALID;
+  const void* host_dev = nullptr;
+  if (host_kv != nullptr) {
+    if (n_cap < after.N) return SPC_ERR_INVALID;
+    st = mapped_device_pointer(host_kv, &host_dev);
+    if (st != SPC_OK) return st;
+  }
+  return spc::launch_extend(d, n, k_new, v_new, k_layout, v_layout, records, resid,
+                            static_cast<uint16_t*>(const_cast<void*>(host_dev)), n_cap,
+                            reinterpret_cast<cudaStream_t>(stream));
+}
+
+spc_status spc_dequantize_kv(const spc_dims* d, const void* records, const uint16_t* resid, int32_t first, int32_t n,
+                             uint16_t* k, uint16_t* v, const spc_layout* k_layout, const spc_layout* v_layout,
+                             spc_stream stream) {
+  spc_status st = check_dims(d);
+  if (st != SPC_OK) return st;
+  if (first < 0 || n < 0 || (int64_t)first + n > d->N) return SPC_ERR_INVALID;
+  if (n == 0) return SPC_OK;
+  const int32_t nq = spc::num_quantized(d->N, d->R, d->group);
+  if (k == nullptr || v == nullptr || k_layout == nullptr || v_layout == nullptr) return SPC_ERR_INVALID;
+  if ((first < nq && records == nullptr) || (first + n > nq && resid == nullptr)) return SPC_ERR_INVALID;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(records) || !aligned16(resid)) return SPC_ERR_INVALID;
+  if (!layout_ok(*k_layout, d->B, n, d->Hkv) || !layout_ok(*v_layout, d->B, n, d->Hkv)) return SPC_ERR_INVALID;
+  const size_t res = spc_resid_bytes(d), rec = spc_records_bytes(d);
+  const size_t kb = layout_bytes(*k_layout, d->B, n, d->Hkv), vb = layout_bytes(*v_layout, d->B, n, d->Hkv);
+  if (overlap(k, kb, resid, res) || overlap(v, vb, resid, res) || overlap(k, kb, records, rec) ||
+      overlap(v, vb, records, rec))
+    return SPC_ERR_INVALID;
+  return spc::launch_dequantize(d, records, resid, first, n, k, v, k_layout, v_layout,
+                                reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -365,6 +365,156 @@ spc_status spc_offload_kv(const spc_dims* d, const uint16_t* k, const uint16_t* 
                           int64_t n_cap, spc_stream stream);
 
 /*
+ * Where the elements of a [batch][token][head][D] tensor lie: strides in
+ * elements (bf16); the D elements of a head's row are contiguous.  Strides are
+ * multiples of 8 (rows on 16-byte boundaries); t and h are positive, b is not
+ * negative, and no two rows share a byte.  The calls below take such views, so
+ * that projections are used where they are: a fused projection
+ * [B][T][Hq + 2 Hkv][D] is three views of it, and a cache buffer
+ * [B][Hkv][cap][D] is the view {Hkv*cap*D, D, cap*D}.
+ */
+typedef struct spc_layout {
+  int64_t b, t, h;
+} spc_layout;
+
+/*
+ * Rotary positions.  Pair i (0 <= i < rot/2) of a head's row at position p is
+ * turned by the angle p * f_i and scaled by mscale:
+ *   (x, y) -> mscale * (x cos - y sin, x sin + y cos),
+ * elements rot..D-1 stay as they are.  Pairs are (i, i + rot/2) (the half
+ * layout) or (2i, 2i + 1) (interleaved).  The frequencies are kept as 64-bit
+ * fractions of a turn per position, turns[i] = 2^64 f_i / 2 pi: the angle is
+ * the integer product p * turns[i] mod 2^64, exact at any position, so far
+ * positions lose nothing.
+ */
+typedef enum spc_rope_kind {
+  SPC_ROPE_PLAIN = 0,  /* f_i = theta^(-2i/rot) */
+  SPC_ROPE_LINEAR = 1, /* f_i / factor (positions stretched) */
+  SPC_ROPE_BANDS = 2,  /* by the pair's turns within context positions: at least high: f_i; at most low:
+                          f_i / factor; between, the straight mix of the two in the number of turns */
+  SPC_ROPE_RAMP = 3    /* by the pair's index ("YaRN", arXiv 2309.00071): f_i up to the pair that makes `high`
+                          turns within context (rounded down), f_i / factor from the one that makes `low` on
+                          (rounded up), a straight ramp between; mscale = 0.1 ln(factor) + 1 */
+} spc_rope_kind;
+
+typedef struct spc_rope_scaling {
+  int32_t kind;     /* spc_rope_kind */
+  double theta;     /* base, > 1 */
+  double factor;    /* >= 1; not PLAIN */
+  double low, high; /* BANDS, RAMP: numbers of turns, 0 < low < high (e.g. 1 and 4; 1 and 32) */
+  double context;   /* BANDS, RAMP: positions of the unscaled context, > 0 */
+} spc_rope_scaling;
+
+/* Fills turns (HOST, rot/2 words; the caller uploads them once) and mscale
+ * (HOST) for a rule.  A host-side computation in binary64. */
+spc_status spc_rope_frequencies(const spc_rope_scaling* s, int32_t rot, uint64_t* turns, float* mscale);
+
+typedef struct spc_rope_dims {
+  int32_t B, T, Hq, Hkv, D; /* D = 128 */
+  int32_t rot;              /* rotated elements of a head: a multiple of 16, 16 .. 128 */
+  int32_t interleaved;      /* 0: pairs (i, i + rot/2); 1: pairs (2i, 2i + 1) */
+  float mscale;             /* finite; 1 for most rules */
+  spc_layout q, k, v, q_out, k_out, v_out;
+} spc_rope_dims;
+
+/*
+ * Rotates T tokens' query and key rows, and copies their value rows, from the
+ * projection to where they are used (the cache's rows, say), in one launch.
+ *   pos    : int32 [B][T] (device), each token's position; any int32.
+ *   turns  : uint64 [rot/2] (device).
+ *   q, k   : bf16 views [B][T][Hq][D] and [B][T][Hkv][D]; v [B][T][Hkv][D] or
+ *            NULL (no values).  Either of q and k may be NULL with Hq or
+ *            Hkv 0 (v needs Hkv).
+ *   *_out  : where the rows go; in place when pointer and layout equal the
+ *            input's, else sharing no byte range with it.  No output row may
+ *            share a byte with another tensor's rows.
+ * Products and sums are binary32 (fused), rounded once to bf16.
+ */
+spc_status spc_rope(const spc_rope_dims* d, const int32_t* pos, const uint64_t* turns, const uint16_t* q,
+                    const uint16_t* k, const uint16_t* v, uint16_t* q_out, uint16_t* k_out, uint16_t* v_out,
+                    spc_stream stream);
+
+/*
+ * Causal attention of prompts over 16-bit keys and values (SpeCache page,
+ * section 3 "Prefilling": the attention that Quant and Offload follow).
+ * S sequences; sequence s has lq query tokens, the last of its lk tokens, and
+ * query i sees keys j <= i + lk - lq:
+ *   o_i = sum_j softmax_j(scale * q_i.k_j) v_j,  lse_i the natural log of the
+ * normaliser.  Query head h uses KV head h / G, G = Hq / Hkv (1 .. 128).  A
+ * query that sees no key (lk < lq) gets o = 0 and lse = -infinity.
+ * What keys and values hold in places that a query does not see does not
+ * change its output, infinities and NaN included.
+ */
+typedef struct spc_prompt_dims {
+  int32_t S, Hq, Hkv, D;      /* D = 128 */
+  int32_t q_tokens, k_tokens; /* tokens that the token axes of q, o and of k, v hold */
+  int32_t q_max, k_max;       /* no sequence has more query tokens / keys than these */
+  float scale;
+  spc_layout q, k, v, o;      /* b = 0: the sequences lie on one token axis (packed); else sequence s at s * b.
+                                 q and o alike, k and v alike */
+} spc_prompt_dims;
+
+/* Bytes of device workspace of spc_prompt_attn on the current device: a status
+ * word (256 bytes; zero-filled once by the caller for
+ * spc_prompt_attn_status, never needed otherwise) and, where few queries leave
+ * SMs idle and the keys are split, the splits' partial results.  Calls that
+ * share a workspace must not overlap on the GPU.  0 for an invalid shape. */
+size_t spc_prompt_attn_workspace_bytes(const spc_prompt_dims* d);
+
+/*
+ *   q, k, v : bf16 views; k and v may be NULL when k_max = 0.
+ *   q_begin, q_len, k_begin, k_len : int32 [S] (device) or NULL: each
+ *            sequence's first token on its token axis (NULL: 0) and its
+ *            length (NULL: q_max, k_max).  Values are held to the tensors
+ *            (0 .. q_tokens and so on) and to q_max, k_max.
+ *   o       : bf16, rows of no sequence are left as they were; sequences'
+ *            rows must not overlap, nor share bytes with an input.
+ *   lse     : fp32 [q_tokens][Hq] (packed) or [S][q_tokens][Hq], or NULL.
+ *   ws      : at least spc_prompt_attn_workspace_bytes(d) bytes.
+ * One launch, and a second, small one where the keys are split.
+ */
+spc_status spc_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                           const int32_t* q_begin, const int32_t* q_len, const int32_t* k_begin,
+                           const int32_t* k_len, uint16_t* o, float* lse, void* ws, size_t ws_bytes,
+                           spc_stream stream);
+
+/* Reads and clears the status word of a workspace of spc_prompt_attn:
+ * SPC_ERR_TIMEOUT if a bounded wait ran out since, else SPC_OK.  Synchronises
+ * `stream`. */
+spc_status spc_prompt_attn_status(void* ws, spc_stream stream);
+
+/*
+ * A run of n new tokens joins the cache (SpeCache page, Algorithm 1 for a
+ * prompt: d->N = 0; a follow-up prompt of a conversation: d->N > 0).  The
+ * result is bit-identical to n calls of spc_append_kv, and so to
+ * spc_quantize_kv over all N + n tokens.  d describes the cache BEFORE the
+ * call; the caller then advances d->N by n.
+ *   k_new, v_new: bf16 views [B][n][Hkv][D] of the tokens N .. N+n-1 (device).
+ *   records, resid: the cache (device), updated in place.
+ *   host_kv: HOST pointer to the pinned, mapped cache [B][Hkv][n_cap][2][D]
+ *            (rows N .. N+n-1 are written), or NULL for no offload;
+ *            SPC_ERR_NOT_MAPPED if not mapped; n_cap >= N + n.
+ * Needs q_groups_cap >= N_q'/32 and resid_cap >= N + n - N_q' and the old
+ * N - N_q (SPC_ERR_INVALID otherwise), N_q' the quantised tokens of N + n.
+ */
+spc_status spc_extend_kv(const spc_dims* d, int32_t n, const uint16_t* k_new, const uint16_t* v_new,
+                         const spc_layout* k_layout, const spc_layout* v_layout, void* records, uint16_t* resid,
+                         uint16_t* host_kv, int64_t n_cap, spc_stream stream);
+
+/*
+ * Reads tokens first .. first+n-1 of the cache back as 16-bit rows, for a
+ * follow-up prompt's attention over the history: a quantised token's elements
+ * are fl(z + fl(s * code)) in binary32 (z and s from the group's min and max
+ * as under spc_records_bytes), rounded once to bf16; a residual token's are
+ * its 16-bit rows.
+ *   k, v: bf16 views [B][n][Hkv][D] (device); other rows are left as they were.
+ * first >= 0, n >= 0, first + n <= N.
+ */
+spc_status spc_dequantize_kv(const spc_dims* d, const void* records, const uint16_t* resid, int32_t first, int32_t n,
+                             uint16_t* k, uint16_t* v, const spc_layout* k_layout, const spc_layout* v_layout,
+                             spc_stream stream);
+
+/*
  * Decode-time append (SpeCache page, section 3 "Decoding", Algorithm 3: the
  * new token's K/V joins the cache; section 3: the full-precision cache is
  * offloaded to CPU memory).  d describes the cache BEFORE the call: N tokens
