@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes as C
 import math
 import os
+import struct
 
 import torch
 
@@ -91,7 +92,6 @@ class spc_prompt_dims(C.Structure):
 
 _P = C.c_void_p
 _D = C.POINTER(spc_dims)
-_L = C.POINTER(spc_layout)
 _sig = {
     "spc_abi_version": (C.c_int32, []),
     "spc_status_string": (C.c_char_p, [C.c_int]),
@@ -125,12 +125,12 @@ _sig = {
                                        _P]),
     "spc_read_device_status": (C.c_int, [_P, _D, _P]),
     "spc_rope_frequencies": (C.c_int, [C.POINTER(spc_rope_scaling), C.c_int32, _P, C.POINTER(C.c_float)]),
-    "spc_rope": (C.c_int, [C.POINTER(spc_rope_dims), _P, _P, _P, _P, _P, _P, _P, _P, _P]),
-    "spc_prompt_attn_workspace_bytes": (C.c_size_t, [C.POINTER(spc_prompt_dims)]),
-    "spc_prompt_attn": (C.c_int, [C.POINTER(spc_prompt_dims), _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, C.c_size_t, _P]),
+    "spc_rope": (C.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "spc_prompt_attn_workspace_bytes": (C.c_size_t, [_P]),
+    "spc_prompt_attn": (C.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, C.c_size_t, _P]),
     "spc_prompt_attn_status": (C.c_int, [_P, _P]),
-    "spc_extend_kv": (C.c_int, [_D, C.c_int32, _P, _P, _L, _L, _P, _P, _P, C.c_int64, _P]),
-    "spc_dequantize_kv": (C.c_int, [_D, _P, _P, C.c_int32, C.c_int32, _P, _P, _L, _L, _P]),
+    "spc_extend_kv": (C.c_int, [_D, C.c_int32, _P, _P, _P, _P, _P, _P, _P, C.c_int64, _P]),
+    "spc_dequantize_kv": (C.c_int, [_D, _P, _P, C.c_int32, C.c_int32, _P, _P, _P, _P, _P]),
 }
 for _name, (_res, _args) in _sig.items():
     _f = getattr(_lib, _name)
@@ -317,37 +317,59 @@ def spc_host_gather_prev(d, host_kv, n_cap, idx, k, staging, src, prev_staging, 
 # These calls take tensors of any strides (views of a fused projection, of a
 # cache buffer), so they read shapes and strides from the tensors and check
 # what a pointer cannot say: rank, shapes, 16-bit elements, the last axis
-# contiguous, and that every tensor is on the current CUDA device.
+# contiguous, and that every tensor is on the current CUDA device.  The dims
+# structs are packed in one go: short calls are bound by this marshalling.
 
 ROPE_KINDS = {"plain": 0, "linear": 1, "bands": 2, "ramp": 3}
 
+_ROWS = frozenset((torch.bfloat16, torch.int16, torch.uint16))  # bf16 values or their bit patterns
+_ROPE = struct.Struct("=7if18q")
+_PROMPT = struct.Struct("=8if4x12q")
+_LAYOUT = struct.Struct("=3q")
+assert _ROPE.size == C.sizeof(spc_rope_dims) and _PROMPT.size == C.sizeof(spc_prompt_dims)
 
-def _on_device(fn, name, t):
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{fn}: {name} must be on the current CUDA device")
+
+def _device(fn, t):
+    """The current device's index; the call's first tensor is on it."""
+    if t.get_device() < 0:
+        raise ValueError(f"{fn}: tensors must be on the current CUDA device, got one on {t.device}")
+    return torch._C._cuda_getDevice()
 
 
-def _rows(fn, name, t, shape=None):
-    """(shape, layout) of a 16-bit [batch][token][head][D] tensor, or of packed [token][head][D]."""
-    if t.dim() not in (3, 4) or t.element_size() != 2:
-        raise ValueError(f"{fn}: {name} must be a 16-bit tensor [batch][token][head][D] (or packed, without the batch)")
-    _on_device(fn, name, t)
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+def _raw_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _view(fn, name, t, dev):
+    """Sizes [batch, token, head, D] and strides [b, t, h] of a tensor, packed ones with a batch of 1 (an axis of one
+    element has stride 0)."""
+    n, st = t.shape, t.stride()
+    if t.dtype not in _ROWS or t.get_device() != dev:
+        raise ValueError(f"{fn}: {name} must hold bf16 rows (bfloat16, or int16 patterns) on the current CUDA device, "
+                         f"got {t.dtype} on {t.device}")
+    if len(n) == 4:
+        (b, T, h, D), (sb, sT, sh, sd) = n, st
+    elif len(n) == 3:
+        (T, h, D), (sT, sh, sd) = n, st
+        b, sb = 1, 0
+    else:
+        raise ValueError(f"{fn}: {name} must be [batch][token][head][D] (or packed, without the batch)")
+    if sd != 1 and D > 1:
         raise ValueError(f"{fn}: the last axis of {name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    n, st = tuple(t.shape), t.stride()
-    if t.dim() == 3:
-        n, st = (1,) + n, (0,) + tuple(st)
-    return n, spc_layout(st[0] if n[0] > 1 else 0, st[1] if n[1] > 1 else 0, st[2] if n[2] > 1 else 0)
+    return b, T, h, D, (sb if b > 1 else 0, sT if T > 1 else 0, sh if h > 1 else 0)
 
 
-def _words(fn, name, t, dtype, n):
+def _like(fn, name, t, dev, ref):
+    if t.shape != ref.shape:
+        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(ref.shape)}")
+    return _view(fn, name, t, dev)[4]
+
+
+def _words(fn, name, t, dtype, n, dev):
     if t is None:
         return None
-    _on_device(fn, name, t)
-    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor of {n} elements")
+    if t.dtype != dtype or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor of {n} elements on the current CUDA device")
     return t.data_ptr()
 
 
@@ -356,14 +378,13 @@ def spc_rope_frequencies(rot=128, theta=10000.0, kind="plain", factor=1.0, low=1
     of rot/2 64-bit fractions of a turn per position; move it to the device
     once), mscale the factor of the result.  kind: "plain", "linear",
     "bands" or "ramp" (see spc_rope_kind in include/spc.h)."""
+    if kind not in ROPE_KINDS:
+        raise ValueError(f"spc_rope_frequencies: kind is one of {', '.join(ROPE_KINDS)}, got {kind!r}")
     s = spc_rope_scaling(ROPE_KINDS[kind], theta, factor, low, high, context)
-    turns = torch.empty(max(int(rot), 0) // 2, dtype=torch.int64)
     mscale = C.c_float()
     buf = (C.c_uint64 * 64)()
     _check("spc_rope_frequencies", _lib.spc_rope_frequencies(C.byref(s), int(rot), buf, C.byref(mscale)))
-    for i in range(turns.numel()):
-        turns[i] = buf[i]  # below 2^62: positive as int64 too
-    return turns, mscale.value
+    return torch.tensor(buf[:int(rot) // 2], dtype=torch.int64), mscale.value  # below 2^62: positive as int64 too
 
 
 def spc_rope(q, k, pos, turns, rot=128, interleaved=False, mscale=1.0, v=None, q_out=None, k_out=None, v_out=None,
@@ -371,50 +392,59 @@ def spc_rope(q, k, pos, turns, rot=128, interleaved=False, mscale=1.0, v=None, q
     """q [B][T][Hq][D], k (and v) [B][T][Hkv][D], q or k None; the outputs of q
     and k default to in place (v is copied, so it needs v_out)."""
     fn = "spc_rope"
-    if q is None and k is None:
+    x = k if q is None else q
+    if x is None:
         raise ValueError(f"{fn}: neither q nor k")
-    d = spc_rope_dims(D=128, rot=int(rot), interleaved=int(bool(interleaved)), mscale=mscale)
-    ptr = {}
-    for name, x, out in (("q", q, q_out), ("k", k, k_out), ("v", v, v_out)):
-        if x is None:
-            if out is not None:
-                raise ValueError(f"{fn}: {name}_out without {name}")
-            ptr[name] = ptr[name + "_out"] = None
-            continue
-        if name == "v" and (out is None or k is None or x.shape != k.shape):
-            raise ValueError(f"{fn}: v has k's shape and needs v_out")
-        out = x if out is None else out
-        (B, T, H, D), lay = _rows(fn, name, x)
-        _, lay_out = _rows(fn, name + "_out", out, x.shape)
-        if d.B and (d.B, d.T) != (B, T):
-            raise ValueError(f"{fn}: q and k differ in batch or tokens")
-        d.B, d.T, d.D = B, T, D
-        setattr(d, name, lay)
-        setattr(d, name + "_out", lay_out)
-        if name != "v":
-            setattr(d, "Hq" if name == "q" else "Hkv", H)
-        ptr[name], ptr[name + "_out"] = x.data_ptr(), out.data_ptr()
-    pos = _words(fn, "pos", pos, torch.int32, d.B * d.T)
-    turns = _words(fn, "turns", turns, torch.int64, max(d.rot, 0) // 2)
-    if d.T == 0:
+    dev = _device(fn, x)
+    none = (0, 0, 0)
+    ql = kl = vl = qo = ko = vo = none
+    qp = kp = vp = qop = kop = vop = None
+    Hq = Hkv = 0
+    if q is not None:
+        B, T, Hq, D, ql = _view(fn, "q", q, dev)
+        qp = qop = q.data_ptr()
+        qo = ql
+        if q_out is not None:
+            qo, qop = _like(fn, "q_out", q_out, dev, q), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError(f"{fn}: q_out without q")
+    if k is not None:
+        Bk, Tk, Hkv, Dk, kl = _view(fn, "k", k, dev)
+        if q is None:
+            B, T, D = Bk, Tk, Dk
+        elif (Bk, Tk, Dk) != (B, T, D):
+            raise ValueError(f"{fn}: q and k differ in batch, tokens or row")
+        kp = kop = k.data_ptr()
+        ko = kl
+        if k_out is not None:
+            ko, kop = _like(fn, "k_out", k_out, dev, k), k_out.data_ptr()
+    elif k_out is not None or v is not None:
+        raise ValueError(f"{fn}: k_out or v without k")
+    if (v is None) != (v_out is None):
+        raise ValueError(f"{fn}: v is copied, so v and v_out go together")
+    if v is not None:
+        vl, vo = _like(fn, "v", v, dev, k), _like(fn, "v_out", v_out, dev, k)
+        vp, vop = v.data_ptr(), v_out.data_ptr()
+    pos = _words(fn, "pos", pos, torch.int32, B * T, dev)
+    turns = _words(fn, "turns", turns, torch.int64, rot // 2, dev)
+    if T == 0:
         return
-    _check(fn, _lib.spc_rope(C.byref(d), pos, turns, ptr["q"], ptr["k"], ptr["v"], ptr["q_out"], ptr["k_out"],
-                             ptr["v_out"], _stream(stream)))
+    d = _ROPE.pack(B, T, Hq, Hkv, D, rot, 1 if interleaved else 0, mscale, *ql, *kl, *vl, *qo, *ko, *vo)
+    st = _lib.spc_rope(d, pos, turns, qp, kp, vp, qop, kop, vop, _raw_stream(stream, dev))
+    if st:
+        raise SpcError(fn, st)
 
 
-def _prompt_dims(fn, q, k, v, o, S, q_max, k_max, scale):
-    (qs, qt, Hq, D), ql = _rows(fn, "q", q)
-    (ks, kt, Hkv, Dk), kl = _rows(fn, "k", k)
-    _, vl = _rows(fn, "v", v, k.shape)
-    _, ol = _rows(fn, "o", o, q.shape)
+def _prompt_dims(fn, q, k, v, o, S, q_max, k_max, scale, dev):
+    qs, qt, Hq, D, ql = _view(fn, "q", q, dev)
+    ks, kt, Hkv, Dk, kl = _view(fn, "k", k, dev)
+    vl, ol = _like(fn, "v", v, dev, k), _like(fn, "o", o, dev, q)
     if Dk != D:
         raise ValueError(f"{fn}: q has rows of {D} elements, k of {Dk}")
-    for name, t, n in (("q", q, qs), ("k", k, ks)):
-        if t.dim() == 4 and n != S:
-            raise ValueError(f"{fn}: {name} has a batch of {n}, and there are {S} sequences")
-    scale = 1.0 / math.sqrt(D) if scale is None else scale
-    return spc_prompt_dims(S, Hq, Hkv, D, qt, kt, qt if q_max is None else int(q_max),
-                           kt if k_max is None else int(k_max), scale, ql, kl, vl, ol)
+    if (qs != S and q.dim() == 4) or (ks != S and k.dim() == 4):
+        raise ValueError(f"{fn}: batches of {qs} and {ks}, and there are {S} sequences")
+    return _PROMPT.pack(S, Hq, Hkv, D, qt, kt, qt if q_max is None else q_max, kt if k_max is None else k_max,
+                        D ** -0.5 if scale is None else scale, *ql, *kl, *vl, *ol)
 
 
 def _sequences(q, k, *words):
@@ -426,9 +456,9 @@ def _sequences(q, k, *words):
 
 def spc_prompt_attn_workspace_bytes(q, k, v, o, S=None, q_max=None, k_max=None) -> int:
     """Bytes of workspace of spc_prompt_attn over these tensors (S sequences; default: the batch)."""
-    d = _prompt_dims("spc_prompt_attn_workspace_bytes", q, k, v, o, _sequences(q, k) if S is None else int(S), q_max,
-                     k_max, None)
-    return int(_lib.spc_prompt_attn_workspace_bytes(C.byref(d)))
+    fn = "spc_prompt_attn_workspace_bytes"
+    d = _prompt_dims(fn, q, k, v, o, _sequences(q, k) if S is None else S, q_max, k_max, None, _device(fn, q))
+    return int(_lib.spc_prompt_attn_workspace_bytes(d))
 
 
 def spc_prompt_attn(q, k, v, o, lse=None, q_begin=None, q_len=None, k_begin=None, k_len=None, q_max=None, k_max=None,
@@ -440,22 +470,30 @@ def spc_prompt_attn(q, k, v, o, lse=None, q_begin=None, q_len=None, k_begin=None
     workspace is taken from torch's allocator for the call, which needs the
     call to be on the current stream."""
     fn = "spc_prompt_attn"
-    S = _sequences(q, k, q_begin, q_len, k_begin, k_len)
-    d = _prompt_dims(fn, q, k, v, o, S, q_max, k_max, scale)
-    at = [_words(fn, n, t, torch.int32, S) for n, t in (("q_begin", q_begin), ("q_len", q_len), ("k_begin", k_begin),
-                                                       ("k_len", k_len))]
-    lse_ptr = _words(fn, "lse", lse, torch.float32, q.numel() // max(d.D, 1))
+    dev = _device(fn, q)
+    S = _sequences(q, k, q_len, k_len, q_begin, k_begin)
+    d = _prompt_dims(fn, q, k, v, o, S, q_max, k_max, scale, dev)
+    i32 = torch.int32
+    qb, ql = _words(fn, "q_begin", q_begin, i32, S, dev), _words(fn, "q_len", q_len, i32, S, dev)
+    kb, kl = _words(fn, "k_begin", k_begin, i32, S, dev), _words(fn, "k_len", k_len, i32, S, dev)
+    lse_ptr = None if lse is None else _words(fn, "lse", lse, torch.float32, q.numel() // max(q.shape[-1], 1), dev)
+    s = _raw_stream(stream, dev)
     if ws is None:
-        if stream is not None and _stream(stream) != _stream(None):
+        if stream is not None and s != _raw_stream(None, dev):
             raise ValueError(f"{fn}: a call on another stream than the current one needs ws")
-        need = int(_lib.spc_prompt_attn_workspace_bytes(C.byref(d)))
-        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    elif not isinstance(ws, int):
-        _on_device(fn, "ws", ws)
-    if ws_bytes is None:
-        ws_bytes = ws.numel() * ws.element_size()
-    _check(fn, _lib.spc_prompt_attn(C.byref(d), q.data_ptr(), k.data_ptr(), v.data_ptr(), *at, o.data_ptr(), lse_ptr,
-                                    _ptr(ws), ws_bytes, _stream(stream)))
+        ws_bytes = max(_lib.spc_prompt_attn_workspace_bytes(d), 16)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+        w = ws.data_ptr()
+    else:
+        if not isinstance(ws, int) and ws.get_device() != dev:
+            raise ValueError(f"{fn}: ws must be on the current CUDA device")
+        w = _ptr(ws)
+        if ws_bytes is None:
+            ws_bytes = ws.numel() * ws.element_size()
+    st = _lib.spc_prompt_attn(d, q.data_ptr(), k.data_ptr(), v.data_ptr(), qb, ql, kb, kl, o.data_ptr(), lse_ptr, w,
+                              ws_bytes, s)
+    if st:
+        raise SpcError(fn, st)
 
 
 def spc_prompt_attn_status(ws, stream=None) -> int:
@@ -463,39 +501,39 @@ def spc_prompt_attn_status(ws, stream=None) -> int:
     return int(_lib.spc_prompt_attn_status(_ptr(ws), _stream(stream)))
 
 
-def _cache_rows(fn, d, names, tensors, n):
-    got = []
-    for name, t in zip(names, tensors):
-        if t.dim() != 4:
-            raise ValueError(f"{fn}: {name} must be a 16-bit tensor [B][n][Hkv][D]")
-        got.append(_rows(fn, name, t, (d.B, n, d.Hkv, d.D))[1])
-    return got
-
-
-def _cache(fn, d, records, resid):
-    for name, t, need in (("records", records, spc_records_bytes(d)), ("resid", resid, spc_resid_bytes(d))):
+def _cache_call(fn, d, names, k, v, records, resid):
+    """(n, packed layouts of k and v, pointers of the cache, device) of a call on a run of tokens."""
+    dev = _device(fn, k)
+    B, n, h, D, kl = _view(fn, names[0], k, dev)
+    if k.dim() != 4 or (B, h, D) != (d.B, d.Hkv, d.D):
+        raise ValueError(f"{fn}: {names[0]} has shape {tuple(k.shape)}, expected [{d.B}][n][{d.Hkv}][{d.D}]")
+    vl = _like(fn, names[1], v, dev, k)
+    ptr = []
+    for name, t, need in (("records", records, _lib.spc_records_bytes), ("resid", resid, _lib.spc_resid_bytes)):
         if t is None or isinstance(t, int):
+            ptr.append(t)
             continue
-        _on_device(fn, name, t)
-        if not t.is_contiguous() or t.numel() * t.element_size() < need:
-            raise ValueError(f"{fn}: {name} must be contiguous and hold {need} bytes")
+        if t.get_device() != dev or not t.is_contiguous() or t.numel() * t.element_size() < need(C.byref(d)):
+            raise ValueError(f"{fn}: {name} must be contiguous on the current CUDA device and hold {need(C.byref(d))} bytes")
+        ptr.append(t.data_ptr())
+    return n, _LAYOUT.pack(*kl), _LAYOUT.pack(*vl), ptr, dev
 
 
 def spc_extend_kv(d, k_new, v_new, records, resid, host_kv=None, n_cap=0, stream=None):
     """k_new, v_new: 16-bit [B][n][Hkv][D] of any strides; the caller advances d.N by n."""
-    n = k_new.shape[1] if k_new.dim() == 4 else 0
-    lk, lv = _cache_rows("spc_extend_kv", d, ("k_new", "v_new"), (k_new, v_new), n)
-    _cache("spc_extend_kv", d, records, resid)
-    _check("spc_extend_kv", _lib.spc_extend_kv(C.byref(d), n, k_new.data_ptr(), v_new.data_ptr(), C.byref(lk),
-                                               C.byref(lv), _ptr(records), _ptr(resid), _ptr(host_kv), int(n_cap),
-                                               _stream(stream)))
+    fn = "spc_extend_kv"
+    n, lk, lv, (rec, res), dev = _cache_call(fn, d, ("k_new", "v_new"), k_new, v_new, records, resid)
+    st = _lib.spc_extend_kv(C.byref(d), n, k_new.data_ptr(), v_new.data_ptr(), lk, lv, rec, res, _ptr(host_kv), n_cap,
+                            _raw_stream(stream, dev))
+    if st:
+        raise SpcError(fn, st)
 
 
 def spc_dequantize_kv(d, records, resid, first, k, v, stream=None):
     """k, v: 16-bit [B][n][Hkv][D] of any strides, for the tokens first .. first+n-1."""
-    n = k.shape[1] if k.dim() == 4 else 0
-    lk, lv = _cache_rows("spc_dequantize_kv", d, ("k", "v"), (k, v), n)
-    _cache("spc_dequantize_kv", d, records, resid)
-    _check("spc_dequantize_kv", _lib.spc_dequantize_kv(C.byref(d), _ptr(records), _ptr(resid), int(first), n,
-                                                       k.data_ptr(), v.data_ptr(), C.byref(lk), C.byref(lv),
-                                                       _stream(stream)))
+    fn = "spc_dequantize_kv"
+    n, lk, lv, (rec, res), dev = _cache_call(fn, d, ("k", "v"), k, v, records, resid)
+    st = _lib.spc_dequantize_kv(C.byref(d), rec, res, first, n, k.data_ptr(), v.data_ptr(), lk, lv,
+                                _raw_stream(stream, dev))
+    if st:
+        raise SpcError(fn, st)
