@@ -8,6 +8,10 @@ the cache length in the dims struct.
     prefill_layer   Algorithm 1: Quant(K), Quant(V) into the low-bit cache,
                     then Offload(C) of the 16-bit K/V to the pinned host cache
                     on a copy stream (section 3, "Prefilling").
+    prompt_layer    Algorithm 1 from the projections on: rotary positions, the
+                    prompt's causal attention, its K/V into the low-bit cache
+                    and the host cache; also for the follow-up prompts of a
+                    conversation, which attend over the cache read back.
     predecode_layer Algorithm 2: append the first token's K/V, attention of
                     its single query over the cache, ArgTopK over that
                     attention, Pre-fetch of the selected 16-bit rows.
@@ -19,8 +23,9 @@ from __future__ import annotations
 
 import torch
 
-from . import (spc_append_kv, spc_decode_attn2, spc_host_gather, spc_host_gather_prev, spc_merged_attn,
-               spc_offload_kv, spc_quantize_kv, spc_topk_select, spc_topk_select_prev)
+from . import (spc_append_kv, spc_decode_attn2, spc_dequantize_kv, spc_extend_kv, spc_host_gather,
+               spc_host_gather_prev, spc_merged_attn, spc_offload_kv, spc_prompt_attn, spc_quantize_kv, spc_rope,
+               spc_topk_select, spc_topk_select_prev)
 
 
 def prefill_layer(d, k, v, records, resid, host_kv, n_cap, stream=None, copy_stream=None):
@@ -37,6 +42,40 @@ def prefill_layer(d, k, v, records, resid, host_kv, n_cap, stream=None, copy_str
     done = torch.cuda.Event()
     done.record(copy_stream)
     return done
+
+
+def prompt_layer(d, q, k, v, pos, turns, o, records, resid, host_kv=None, n_cap=0, history=None, lse=None, ws=None,
+                 rot=128, interleaved=False, mscale=1.0, stream=None):
+    """A prompt of n tokens per sequence through one layer's attention, and
+    into its cache.  q: 16-bit [B][n][Hq][D], k, v: [B][n][Hkv][D], views of
+    the projections (any strides); pos: int32 [B][n], the tokens' positions;
+    turns (and rot, interleaved, mscale): the rotary rule (spc_rope).  q is
+    rotated in place.  o: [B][n][Hq][D]; lse: fp32 [B][n][Hq] or None.
+
+    An empty cache (d.N = 0): k is rotated in place and the prompt attends to
+    itself.  A follow-up prompt (d.N > 0) attends to the cache as well, read
+    back in 16 bits: history is a pair of buffers [B][Hkv][cap][D] (keys,
+    values) of cap >= d.N + n rows, which then hold the history's rows and the
+    new tokens' behind them; they may be shared by layers that run in turn.
+    The new tokens join records and resid, and host_kv if given; d.N is
+    advanced by n.  Without ws the attention takes its workspace from torch's
+    allocator."""
+    n, N = k.shape[1], d.N
+    if N > 0:
+        if history is None or any(b.shape[2] < N + n for b in history):
+            raise ValueError(f"prompt_layer: a follow-up prompt needs history buffers of {N + n} rows")
+        kk, vv = (b[:, :, :N + n].transpose(1, 2) for b in history)
+    stream = torch.cuda.current_stream() if stream is None else stream
+    with torch.cuda.stream(stream):
+        if N == 0:
+            kk, vv = k, v
+            spc_rope(q, k, pos, turns, rot, interleaved, mscale)
+        else:
+            spc_dequantize_kv(d, records, resid, 0, kk[:, :N], vv[:, :N])
+            spc_rope(q, k, pos, turns, rot, interleaved, mscale, v=v, k_out=kk[:, N:], v_out=vv[:, N:])
+        spc_prompt_attn(q, kk, vv, o, lse, scale=d.scale, ws=ws)
+        spc_extend_kv(d, kk[:, N:], vv[:, N:], records, resid, host_kv, n_cap)
+    d.N += n
 
 
 def predecode_layer(d, records, resid, host_kv, n_cap, q1, k1, v1, k, idx, bitmap, staging, o, lse, logits, ws,
