@@ -15,106 +15,9 @@
 // The kernel streams HBM: 512 B read and 64/96 B written per token and KV head.
 #include <cstddef>
 
-#include "common.cuh"
+#include "quant.cuh"
 
 namespace spc {
-
-// z and s from the group's min and max, in binary32 exactly as written
-// (the __f*_rn intrinsics are never contracted into FMA).
-__device__ __forceinline__ void quant_params(int bits, float lo, float hi, float& z, float& s) {
-  if (bits == 1) {
-    z = __fmul_rn(__fadd_rn(__fmul_rn(3.0f, lo), hi), 0.25f);
-    s = __fmul_rn(__fsub_rn(hi, lo), 0.5f);
-  } else {
-    z = lo;
-    s = __fdiv_rn(__fsub_rn(hi, lo), 3.0f);
-  }
-}
-
-// The multiplier that stands in for a division by s: the correctly rounded
-// reciprocal; 0 when s == 0 (the code is then 0); NaN when 1/s overflows
-// binary32 (s below about 2^-128, a subnormal range), so that every quotient
-// of such a group is settled by the IEEE division in quant_code.
-__device__ __forceinline__ float quant_recip(float s) {
-  if (s == 0.0f) return 0.0f;
-  const float rs = __frcp_rn(s);
-  return isinf(rs) ? __int_as_float(0x7FC00000) : rs;
-}
-
-// clamp(rint(fl((x - z) / s)), 0, 2^bits - 1), 0 when s == 0 (rs == 0 then).
-// The product with the correctly rounded reciprocal rs is within 1e-6 of the
-// IEEE quotient for the quotients that occur (|q| <= 3), so it decides every
-// value whose quotient is farther than 1e-5 from a rounding boundary k + 1/2;
-// the IEEE division settles the rest, and every product that is not a number
-// (a NaN rs, or an infinite x - z times a zero rs).  At 1 bit the code is 1
-// exactly when the quotient exceeds 1/2 (1/2 itself rounds to even, 0); a
-// quotient that is not a number gets code 0.
-template <int BITS>
-__device__ __forceinline__ uint32_t quant_code(float x, float z, float s, float rs) {
-  const float d = __fsub_rn(x, z);
-  float t = __fmul_rn(d, rs);
-  if (BITS == 1) {
-    if (!(fabsf(__fsub_rn(t, 0.5f)) >= 1e-5f) && s != 0.0f) t = __fdiv_rn(d, s);
-    return t > 0.5f ? 1u : 0u;
-  } else {
-    const float fr = __fsub_rn(t, floorf(t));
-    if (!(fabsf(__fsub_rn(fr, 0.5f)) >= 1e-5f) && s != 0.0f) t = __fdiv_rn(d, s);
-    return (uint32_t)fminf(fmaxf(rintf(t), 0.0f), 3.0f);  // fmaxf(NaN, 0) = 0
-  }
-}
-
-// bf16 bit patterns in value order and back: ord increases with the value
-// (-0 just below +0, NaN patterns outside every finite and infinite value).
-__device__ __forceinline__ uint32_t bf16_ord(uint32_t b) { return (b & 0x8000u) ? (b ^ 0xFFFFu) : (b | 0x8000u); }
-__device__ __forceinline__ uint32_t bf16_unord(uint32_t o) { return (o & 0x8000u) ? (o & 0x7FFFu) : (o ^ 0xFFFFu); }
-
-// The smallest bf16 value x of a group's range [lo, hi] whose code
-// quant_code<BITS>(x, z, s, rs) is at least `level` (1 .. 2^BITS - 1), as a
-// float; NaN when no x of the range reaches it.  quant_code is the code of
-// the IEEE quotient fl(fl(x - z) / s), a non-decreasing function of x, so an
-// element of the group has code >= level exactly when x >= the threshold (a
-// NaN element compares false, code 0, as quant_code gives it).  Checked at
-// both ends of the range first (lo's code is not always 0: when 3 min + max
-// overflows binary32, z = -inf and every element codes 1), then in the
-// bracket (lo, hi]: the bf16 value at the analytic point z + (level - 1/2) s
-// and its two neighbours settle it unless binary32 absorbs x - z over a run
-// of bf16 values there (tiny x near a zero midpoint), which bisection then
-// resolves.
-template <int BITS>
-__device__ __forceinline__ float code_threshold(float lo, float hi, float z, float s, float rs, uint32_t level) {
-  auto ge = [&](uint32_t o) {
-    return quant_code<BITS>(__uint_as_float(bf16_unord(o) << 16), z, s, rs) >= level;
-  };
-  uint32_t a = bf16_ord(__float_as_uint(lo) >> 16), b = bf16_ord(__float_as_uint(hi) >> 16);
-  if (!(a <= b) || !ge(b)) return __int_as_float(0x7FC00000);
-  if (ge(a)) return __uint_as_float(bf16_unord(a) << 16);
-  // invariant: code(a) < level <= code(b)
-  const float guess = __fadd_rn(z, __fmul_rn((float)level - 0.5f, s));
-  const uint32_t og = min(max(bf16_ord(__float_as_uint(guess) >> 16), a + 1u), b);
-  if (ge(og)) {
-    b = og;
-    if (og - 1u > a) {
-      if (!ge(og - 1u)) return __uint_as_float(bf16_unord(og) << 16);
-      b = og - 1u;
-    }
-  } else {
-    a = og;
-    if (og + 1u < b) {
-      if (ge(og + 1u)) return __uint_as_float(bf16_unord(og + 1u) << 16);
-      a = og + 1u;
-    }
-  }
-  while (b - a > 1u) {
-    const uint32_t m = (a + b) >> 1;
-    if (ge(m)) b = m; else a = m;
-  }
-  return __uint_as_float(bf16_unord(b) << 16);
-}
-
-// min/max of bf16 values carried as floats; -0.0 is stored as +0.0.
-__device__ __forceinline__ uint32_t bf16_bits_canonical(float f) {
-  return f == 0.0f ? 0u : (__float_as_uint(f) >> 16);
-}
 
 struct QuantArgs {
   const uint16_t* k;
@@ -133,21 +36,6 @@ struct QuantSmem {
   uint32_t rec[256 * 3];             // the record being assembled (up to 3 KB)
   uint16_t tile[2][2][kGroup * kD];  // [tile][keys, values][token][channel]
 };
-
-// Token pair p of a group (tokens 2p, 2p+1) is where value code words
-// (a, t = p & 3, j = 2 * (p >> 3) + ((p >> 2) & 1)) take their bits; the
-// (min, max) of token n, channel group cg is value-minmax word 32 t' + m with
-// t' = (n & 7) >> 1, m = 16 (n >> 4) + 4 (2 ((n & 15) >> 3) + (n & 1)) + cg.
-__device__ __forceinline__ int vmeta_word(int n, int cg) {
-  const int n16 = n & 15;
-  return 32 * ((n16 & 7) >> 1) + 16 * (n >> 4) + 4 * (2 * (n16 >> 3) + (n16 & 1)) + cg;
-}
-// At g = 64 a half's 64 value-minmax words hold token n's (min, max) of
-// channels 64c .. 64c+63 at word 2m + c, where m = 8 ((n >> 1) & 3) +
-// 4 (n >> 4) + 2 ((n >> 3) & 1) + (n & 1) is the lane that reads token n.
-__device__ __forceinline__ int vmeta64_word(int n, int c) {
-  return 2 * (8 * ((n >> 1) & 3) + 4 * (n >> 4) + 2 * ((n >> 3) & 1) + (n & 1)) + c;
-}
 
 // Codes one 32-token group from the tiles ks, vs ([token][channel] bf16 in
 // shared memory) into its record at dst.  At g = 64 the tiles are half `half`
@@ -567,156 +455,6 @@ spc_status launch_append(const spc_dims* d, const uint16_t* k_new, const uint16_
   else
     e = d->group == 64 ? launch_append_k<2, 64>(a, BH, stream) : launch_append_k<2, 32>(a, BH, stream);
   if (e == cudaSuccess) e = cudaGetLastError();
-  if (e != cudaSuccess) {
-    spc_host::set_cuda_error(e);
-    return SPC_ERR_CUDA;
-  }
-  return SPC_OK;
-}
-
-// ------------------------------------------------------- a run of new tokens
-// n new tokens join the cache at once (a prompt, or a follow-up prompt), with
-// the result of n appends: the groups that complete are coded straight from
-// where their rows are (the window's old rows, then the new tokens' views),
-// then the window shifts and takes the rows that stay in 16 bits.
-struct ExtendArgs {
-  const uint16_t* k_new;  // views [B][n][Hkv][D]
-  const uint16_t* v_new;
-  spc_layout lk, lv;
-  uint8_t* records;
-  uint16_t* resid;
-  uint16_t* host;  // device address of [B][Hkv][n_cap][2][D], or null
-  int64_t n_cap, total_groups;
-  int32_t Hkv, N, n, nq, nq1, resid_cap, units_cap;
-  int32_t window_parts;  // CTAs per (b, hkv) that write the window
-};
-
-// 16-byte piece `q` (0-15 key, 16-31 value) of token t of (b, hkv).
-__device__ __forceinline__ const uint4* extend_source(const ExtendArgs& a, int64_t bh, int t, int q) {
-  if (t < a.N) return reinterpret_cast<const uint4*>(a.resid + (bh * a.resid_cap + (t - a.nq)) * 2 * kD) + q;
-  const int64_t b = bh / a.Hkv, h = bh % a.Hkv;
-  return q < 16 ? reinterpret_cast<const uint4*>(a.k_new + b * a.lk.b + (t - a.N) * a.lk.t + h * a.lk.h) + q
-                : reinterpret_cast<const uint4*>(a.v_new + b * a.lv.b + (t - a.N) * a.lv.t + h * a.lv.h) + (q - 16);
-}
-
-template <int BITS, int GROUP>
-__global__ void __launch_bounds__(128) extend_groups_kernel(const __grid_constant__ ExtendArgs a) {
-  extern __shared__ __align__(16) uint8_t qsmem[];
-  QuantSmem& sm = *reinterpret_cast<QuantSmem*>(qsmem);
-  const int tid = threadIdx.x;
-  const int per = (a.nq1 - a.nq) / GROUP;
-  for (int64_t gi = blockIdx.x; gi < a.total_groups; gi += gridDim.x) {
-    const int64_t bh = gi / per;
-    const int g = (int)(gi % per);
-    const int t0 = a.nq + g * GROUP;
-#pragma unroll
-    for (int half = 0; half < GROUP / 32; ++half)
-      for (int i = tid; i < 1024; i += 128) {
-        const int row = i >> 5, q = i & 31;
-        uint16_t* tile = sm.tile[half][q >> 4];
-        cp_async16(tile + row * kD + 8 * (q & 15), extend_source(a, bh, t0 + 32 * half + row, q));
-      }
-    cp_async_commit();
-    cp_async_wait<0>();
-    __syncthreads();
-    uint8_t* rec = a.records + (bh * a.units_cap + a.nq / GROUP + g) * record_bytes(BITS, GROUP);
-    code_group<BITS, GROUP>(sm, sm.tile[0][0], sm.tile[0][1], sm.tile[1][0], rec, 0);
-    if (GROUP == 64) code_group<BITS, GROUP>(sm, sm.tile[1][0], sm.tile[1][1], sm.tile[0][0], rec, 1);
-  }
-}
-
-// The window's rows (tokens nq1 .. N+n-1), and the new rows of the host cache.
-// Old rows that stay move down by nq1 - nq; a CTA that moves them owns the
-// window of its (b, hkv) (window_parts = 1) and moves 32 at a time, each chunk
-// read in full before it is written, before it writes the new rows.
-__global__ void __launch_bounds__(256) extend_window_kernel(const __grid_constant__ ExtendArgs a) {
-  const int64_t bh = blockIdx.x;
-  const int tid = threadIdx.x;
-  if ((int)blockIdx.y < a.window_parts) {
-    uint4* win = reinterpret_cast<uint4*>(a.resid + bh * a.resid_cap * 2 * kD);  // 32 pieces a row
-    const int shift = a.nq1 - a.nq, kept = max(a.N - a.nq1, 0);                   // old rows that stay
-    if (shift > 0) {
-      for (int c0 = 0; c0 < kept; c0 += 32) {
-        const int pieces = 32 * min(32, kept - c0);
-        uint4 v[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int i = tid + 256 * u;
-          if (i < pieces) v[u] = win[(int64_t)(shift + c0) * 32 + i];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int i = tid + 256 * u;
-          if (i < pieces) win[(int64_t)c0 * 32 + i] = v[u];
-        }
-        __syncthreads();
-      }
-    }
-    const int first = max(a.N, a.nq1);  // the first new token that stays
-    const int64_t pieces = (int64_t)(a.N + a.n - first) * 32;
-    for (int64_t i = blockIdx.y * 256 + tid; i < pieces; i += 256 * a.window_parts) {
-      const int t = first + (int)(i >> 5);
-      win[(int64_t)(t - a.nq1) * 32 + (i & 31)] = *extend_source(a, bh, t, (int)(i & 31));
-    }
-  } else {
-    uint4* host = reinterpret_cast<uint4*>(a.host + (bh * a.n_cap + a.N) * 2 * kD);
-    const int64_t pieces = (int64_t)a.n * 32;
-    const int parts = gridDim.y - a.window_parts;
-    for (int64_t i = (blockIdx.y - a.window_parts) * 256 + tid; i < pieces; i += 256 * parts)
-      host[i] = *extend_source(a, bh, a.N + (int)(i >> 5), (int)(i & 31));
-  }
-}
-
-template <int BITS, int GROUP>
-static cudaError_t launch_extend_k(const ExtendArgs& a, cudaStream_t stream) {
-  const int smem = GROUP == 32 ? (int)offsetof(QuantSmem, tile[1]) : (int)sizeof(QuantSmem);
-  static unsigned long long configured = 0ull;
-  const cudaError_t e = spc_host::ensure_smem_limit(configured, extend_groups_kernel<BITS, GROUP>, smem);
-  if (e != cudaSuccess) return e;
-  const int64_t grid = std::min<int64_t>(a.total_groups, (int64_t)spc_host::sm_count() * 8);
-  extend_groups_kernel<BITS, GROUP><<<(unsigned)grid, 128, smem, stream>>>(a);
-  return cudaGetLastError();
-}
-
-spc_status launch_extend(const spc_dims* d, int32_t n, const uint16_t* k_new, const uint16_t* v_new,
-                         const spc_layout* lk, const spc_layout* lv, void* records, uint16_t* resid,
-                         uint16_t* host_dev, int64_t n_cap, cudaStream_t stream) {
-  ExtendArgs a = {};
-  a.k_new = k_new;
-  a.v_new = v_new;
-  a.lk = *lk;
-  a.lv = *lv;
-  a.records = static_cast<uint8_t*>(records);
-  a.resid = resid;
-  a.host = host_dev;
-  a.n_cap = n_cap;
-  a.Hkv = d->Hkv;
-  a.N = d->N;
-  a.n = n;
-  a.nq = num_quantized(d->N, d->R, d->group);
-  a.nq1 = num_quantized(d->N + n, d->R, d->group);
-  a.resid_cap = d->resid_cap;
-  a.units_cap = records_cap(d->group, d->q_groups_cap);
-  const int64_t BH = (int64_t)d->B * d->Hkv;
-  a.total_groups = BH * ((a.nq1 - a.nq) / d->group);
-  cudaError_t e = cudaSuccess;
-  if (a.total_groups > 0) {
-    if (d->bits == 1)
-      e = d->group == 64 ? launch_extend_k<1, 64>(a, stream) : launch_extend_k<1, 32>(a, stream);
-    else
-      e = d->group == 64 ? launch_extend_k<2, 64>(a, stream) : launch_extend_k<2, 32>(a, stream);
-  }
-  if (e == cudaSuccess) {
-    const bool moves = a.nq1 > a.nq && a.N > a.nq1;
-    const int32_t rows = a.N + n - std::max(a.N, a.nq1);
-    a.window_parts = moves ? 1 : (int32_t)std::min<int64_t>(64, (rows + 31) / 32);
-    const int host_parts = host_dev != nullptr ? (int)std::min<int64_t>(64, (n + 31) / 32) : 0;
-    if (a.window_parts + host_parts > 0) {
-      extend_window_kernel<<<dim3((unsigned)BH, (unsigned)(a.window_parts + host_parts)), 256, 0, stream>>>(a);
-      e = cudaGetLastError();
-    }
-  }
   if (e != cudaSuccess) {
     spc_host::set_cuda_error(e);
     return SPC_ERR_CUDA;

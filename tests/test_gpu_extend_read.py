@@ -222,3 +222,24 @@ def test_prompt_at_a_workload_shape(bits, group):
     d0 = spc.Dims(B, Hq, Hkv, 0, R, bits, q_groups_cap=d.q_groups_cap, resid_cap=d.resid_cap, group=group)
     spc.spc_extend_kv(d0, k, v, rec[1], res[1])
     assert torch.equal(rec[0], rec[1]) and torch.equal(res[0], res[1])
+
+
+@pytest.mark.parametrize("bits,group", [(1, 32), (2, 32), (1, 64), (2, 64)])
+def test_non_finite_elements_as_the_quantiser_codes_them(bits, group):
+    """Infinities and NaN among the elements: the same records as spc_quantize_kv's."""
+    import bit_kv_cache_spc_gb300 as spc
+    B, Hkv, N = 2, 2, 8 * group
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    kv = torch.randn((2, B, Hkv, N, D), generator=g, device="cuda").to(torch.bfloat16)
+    at = torch.rand((2, B, Hkv, N, D), generator=g, device="cuda")
+    for i, x in enumerate((float("nan"), float("inf"), -float("inf"))):
+        kv[(at > 0.002 * i) & (at < 0.002 * i + 0.001)] = x
+    kv[:, 0, 0, :group] = float("nan")  # groups of nothing else
+    kv[:, 0, 1, :group, :64] = float("inf")
+    d = spc.Dims(B, Hkv, Hkv, N, 0, bits, group=group)
+    rec = torch.zeros((2, spc.spc_records_bytes(d)), dtype=torch.uint8, device="cuda")
+    spc.spc_quantize_kv(d, kv[0], kv[1], rec[0], None)
+    d0 = spc.Dims(B, Hkv, Hkv, 0, 0, bits, q_groups_cap=d.q_groups_cap, group=group)
+    spc.spc_extend_kv(d0, kv[0].transpose(1, 2), kv[1].transpose(1, 2), rec[1], None)
+    assert torch.equal(rec[0], rec[1])
