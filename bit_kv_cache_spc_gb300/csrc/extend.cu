@@ -81,10 +81,7 @@ template <int BITS>
 __device__ __forceinline__ uint32_t group_thresholds(float lo, float hi, uint32_t* thr) {
   float z, s;
   quant_params(BITS, lo, hi, z, s);
-  const float rs = quant_recip(s);
-#pragma unroll
-  for (int l = 1; l < (1 << BITS); ++l)
-    thr[l - 1] = __float_as_uint(code_threshold<BITS>(lo, hi, z, s, rs, (uint32_t)l)) >> 16;
+  code_thresholds<BITS>(lo, hi, z, s, thr);
   return bf16_bits_canonical(lo) | (bf16_bits_canonical(hi) << 16);
 }
 
@@ -239,9 +236,16 @@ __global__ void __launch_bounds__(128) extend_groups_kernel(const __grid_constan
     const int g = (int)(gi % per);
     const int t0 = a.nq + g * GROUP, q = tid & 31;
     uint16_t* tile = (q < 16 ? sm.k : sm.v) + 8 * (q & 15);
+    const int64_t b = bh / a.Hkv, h = bh % a.Hkv;
+    const uint16_t* fresh = (q < 16 ? a.k_new + b * a.lk.b + h * a.lk.h : a.v_new + b * a.lv.b + h * a.lv.h) + 8 * (q & 15);
+    const int64_t step = q < 16 ? a.lk.t : a.lv.t;
+    if (t0 >= a.N) {  // none of the window's rows
+      const uint16_t* src = fresh + (t0 - a.N + (tid >> 5)) * step;
 #pragma unroll 8
-    for (int row = tid >> 5; row < GROUP; row += 4)
-      cp_async16(tile + row * kPitch, extend_source(a, bh, t0 + row, q));
+      for (int row = tid >> 5; row < GROUP; row += 4, src += 4 * step) cp_async16(tile + row * kPitch, src);
+    } else {
+      for (int row = tid >> 5; row < GROUP; row += 4) cp_async16(tile + row * kPitch, extend_source(a, bh, t0 + row, q));
+    }
     cp_async_commit();
     cp_async_wait<0>();
     __syncthreads();

@@ -99,6 +99,52 @@ __device__ __forceinline__ float code_threshold(float lo, float hi, float z, flo
   return __uint_as_float(bf16_unord(b) << 16);
 }
 
+// Whether x has a code of at least `level`, for s in [2^-100, 2^100], without
+// the quotient.  With d = fl(x - z), the code's fl(d / s) is above 1/2 exactly
+// when 2 d > s; at least 3/2 when d / s >= 3/2 - 2^-24 and above 5/2 when
+// d / s > 5/2 + 2^-23 (the ties at those half steps round to the even 3/2 and
+// 5/2).  Both sides of those comparisons are multiples of half an ulp of s
+// and, where they are close, a few of them, so one rounding decides them
+// exactly.
+template <int BITS>
+__device__ __forceinline__ bool code_reaches(float x, float z, float s, int level) {
+  const float d = __fsub_rn(x, z);
+  if (BITS == 1 || level == 1) return __fadd_rn(d, d) > s;
+  if (level == 2) return __fmaf_rn(-1.5f, s, d) >= s * -5.9604644775390625e-8f;
+  return __fmaf_rn(-2.5f, s, d) > s * 1.1920928955078125e-7f;
+}
+
+// The bf16 patterns of code_threshold for every level at once: the bf16 value
+// nearest to z + (level - 1/2) s or one of its neighbours, where code_reaches
+// says so (a threshold below lo or above hi serves as well: no element lies
+// there); else (a range near zero or overflow, binary32 absorbing x - z over a
+// run of bf16 values) by code_threshold's search.
+template <int BITS>
+__device__ __forceinline__ void code_thresholds(float lo, float hi, float z, float s, uint32_t* thr) {
+  bool found = s >= 7.888609052210118e-31f && s <= 1.2676506002282294e30f;
+#pragma unroll
+  for (int l = 1; l < (1 << BITS); ++l) {
+    const float guess = __fmaf_rn((float)l - 0.5f, s, z);
+    uint16_t b;
+    asm("cvt.rn.bf16.f32 %0, %1;\n" : "=h"(b) : "f"(guess));
+    const uint32_t o = bf16_ord(b), down = bf16_unord(o - 1u), up = bf16_unord(o + 1u);
+    const bool at = code_reaches<BITS>(bf16_to_f32(b), z, s, l);
+    const bool below = code_reaches<BITS>(bf16_to_f32(down), z, s, l);
+    const bool above = code_reaches<BITS>(bf16_to_f32(up), z, s, l);
+    thr[l - 1] = at ? b : up;
+    found = found && !below && above;
+  }
+  if (found) return;
+  const float rs = quant_recip(s);
+#pragma unroll 1
+  for (int l = 1; l < (1 << BITS); ++l) {
+    const uint32_t t = __float_as_uint(code_threshold<BITS>(lo, hi, z, s, rs, (uint32_t)l)) >> 16;
+    if (l == 1) thr[0] = t;
+    if (BITS == 2 && l == 2) thr[BITS - 1] = t;
+    if (BITS == 2 && l == 3) thr[2 * BITS - 2] = t;
+  }
+}
+
 // min/max of bf16 values carried as floats; -0.0 is stored as +0.0.
 __device__ __forceinline__ uint32_t bf16_bits_canonical(float f) {
   return f == 0.0f ? 0u : (__float_as_uint(f) >> 16);
