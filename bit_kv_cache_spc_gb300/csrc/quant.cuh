@@ -124,7 +124,15 @@ __device__ __forceinline__ void code_thresholds(float lo, float hi, float z, flo
   bool found = s >= 7.888609052210118e-31f && s <= 1.2676506002282294e30f;
 #pragma unroll
   for (int l = 1; l < (1 << BITS); ++l) {
-    const float guess = __fmaf_rn((float)l - 0.5f, s, z);
+    float guess = __fmaf_rn((float)l - 0.5f, s, z);
+    // Where the guess is near zero (lo = -hi), every x within half an ulp of x - z does as well as it: the
+    // threshold is half an ulp above it, or below it if it reaches the level itself.
+    if (BITS == 1) {
+      guess += __uint_as_float((__float_as_uint(s) & 0x7F800000u) - (25u << 23));
+    } else if (l == 2) {
+      const float half_ulp = __uint_as_float((__float_as_uint(__fsub_rn(guess, z)) & 0x7F800000u) - (24u << 23));
+      guess += code_reaches<BITS>(guess, z, s, l) ? -half_ulp : half_ulp;
+    }
     uint16_t b;
     asm("cvt.rn.bf16.f32 %0, %1;\n" : "=h"(b) : "f"(guess));
     const uint32_t o = bf16_ord(b), down = bf16_unord(o - 1u), up = bf16_unord(o + 1u);
