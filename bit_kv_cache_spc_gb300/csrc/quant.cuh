@@ -99,16 +99,14 @@ __device__ __forceinline__ float code_threshold(float lo, float hi, float z, flo
   return __uint_as_float(bf16_unord(b) << 16);
 }
 
-// Whether x has a code of at least `level`, for s in [2^-100, 2^100], without
-// the quotient.  With d = fl(x - z), the code's fl(d / s) is above 1/2 exactly
-// when 2 d > s; at least 3/2 when d / s >= 3/2 - 2^-24 and above 5/2 when
+// Whether an x with d = fl(x - z) has a code of at least `level`, for s in
+// [2^-100, 2^100], without the quotient.  fl(d / s) is above 1/2 exactly when 2 d > s; at least 3/2 when d / s >= 3/2 - 2^-24 and above 5/2 when
 // d / s > 5/2 + 2^-23 (the ties at those half steps round to the even 3/2 and
 // 5/2).  Both sides of those comparisons are multiples of half an ulp of s
 // and, where they are close, a few of them, so one rounding decides them
 // exactly.
 template <int BITS>
-__device__ __forceinline__ bool code_reaches(float x, float z, float s, int level) {
-  const float d = __fsub_rn(x, z);
+__device__ __forceinline__ bool code_reaches(float d, float s, int level) {
   if (BITS == 1 || level == 1) return __fadd_rn(d, d) > s;
   if (level == 2) return __fmaf_rn(-1.5f, s, d) >= s * -5.9604644775390625e-8f;
   return __fmaf_rn(-2.5f, s, d) > s * 1.1920928955078125e-7f;
@@ -125,20 +123,22 @@ __device__ __forceinline__ void code_thresholds(float lo, float hi, float z, flo
 #pragma unroll
   for (int l = 1; l < (1 << BITS); ++l) {
     float guess = __fmaf_rn((float)l - 0.5f, s, z);
-    // Where the guess is near zero (lo = -hi), every x within half an ulp of x - z does as well as it: the
-    // threshold is half an ulp above it, or below it if it reaches the level itself.
+    // Where the guess is near zero (lo = -hi) the bf16 values about it are far finer than x - z: the threshold
+    // is half an ulp below the first difference that reaches the level.
     if (BITS == 1) {
-      guess += __uint_as_float((__float_as_uint(s) & 0x7F800000u) - (25u << 23));
+      guess += __uint_as_float((__float_as_uint(s) & 0x7F800000u) - (25u << 23));  // the one above s / 2
     } else if (l == 2) {
-      const float half_ulp = __uint_as_float((__float_as_uint(__fsub_rn(guess, z)) & 0x7F800000u) - (24u << 23));
-      guess += code_reaches<BITS>(guess, z, s, l) ? -half_ulp : half_ulp;
+      const float d = __fsub_rn(guess, z);
+      const float half_ulp = __uint_as_float((__float_as_uint(d) & 0x7F800000u) - (24u << 23));
+      const float at = code_reaches<BITS>(d, s, l) ? 1.0f : -1.0f;
+      guess = __fadd_rn(z, d) - half_ulp * (code_reaches<BITS>(d - 2.0f * half_ulp, s, l) ? 3.0f : at);
     }
     uint16_t b;
     asm("cvt.rn.bf16.f32 %0, %1;\n" : "=h"(b) : "f"(guess));
     const uint32_t o = bf16_ord(b), down = bf16_unord(o - 1u), up = bf16_unord(o + 1u);
-    const bool at = code_reaches<BITS>(bf16_to_f32(b), z, s, l);
-    const bool below = code_reaches<BITS>(bf16_to_f32(down), z, s, l);
-    const bool above = code_reaches<BITS>(bf16_to_f32(up), z, s, l);
+    const bool at = code_reaches<BITS>(__fsub_rn(bf16_to_f32(b), z), s, l);
+    const bool below = code_reaches<BITS>(__fsub_rn(bf16_to_f32(down), z), s, l);
+    const bool above = code_reaches<BITS>(__fsub_rn(bf16_to_f32(up), z), s, l);
     thr[l - 1] = at ? b : up;
     found = found && !below && above;
   }
