@@ -6,15 +6,22 @@
 //
 // One CTA takes two tiles of 128 query rows (a row is a token and one of the
 // G query heads that share the KV head, so K and V are read once per group)
-// and walks its keys in tiles of 128 with a running maximum and sum:
-//   S = Q K^T (128 x 128 x 128) and O += P V go to the tensor cores
-//   (tcgen05.mma, bf16 in, fp32 accumulators in TMEM: S of both tiles in columns
-//   0-255, O in 256-511); P replaces S in TMEM as bf16 and is read from there;
-//   K and V tiles arrive by TMA in a ring of five 32 KB stages.
+// and walks its keys in blocks of 64 with a running maximum and sum:
+//   S = Q K^T (128 x 64 x 128) and O += P V (128 x 128 x 64) go to the tensor
+//   cores (tcgen05.mma, bf16 in, fp32 accumulators in TMEM: two S blocks of
+//   each tile in columns 0-255, O in 256-511); P replaces its S in TMEM as
+//   bf16 and is read from there; K and V arrive by TMA, 128 keys at a time, in
+//   a ring of five 32 KB stages.
 // Warps 0-3 and 4-7 do the softmax of one tile each, a thread per row, and the
-// output; warp 8 issues the copies, warp 9 the products, warps 10-11 look
-// after values in masked places (below).  While one tile's softmax runs, the
-// tensor cores work on the other tile's products.
+// output; warp 8 issues the copies, warps 9 and 10 the products of one tile
+// each, warps 12-15 look after values in masked places (below).
+// Why two S blocks per tile: with one block of 128 keys the softmax of a tile
+// and its products alternate, and each turn pays the barriers' and the
+// loads' latencies (3860 cycles for 2 x 128 keys, of which the tensor cores
+// work 2048); with two, the next block's S is there when the softmax ends.
+// Why a product warp per tile: a product's issue lasts nearly as long as its
+// execution, so what one warp spends on waiting and committing between the
+// tiles' products leaves the tensor cores idle.
 //
 // Bounds: 4*128 operations per visible (query head, key) pair for a prompt;
 // for a few queries over a long history the bytes of K and V.
@@ -25,7 +32,7 @@
 // Masked places: a masked score is replaced by -inf, so what K holds there
 // does not matter, but 0 * V would still turn an infinity or a NaN of a masked
 // value row into NaN.  Only tiles that some row of the pair does not see in
-// full can hold such rows: warps 10-11 replace the non-finite elements of
+// full can hold such rows: warps 12-15 replace the non-finite elements of
 // their value tiles by zeros before the product, and when there were any, the
 // epilogue adds the non-finite elements of the visible keys back (their
 // weights are positive, so an infinity keeps its sign).
@@ -39,10 +46,11 @@
 namespace spc {
 namespace {
 
-constexpr int kTile = 128;                   // query rows per tile and keys per tile
+constexpr int kTile = 128;                   // query rows per tile, and keys per copy
+constexpr int kBlock = 64;                   // keys per S block
 constexpr int kStageBytes = kTile * kD * 2;  // one K or V tile, or one Q tile
 constexpr int kStages = 5;
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -75,9 +83,9 @@ struct __align__(8) PromptBars {
   uint64_t kv_free[kStages];
   uint64_t v_scan;   // the next value tile that may hold masked places has arrived
   uint64_t v_clean;  // and holds only finite elements
-  uint64_t s_full[2];
-  uint64_t p_full[2];
-  uint64_t o_full[2];
+  // per query tile and S buffer: block i's scores are there, and so is the product of block i - 2's weights
+  uint64_t s_full[2][2];
+  uint64_t p_full[2][2];  // its weights are
   uint32_t tmem;
   uint32_t bad;            // a masked tile held a non-finite value
   volatile uint32_t stop;  // a wait ran out
@@ -107,8 +115,11 @@ __device__ __forceinline__ bool mbar_try(uint64_t* b, uint32_t parity) {
 }
 // Waits for the phase; false once this or another wait of the CTA has run out
 // (two seconds; the longest regular wait is far below a millisecond).
+// The timer is read only after many tries: reading it takes longer than a
+// regular wait.
 __device__ __forceinline__ bool mbar_wait(PromptBars& bars, uint64_t* b, uint32_t parity) {
-  if (mbar_try(b, parity)) return true;
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try(b, parity)) return true;
   uint64_t start, now;
   asm volatile("mov.u64 %0, %%globaltimer;\n" : "=l"(start));
   for (;;) {
@@ -121,6 +132,11 @@ __device__ __forceinline__ bool mbar_wait(PromptBars& bars, uint64_t* b, uint32_
       return false;
     }
   }
+}
+
+// For a whole warp: one outcome for all lanes.
+__device__ __forceinline__ bool mbar_wait_warp(PromptBars& bars, uint64_t* b, uint32_t parity) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bars, b, parity));
 }
 
 __device__ __forceinline__ void tma_load4(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
@@ -151,7 +167,22 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float* r) {
         "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
       : "r"(addr));
 }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+// Ends the loads in flight; r (32 loaded values) is named so that no use of it moves before the wait.
+__device__ __forceinline__ void tmem_wait_ld(float* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]), 
+                 "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]), 
+                 "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]), 
+                 "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31])
+               :
+               : "memory");
+}
+// max(a, b, c), NaN only when all are
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* u) {
   asm volatile(
@@ -167,13 +198,14 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return r;
 }
 
-// Instruction word of a bf16 product with fp32 sums, M = 128, N = 128; B either
-// with the contraction contiguous (keys of S) or with N contiguous (values).
-__host__ __device__ constexpr uint32_t mma_word(bool b_n_contiguous) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_n_contiguous ? 1u : 0u) << 16) | ((128u / 8) << 17) |
+// Instruction word of a bf16 product with fp32 sums, M = 128; B either with
+// the contraction contiguous (keys of S) or with N contiguous (values).
+__host__ __device__ constexpr uint32_t mma_word(uint32_t n, bool b_n_contiguous) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_n_contiguous ? 1u : 0u) << 16) | ((n / 8) << 17) |
          ((128u / 16) << 24);
 }
-// Shared-memory operand with 128-byte swizzle; offsets in bytes.
+// Shared-memory operand with 128-byte swizzle; offsets in bytes.  A step of x
+// bytes is an addition of x / 16 (addresses stay below 2^18).
 __device__ __forceinline__ uint64_t smem_operand(uint32_t addr, uint32_t lead, uint32_t stride) {
   return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) |
          (1ull << 46) | (2ull << 61);
@@ -191,22 +223,27 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "r"(a), "l"(b), "r"(word), "r"((uint32_t)add)
       : "memory");
 }
-// S = Q K^T: both tiles are two halves of 64 columns, [128 rows][128 bytes]
-// each, rows in groups of eight 1024 bytes apart; 16 columns (32 bytes) a step.
-__device__ __forceinline__ void product_s(uint32_t d, uint32_t q, uint32_t k) {
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t yes;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(yes));
+  return yes != 0;
+}
+// S = Q K^T of 64 keys: operands are two halves of 64 columns, rows of 128
+// bytes in groups of eight 1024 bytes apart; 16 columns (32 bytes) a step.
+__device__ __forceinline__ void product_s(uint32_t d, uint64_t q, uint64_t k) {
 #pragma unroll
   for (int s = 0; s < 8; ++s) {
-    const uint32_t off = (uint32_t)(s >> 2) * 16384u + (uint32_t)(s & 3) * 32u;
-    mma_ss(d, smem_operand(q + off, 16, 1024), smem_operand(k + off, 16, 1024), mma_word(false), s > 0);
+    const uint32_t off = ((uint32_t)(s >> 2) * 16384u + (uint32_t)(s & 3) * 32u) / 16;
+    mma_ss(d, q + off, k + off, mma_word(kBlock, false), s > 0);
   }
 }
-// O += P V: V's halves hold channels 0-63 and 64-127 of each key (N contiguous,
-// the halves 16384 bytes apart, groups of eight keys 1024 bytes apart); 16 keys
-// (2048 bytes, and eight TMEM columns of P) a step.
-__device__ __forceinline__ void product_o(uint32_t d, uint32_t p, uint32_t v, bool add) {
+// O += P V of 64 keys: V's halves hold channels 0-63 and 64-127 of each key (N
+// contiguous, the halves 16384 bytes apart, groups of eight keys 1024 bytes
+// apart); 16 keys (2048 bytes, and eight TMEM columns of P) a step.
+__device__ __forceinline__ void product_o(uint32_t d, uint32_t p, uint64_t v, bool add) {
 #pragma unroll
-  for (int s = 0; s < 8; ++s)
-    mma_ts(d, p + 8 * s, smem_operand(v + 2048u * s, 16384, 1024), mma_word(true), add || s > 0);
+  for (int s = 0; s < 4; ++s) mma_ts(d, p + 8 * s, v + 2048u / 16 * s, mma_word(kD, true), add || s > 0);
 }
 
 // What a CTA works on.
@@ -215,6 +252,7 @@ struct PromptItem {
   int lq, lk, qb, kb;  // lengths and first tokens of the sequence
   int tok0;            // first query token of the pair
   int lo, hi;          // key tiles [lo, hi)
+  int blocks;          // 64-key blocks of them that some row sees
   int edge;            // first key tile that some row does not see in full
   bool two;            // the second query tile has rows
 };
@@ -251,16 +289,17 @@ __device__ __forceinline__ PromptItem prompt_item(const PromptArgs& a, int64_t i
   const int per = (n + a.splits - 1) / a.splits;
   w.lo = min(w.split * per, n);
   w.hi = min(w.lo + per, n);
+  w.blocks = max(0, min(2 * (w.hi - w.lo), (most - w.lo * kTile + kBlock - 1) / kBlock));
   w.edge = least / kTile;
   return w;
 }
 
-// exp2(x c - m c) of a row's 128 scores, as bf16 pairs into P, and their sum.
+// exp2(x c - m c) of a row's 64 scores, as bf16 pairs into P, and their sum.
 __device__ __forceinline__ float row_weights(float* x, float c, float mc, uint32_t p_addr) {
   float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
   const float2 c2 = {c, c}, m2 = {-mc, -mc};
 #pragma unroll
-  for (int b = 0; b < 4; ++b) {
+  for (int b = 0; b < 2; ++b) {
     uint32_t u[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -271,8 +310,8 @@ __device__ __forceinline__ float row_weights(float* x, float c, float mc, uint32
     }
     tmem_st16(p_addr + 16 * b, u);
   }
-  const float2 s = f2_add(sum[0], sum[1]);
-  return s.x + s.y;
+  const float2 all = f2_add(sum[0], sum[1]);
+  return all.x + all.y;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -296,16 +335,17 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.q_full[i], 1);
-      mbar_init(&bars.s_full[i], 1);
-      mbar_init(&bars.p_full[i], 4);
-      mbar_init(&bars.o_full[i], 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&bars.s_full[i][b], 1);
+        mbar_init(&bars.p_full[i][b], 4);
+      }
     }
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bars.kv_full[i], 1);
-      mbar_init(&bars.kv_free[i], 1);
+      mbar_init(&bars.kv_free[i], w.two ? 2 : 1);
     }
-    mbar_init(&bars.v_scan, 1);
-    mbar_init(&bars.v_clean, 2);
+    mbar_init(&bars.v_scan, w.two ? 2 : 1);
+    mbar_init(&bars.v_clean, 4);
     bars.bad = 0;
     bars.stop = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -316,7 +356,6 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
   const uint32_t tmem = bars.tmem;
 
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
     if (warp == 8) {
       // ---- copies: Q tiles, then K_lo, V_lo, K_lo+1, V_lo+1, ... through the ring ----
       if (lane == 0 && n > 0) {
@@ -346,59 +385,75 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
           if (j + 1 < n) load_kv(2 * j + 2, &kmap, w.lo + j + 1);
         }
       }
-    } else if (warp == 9) {
-      // ---- products ----
-      if (lane == 0 && n > 0) {
-        const uint32_t qa = smem_addr(base), ra = smem_addr(ring);
-        const int tiles = w.two ? 2 : 1;
-        uint32_t scans = 0;
-        bool ok = mbar_wait(bars, &bars.kv_full[0], 0);
-        for (int t = 0; t < tiles && ok; ++t) {
-          ok = mbar_wait(bars, &bars.q_full[t], 0);
+    } else if (warp == 9 || (warp == 10 && w.two)) {
+      // ---- products of a tile: the whole warp walks the blocks, converged, so that operands are formed in uniform
+      // registers (a lane alone issued a product every 55 cycles), and one lane issues ----
+      const bool lead = elect_lane();
+      const int t = __shfl_sync(0xFFFFFFFFu, warp - 9, 0);
+      const int blocks = __shfl_sync(0xFFFFFFFFu, w.blocks, 0);
+      const int edge = __shfl_sync(0xFFFFFFFFu, w.edge - w.lo, 0);  // the first tile to be scanned
+      const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+      const uint32_t base_addr = __shfl_sync(0xFFFFFFFFu, smem_addr(base), 0);
+      const uint64_t qd = smem_operand(base_addr + kStageBytes * t, 16, 1024);
+      const uint64_t kd = smem_operand(base_addr + 2 * kStageBytes, 16, 1024);
+      const uint64_t vd = smem_operand(base_addr + 2 * kStageBytes, 16384, 1024);
+      const uint32_t sp = tm + 128 * t, op = tm + 256 + 128 * t;
+      constexpr uint32_t kStep = kStageBytes / 16, kHalf = kBlock * 128 / 16;  // a stage, 64 of its rows
+      uint32_t scans = 0;
+      bool ok = blocks > 0 && mbar_wait_warp(bars, &bars.kv_full[0], 0) && mbar_wait_warp(bars, &bars.q_full[t], 0);
+      if (ok && lead) {
+        product_s(sp, qd, kd);
+        tc_commit(&bars.s_full[t][0]);
+        if (blocks > 1) product_s(sp + kBlock, qd, kd + kHalf);
+        tc_commit(&bars.s_full[t][1]);
+        tc_commit(&bars.kv_free[0]);
+      }
+      __syncwarp();
+      int sv = 1, sk = 2;       // stages of V_j and K_j+1
+      uint32_t pv = 0, pk = 0;  // and the phases of their barriers
+      for (int j = 0; 2 * j < blocks && ok; ++j) {
+        ok = mbar_wait_warp(bars, &bars.kv_full[sv], pv);
+        if (ok && j >= edge) {
+          if (lead) mbar_arrive(&bars.v_scan);
+          __syncwarp();
+          ok = mbar_wait_warp(bars, &bars.v_clean, scans++ & 1u);
+        }
+        if (ok && 2 * j + 2 < blocks) ok = mbar_wait_warp(bars, &bars.kv_full[sk], pk);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          if (2 * j + b >= blocks || !ok) break;
+          ok = mbar_wait_warp(bars, &bars.p_full[t][b], j & 1);
           if (!ok) break;
           tc_fence_after();
-          product_s(tmem + 128 * t, qa + t * kStageBytes, ra);
-          tc_commit(&bars.s_full[t]);
-        }
-        if (ok) tc_commit(&bars.kv_free[0]);
-        for (int j = 0; j < n && ok; ++j) {
-          const int iv = 2 * j + 1, sv = iv % kStages;
-          const int ik = 2 * j + 2, sk = ik % kStages;
-          if (!mbar_wait(bars, &bars.kv_full[sv], (iv / kStages) & 1)) break;
-          if (w.lo + j >= w.edge) {
-            mbar_arrive(&bars.v_scan);
-            if (!mbar_wait(bars, &bars.v_clean, scans++ & 1u)) break;
+          if (lead) {
+            product_o(op, sp + kBlock * b, vd + kStep * sv + kHalf * b, j + b > 0);
+            if (2 * j + b + 2 < blocks) product_s(sp + kBlock * b, qd, kd + kStep * sk + kHalf * b);
+            tc_commit(&bars.s_full[t][b]);
           }
-          for (int t = 0; t < tiles; ++t) {
-            ok = mbar_wait(bars, &bars.p_full[t], j & 1);
-            if (!ok) break;
-            tc_fence_after();
-            product_o(tmem + 256 + 128 * t, tmem + 128 * t, ra + sv * kStageBytes, j > 0);
-            if (t == tiles - 1) tc_commit(&bars.kv_free[sv]);
-            if (j + 1 < n) {
-              if (t == 0) ok = mbar_wait(bars, &bars.kv_full[sk], (ik / kStages) & 1);
-              if (!ok) break;
-              product_s(tmem + 128 * t, qa + t * kStageBytes, ra + sk * kStageBytes);
-              tc_commit(&bars.s_full[t]);
-              if (t == tiles - 1) tc_commit(&bars.kv_free[sk]);
-            } else {
-              tc_commit(&bars.o_full[t]);
-            }
-          }
+          __syncwarp();
         }
+        if (ok && lead) {
+          tc_commit(&bars.kv_free[sv]);
+          if (2 * j + 2 < blocks) tc_commit(&bars.kv_free[sk]);
+        }
+        __syncwarp();
+        sv += 2;
+        if (sv >= kStages) { sv -= kStages; pv ^= 1; }
+        sk += 2;
+        if (sk >= kStages) { sk -= kStages; pk ^= 1; }
       }
-    } else {
+    } else if (warp >= 12) {
       // ---- values in masked places: tile by tile as the product warp asks (a wait on the stage alone could
       // take an earlier phase of its barrier for the awaited one) ----
       uint32_t scans = 0;
       for (int j = max(w.edge - w.lo, 0); j < n; ++j) {
         const int iv = 2 * j + 1, sv = iv % kStages;
-        if (!mbar_wait(bars, &bars.v_scan, scans++ & 1u)) break;
-        if (!mbar_wait(bars, &bars.kv_full[sv], (iv / kStages) & 1)) break;
+        if (!mbar_wait_warp(bars, &bars.v_scan, scans++ & 1u)) break;
+        if (!mbar_wait_warp(bars, &bars.kv_full[sv], (iv / kStages) & 1)) break;
         uint4* tile = reinterpret_cast<uint4*>(ring + sv * kStageBytes);
         bool touched = false;
 #pragma unroll 4
-        for (int i = tid - 320; i < kStageBytes / 16; i += 64) {
+        for (int i = tid - 384; i < kStageBytes / 16; i += 128) {
           const uint4 x = tile[i];
           // 16-bit halves with an exponent of all ones
           const uint32_t m0 = __vcmpeq2(x.x & 0x7F807F80u, 0x7F807F80u), m1 = __vcmpeq2(x.y & 0x7F807F80u, 0x7F807F80u);
@@ -415,7 +470,6 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;\n");
     // ---- softmax of one tile, a thread per row ----
     const int t = warp >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // TMEM lane 32 * (warp % 4)
@@ -429,51 +483,61 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     if (active) {
-      for (int j = 0; j < n; ++j) {
-        ok = mbar_wait(bars, &bars.s_full[t], j & 1);
+      for (int i = 0; i < w.blocks; ++i) {
+        const int b = i & 1;
+        const uint32_t sp = s_addr + kBlock * b;
+        ok = mbar_wait_warp(bars, &bars.s_full[t][b], (i >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
-        float x[128];
+        float x[kBlock];
+        tmem_ld32(sp, x);
+        tmem_ld32(sp + 32, x + 32);
+        tmem_wait_ld(x);
+        tmem_wait_ld(x + 32);
+        if (w.lo + (i >> 1) >= w.edge) {
+          const int vis = seen - w.lo * kTile - i * kBlock;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) tmem_ld32(s_addr + 32 * b, x + 32 * b);
-        tmem_wait_ld();
-        const int vis = seen - (w.lo + j) * kTile;
-        if (w.lo + j >= w.edge) {
-#pragma unroll
-          for (int i = 0; i < 128; ++i) x[i] = i < vis ? x[i] : -INFINITY;
+          for (int e = 0; e < kBlock; ++e) x[e] = e < vis ? x[e] : -INFINITY;
         }
         float top[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int i = 4; i < 128; ++i) top[i & 3] = fmaxf(top[i & 3], x[i]);
-        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        for (int e = 4; e < kBlock; e += 8)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            top[u] = e + 4 + u < kBlock ? max3(top[u], x[e + u], x[e + 4 + u]) : fmaxf(top[u], x[e + u]);
+        const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]);
         const bool grow = mx > m && !((mx - m) * c <= kSlack);
         if (__any_sync(0xFFFFFFFFu, grow)) {
           const float f = grow ? fast_exp2((m - mx) * c) : 1.f;  // m = -inf: 0
           if (grow) m = mx;
           l *= f;
-          if (j > 0) {  // the product before is complete: S was issued after it
+          if (i > 0) {
+            // the product of the block before has to be complete: the next use of the other buffer says so
+            ok = mbar_wait_warp(bars, &bars.s_full[t][b ^ 1], ((i + 1) >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
+            for (int q = 0; q < 4; ++q) {
               float y[32];
-              tmem_ld32(o_addr + 32 * b, y);
-              tmem_wait_ld();
+              tmem_ld32(o_addr + 32 * q, y);
+              tmem_wait_ld(y);
               uint32_t u[32];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(y[i] * f);
-              tmem_st16(o_addr + 32 * b, u);
-              tmem_st16(o_addr + 32 * b + 16, u + 16);
+              for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(y[e] * f);
+              tmem_st16(o_addr + 32 * q, u);
+              tmem_st16(o_addr + 32 * q + 16, u + 16);
             }
           }
         }
-        l += row_weights(x, c, m == -INFINITY ? 0.f : m * c, s_addr);
+        l += row_weights(x, c, m == -INFINITY ? 0.f : m * c, sp);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.p_full[t]);
+        if (lane == 0) mbar_arrive(&bars.p_full[t][b]);
       }
       // ---- output ----
       const int64_t part = ((int64_t)blockIdx.x * 2 + t) * kTile + r;  // splits are fastest in the grid
-      if (n > 0 && ok) ok = mbar_wait(bars, &bars.o_full[t], 0);
+      if (n > 0 && ok) ok = mbar_wait_warp(bars, &bars.s_full[t][(w.blocks + 1) & 1], ((w.blocks + 1) >> 1) & 1);
       if (ok) {
         tc_fence_after();
         const bool bad = *(volatile uint32_t*)&bars.bad != 0u;
@@ -486,7 +550,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
           float y[32];
           if (n > 0) {
             tmem_ld32(o_addr + 32 * b, y);
-            tmem_wait_ld();
+            tmem_wait_ld(y);
           }
           if (!any) {
 #pragma unroll
