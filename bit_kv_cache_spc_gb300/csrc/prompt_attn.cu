@@ -4,24 +4,35 @@
 // lengths, and queries that follow a history:
 //   o_i = sum_{j <= i + lk - lq} p_ij v_j,  p_ij = exp(scale q_i.k_j - lse_i).
 //
-// One CTA takes two tiles of 128 query rows (a row is a token and one of the
-// G query heads that share the KV head, so K and V are read once per group)
-// and walks its keys in blocks of 64 with a running maximum and sum:
+// A CTA takes one or two tiles of 128 query rows (a row is a token and one of
+// the G query heads that share the KV head, so K and V are read once per
+// group) and walks its keys in blocks of 64 with a running maximum and sum:
 //   S = Q K^T (128 x 64 x 128) and O += P V (128 x 128 x 64) go to the tensor
-//   cores (tcgen05.mma, bf16 in, fp32 accumulators in TMEM: two S blocks of
-//   each tile in columns 0-255, O in 256-511); P replaces its S in TMEM as
-//   bf16 and is read from there; K and V arrive by TMA, 128 keys at a time, in
-//   a ring of five 32 KB stages.
-// Warps 0-3 and 4-7 do the softmax of one tile each, a thread per row, and the
-// output; warp 8 issues the copies, warps 9 and 10 the products of one tile
-// each, warps 12-15 look after values in masked places (below).
+//   cores (tcgen05.mma, bf16 in, fp32 accumulators in TMEM: two S blocks and O
+//   of each tile); P replaces its S in TMEM as bf16 and is read from there; K
+//   and V arrive by TMA in a ring of stages.
+// Four warps per tile do its softmax, a thread per row, and the output; one
+// warp issues the copies, one per tile the products, and some look after
+// values in masked places (below).
+// Two tiles (256 rows) share every K and V stage, 128 keys each: prompts,
+// bound by the tensor cores.  One tile, where a sequence's rows fit into it
+// (single tokens, short turns: bound by the bytes of K and V): half the TMEM
+// and shared memory, 64 keys a stage, so that two CTAs share an SM and one's
+// start and output overlap the other's copies.
 // Why two S blocks per tile: with one block of 128 keys the softmax of a tile
 // and its products alternate, and each turn pays the barriers' and the
 // loads' latencies (3860 cycles for 2 x 128 keys, of which the tensor cores
-// work 2048); with two, the next block's S is there when the softmax ends.
+// work 2048); with two, the next block's S is there when the softmax ends
+// (2620 cycles; S of 64 keys is bound by shared memory, 384 cycles where its
+// operations would take 256, so 2480 is the least).
 // Why a product warp per tile: a product's issue lasts nearly as long as its
 // execution, so what one warp spends on waiting and committing between the
-// tiles' products leaves the tensor cores idle.
+// tiles' products leaves the tensor cores idle (3980 cycles).
+// Items are numbered densely over the sequences' actual lengths, longer rows
+// of keys first.  CTAs that stay and take item after item measured slower
+// (a 32768-token prompt 5.68 ms against 5.43, eight single tokens over up to
+// 32768 keys 140 us against 103): the next item's copies wait for Q's place,
+// and its softmax for the last one's output, all the same.
 //
 // Bounds: 4*128 operations per visible (query head, key) pair for a prompt;
 // for a few queries over a long history the bytes of K and V.
@@ -32,7 +43,7 @@
 // Masked places: a masked score is replaced by -inf, so what K holds there
 // does not matter, but 0 * V would still turn an infinity or a NaN of a masked
 // value row into NaN.  Only tiles that some row of the pair does not see in
-// full can hold such rows: warps 12-15 replace the non-finite elements of
+// full can hold such rows: the scan warps replace the non-finite elements of
 // their value tiles by zeros before the product, and when there were any, the
 // epilogue adds the non-finite elements of the visible keys back (their
 // weights are positive, so an infinity keeps its sign).
@@ -46,12 +57,29 @@
 namespace spc {
 namespace {
 
-constexpr int kTile = 128;                   // query rows per tile, and keys per copy
-constexpr int kBlock = 64;                   // keys per S block
-constexpr int kStageBytes = kTile * kD * 2;  // one K or V tile, or one Q tile
-constexpr int kStages = 5;
-constexpr int kThreads = 512;
-constexpr uint32_t kTmemCols = 512;
+constexpr int kTile = 128;                  // query rows per tile
+constexpr int kBlock = 64;                  // keys per S block
+constexpr int kTileBytes = kTile * kD * 2;  // of a Q tile
+
+// What depends on the number of query tiles of a CTA.
+template <int TILES>
+struct Shape {
+  static constexpr int kKeys = TILES == 2 ? 128 : 64;  // keys per stage
+  static constexpr int kPerStage = kKeys / kBlock;     // S blocks of a stage
+  static constexpr int kAhead = 2 / kPerStage;         // K stages before the first V
+  static constexpr int kStages = TILES == 2 ? 5 : 4;
+  static constexpr int kStageBytes = kKeys * kD * 2;
+  static constexpr int kSoftmaxWarps = 4 * TILES;
+  static constexpr int kCopyWarp = kSoftmaxWarps;
+  static constexpr int kProductWarp = kCopyWarp + 1;              // and the next one
+  static constexpr int kScanWarp = TILES == 2 ? 12 : 6;           // from here on
+  static constexpr int kThreads = TILES == 2 ? 512 : 256;
+  static constexpr uint32_t kTmemCols = 256 * TILES;              // S of all tiles, then O
+  static constexpr int kSmemBytes = TILES * kTileBytes + kStages * kStageBytes + 1024 + 512;
+};
+static_assert(Shape<2>::kSmemBytes <= 232448 && 2 * (Shape<1>::kSmemBytes + 1024) <= 233472,
+              "more shared memory than an SM has");
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // The running maximum is only moved when it grows by more than this (in powers
@@ -67,33 +95,43 @@ struct PromptArgs {
   const int32_t* q_len;
   const int32_t* k_begin;
   const int32_t* k_len;
-  float* part_o;    // [item][split][tile rows][D]
-  float2* part_ml;  // [item][split][tile rows]
+  float* part_o;    // [split][sequence][q_max][query head][D]
+  float2* part_ml;  // and their (maximum, sum)
+  int64_t part_rows;
   uint32_t* fault;
-  int64_t v_b, v_t, v_h, o_b, o_t, o_h, lse_b;
-  int32_t S, Hq, Hkv, G, tile_tokens, pairs, splits;
+  int64_t v_b, v_t, v_h, o_b, o_t, o_h;
+  int32_t S, Hq, Hkv, G, tile_tokens, pair_tokens, pairs, splits;
   int32_t q_tokens, k_tokens, q_max, k_max;
   int32_t q_batched, k_batched;  // sequence s lies at s * stride (else on one token axis)
   float scale;
 };
 
-struct __align__(8) PromptBars {
+// What a CTA works on.
+struct PromptItem {
+  int s, hkv, pair, split;  // s < 0: nothing
+  int lq, lk, qb, kb;       // lengths and first tokens of the sequence
+  int tok0;                 // first query token
+  int lo, hi;               // stages of keys [lo, hi)
+  int blocks;               // 64-key blocks of them that some row sees
+  int edge;                 // first stage that some row does not see in full
+  int two;                  // the second query tile has rows
+};
+
+struct __align__(16) PromptBars {
+  PromptItem item;
   uint64_t q_full[2];
-  uint64_t kv_full[kStages];
-  uint64_t kv_free[kStages];
-  uint64_t v_scan;   // the next value tile that may hold masked places has arrived
+  uint64_t kv_full[5];
+  uint64_t kv_free[5];
+  uint64_t v_scan;   // the next value stage that may hold masked places has arrived
   uint64_t v_clean;  // and holds only finite elements
   // per query tile and S buffer: block i's scores are there, and so is the product of block i - 2's weights
   uint64_t s_full[2][2];
   uint64_t p_full[2][2];  // its weights are
   uint32_t tmem;
-  uint32_t bad;            // a masked tile held a non-finite value
+  uint32_t bad;            // a masked stage held a non-finite value
   volatile uint32_t stop;  // a wait ran out
 };
-
-constexpr int kSmemBytes = (2 + kStages) * kStageBytes + 1024 + 512;
 static_assert(sizeof(PromptBars) <= 512, "barriers outgrow their place");
-static_assert(kSmemBytes <= 232448, "more shared memory than an SM has");
 
 __device__ __forceinline__ void mbar_init(uint64_t* b, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(smem_addr(b)), "r"(count) : "memory");
@@ -229,33 +267,22 @@ __device__ __forceinline__ bool elect_lane() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(yes));
   return yes != 0;
 }
-// S = Q K^T of 64 keys: operands are two halves of 64 columns, rows of 128
-// bytes in groups of eight 1024 bytes apart; 16 columns (32 bytes) a step.
-__device__ __forceinline__ void product_s(uint32_t d, uint64_t q, uint64_t k) {
+// S = Q K^T of 64 keys: operands are two halves of 64 columns (k_half bytes
+// apart), rows of 128 bytes in groups of eight 1024 bytes apart; 16 columns
+// (32 bytes) a step.
+__device__ __forceinline__ void product_s(uint32_t d, uint64_t q, uint64_t k, uint32_t k_half) {
 #pragma unroll
-  for (int s = 0; s < 8; ++s) {
-    const uint32_t off = ((uint32_t)(s >> 2) * 16384u + (uint32_t)(s & 3) * 32u) / 16;
-    mma_ss(d, q + off, k + off, mma_word(kBlock, false), s > 0);
-  }
+  for (int s = 0; s < 8; ++s)
+    mma_ss(d, q + ((s >> 2) * (kTileBytes / 2) + (s & 3) * 32) / 16, k + ((s >> 2) * k_half + (s & 3) * 32) / 16,
+           mma_word(kBlock, false), s > 0);
 }
 // O += P V of 64 keys: V's halves hold channels 0-63 and 64-127 of each key (N
-// contiguous, the halves 16384 bytes apart, groups of eight keys 1024 bytes
-// apart); 16 keys (2048 bytes, and eight TMEM columns of P) a step.
+// contiguous, groups of eight keys 1024 bytes apart); 16 keys (2048 bytes, and
+// eight TMEM columns of P) a step.
 __device__ __forceinline__ void product_o(uint32_t d, uint32_t p, uint64_t v, bool add) {
 #pragma unroll
   for (int s = 0; s < 4; ++s) mma_ts(d, p + 8 * s, v + 2048u / 16 * s, mma_word(kD, true), add || s > 0);
 }
-
-// What a CTA works on.
-struct PromptItem {
-  int s, hkv, pair, split;
-  int lq, lk, qb, kb;  // lengths and first tokens of the sequence
-  int tok0;            // first query token of the pair
-  int lo, hi;          // key tiles [lo, hi)
-  int blocks;          // 64-key blocks of them that some row sees
-  int edge;            // first key tile that some row does not see in full
-  bool two;            // the second query tile has rows
-};
 
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return min(max(x, lo), hi); }
 
@@ -268,30 +295,96 @@ __device__ __forceinline__ void sequence(const PromptArgs& a, int s, int& lq, in
   lk = clampi(a.k_len ? a.k_len[s] : a.k_max, 0, min(a.k_max, a.k_tokens - kb));
 }
 
-// Item `i` of the grid: later pairs (more keys) first, KV heads and sequences
-// fastest, so that CTAs that run together read different heads' keys at the
-// same depth and several pairs of a head share them in L2.
-__device__ __forceinline__ PromptItem prompt_item(const PromptArgs& a, int64_t i) {
-  PromptItem w;
+// CTAs that a sequence's query rows take ("pairs", of one or two tiles).
+__device__ __forceinline__ int pairs_of(const PromptArgs& a, int lq) { return (lq + a.pair_tokens - 1) / a.pair_tokens; }
+__device__ __forceinline__ int sequence_pairs(const PromptArgs& a, int s) {
+  int lq, lk, qb, kb;
+  sequence(a, s, lq, lk, qb, kb);
+  return pairs_of(a, lq);
+}
+
+// Sum over the sequences of the pairs from pair p on (a whole warp; `mine` the
+// pairs of the lane's sequence among the first 32).
+__device__ __forceinline__ int pairs_from(const PromptArgs& a, int p, int mine) {
+  int n = max(0, mine - p);
+  for (int s = 32 + (threadIdx.x & 31); s < a.S; s += 32) n += max(0, sequence_pairs(a, s) - p);
+  return __reduce_add_sync(0xFFFFFFFFu, n);
+}
+
+// Item i of all (a whole warp): split fastest, then KV head, then sequence,
+// then pair, later pairs (more keys) first, over the pairs that exist.  CTAs
+// that run together then read different heads' keys at the same depth, and
+// several pairs of a head share them in L2.  False behind the last one.
+template <int TILES>
+__device__ __forceinline__ bool prompt_item(const PromptArgs& a, uint32_t i, PromptItem& w) {
+  constexpr int kKeys = Shape<TILES>::kKeys;
+  const int lane = threadIdx.x & 31;
+  int lq = 0, lk = 0, qb = 0, kb = 0;  // of sequence `lane`
+  if (lane < a.S) sequence(a, lane, lq, lk, qb, kb);
   w.split = (int)(i % a.splits);
   i /= a.splits;
   w.hkv = (int)(i % a.Hkv);
   i /= a.Hkv;
-  w.s = (int)(i % a.S);
-  w.pair = a.pairs - 1 - (int)(i / a.S);
-  sequence(a, w.s, w.lq, w.lk, w.qb, w.kb);
-  w.tok0 = w.pair * 2 * a.tile_tokens;
-  w.two = w.tok0 + a.tile_tokens < w.lq;
-  const int last = min(w.tok0 + 2 * a.tile_tokens, w.lq) - 1;  // last query token
+  if (a.q_len == nullptr && a.q_begin == nullptr) {  // equal sequences
+    w.s = (int)(i % a.S);
+    w.pair = a.pairs - 1 - (int)(i / a.S);
+    if (w.pair < 0) return false;
+  } else {
+    const int mine = pairs_of(a, lq), k0 = (int)i;
+    int lo = 0, hi = a.pairs, behind = 0;  // pairs_from(lo) > k0 >= pairs_from(hi) = behind
+    if (pairs_from(a, 0, mine) <= k0) return false;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2, n = pairs_from(a, mid, mine);
+      if (n > k0) {
+        lo = mid;
+      } else {
+        hi = mid;
+        behind = n;
+      }
+    }
+    w.pair = lo;
+    int k = k0 - behind;  // the k-th sequence that has this pair
+    for (int s0 = 0;; s0 += 32) {
+      const bool has = s0 + lane < a.S && (s0 == 0 ? mine : sequence_pairs(a, s0 + lane)) > lo;
+      const uint32_t who = __ballot_sync(0xFFFFFFFFu, has);
+      const int n = __popc(who);
+      if (k < n) {
+        const bool it = has && __popc(who & ((1u << lane) - 1u)) == k;
+        w.s = s0 + __ffs((int)__ballot_sync(0xFFFFFFFFu, it)) - 1;
+        break;
+      }
+      k -= n;
+      if (s0 + 32 >= a.S) return false;  // the lengths changed under the call
+    }
+  }
+  if (w.s < 32) {
+    w.lq = __shfl_sync(0xFFFFFFFFu, lq, w.s);
+    w.lk = __shfl_sync(0xFFFFFFFFu, lk, w.s);
+    w.qb = __shfl_sync(0xFFFFFFFFu, qb, w.s);
+    w.kb = __shfl_sync(0xFFFFFFFFu, kb, w.s);
+  } else {
+    sequence(a, w.s, w.lq, w.lk, w.qb, w.kb);
+  }
+  w.tok0 = w.pair * a.pair_tokens;
+  w.two = TILES == 2 && w.tok0 + a.tile_tokens < w.lq;
+  const int last = min(w.tok0 + a.pair_tokens, w.lq) - 1;  // last query token
   const int most = w.tok0 < w.lq ? clampi(last + w.lk - w.lq + 1, 0, w.lk) : 0;
   const int least = clampi(w.tok0 + w.lk - w.lq + 1, 0, w.lk);
-  const int n = (most + kTile - 1) / kTile;
+  const int n = (most + kKeys - 1) / kKeys;
   const int per = (n + a.splits - 1) / a.splits;
   w.lo = min(w.split * per, n);
   w.hi = min(w.lo + per, n);
-  w.blocks = max(0, min(2 * (w.hi - w.lo), (most - w.lo * kTile + kBlock - 1) / kBlock));
-  w.edge = least / kTile;
-  return w;
+  w.blocks = max(0, min(Shape<TILES>::kPerStage * (w.hi - w.lo), (most - w.lo * kKeys + kBlock - 1) / kBlock));
+  w.edge = least / kKeys;
+  return true;
+}
+
+// A query row's place in lse, and among the partial results of a split.
+__device__ __forceinline__ int64_t lse_place(const PromptArgs& a, int s, int token, int head) {
+  return ((a.q_batched ? (int64_t)s * a.q_tokens : 0) + token) * a.Hq + head;
+}
+__device__ __forceinline__ int64_t part_place(const PromptArgs& a, int split, int s, int tok, int head) {
+  return split * a.part_rows + ((int64_t)s * a.q_max + tok) * a.Hq + head;
 }
 
 // exp2(x c - m c) of a row's 64 scores, as bf16 pairs into P, and their sum.
@@ -314,26 +407,29 @@ __device__ __forceinline__ float row_weights(float* x, float c, float mc, uint32
   return all.x + all.y;
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+template <int TILES>
+__global__ void __launch_bounds__(Shape<TILES>::kThreads, TILES == 2 ? 1 : 2)
 prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap, const __grid_constant__ PromptArgs a) {
+  using H = Shape<TILES>;
+  constexpr int kStages = H::kStages;
   extern __shared__ uint8_t prompt_smem[];
-  const PromptItem w = prompt_item(a, blockIdx.x);
-  if (w.tok0 >= w.lq) return;  // uniform: no query rows
   uint8_t* base = prompt_smem + ((1024u - (smem_addr(prompt_smem) & 1023u)) & 1023u);
-  PromptBars& bars = *reinterpret_cast<PromptBars*>(base + (2 + kStages) * kStageBytes);
-  uint8_t* ring = base + 2 * kStageBytes;
+  uint8_t* ring = base + TILES * kTileBytes;
+  PromptBars& bars = *reinterpret_cast<PromptBars*>(ring + kStages * H::kStageBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int n = w.hi - w.lo;
 
-  if (warp == 9) {
+  if (warp == 0) {
+    PromptItem w;
+    if (!prompt_item<TILES>(a, blockIdx.x, w)) w.s = -1;
+    if (lane == 0) bars.item = w;
+  } else if (warp == H::kProductWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_addr(&bars.tmem)),
-                 "r"(kTmemCols)
+                 "r"(H::kTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
-  }
-  if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
+  } else if (warp == H::kScanWarp && lane == 0) {
+    for (int i = 0; i < TILES; ++i) {
       mbar_init(&bars.q_full[i], 1);
       for (int b = 0; b < 2; ++b) {
         mbar_init(&bars.s_full[i][b], 1);
@@ -342,10 +438,10 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
     }
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bars.kv_full[i], 1);
-      mbar_init(&bars.kv_free[i], w.two ? 2 : 1);
+      mbar_init(&bars.kv_free[i], TILES);
     }
-    mbar_init(&bars.v_scan, w.two ? 2 : 1);
-    mbar_init(&bars.v_clean, 4);
+    mbar_init(&bars.v_scan, TILES);
+    mbar_init(&bars.v_clean, H::kThreads / 32 - H::kScanWarp);
     bars.bad = 0;
     bars.stop = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -354,112 +450,138 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars.tmem;
+  const PromptItem& w = bars.item;
+  const int n = w.s < 0 ? 0 : w.hi - w.lo;  // stages of keys
 
-  if (warp >= 8) {
-    if (warp == 8) {
-      // ---- copies: Q tiles, then K_lo, V_lo, K_lo+1, V_lo+1, ... through the ring ----
+  // Registers: a thread starts with 128, half of the threads do the softmax (168 + 88 = 2 * 128).
+  if (warp >= H::kSoftmaxWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
+    if (warp == H::kCopyWarp) {
+      // ---- copies: the first K, Q, then V_j and K_j+kAhead by turns, through the ring ----
       if (lane == 0 && n > 0) {
-        const int tile_bytes = a.tile_tokens * a.G * kD * 2;
-        auto load_q = [&](int t) {
-          mbar_expect(&bars.q_full[t], tile_bytes);
-          const int tok = w.qb + w.tok0 + t * a.tile_tokens;
-          for (int h = 0; h < 2; ++h)
-            tma_load4(base + t * kStageBytes + h * 16384, &qmap, &bars.q_full[t], 64 * h, w.hkv * a.G, tok,
-                      a.q_batched ? w.s : 0);
-        };
+        const int tile_bytes = a.tile_tokens * a.G * kD * 2, qz = a.q_batched ? w.s : 0, kz = a.k_batched ? w.s : 0;
         bool ok = true;
-        auto load_kv = [&](int it, const CUtensorMap* map, int j) {
-          const int st = it % kStages;
-          ok = ok && mbar_wait(bars, &bars.kv_free[st], ((it / kStages) & 1) ^ 1);
+        int x = 0;
+        auto load_kv = [&](const CUtensorMap* map, int j) {
+          const int st = x % kStages;
+          ok = ok && mbar_wait(bars, &bars.kv_free[st], ((x / kStages) & 1) ^ 1);
           if (!ok) return;
-          mbar_expect(&bars.kv_full[st], kStageBytes);
+          ++x;
+          mbar_expect(&bars.kv_full[st], H::kStageBytes);
           for (int h = 0; h < 2; ++h)
-            tma_load4(ring + st * kStageBytes + h * 16384, map, &bars.kv_full[st], 64 * h, w.hkv, w.kb + j * kTile,
-                      a.k_batched ? w.s : 0);
+            tma_load4(ring + st * H::kStageBytes + h * (H::kStageBytes / 2), map, &bars.kv_full[st], 64 * h, w.hkv,
+                      w.kb + (w.lo + j) * H::kKeys, kz);
         };
-        load_q(0);
-        load_kv(0, &kmap, w.lo);
-        if (w.two) load_q(1);
+        load_kv(&kmap, 0);
+        for (int t = 0; t < (w.two ? 2 : 1); ++t) {
+          mbar_expect(&bars.q_full[t], tile_bytes);
+          for (int h = 0; h < 2; ++h)
+            tma_load4(base + t * kTileBytes + h * (kTileBytes / 2), &qmap, &bars.q_full[t], 64 * h, w.hkv * a.G,
+                      w.qb + w.tok0 + t * a.tile_tokens, qz);
+        }
+        for (int j = 1; j < H::kAhead && j < n; ++j) load_kv(&kmap, j);
         for (int j = 0; j < n && ok; ++j) {
-          load_kv(2 * j + 1, &vmap, w.lo + j);
-          if (j + 1 < n) load_kv(2 * j + 2, &kmap, w.lo + j + 1);
+          load_kv(&vmap, j);
+          if (j + H::kAhead < n) load_kv(&kmap, j + H::kAhead);
         }
       }
-    } else if (warp == 9 || (warp == 10 && w.two)) {
+    } else if (warp >= H::kProductWarp && warp < H::kProductWarp + TILES) {
       // ---- products of a tile: the whole warp walks the blocks, converged, so that operands are formed in uniform
       // registers (a lane alone issued a product every 55 cycles), and one lane issues ----
       const bool lead = elect_lane();
-      const int t = __shfl_sync(0xFFFFFFFFu, warp - 9, 0);
-      const int blocks = __shfl_sync(0xFFFFFFFFu, w.blocks, 0);
-      const int edge = __shfl_sync(0xFFFFFFFFu, w.edge - w.lo, 0);  // the first tile to be scanned
+      const int t = __shfl_sync(0xFFFFFFFFu, warp - H::kProductWarp, 0);
+      const int stages = __shfl_sync(0xFFFFFFFFu, n, 0);
+      const int blocks = stages > 0 ? __shfl_sync(0xFFFFFFFFu, w.blocks, 0) : 0;
+      const int edge = __shfl_sync(0xFFFFFFFFu, w.edge - w.lo, 0);  // the first stage to be scanned
+      const bool here = __shfl_sync(0xFFFFFFFFu, t == 0 || w.two, 0);
       const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
       const uint32_t base_addr = __shfl_sync(0xFFFFFFFFu, smem_addr(base), 0);
-      const uint64_t qd = smem_operand(base_addr + kStageBytes * t, 16, 1024);
-      const uint64_t kd = smem_operand(base_addr + 2 * kStageBytes, 16, 1024);
-      const uint64_t vd = smem_operand(base_addr + 2 * kStageBytes, 16384, 1024);
-      const uint32_t sp = tm + 128 * t, op = tm + 256 + 128 * t;
-      constexpr uint32_t kStep = kStageBytes / 16, kHalf = kBlock * 128 / 16;  // a stage, 64 of its rows
+      const uint64_t qd = smem_operand(base_addr + kTileBytes * t, 16, 1024);
+      const uint64_t kd = smem_operand(base_addr + TILES * kTileBytes, 16, 1024);
+      const uint64_t vd = smem_operand(base_addr + TILES * kTileBytes, H::kStageBytes / 2, 1024);
+      const uint32_t sp = tm + 2 * kBlock * t, op = tm + 2 * kBlock * TILES + kD * t;
+      constexpr uint32_t kStep = H::kStageBytes / 16, kNext = kBlock * 128 / 16;  // a stage, 64 of its rows
       uint32_t scans = 0;
-      bool ok = blocks > 0 && mbar_wait_warp(bars, &bars.kv_full[0], 0) && mbar_wait_warp(bars, &bars.q_full[t], 0);
-      if (ok && lead) {
-        product_s(sp, qd, kd);
-        tc_commit(&bars.s_full[t][0]);
-        if (blocks > 1) product_s(sp + kBlock, qd, kd + kHalf);
-        tc_commit(&bars.s_full[t][1]);
-        tc_commit(&bars.kv_free[0]);
+      bool ok = true;
+      int first = min(H::kAhead, stages);  // K stages of the first two blocks
+      for (int k = 0; k < first && ok; ++k) ok = mbar_wait_warp(bars, &bars.kv_full[k], 0);
+      if (here && blocks > 0) {
+        ok = ok && mbar_wait_warp(bars, &bars.q_full[t], 0);
+        if (ok && lead) {
+          product_s(sp, qd, kd, H::kStageBytes / 2);
+          tc_commit(&bars.s_full[t][0]);
+          if (blocks > 1) product_s(sp + kBlock, qd, kd + (H::kPerStage == 2 ? kNext : kStep), H::kStageBytes / 2);
+          tc_commit(&bars.s_full[t][1]);
+        }
+        __syncwarp();
       }
+      for (int k = 0; k < first && ok; ++k)
+        if (lead) {
+          if (here)
+            tc_commit(&bars.kv_free[k]);
+          else
+            mbar_arrive(&bars.kv_free[k]);  // a tile without rows only keeps step
+        }
       __syncwarp();
-      int sv = 1, sk = 2;       // stages of V_j and K_j+1
-      uint32_t pv = 0, pk = 0;  // and the phases of their barriers
-      for (int j = 0; 2 * j < blocks && ok; ++j) {
-        ok = mbar_wait_warp(bars, &bars.kv_full[sv], pv);
+      int x = first;
+      for (int j = 0; j < stages && ok; ++j) {
+        const int xv = x++, sv = xv % kStages;
+        const bool more = j + H::kAhead < stages;
+        const int xk = more ? x++ : xv, sk = xk % kStages;
+        ok = mbar_wait_warp(bars, &bars.kv_full[sv], (xv / kStages) & 1);
         if (ok && j >= edge) {
           if (lead) mbar_arrive(&bars.v_scan);
           __syncwarp();
           ok = mbar_wait_warp(bars, &bars.v_clean, scans++ & 1u);
         }
-        if (ok && 2 * j + 2 < blocks) ok = mbar_wait_warp(bars, &bars.kv_full[sk], pk);
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          if (2 * j + b >= blocks || !ok) break;
-          ok = mbar_wait_warp(bars, &bars.p_full[t][b], j & 1);
+        if (ok && more) ok = mbar_wait_warp(bars, &bars.kv_full[sk], (xk / kStages) & 1);
+        if (!here) {
+          if (ok && lead) {
+            mbar_arrive(&bars.kv_free[sv]);
+            if (more) mbar_arrive(&bars.kv_free[sk]);
+          }
+          __syncwarp();
+          continue;
+        }
+  #pragma unroll
+        for (int h = 0; h < H::kPerStage; ++h) {
+          const int i = H::kPerStage * j + h, b = i & 1;
+          if (i >= blocks || !ok) break;
+          ok = mbar_wait_warp(bars, &bars.p_full[t][b], (i >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
           if (lead) {
-            product_o(op, sp + kBlock * b, vd + kStep * sv + kHalf * b, j + b > 0);
-            if (2 * j + b + 2 < blocks) product_s(sp + kBlock * b, qd, kd + kStep * sk + kHalf * b);
+            product_o(op, sp + kBlock * b, vd + kStep * sv + kNext * h, i > 0);
+            if (i + 2 < blocks) product_s(sp + kBlock * b, qd, kd + kStep * sk + kNext * h, H::kStageBytes / 2);
             tc_commit(&bars.s_full[t][b]);
           }
           __syncwarp();
         }
         if (ok && lead) {
           tc_commit(&bars.kv_free[sv]);
-          if (2 * j + 2 < blocks) tc_commit(&bars.kv_free[sk]);
+          if (more) tc_commit(&bars.kv_free[sk]);
         }
         __syncwarp();
-        sv += 2;
-        if (sv >= kStages) { sv -= kStages; pv ^= 1; }
-        sk += 2;
-        if (sk >= kStages) { sk -= kStages; pk ^= 1; }
       }
-    } else if (warp >= 12) {
-      // ---- values in masked places: tile by tile as the product warp asks (a wait on the stage alone could
-      // take an earlier phase of its barrier for the awaited one) ----
+    } else if (warp >= H::kScanWarp) {
+      // ---- values in masked places: stage by stage as the product warps ask (a wait on the stage alone could take an
+      // earlier phase of its barrier for the awaited one) ----
       uint32_t scans = 0;
+      const int first = min(H::kAhead, n);
       for (int j = max(w.edge - w.lo, 0); j < n; ++j) {
-        const int iv = 2 * j + 1, sv = iv % kStages;
+        const int xv = first + j + min(j, n - first), sv = xv % kStages;
         if (!mbar_wait_warp(bars, &bars.v_scan, scans++ & 1u)) break;
-        if (!mbar_wait_warp(bars, &bars.kv_full[sv], (iv / kStages) & 1)) break;
-        uint4* tile = reinterpret_cast<uint4*>(ring + sv * kStageBytes);
+        if (!mbar_wait_warp(bars, &bars.kv_full[sv], (xv / kStages) & 1)) break;
+        uint4* tile = reinterpret_cast<uint4*>(ring + sv * H::kStageBytes);
         bool touched = false;
-#pragma unroll 4
-        for (int i = tid - 384; i < kStageBytes / 16; i += 128) {
-          const uint4 x = tile[i];
+  #pragma unroll 4
+        for (int i = tid - 32 * H::kScanWarp; i < H::kStageBytes / 16; i += H::kThreads - 32 * H::kScanWarp) {
+          const uint4 v = tile[i];
           // 16-bit halves with an exponent of all ones
-          const uint32_t m0 = __vcmpeq2(x.x & 0x7F807F80u, 0x7F807F80u), m1 = __vcmpeq2(x.y & 0x7F807F80u, 0x7F807F80u);
-          const uint32_t m2 = __vcmpeq2(x.z & 0x7F807F80u, 0x7F807F80u), m3 = __vcmpeq2(x.w & 0x7F807F80u, 0x7F807F80u);
+          const uint32_t m0 = __vcmpeq2(v.x & 0x7F807F80u, 0x7F807F80u), m1 = __vcmpeq2(v.y & 0x7F807F80u, 0x7F807F80u);
+          const uint32_t m2 = __vcmpeq2(v.z & 0x7F807F80u, 0x7F807F80u), m3 = __vcmpeq2(v.w & 0x7F807F80u, 0x7F807F80u);
           if (m0 | m1 | m2 | m3) {
-            tile[i] = make_uint4(x.x & ~m0, x.y & ~m1, x.z & ~m2, x.w & ~m3);
+            tile[i] = make_uint4(v.x & ~m0, v.y & ~m1, v.z & ~m2, v.w & ~m3);
             touched = true;
           }
         }
@@ -470,122 +592,127 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
       }
     }
   } else {
-    // ---- softmax of one tile, a thread per row ----
-    const int t = warp >> 2, r = tid & 127;
-    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // TMEM lane 32 * (warp % 4)
-    const uint32_t s_addr = tmem + lanes + 128 * t, o_addr = tmem + lanes + 256 + 128 * t;
-    const int tok = w.tok0 + t * a.tile_tokens + r / a.G;
-    const int head = w.hkv * a.G + r % a.G;
-    const bool row = r < a.tile_tokens * a.G && tok < w.lq;
-    const int seen = row ? clampi(tok + w.lk - w.lq + 1, 0, w.lk) : w.lk;  // keys of this row
-    const float c = a.scale * kLog2e;
-    const bool active = t == 0 || w.two;
-    float m = -INFINITY, l = 0.f;
-    bool ok = true;
-    if (active) {
-      for (int i = 0; i < w.blocks; ++i) {
-        const int b = i & 1;
-        const uint32_t sp = s_addr + kBlock * b;
-        ok = mbar_wait_warp(bars, &bars.s_full[t][b], (i >> 1) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        float x[kBlock];
-        tmem_ld32(sp, x);
-        tmem_ld32(sp + 32, x + 32);
-        tmem_wait_ld(x);
-        tmem_wait_ld(x + 32);
-        if (w.lo + (i >> 1) >= w.edge) {
-          const int vis = seen - w.lo * kTile - i * kBlock;
-#pragma unroll
-          for (int e = 0; e < kBlock; ++e) x[e] = e < vis ? x[e] : -INFINITY;
-        }
-        float top[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-        for (int e = 4; e < kBlock; e += 8)
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            top[u] = e + 4 + u < kBlock ? max3(top[u], x[e + u], x[e + 4 + u]) : fmaxf(top[u], x[e + u]);
-        const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]);
-        const bool grow = mx > m && !((mx - m) * c <= kSlack);
-        if (__any_sync(0xFFFFFFFFu, grow)) {
-          const float f = grow ? fast_exp2((m - mx) * c) : 1.f;  // m = -inf: 0
-          if (grow) m = mx;
-          l *= f;
-          if (i > 0) {
-            // the product of the block before has to be complete: the next use of the other buffer says so
-            ok = mbar_wait_warp(bars, &bars.s_full[t][b ^ 1], ((i + 1) >> 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              float y[32];
-              tmem_ld32(o_addr + 32 * q, y);
-              tmem_wait_ld(y);
-              uint32_t u[32];
-#pragma unroll
-              for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(y[e] * f);
-              tmem_st16(o_addr + 32 * q, u);
-              tmem_st16(o_addr + 32 * q + 16, u + 16);
-            }
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;\n");
+    if (w.s >= 0) {
+      // ---- softmax and output of one tile, a thread per row ----
+      const int t = warp >> 2, r = tid & 127;
+      const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // TMEM lane 32 * (warp % 4)
+      const uint32_t s_addr = tmem + lanes + 2 * kBlock * t, o_addr = tmem + lanes + 2 * kBlock * TILES + kD * t;
+      const int tok = w.tok0 + t * a.tile_tokens + r / a.G;
+      const int head = w.hkv * a.G + r % a.G;
+      const bool row = r < a.tile_tokens * a.G && tok < w.lq;
+      const int seen = row ? clampi(tok + w.lk - w.lq + 1, 0, w.lk) : w.lk;  // keys of this row
+      const int from = w.lo * H::kKeys, blocks = w.blocks;
+      const int masked = H::kPerStage * (w.edge - w.lo);  // the first block that some row does not see in full
+      const float c = a.scale * kLog2e;
+      float m = -INFINITY, l = 0.f;
+      bool ok = true;
+      if (t == 0 || w.two) {
+        for (int i = 0; i < blocks; ++i) {
+          const int b = i & 1;
+          const uint32_t sp = s_addr + kBlock * b;
+          ok = mbar_wait_warp(bars, &bars.s_full[t][b], (i >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          float x[kBlock];
+          tmem_ld32(sp, x);
+          tmem_ld32(sp + 32, x + 32);
+          tmem_wait_ld(x);
+          tmem_wait_ld(x + 32);
+          if (i >= masked) {
+            const int vis = seen - from - i * kBlock;
+  #pragma unroll
+            for (int e = 0; e < kBlock; ++e) x[e] = e < vis ? x[e] : -INFINITY;
           }
-        }
-        l += row_weights(x, c, m == -INFINITY ? 0.f : m * c, sp);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.p_full[t][b]);
-      }
-      // ---- output ----
-      const int64_t part = ((int64_t)blockIdx.x * 2 + t) * kTile + r;  // splits are fastest in the grid
-      if (n > 0 && ok) ok = mbar_wait_warp(bars, &bars.s_full[t][(w.blocks + 1) & 1], ((w.blocks + 1) >> 1) & 1);
-      if (ok) {
-        tc_fence_after();
-        const bool bad = *(volatile uint32_t*)&bars.bad != 0u;
-        const int first = max(w.edge, w.lo) * kTile, end = min(seen, w.hi * kTile);
-        // no visible key: 0; otherwise the sum is positive, or not a number when the scores are not
-        const bool any = seen > w.lo * kTile;
-        const float inv = a.splits > 1 ? 1.f : (any ? 1.f / l : 0.f);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          float y[32];
-          if (n > 0) {
-            tmem_ld32(o_addr + 32 * b, y);
-            tmem_wait_ld(y);
-          }
-          if (!any) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) y[i] = 0.f;
-          }
-          if (bad && row) {
-            const uint16_t* vr = a.v + w.s * a.v_b + (int64_t)(w.kb + first) * a.v_t + w.hkv * a.v_h + 32 * b;
-            for (int key = first; key < end; ++key, vr += a.v_t) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const uint32_t e = vr[i];
-                if ((e & 0x7F80u) == 0x7F80u) y[i] += bf16_to_f32(e);
+          float top[4] = {x[0], x[1], x[2], x[3]};
+  #pragma unroll
+          for (int e = 4; e < kBlock; e += 8)
+  #pragma unroll
+            for (int u = 0; u < 4; ++u)
+              top[u] = e + 4 + u < kBlock ? max3(top[u], x[e + u], x[e + 4 + u]) : fmaxf(top[u], x[e + u]);
+          const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+          const bool grow = mx > m && !((mx - m) * c <= kSlack);
+          if (__any_sync(0xFFFFFFFFu, grow)) {
+            const float f = grow ? fast_exp2((m - mx) * c) : 1.f;  // m = -inf: 0
+            if (grow) m = mx;
+            l *= f;
+            if (i > 0) {
+              // the product of the block before has to be complete: the next use of the other buffer says so
+              ok = mbar_wait_warp(bars, &bars.s_full[t][b ^ 1], ((i + 1) >> 1) & 1);
+              if (!ok) break;
+              tc_fence_after();
+  #pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                float y[32];
+                tmem_ld32(o_addr + 32 * q, y);
+                tmem_wait_ld(y);
+                uint32_t u[32];
+  #pragma unroll
+                for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(y[e] * f);
+                tmem_st16(o_addr + 32 * q, u);
+                tmem_st16(o_addr + 32 * q + 16, u + 16);
               }
             }
           }
-          if (!row) continue;
-          if (a.splits > 1) {
-            float4* po = reinterpret_cast<float4*>(a.part_o + part * kD + 32 * b);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) po[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-          } else {
-            uint4* po = reinterpret_cast<uint4*>(a.o + w.s * a.o_b + (int64_t)(w.qb + tok) * a.o_t + head * a.o_h + 32 * b);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              po[i] = make_uint4(pack_bf16x2(y[8 * i] * inv, y[8 * i + 1] * inv),
-                                 pack_bf16x2(y[8 * i + 2] * inv, y[8 * i + 3] * inv),
-                                 pack_bf16x2(y[8 * i + 4] * inv, y[8 * i + 5] * inv),
-                                 pack_bf16x2(y[8 * i + 6] * inv, y[8 * i + 7] * inv));
-          }
+          l += row_weights(x, c, m == -INFINITY ? 0.f : m * c, sp);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.p_full[t][b]);
         }
-        if (row) {
-          if (a.splits > 1)
-            a.part_ml[part] = make_float2(any ? m * c : -INFINITY, any ? l : 0.f);
-          else if (a.lse)
-            a.lse[w.s * a.lse_b + (int64_t)(w.qb + tok) * a.Hq + head] = any ? m * a.scale + logf(l) : -INFINITY;
+        // ---- output ----
+        if (blocks > 0 && ok) ok = mbar_wait_warp(bars, &bars.s_full[t][(blocks + 1) & 1], ((blocks + 1) >> 1) & 1);
+        if (ok) {
+          tc_fence_after();
+          const bool bad = *(volatile uint32_t*)&bars.bad != 0u;
+          const int first = max(w.edge, w.lo) * H::kKeys, end = min(seen, w.hi * H::kKeys);
+          // no visible key: 0; otherwise the sum is positive, or not a number when the scores are not
+          const bool any = seen > from;
+          const float inv = a.splits > 1 ? 1.f : (any ? 1.f / l : 0.f);
+          const int64_t part = part_place(a, w.split, w.s, tok, head);
+  #pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float y[32];
+            if (blocks > 0) {
+              tmem_ld32(o_addr + 32 * q, y);
+              tmem_wait_ld(y);
+            }
+            if (!any) {
+  #pragma unroll
+              for (int i = 0; i < 32; ++i) y[i] = 0.f;
+            }
+            if (bad && row) {
+              const uint16_t* vr = a.v + w.s * a.v_b + (int64_t)(w.kb + first) * a.v_t + w.hkv * a.v_h + 32 * q;
+              for (int key = first; key < end; ++key, vr += a.v_t) {
+  #pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const uint32_t e = vr[i];
+                  if ((e & 0x7F80u) == 0x7F80u) y[i] += bf16_to_f32(e);
+                }
+              }
+            }
+            if (!row) continue;
+            if (a.splits > 1) {
+              float4* po = reinterpret_cast<float4*>(a.part_o + part * kD + 32 * q);
+  #pragma unroll
+              for (int i = 0; i < 8; ++i) po[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            } else {
+              uint4* po =
+                  reinterpret_cast<uint4*>(a.o + w.s * a.o_b + (int64_t)(w.qb + tok) * a.o_t + head * a.o_h + 32 * q);
+  #pragma unroll
+              for (int i = 0; i < 4; ++i)
+                po[i] = make_uint4(pack_bf16x2(y[8 * i] * inv, y[8 * i + 1] * inv),
+                                   pack_bf16x2(y[8 * i + 2] * inv, y[8 * i + 3] * inv),
+                                   pack_bf16x2(y[8 * i + 4] * inv, y[8 * i + 5] * inv),
+                                   pack_bf16x2(y[8 * i + 6] * inv, y[8 * i + 7] * inv));
+            }
+          }
+          if (row) {
+            if (a.splits > 1)
+              a.part_ml[part] = make_float2(any ? m * c : -INFINITY, any ? l : 0.f);
+            else if (a.lse)
+              a.lse[lse_place(a, w.s, w.qb + tok, head)] = any ? m * a.scale + logf(l) : -INFINITY;
+          }
         }
       }
     }
@@ -597,49 +724,48 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == H::kProductWarp) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(H::kTmemCols) : "memory");
   }
 }
 
-// Joins the splits of a row: o = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s,
-// in the order of the splits.  One warp per row, four channels a lane.
-__global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant__ PromptArgs a) {
-  const int64_t rows_per_pair = 2 * (int64_t)a.tile_tokens * a.G;
-  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int64_t item = i / rows_per_pair;  // as the grid numbers them, without the split
-  if (item >= (int64_t)a.S * a.Hkv * a.pairs) return;
-  const int in_pair = (int)(i % rows_per_pair);
-  const int per_tile = a.tile_tokens * a.G;
-  const int t = in_pair / per_tile, r = in_pair % per_tile;
-  const int lane = threadIdx.x & 31;
-  const int hkv = (int)(item % a.Hkv), s = (int)(item / a.Hkv % a.S);
-  const int pair = a.pairs - 1 - (int)(item / a.Hkv / a.S);
+// Joins the splits of a row: o = sum_z 2^(m_z - m) o_z / sum_z 2^(m_z - m) l_z,
+// in the order of the splits.  One warp per row (sequence in blockIdx.y), four
+// channels a lane; lane z holds split z's maximum and sum (two each past 32).
+__global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant__ PromptArgs a) {
+  const int row = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31, s = blockIdx.y;
+  const int tok = row / a.Hq, head = row - tok * a.Hq;
   int lq, lk, qb, kb;
   sequence(a, s, lq, lk, qb, kb);
-  const int tok = (pair * 2 + t) * a.tile_tokens + r / a.G, head = hkv * a.G + r % a.G;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the partial results are there
   if (tok >= lq) return;
-  float m = -INFINITY;
-  for (int z = 0; z < a.splits; ++z) m = fmaxf(m, a.part_ml[((item * a.splits + z) * 2 + t) * kTile + r].x);
-  float l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   const bool any = tok + lk - lq + 1 > 0 && lk > 0;
-  if (any) {
-    for (int z = 0; z < a.splits; ++z) {
-      const int64_t part = ((item * a.splits + z) * 2 + t) * kTile + r;
-      const float2 ml = a.part_ml[part];
-      if (ml.y == 0.f) continue;  // nothing visible in this split
-      const float f = exp2f(ml.x - m);
-      const float4 x = reinterpret_cast<const float4*>(a.part_o + part * kD)[lane];
-      l += f * ml.y;
-      o = make_float4(o.x + f * x.x, o.y + f * x.y, o.z + f * x.z, o.w + f * x.w);
-    }
+  float2 ml[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int z = lane + 32 * u;
+    ml[u] = z < a.splits ? a.part_ml[part_place(a, z, s, tok, head)] : make_float2(-INFINITY, 0.f);
+  }
+  float m = fmaxf(ml[0].x, ml[1].x);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
+  float f[2], l = 0.f;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) f[u] = ml[u].y == 0.f ? 0.f : exp2f(ml[u].x - m);  // a sum of 0: nothing visible there
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int z = 0; z < a.splits; ++z) {
+    const float g = __shfl_sync(0xFFFFFFFFu, z < 32 ? f[0] : f[1], z & 31);
+    const float sum = __shfl_sync(0xFFFFFFFFu, z < 32 ? ml[0].y : ml[1].y, z & 31);
+    if (sum == 0.f) continue;
+    const float4 x = reinterpret_cast<const float4*>(a.part_o + part_place(a, z, s, tok, head) * kD)[lane];
+    l += g * sum;
+    o = make_float4(o.x + g * x.x, o.y + g * x.y, o.z + g * x.z, o.w + g * x.w);
   }
   const float inv = any ? 1.f / l : 0.f;
   uint2* po = reinterpret_cast<uint2*>(a.o + s * a.o_b + (int64_t)(qb + tok) * a.o_t + head * a.o_h) + lane;
   *po = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-  if (lane == 0 && a.lse) a.lse[s * a.lse_b + (int64_t)(qb + tok) * a.Hq + head] = any ? m * kLn2 + logf(l) : -INFINITY;
+  if (lane == 0 && a.lse) a.lse[lse_place(a, s, qb + tok, head)] = any ? m * kLn2 + logf(l) : -INFINITY;
 }
 
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -676,28 +802,78 @@ bool encode_map(CUtensorMap* map, const uint16_t* p, int64_t batch, int64_t toke
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Grid of a call: pairs of query tiles per (sequence, KV head), and splits of
-// the keys where the pairs alone do not fill the GPU.
-void prompt_grid(const spc_prompt_dims* d, int& tile_tokens, int& pairs, int& splits) {
+// Grid of a call.  One query tile per CTA where every sequence's rows fit into
+// it, else two; the items without splits that there can be (packed sequences
+// share the tokens of one axis); and splits of the keys where these do not
+// fill the GPU.
+//
+// The number of splits is the one for which this estimate is least (in ns, of
+// measurements): an item costs its start and output and its 64-key blocks; a
+// block takes what its products take, or its 32 KB at the rate of HBM where
+// one tile streams them.  Items of one sequence within the CTAs' places end
+// together; others are taken as they come (sequences may be shorter than
+// k_max, so rounds are not counted on), and the last one ends alone.  A split's partial results are written and read back,
+// and joined in a launch of their own.  Measured against it: one token over
+// 32768 keys 391 us in one piece, 106 in 4, 43 in 14, 38 in 28 and 41 in 38;
+// eight over up to 32768 keys 206 in 2, 135 in 4, 108 in 7 and in 14, 120 in
+// 28; 500 tokens over 32768 keys 373 in one, 205 in 2, 277 in 3, 213 in 7 and
+// 267 in 14; a 1024-token prompt 23 in one and 43 in 2.
+constexpr int kMaxSplits = 64;
+
+struct PromptGrid {
+  int tiles, tile_tokens, pair_tokens, pairs, splits;
+  int64_t items;
+};
+
+PromptGrid prompt_grid(const spc_prompt_dims* d) {
+  PromptGrid g;
   const int G = d->Hq / d->Hkv;
-  tile_tokens = kTile / G;
-  pairs = (int)(((int64_t)d->q_max + 2 * tile_tokens - 1) / (2 * tile_tokens));
-  const int64_t items = (int64_t)d->S * d->Hkv * pairs;
-  const int64_t sms = spc_host::sm_count();
-  const int64_t ktiles = ((int64_t)d->k_max + kTile - 1) / kTile;
-  splits = 1;
-  if (items > 0 && items < sms) splits = (int)std::max<int64_t>(1, std::min<int64_t>(ktiles / 4, 4 * sms / items));
+  g.tile_tokens = kTile / G;
+  g.tiles = d->q_max <= g.tile_tokens ? 1 : 2;
+  g.pair_tokens = g.tiles * g.tile_tokens;
+  g.pairs = (d->q_max + g.pair_tokens - 1) / g.pair_tokens;
+  int64_t all = (int64_t)d->S * g.pairs;
+  if (d->q.b == 0) all = std::min(all, d->S + (int64_t)d->q_tokens / g.pair_tokens);
+  g.items = all * d->Hkv;
+  g.splits = 1;
+  const int64_t places = spc_host::sm_count() * (g.tiles == 1 ? 2 : 1);
+  const int64_t blocks = ((int64_t)d->k_max + kBlock - 1) / kBlock;
+  const int64_t rows = (int64_t)d->S * d->q_max * d->Hq;
+  if (g.items >= places) return g;
+  int64_t best = 0;
+  for (int64_t z = 1; z <= std::max<int64_t>(1, std::min<int64_t>(blocks / 4, kMaxSplits)); ++z) {
+    const int64_t busy = std::min(g.items * z, places), share = (blocks + z - 1) / z, start = 4000;
+    const int64_t alone = g.tiles == 2 ? 690 : 760, block = g.tiles == 2 ? 690 : std::max<int64_t>(760, busy * 5);
+    int64_t cost = d->S == 1 && g.items * z <= places ? share * block + start
+                                                      : g.items * (blocks * block + z * start) / places + share * alone;
+    if (z > 1) cost += 3000 + z * rows / 5;
+    if (z == 1 || cost < best) {
+      best = cost;
+      g.splits = (int)z;
+    }
+  }
+  return g;
 }
 
 constexpr size_t kPromptHead = 256;  // the fault word
 
+template <int TILES>
+cudaError_t launch_prompt_k(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const PromptArgs& a,
+                            int64_t grid, cudaStream_t stream) {
+  static unsigned long long configured = 0ull;
+  const cudaError_t e =
+      spc_host::ensure_smem_limit(configured, prompt_attn_kernel<TILES>, Shape<TILES>::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  prompt_attn_kernel<TILES><<<(unsigned)grid, Shape<TILES>::kThreads, Shape<TILES>::kSmemBytes, stream>>>(qm, km, vm, a);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 size_t prompt_workspace_bytes(const spc_prompt_dims* d) {
-  int tile_tokens, pairs, splits;
-  prompt_grid(d, tile_tokens, pairs, splits);
-  if (splits == 1) return kPromptHead;
-  const size_t rows = (size_t)d->S * d->Hkv * pairs * splits * 2 * kTile;
+  const PromptGrid g = prompt_grid(d);
+  if (g.splits == 1) return kPromptHead;
+  const size_t rows = (size_t)d->S * d->q_max * d->Hq * g.splits;
   return kPromptHead + rows * (kD * sizeof(float) + sizeof(float2));
 }
 
@@ -720,7 +896,6 @@ spc_status launch_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const
   a.o_h = d->o.h;
   a.q_batched = d->q.b != 0;
   a.k_batched = d->k.b != 0;
-  a.lse_b = a.q_batched ? (int64_t)d->q_tokens * d->Hq : 0;
   a.S = d->S;
   a.Hq = d->Hq;
   a.Hkv = d->Hkv;
@@ -730,30 +905,38 @@ spc_status launch_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const
   a.q_max = d->q_max;
   a.k_max = d->k_max;
   a.scale = d->scale;
-  prompt_grid(d, a.tile_tokens, a.pairs, a.splits);
+  const PromptGrid g = prompt_grid(d);
+  a.tile_tokens = g.tile_tokens;
+  a.pair_tokens = g.pair_tokens;
+  a.pairs = g.pairs;
+  a.splits = g.splits;
   a.fault = static_cast<uint32_t*>(ws);
-  const int64_t items = (int64_t)d->S * d->Hkv * a.pairs;
-  const size_t rows = (size_t)items * a.splits * 2 * kTile;
+  a.part_rows = (int64_t)d->S * d->q_max * d->Hq;
   a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kPromptHead);
-  a.part_ml = reinterpret_cast<float2*>(a.part_o + rows * kD);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + a.part_rows * a.splits * kD);
   CUtensorMap qm, km, vm;
   const int64_t kt = std::max(d->k_tokens, 1);  // no keys at all: the maps are never read through
+  const uint32_t keys = g.tiles == 2 ? Shape<2>::kKeys : Shape<1>::kKeys;
   if (!encode_map(&qm, q, a.q_batched ? d->S : 1, d->q_tokens, d->Hq, d->q, a.G, a.tile_tokens) ||
-      !encode_map(&km, k ? k : q, a.k_batched ? d->S : 1, kt, d->Hkv, d->k, 1, kTile) ||
-      !encode_map(&vm, v ? v : q, a.k_batched ? d->S : 1, kt, d->Hkv, d->v, 1, kTile)) {
+      !encode_map(&km, k ? k : q, a.k_batched ? d->S : 1, kt, d->Hkv, d->k, 1, keys) ||
+      !encode_map(&vm, v ? v : q, a.k_batched ? d->S : 1, kt, d->Hkv, d->v, 1, keys)) {
     spc_host::set_cuda_error(cudaErrorInvalidValue);
     return SPC_ERR_CUDA;
   }
-  static unsigned long long configured = 0ull;
-  cudaError_t e = spc_host::ensure_smem_limit(configured, prompt_attn_kernel, kSmemBytes);
-  if (e == cudaSuccess) {
-    prompt_attn_kernel<<<(unsigned)(items * a.splits), kThreads, kSmemBytes, stream>>>(qm, km, vm, a);
-    e = cudaGetLastError();
-  }
+  const int64_t grid = g.items * a.splits;
+  cudaError_t e = g.tiles == 2 ? launch_prompt_k<2>(qm, km, vm, a, grid, stream)
+                               : launch_prompt_k<1>(qm, km, vm, a, grid, stream);
   if (e == cudaSuccess && a.splits > 1) {
-    const int64_t warps = items * 2 * a.tile_tokens * a.G;
-    prompt_join_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(a);
-    e = cudaGetLastError();
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(((int64_t)d->q_max * d->Hq + 3) / 4), (unsigned)d->S);
+    cfg.blockDim = dim3(128);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, prompt_join_kernel, a);
   }
   if (e != cudaSuccess) {
     spc_host::set_cuda_error(e);
