@@ -122,8 +122,8 @@ struct __align__(16) PromptBars {
   uint64_t q_full[2];
   uint64_t kv_full[5];
   uint64_t kv_free[5];
-  uint64_t v_scan;   // the next value stage that may hold masked places has arrived
-  uint64_t v_clean;  // and holds only finite elements
+  uint64_t v_scan[2];   // a value stage that may hold masked places is on its way (requests by turns)
+  uint64_t v_clean[5];  // the stage has arrived and holds only finite elements
   // per query tile and S buffer: block i's scores are there, and so is the product of block i - 2's weights
   uint64_t s_full[2][2];
   uint64_t p_full[2][2];  // its weights are
@@ -184,6 +184,10 @@ __device__ __forceinline__ void tma_load4(void* dst, const CUtensorMap* map, uin
       "[%2];\n" ::"r"(smem_addr(dst)),
       "l"(map), "r"(smem_addr(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
       : "memory");
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];\n" ::"l"(map) : "memory");
 }
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
@@ -419,32 +423,66 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
   PromptBars& bars = *reinterpret_cast<PromptBars*>(ring + kStages * H::kStageBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  if (warp == 0) {
+  int x = 0;  // the copy warp: stages filled so far
+  const auto load_kv = [&](const PromptItem& w, const CUtensorMap* map, int j) {
+    const int st = x % kStages;
+    if (!mbar_wait(bars, &bars.kv_free[st], ((x / kStages) & 1) ^ 1)) return false;
+    ++x;
+    mbar_expect(&bars.kv_full[st], H::kStageBytes);
+    for (int h = 0; h < 2; ++h)
+      tma_load4(ring + st * H::kStageBytes + h * (H::kStageBytes / 2), map, &bars.kv_full[st], 64 * h, w.hkv,
+                w.kb + (w.lo + j) * H::kKeys, a.k_batched ? w.s : 0);
+    return true;
+  };
+  if (warp == H::kCopyWarp) {
+    // sets up the barriers, looks the item up and starts the first copies before the others are ready
+    if (lane == 0) {
+      prefetch_map(&kmap);
+      prefetch_map(&qmap);
+      prefetch_map(&vmap);
+      for (int i = 0; i < TILES; ++i) {
+        mbar_init(&bars.q_full[i], 1);
+        for (int b = 0; b < 2; ++b) {
+          mbar_init(&bars.s_full[i][b], 1);
+          mbar_init(&bars.p_full[i][b], 4);
+        }
+      }
+      for (int i = 0; i < kStages; ++i) {
+        mbar_init(&bars.kv_full[i], 1);
+        mbar_init(&bars.kv_free[i], TILES);
+        mbar_init(&bars.v_clean[i], H::kThreads / 32 - H::kScanWarp);
+      }
+      for (int i = 0; i < 2; ++i) mbar_init(&bars.v_scan[i], 1);
+      bars.bad = 0;
+      bars.stop = 0;
+      asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+    }
+    __syncwarp();
     PromptItem w;
-    if (!prompt_item<TILES>(a, blockIdx.x, w)) w.s = -1;
-    if (lane == 0) bars.item = w;
+    if (!prompt_item<TILES>(a, blockIdx.x, w)) {
+      w.s = -1;
+      w.lo = w.hi = 0;
+    }
+    if (lane == 0) {
+      bars.item = w;
+      if (w.hi > w.lo) {
+        load_kv(w, &kmap, 0);
+        for (int t = 0; t < (w.two ? 2 : 1); ++t) {
+          mbar_expect(&bars.q_full[t], a.tile_tokens * a.G * kD * 2);
+          for (int h = 0; h < 2; ++h)
+            tma_load4(base + t * kTileBytes + h * (kTileBytes / 2), &qmap, &bars.q_full[t], 64 * h, w.hkv * a.G,
+                      w.qb + w.tok0 + t * a.tile_tokens, a.q_batched ? w.s : 0);
+        }
+        for (int j = 1; j < H::kAhead && w.lo + j < w.hi; ++j) load_kv(w, &kmap, j);
+      }
+    }
+    __syncwarp();
   } else if (warp == H::kProductWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_addr(&bars.tmem)),
                  "r"(H::kTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
-  } else if (warp == H::kScanWarp && lane == 0) {
-    for (int i = 0; i < TILES; ++i) {
-      mbar_init(&bars.q_full[i], 1);
-      for (int b = 0; b < 2; ++b) {
-        mbar_init(&bars.s_full[i][b], 1);
-        mbar_init(&bars.p_full[i][b], 4);
-      }
-    }
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&bars.kv_full[i], 1);
-      mbar_init(&bars.kv_free[i], TILES);
-    }
-    mbar_init(&bars.v_scan, TILES);
-    mbar_init(&bars.v_clean, H::kThreads / 32 - H::kScanWarp);
-    bars.bad = 0;
-    bars.stop = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
@@ -457,32 +495,12 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
   if (warp >= H::kSoftmaxWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
     if (warp == H::kCopyWarp) {
-      // ---- copies: the first K, Q, then V_j and K_j+kAhead by turns, through the ring ----
-      if (lane == 0 && n > 0) {
-        const int tile_bytes = a.tile_tokens * a.G * kD * 2, qz = a.q_batched ? w.s : 0, kz = a.k_batched ? w.s : 0;
+      // ---- copies: V_j and K_j+kAhead by turns, through the ring ----
+      if (lane == 0) {
         bool ok = true;
-        int x = 0;
-        auto load_kv = [&](const CUtensorMap* map, int j) {
-          const int st = x % kStages;
-          ok = ok && mbar_wait(bars, &bars.kv_free[st], ((x / kStages) & 1) ^ 1);
-          if (!ok) return;
-          ++x;
-          mbar_expect(&bars.kv_full[st], H::kStageBytes);
-          for (int h = 0; h < 2; ++h)
-            tma_load4(ring + st * H::kStageBytes + h * (H::kStageBytes / 2), map, &bars.kv_full[st], 64 * h, w.hkv,
-                      w.kb + (w.lo + j) * H::kKeys, kz);
-        };
-        load_kv(&kmap, 0);
-        for (int t = 0; t < (w.two ? 2 : 1); ++t) {
-          mbar_expect(&bars.q_full[t], tile_bytes);
-          for (int h = 0; h < 2; ++h)
-            tma_load4(base + t * kTileBytes + h * (kTileBytes / 2), &qmap, &bars.q_full[t], 64 * h, w.hkv * a.G,
-                      w.qb + w.tok0 + t * a.tile_tokens, qz);
-        }
-        for (int j = 1; j < H::kAhead && j < n; ++j) load_kv(&kmap, j);
         for (int j = 0; j < n && ok; ++j) {
-          load_kv(&vmap, j);
-          if (j + H::kAhead < n) load_kv(&kmap, j + H::kAhead);
+          ok = load_kv(w, &vmap, j);
+          if (ok && j + H::kAhead < n) ok = load_kv(w, &kmap, j + H::kAhead);
         }
       }
     } else if (warp >= H::kProductWarp && warp < H::kProductWarp + TILES) {
@@ -501,7 +519,12 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
       const uint64_t vd = smem_operand(base_addr + TILES * kTileBytes, H::kStageBytes / 2, 1024);
       const uint32_t sp = tm + 2 * kBlock * t, op = tm + 2 * kBlock * TILES + kD * t;
       constexpr uint32_t kStep = H::kStageBytes / 16, kNext = kBlock * 128 / 16;  // a stage, 64 of its rows
-      uint32_t scans = 0;
+      uint32_t requests = 0, clean = 0;  // scans asked for; phases of v_clean
+      const auto request = [&]() {
+        if (t == 0 && lead) mbar_arrive(&bars.v_scan[requests & 1u]);
+        ++requests;
+        __syncwarp();
+      };
       bool ok = true;
       int first = min(H::kAhead, stages);  // K stages of the first two blocks
       for (int k = 0; k < first && ok; ++k) ok = mbar_wait_warp(bars, &bars.kv_full[k], 0);
@@ -524,15 +547,17 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         }
       __syncwarp();
       int x = first;
+      if (edge <= 0 && stages > 0) request();
       for (int j = 0; j < stages && ok; ++j) {
         const int xv = x++, sv = xv % kStages;
         const bool more = j + H::kAhead < stages;
         const int xk = more ? x++ : xv, sk = xk % kStages;
         ok = mbar_wait_warp(bars, &bars.kv_full[sv], (xv / kStages) & 1);
+        // the scan of the next stage may begin: the copy before in its place has been waited for above
+        if (ok && j + 1 >= edge && j + 1 > 0 && j + 1 < stages) request();
         if (ok && j >= edge) {
-          if (lead) mbar_arrive(&bars.v_scan);
-          __syncwarp();
-          ok = mbar_wait_warp(bars, &bars.v_clean, scans++ & 1u);
+          ok = mbar_wait_warp(bars, &bars.v_clean[sv], (clean >> sv) & 1u);
+          clean ^= 1u << sv;
         }
         if (ok && more) ok = mbar_wait_warp(bars, &bars.kv_full[sk], (xk / kStages) & 1);
         if (!here) {
@@ -564,13 +589,13 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         __syncwarp();
       }
     } else if (warp >= H::kScanWarp) {
-      // ---- values in masked places: stage by stage as the product warps ask (a wait on the stage alone could take an
-      // earlier phase of its barrier for the awaited one) ----
+      // ---- values in masked places: stage by stage as the first product warp asks, one ahead of its own (a wait
+      // on the stage alone could take an earlier phase of its barrier for the awaited one) ----
       uint32_t scans = 0;
       const int first = min(H::kAhead, n);
-      for (int j = max(w.edge - w.lo, 0); j < n; ++j) {
+      for (int j = max(w.edge - w.lo, 0); j < n; ++j, ++scans) {
         const int xv = first + j + min(j, n - first), sv = xv % kStages;
-        if (!mbar_wait_warp(bars, &bars.v_scan, scans++ & 1u)) break;
+        if (!mbar_wait_warp(bars, &bars.v_scan[scans & 1u], (scans >> 1) & 1u)) break;
         if (!mbar_wait_warp(bars, &bars.kv_full[sv], (xv / kStages) & 1)) break;
         uint4* tile = reinterpret_cast<uint4*>(ring + sv * H::kStageBytes);
         bool touched = false;
@@ -588,7 +613,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         if (touched) bars.bad = 1u;
         asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.v_clean);
+        if (lane == 0) mbar_arrive(&bars.v_clean[sv]);
       }
     }
   } else {
@@ -670,7 +695,26 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
           const bool any = seen > from;
           const float inv = a.splits > 1 ? 1.f : (any ? 1.f / l : 0.f);
           const int64_t part = part_place(a, w.split, w.s, tok, head);
-  #pragma unroll
+          // Through shared memory (the tile's Q has been used up), 256 bytes of every row at a time, so that a warp
+          // stores whole rows: chunk c of row i of the warp lies at chunk c ^ (i % 8).
+          uint4* stage = reinterpret_cast<uint4*>(base + t * kTileBytes) + (warp & 3) * 512;
+          uint4* mine = stage + lane * 16;
+          uint64_t out = 0;  // where the row goes
+          if (row)
+            out = a.splits > 1 ? (uint64_t)(a.part_o + part * kD)
+                               : (uint64_t)(a.o + w.s * a.o_b + (int64_t)(w.qb + tok) * a.o_t + head * a.o_h);
+          const auto store_rows = [&](int offset) {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {  // two rows at a time
+              const int rr = 2 * i + (lane >> 4), cc = lane & 15;
+              const uint64_t to = __shfl_sync(0xFFFFFFFFu, out, rr);
+              const uint4 v = stage[rr * 16 + (cc ^ (rr & 7))];
+              if (to != 0) reinterpret_cast<uint4*>(to + offset)[cc] = v;
+            }
+            __syncwarp();
+          };
+#pragma unroll
           for (int q = 0; q < 4; ++q) {
             float y[32];
             if (blocks > 0) {
@@ -678,33 +722,34 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
               tmem_wait_ld(y);
             }
             if (!any) {
-  #pragma unroll
+#pragma unroll
               for (int i = 0; i < 32; ++i) y[i] = 0.f;
             }
             if (bad && row) {
               const uint16_t* vr = a.v + w.s * a.v_b + (int64_t)(w.kb + first) * a.v_t + w.hkv * a.v_h + 32 * q;
               for (int key = first; key < end; ++key, vr += a.v_t) {
-  #pragma unroll
+#pragma unroll
                 for (int i = 0; i < 32; ++i) {
                   const uint32_t e = vr[i];
                   if ((e & 0x7F80u) == 0x7F80u) y[i] += bf16_to_f32(e);
                 }
               }
             }
-            if (!row) continue;
             if (a.splits > 1) {
-              float4* po = reinterpret_cast<float4*>(a.part_o + part * kD + 32 * q);
-  #pragma unroll
-              for (int i = 0; i < 8; ++i) po[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                mine[(8 * (q & 1) + i) ^ (lane & 7)] =
+                    make_uint4(__float_as_uint(y[4 * i]), __float_as_uint(y[4 * i + 1]), __float_as_uint(y[4 * i + 2]),
+                               __float_as_uint(y[4 * i + 3]));
+              if (q & 1) store_rows(256 * (q >> 1));
             } else {
-              uint4* po =
-                  reinterpret_cast<uint4*>(a.o + w.s * a.o_b + (int64_t)(w.qb + tok) * a.o_t + head * a.o_h + 32 * q);
-  #pragma unroll
+#pragma unroll
               for (int i = 0; i < 4; ++i)
-                po[i] = make_uint4(pack_bf16x2(y[8 * i] * inv, y[8 * i + 1] * inv),
-                                   pack_bf16x2(y[8 * i + 2] * inv, y[8 * i + 3] * inv),
-                                   pack_bf16x2(y[8 * i + 4] * inv, y[8 * i + 5] * inv),
-                                   pack_bf16x2(y[8 * i + 6] * inv, y[8 * i + 7] * inv));
+                mine[(4 * q + i) ^ (lane & 7)] = make_uint4(pack_bf16x2(y[8 * i] * inv, y[8 * i + 1] * inv),
+                                                            pack_bf16x2(y[8 * i + 2] * inv, y[8 * i + 3] * inv),
+                                                            pack_bf16x2(y[8 * i + 4] * inv, y[8 * i + 5] * inv),
+                                                            pack_bf16x2(y[8 * i + 6] * inv, y[8 * i + 7] * inv));
+              if (q == 3) store_rows(0);
             }
           }
           if (row) {
