@@ -434,12 +434,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
                 w.kb + (w.lo + j) * H::kKeys, a.k_batched ? w.s : 0);
     return true;
   };
-  if (warp == H::kCopyWarp) {
-    // sets up the barriers, looks the item up and starts the first copies before the others are ready
+  if (warp == H::kScanWarp) {
     if (lane == 0) {
-      prefetch_map(&kmap);
-      prefetch_map(&qmap);
-      prefetch_map(&vmap);
       for (int i = 0; i < TILES; ++i) {
         mbar_init(&bars.q_full[i], 1);
         for (int b = 0; b < 2; ++b) {
@@ -459,11 +455,21 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
     }
     __syncwarp();
+    asm volatile("bar.sync 1, 64;\n" ::: "memory");
+  } else if (warp == H::kCopyWarp) {
+    // looks the item up while the barriers are set up, and starts the first copies before all others are ready
+    if (lane == 0) {
+      prefetch_map(&kmap);
+      prefetch_map(&qmap);
+      prefetch_map(&vmap);
+    }
+    __syncwarp();
     PromptItem w;
     if (!prompt_item<TILES>(a, blockIdx.x, w)) {
       w.s = -1;
       w.lo = w.hi = 0;
     }
+    asm volatile("bar.sync 1, 64;\n" ::: "memory");
     if (lane == 0) {
       bars.item = w;
       if (w.hi > w.lo) {
@@ -703,18 +709,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
           if (row)
             out = a.splits > 1 ? (uint64_t)(a.part_o + part * kD)
                                : (uint64_t)(a.o + w.s * a.o_b + (int64_t)(w.qb + tok) * a.o_t + head * a.o_h);
-          const auto store_rows = [&](int offset) {
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {  // two rows at a time
-              const int rr = 2 * i + (lane >> 4), cc = lane & 15;
-              const uint64_t to = __shfl_sync(0xFFFFFFFFu, out, rr);
-              const uint4 v = stage[rr * 16 + (cc ^ (rr & 7))];
-              if (to != 0) reinterpret_cast<uint4*>(to + offset)[cc] = v;
-            }
-            __syncwarp();
-          };
-#pragma unroll
+          // Rolled loops: this runs once per item, and unrolled it is bound by fetching its instructions.
+#pragma unroll 1
           for (int q = 0; q < 4; ++q) {
             float y[32];
             if (blocks > 0) {
@@ -735,13 +731,14 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
                 }
               }
             }
+            bool full;  // 256 bytes of every row are staged
             if (a.splits > 1) {
 #pragma unroll
               for (int i = 0; i < 8; ++i)
                 mine[(8 * (q & 1) + i) ^ (lane & 7)] =
                     make_uint4(__float_as_uint(y[4 * i]), __float_as_uint(y[4 * i + 1]), __float_as_uint(y[4 * i + 2]),
                                __float_as_uint(y[4 * i + 3]));
-              if (q & 1) store_rows(256 * (q >> 1));
+              full = q & 1;
             } else {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
@@ -749,8 +746,18 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
                                                             pack_bf16x2(y[8 * i + 2] * inv, y[8 * i + 3] * inv),
                                                             pack_bf16x2(y[8 * i + 4] * inv, y[8 * i + 5] * inv),
                                                             pack_bf16x2(y[8 * i + 6] * inv, y[8 * i + 7] * inv));
-              if (q == 3) store_rows(0);
+              full = q == 3;
             }
+            if (!full) continue;
+            __syncwarp();
+#pragma unroll 4
+            for (int i = 0; i < 16; ++i) {  // two rows at a time
+              const int rr = 2 * i + (lane >> 4), cc = lane & 15;
+              const uint64_t to = __shfl_sync(0xFFFFFFFFu, out, rr);
+              const uint4 v = stage[rr * 16 + (cc ^ (rr & 7))];
+              if (to != 0) reinterpret_cast<uint4*>(to)[(a.splits > 1 ? 16 * (q >> 1) : 0) + cc] = v;
+            }
+            __syncwarp();
           }
           if (row) {
             if (a.splits > 1)
@@ -799,13 +806,21 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant_
 #pragma unroll
   for (int u = 0; u < 2; ++u) f[u] = ml[u].y == 0.f ? 0.f : exp2f(ml[u].x - m);  // a sum of 0: nothing visible there
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int z = 0; z < a.splits; ++z) {
-    const float g = __shfl_sync(0xFFFFFFFFu, z < 32 ? f[0] : f[1], z & 31);
-    const float sum = __shfl_sync(0xFFFFFFFFu, z < 32 ? ml[0].y : ml[1].y, z & 31);
-    if (sum == 0.f) continue;
-    const float4 x = reinterpret_cast<const float4*>(a.part_o + part_place(a, z, s, tok, head) * kD)[lane];
-    l += g * sum;
-    o = make_float4(o.x + g * x.x, o.y + g * x.y, o.z + g * x.z, o.w + g * x.w);
+  for (int z0 = 0; z0 < a.splits; z0 += 8) {  // eight splits' loads in flight
+    float4 x[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (z0 + u < a.splits)
+        x[u] = reinterpret_cast<const float4*>(a.part_o + part_place(a, z0 + u, s, tok, head) * kD)[lane];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int z = z0 + u;
+      const float g = __shfl_sync(0xFFFFFFFFu, z < 32 ? f[0] : f[1], z & 31);
+      const float sum = __shfl_sync(0xFFFFFFFFu, z < 32 ? ml[0].y : ml[1].y, z & 31);
+      if (z >= a.splits || sum == 0.f) continue;
+      l += g * sum;
+      o = make_float4(o.x + g * x[u].x, o.y + g * x[u].y, o.z + g * x[u].z, o.w + g * x[u].w);
+    }
   }
   const float inv = any ? 1.f / l : 0.f;
   uint2* po = reinterpret_cast<uint2*>(a.o + s * a.o_b + (int64_t)(qb + tok) * a.o_t + head * a.o_h) + lane;
