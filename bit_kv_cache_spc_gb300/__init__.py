@@ -467,8 +467,8 @@ def spc_prompt_attn(q, k, v, o, lse=None, q_begin=None, q_len=None, k_begin=None
     [T][Hkv][D] or [S][T][Hkv][D].  q_begin, q_len, k_begin, k_len: int32 [S]
     on the device, or None.  q_max, k_max bound the lengths (default: the
     token axis).  lse: fp32 of o's shape without D, contiguous.  Without ws a
-    workspace is taken from torch's allocator for the call, which needs the
-    call to be on the current stream."""
+    workspace, where one is needed, is taken from torch's allocator for the
+    call, which needs the call to be on the current stream."""
     fn = "spc_prompt_attn"
     dev = _device(fn, q)
     S = _sequences(q, k, q_len, k_len, q_begin, k_begin)
@@ -481,9 +481,12 @@ def spc_prompt_attn(q, k, v, o, lse=None, q_begin=None, q_len=None, k_begin=None
     if ws is None:
         if stream is not None and s != _raw_stream(None, dev):
             raise ValueError(f"{fn}: a call on another stream than the current one needs ws")
-        ws_bytes = max(_lib.spc_prompt_attn_workspace_bytes(d), 16)
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-        w = ws.data_ptr()
+        w, ws_bytes = None, _lib.spc_prompt_attn_workspace_bytes(d)
+        if ws_bytes > 256:  # the keys are split; else the call needs none
+            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+            w = ws.data_ptr()
+        else:
+            ws_bytes = 0
     else:
         if not isinstance(ws, int) and ws.get_device() != dev:
             raise ValueError(f"{fn}: ws must be on the current CUDA device")

@@ -972,8 +972,10 @@ spc_status launch_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const
   a.splits = g.splits;
   a.fault = static_cast<uint32_t*>(ws);
   a.part_rows = (int64_t)d->S * d->q_max * d->Hq;
-  a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kPromptHead);
-  a.part_ml = reinterpret_cast<float2*>(a.part_o + a.part_rows * a.splits * kD);
+  if (a.splits > 1) {
+    a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kPromptHead);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + a.part_rows * a.splits * kD);
+  }
   CUtensorMap qm, km, vm;
   const int64_t kt = std::max(d->k_tokens, 1);  // no keys at all: the maps are never read through
   const uint32_t keys = g.tiles == 2 ? Shape<2>::kKeys : Shape<1>::kKeys;

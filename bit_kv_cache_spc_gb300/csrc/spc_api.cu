@@ -682,8 +682,9 @@ spc_status spc_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const ui
   if (d->q_max == 0) return SPC_OK;
   if (q == nullptr || o == nullptr || (d->k_max > 0 && (k == nullptr || v == nullptr))) return SPC_ERR_INVALID;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return SPC_ERR_INVALID;
-  if (ws == nullptr || !aligned16(ws)) return SPC_ERR_INVALID;
-  if (ws_bytes < spc::prompt_workspace_bytes(d)) return SPC_ERR_WORKSPACE;
+  const size_t need = spc::prompt_workspace_bytes(d);
+  if ((ws == nullptr && (need > 256 || ws_bytes != 0)) || !aligned16(ws)) return SPC_ERR_INVALID;
+  if (ws != nullptr && ws_bytes < need) return SPC_ERR_WORKSPACE;
   return spc::launch_prompt_attn(d, q, k, v, q_begin, q_len, k_begin, k_len, o, lse, ws,
                                  reinterpret_cast<cudaStream_t>(stream));
 }

@@ -456,8 +456,9 @@ typedef struct spc_prompt_dims {
 
 /* Bytes of device workspace of spc_prompt_attn on the current device: a status
  * word (256 bytes; zero-filled once by the caller for
- * spc_prompt_attn_status, never needed otherwise) and, where few queries leave
- * SMs idle and the keys are split, the splits' partial results.  Calls that
+ * spc_prompt_attn_status) and, where few queries leave SMs idle and the keys
+ * are split, the splits' partial results.  256 says that there is no split:
+ * the call then also takes ws = NULL (and reports no status).  Calls that
  * share a workspace must not overlap on the GPU.  0 for an invalid shape. */
 size_t spc_prompt_attn_workspace_bytes(const spc_prompt_dims* d);
 
@@ -470,7 +471,8 @@ size_t spc_prompt_attn_workspace_bytes(const spc_prompt_dims* d);
  *   o       : bf16, rows of no sequence are left as they were; sequences'
  *            rows must not overlap, nor share bytes with an input.
  *   lse     : fp32 [q_tokens][Hq] (packed) or [S][q_tokens][Hq], or NULL.
- *   ws      : at least spc_prompt_attn_workspace_bytes(d) bytes.
+ *   ws      : at least spc_prompt_attn_workspace_bytes(d) bytes, or NULL with
+ *            ws_bytes 0 where that is 256.
  * One launch, and a second, small one where the keys are split.
  */
 spc_status spc_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const uint16_t* k, const uint16_t* v,

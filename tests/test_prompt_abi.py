@@ -136,6 +136,14 @@ def test_prompt_attn_of_no_queries_is_nothing():
     assert prompt_call(prompt_dims(q_max=0)) == 0
 
 
+def test_prompt_attn_without_a_workspace():
+    """NULL is for calls that need none, and then with no bytes."""
+    kl = lay(8192 * 256, 256, 128)
+    split = prompt_dims(q_max=1, k_tokens=8192, k_max=8192, k=kl, v=kl)
+    assert prompt_call(split, ws=None, ws_bytes=0) == INVALID
+    assert prompt_call(prompt_dims(), ws=None, ws_bytes=256) == INVALID
+
+
 def test_prompt_attn_workspace_grows_where_the_keys_are_split():
     d = prompt_dims()
     assert _lib.spc_prompt_attn_workspace_bytes(C.byref(d)) == 256  # no key tiles to share out
