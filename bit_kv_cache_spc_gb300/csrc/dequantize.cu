@@ -2,19 +2,22 @@
 // the attention of a follow-up prompt over its history.
 //
 // A CTA takes 32 tokens of one (b, hkv), half a g = 64 record, a g = 32 record
-// or 32 rows of the residual window: 128 threads the keys, 128 the values.  An element of
-// the record stands for one of 2 or 4 levels of its group, fl(z + fl(s code)),
-// so the levels are formed and rounded once per group and lane, and an
-// element costs a bit mask and a select of packed pairs:
+// or 32 rows of the residual window: 128 threads the keys, 128 the values.  An
+// element of the record stands for one of 2 or 4 levels of its group,
+// fl(z + fl(s code)), so the levels are formed and rounded once per group (in
+// shared memory), and an element costs a bit mask and a select of packed
+// pairs:
 //   - keys: lane (token row, 8 channels) finds its channels' pairs (2t, 2t+1)
 //     in four words, the pair's two bits 16 apart (spc.h: rotated left by 4i,
 //     bits 11 + n and 27 + n);
 //   - values: a word holds two tokens' bits of one channel (mod 8) 16 apart,
 //     so a lane takes a token pair and eight channels from eight words.
 // Bound by HBM: 512 bytes written per token and KV head against 48 to 96 read.
-// A CTA per tile: CTAs that walk over tiles, 16 per SM, wait for each tile's
-// words with nothing else to do (219 us against 179 for eight 32768-token
-// caches of 8 KV heads at 1 bit, 1.21 GB; 179 us are the measured copy rate).
+// Eight 32768-token caches of 8 KV heads at 1 bit (1.21 GB) take 181 us, the
+// measured copy rate; at 2 bits (1.28 GB) 240, bound by the selects' issue
+// (levels per thread instead of per group: 24 us against 18 for two 2-bit
+// caches of 32 heads and 2003 tokens).  CTAs that walk over tiles, 16 per SM,
+// wait for each tile's words with nothing else to do (219 us).
 #include "common.cuh"
 
 namespace spc {
@@ -50,122 +53,154 @@ __device__ __forceinline__ uint32_t read_pack(float lo, float hi) {
   return r;
 }
 
+// 0xFFFF in a half for each of two picked bytes whose top bit is set: selector
+// nibbles 8 + byte of (a, b).
+template <uint32_t SEL>
+__device__ __forceinline__ uint32_t top_bits(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;\n" : "=r"(r) : "r"(a), "r"(b), "n"(SEL));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t pick(uint32_t mask, uint32_t yes, uint32_t no) { return (yes & mask) | (no & ~mask); }
 
 template <int BITS, int GROUP>
-__global__ void __launch_bounds__(256) dequantize_kernel(const __grid_constant__ ReadArgs a) {
+__global__ void __launch_bounds__(256, BITS == 1 ? 6 : 5) dequantize_kernel(const __grid_constant__ ReadArgs a) {
   constexpr int kWords = GROUP == 32 ? 256 * (BITS + 1) : 512 * BITS + 256;  // of a record
   constexpr int kCodes = 128 * BITS;                                        // words of 32 tokens' codes
   constexpr int L = 1 << BITS;
-  const int tid = threadIdx.x & 127;
   const bool keys = threadIdx.x < 128;
-  const int64_t bh = blockIdx.x / a.tiles_per;
-  const int tile = a.tile0 + (int)(blockIdx.x % a.tiles_per);
-  const int64_t b = bh / a.Hkv, h = bh % a.Hkv;
-  uint16_t* kd = a.k + b * a.lk.b + h * a.lk.h;
-  uint16_t* vd = a.v + b * a.lv.b + h * a.lv.h;
-  const int chunk = tid & 15, e = 8 * chunk;  // this lane's channels e .. e+7
-  if (tile >= a.low_tiles) {                  // the residual window
-    const int t0 = a.nq + 32 * (tile - a.low_tiles);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int t = t0 + 8 * r + (tid >> 4);
-      if (t < a.first || t >= a.end) continue;
-      const uint16_t* row = a.resid + (bh * a.resid_cap + (t - a.nq)) * 2 * kD + (keys ? 0 : kD);
-      uint16_t* to = keys ? kd + (int64_t)(t - a.first) * a.lk.t : vd + (int64_t)(t - a.first) * a.lv.t;
-      *reinterpret_cast<uint4*>(to + e) = *reinterpret_cast<const uint4*>(row + e);
-    }
+  const int tid = threadIdx.x & 127, row = tid >> 4, chunk = tid & 15, e = 8 * chunk;  // channels e .. e+7
+  const uint32_t bh = blockIdx.x / (uint32_t)a.tiles_per, tile = a.tile0 + blockIdx.x % (uint32_t)a.tiles_per;
+  const uint32_t b = bh / (uint32_t)a.Hkv, h = bh - b * a.Hkv;
+  const bool low = tile < (uint32_t)a.low_tiles;
+  const int t0 = low ? 32 * (int)tile : a.nq + 32 * (int)(tile - a.low_tiles);  // the tile's first token
+  // where the tile's first token would go, and the stride of tokens
+  const int64_t step = keys ? a.lk.t : a.lv.t;
+  uint16_t* to = (keys ? a.k + b * a.lk.b + h * a.lk.h : a.v + b * a.lv.b + h * a.lv.h) + (t0 - a.first) * step + e;
+  const int skip = a.first - t0, count = a.end - a.first;  // token i of the tile is wanted: 0 <= i - skip < count
+  const auto store = [&](int i, uint16_t* at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    if ((uint32_t)(i - skip) < (uint32_t)count) *reinterpret_cast<uint4*>(at) = make_uint4(x, y, z, w);
+  };
+  if (!low) {  // the residual window
+    const uint16_t* from = a.resid + (bh * (int64_t)a.resid_cap + (t0 - a.nq)) * 2 * kD + (keys ? 0 : kD) + e;
+    for (int i = row; i < 32; i += 8)
+      if ((uint32_t)(i - skip) < (uint32_t)count)
+        *reinterpret_cast<uint4*>(to + i * step) = *reinterpret_cast<const uint4*>(from + i * 2 * kD);
     return;
   }
-  const int unit = GROUP == 32 ? tile : tile >> 1, half = GROUP == 32 ? 0 : tile & 1;
-  const uint32_t* rec = reinterpret_cast<const uint32_t*>(a.records) + (bh * a.units_cap + unit) * kWords;
-  const uint32_t* kc = rec + half * kCodes;
-  const uint32_t* km = rec + (GROUP / 32) * kCodes;
-  const uint32_t* vc = km + 128 + half * kCodes;
-  const uint32_t* vm = km + 128 + (GROUP / 32) * kCodes + 64 * half;  // g = 32: half = 0
-  const int t0 = 32 * tile;
+  const uint32_t unit = GROUP == 32 ? tile : tile >> 1, half = GROUP == 32 ? 0 : tile & 1;
+  const uint32_t* rec = reinterpret_cast<const uint32_t*>(a.records) + (bh * (int64_t)a.units_cap + unit) * kWords;
+  constexpr int kKeyMeta = GROUP / 32 * kCodes, kValueCodes = kKeyMeta + 128, kValueMeta = kValueCodes + kKeyMeta;
 
+  // ---- the levels, a group per thread, into shared memory; the code words are on their way meanwhile ----
+  __shared__ __align__(16) uint16_t klev[L][kD];  // of a channel
+  __shared__ uint32_t vlev[L][128];               // of a token's group, twice in a word
+  constexpr int kVGroups = kD / GROUP;            // groups of a token
+  uint32_t w[BITS][16];  // keys: words 4t + j of row a; values: eight words of each of two token pairs
   if (keys) {
-    // ---- keys: rows a, a + 8, a + 16, a + 24 of lane a = tid >> 4 ----
-    const int row = tid >> 4, j = chunk >> 2, rot = 4 * (chunk & 3);
-    uint32_t lev[4][L];  // of channel pairs e + 2t, e + 2t + 1
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      // channel 16 k + 8 h + 2t + x stands at minmax word 32 t + 4 k + 2 h + x
-      const uint2 mm = *reinterpret_cast<const uint2*>(km + 32 * t + 2 * chunk);
-      float p[L], q[L];
-      levels<BITS>(mm.x, p);
-      levels<BITS>(mm.y, q);
-#pragma unroll
-      for (int c = 0; c < L; ++c) lev[t][c] = read_pack(p[c], q[c]);
-    }
-    uint32_t w[BITS][4];
+    const uint32_t* kc = rec + half * kCodes + 16 * row + (chunk >> 2);
 #pragma unroll
     for (int p = 0; p < BITS; ++p)
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const uint32_t x = kc[128 * p + 16 * row + 4 * t + j];
-        w[p][t] = __funnelshift_l(x, x, rot + 21);  // row 8n + a's two bits at n and 16 + n
+      for (int t = 0; t < 4; ++t) w[p][t] = kc[128 * p + 4 * t];
+    const int t = tid >> 5, m = tid & 31;  // word 32 t + m
+    float lv[L];
+    levels<BITS>(rec[kKeyMeta + tid], lv);
+#pragma unroll
+    for (int c = 0; c < L; ++c)
+      klev[c][16 * (m >> 2) + 2 * t + 8 * ((m >> 1) & 1) + (m & 1)] = (uint16_t)read_pack(lv[c], lv[c]);
+  } else {
+    // pair 8 r + row, tokens 8 j + 2 t + {0, 1} with t = row % 4, j = 2 r + row / 4
+    const uint32_t* vc = rec + kValueCodes + half * kCodes + 4 * (row & 3) + (row >> 2);
+#pragma unroll
+    for (int p = 0; p < BITS; ++p)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int u = 0; u < 8; ++u) w[p][8 * r + u] = vc[128 * p + 16 * u + 2 * r];
+    if (tid < 32 * kVGroups) {
+      int token, group;
+      if (GROUP == 32) {
+        const int t = tid >> 5, m = tid & 31;
+        token = 16 * (m >> 4) + 8 * ((m >> 3) & 1) + 2 * t + ((m >> 2) & 1);
+        group = m & 3;
+      } else {
+        const int m = tid >> 1;
+        token = 16 * ((m >> 2) & 1) + 8 * ((m >> 1) & 1) + 2 * (m >> 3) + (m & 1);
+        group = tid & 1;
       }
+      float lv[L];
+      levels<BITS>(rec[kValueMeta + 64 * half + tid], lv);
+#pragma unroll
+      for (int c = 0; c < L; ++c) vlev[c][kVGroups * token + group] = read_pack(lv[c], lv[c]);
+    }
+  }
+  __syncthreads();
+
+  if (keys) {
+    // ---- rows a, a + 8, a + 16, a + 24 of lane a = tid >> 4: channel pairs e + 2t, e + 2t + 1 ----
+    uint32_t lev[L][4];
+#pragma unroll
+    for (int c = 0; c < L; ++c) {
+      const uint4 x = *reinterpret_cast<const uint4*>(&klev[c][e]);
+      lev[c][0] = x.x;
+      lev[c][1] = x.y;
+      lev[c][2] = x.z;
+      lev[c][3] = x.w;
+    }
+#pragma unroll
+    for (int p = 0; p < BITS; ++p)
+#pragma unroll
+      for (int t = 0; t < 4; ++t)  // row 8n + a's two bits to n and 16 + n
+        w[p][t] = __funnelshift_l(w[p][t], w[p][t], 4 * (chunk & 3) + 21);
+    to += row * step;
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
-      const int t = t0 + 8 * n + row;
       uint32_t out[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const uint32_t m0 = ((w[0][u] >> n) & 0x00010001u) * 0xFFFFu;
+        const uint32_t m0 = top_bits<0xBB99>(w[0][u] << (15 - n), 0u);  // bits 16 + n and n
         if (BITS == 1) {
-          out[u] = pick(m0, lev[u][1], lev[u][0]);
+          out[u] = pick(m0, lev[1][u], lev[0][u]);
         } else {
-          const uint32_t m1 = ((w[BITS - 1][u] >> n) & 0x00010001u) * 0xFFFFu;
-          out[u] = pick(m1, pick(m0, lev[u][L - 1], lev[u][L - 2]), pick(m0, lev[u][1], lev[u][0]));
+          const uint32_t m1 = top_bits<0xBB99>(w[BITS - 1][u] << (15 - n), 0u);
+          out[u] = pick(m1, pick(m0, lev[L - 1][u], lev[L - 2][u]), pick(m0, lev[1][u], lev[0][u]));
         }
       }
-      if (t >= a.first && t < a.end)
-        *reinterpret_cast<uint4*>(kd + (int64_t)(t - a.first) * a.lk.t + e) = make_uint4(out[0], out[1], out[2], out[3]);
+      store(8 * n + row, to, out[0], out[1], out[2], out[3]);
+      to += 8 * step;
     }
-    return;
-  }
-  // ---- values: token pairs 2p, 2p + 1 for p = tid >> 4 and 8 + (tid >> 4) ----
+  } else {
+    // ---- token pairs ----
+    to += 2 * row * step;
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int p = 8 * r + (tid >> 4), j = p >> 2, t = p & 3;  // tokens 8 j + 2 t + {0, 1}
-    uint32_t lev[2][L];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      uint32_t mm;
-      if (GROUP == 32)
-        mm = vm[32 * t + 16 * (j >> 1) + 8 * (j & 1) + 4 * x + (chunk >> 2)];
-      else
-        mm = vm[2 * (8 * t + 4 * (j >> 1) + 2 * (j & 1) + x) + (chunk >> 3)];
-      float lv[L];
-      levels<BITS>(mm, lv);
-#pragma unroll
-      for (int c = 0; c < L; ++c) lev[x][c] = read_pack(lv[c], lv[c]);
-    }
-    uint32_t out[2][4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {  // channels e + 2u, e + 2u + 1
-      uint32_t m[2][BITS];
-#pragma unroll
-      for (int q = 0; q < BITS; ++q) {
-        const uint32_t x = (vc[128 * q + 16 * (2 * u) + 4 * t + j] >> chunk) & 0x00010001u;
-        const uint32_t y = (vc[128 * q + 16 * (2 * u + 1) + 4 * t + j] >> chunk) & 0x00010001u;
-        m[0][q] = __byte_perm(x, y, 0x5410) * 0xFFFFu;
-        m[1][q] = __byte_perm(x, y, 0x7632) * 0xFFFFu;
-      }
+    for (int r = 0; r < 2; ++r) {
+      const int first = 2 * (8 * r + row);  // the pair's first token
+      uint32_t lev[2][L];
 #pragma unroll
       for (int x = 0; x < 2; ++x)
-        out[x][u] = BITS == 1 ? pick(m[x][0], lev[x][1], lev[x][0])
-                              : pick(m[x][BITS - 1], pick(m[x][0], lev[x][L - 1], lev[x][L - 2]),
-                                     pick(m[x][0], lev[x][1], lev[x][0]));
-    }
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int tok = t0 + 2 * p + x;
-      if (tok >= a.first && tok < a.end)
-        *reinterpret_cast<uint4*>(vd + (int64_t)(tok - a.first) * a.lv.t + e) =
-            make_uint4(out[x][0], out[x][1], out[x][2], out[x][3]);
+        for (int c = 0; c < L; ++c) lev[x][c] = vlev[c][kVGroups * (first + x) + e / GROUP];
+      uint32_t out[2][4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {  // channels e + 2u, e + 2u + 1
+        uint32_t m[2][BITS];
+#pragma unroll
+        for (int q = 0; q < BITS; ++q) {
+          const uint32_t x = w[q][8 * r + 2 * u] << (15 - chunk), y = w[q][8 * r + 2 * u + 1] << (15 - chunk);
+          m[0][q] = top_bits<0xDD99>(x, y);  // the first token: bits chunk
+          m[1][q] = top_bits<0xFFBB>(x, y);  // the second: bits 16 + chunk
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          out[x][u] = BITS == 1 ? pick(m[x][0], lev[x][1], lev[x][0])
+                                : pick(m[x][BITS - 1], pick(m[x][0], lev[x][L - 1], lev[x][L - 2]),
+                                       pick(m[x][0], lev[x][1], lev[x][0]));
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) store(first + x, to + x * step, out[x][0], out[x][1], out[x][2], out[x][3]);
+      to += 16 * step;
     }
   }
 }
