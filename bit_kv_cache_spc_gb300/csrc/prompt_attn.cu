@@ -112,7 +112,7 @@ struct PromptItem {
   int lq, lk, qb, kb;       // lengths and first tokens of the sequence
   int tok0;                 // first query token
   int lo, hi;               // stages of keys [lo, hi)
-  int blocks;               // 64-key blocks of them that some row sees
+  int blocks[2];            // 64-key blocks of them that some row of each tile sees
   int edge;                 // first stage that some row does not see in full
   int two;                  // the second query tile has rows
 };
@@ -378,7 +378,12 @@ __device__ __forceinline__ bool prompt_item(const PromptArgs& a, uint32_t i, Pro
   const int per = (n + a.splits - 1) / a.splits;
   w.lo = min(w.split * per, n);
   w.hi = min(w.lo + per, n);
-  w.blocks = max(0, min(Shape<TILES>::kPerStage * (w.hi - w.lo), (most - w.lo * kKeys + kBlock - 1) / kBlock));
+  const int last0 = min(w.tok0 + a.tile_tokens, w.lq) - 1, most0 = min(most, clampi(last0 + w.lk - w.lq + 1, 0, w.lk));
+  const auto blocks = [&](int keys) {
+    return max(0, min(Shape<TILES>::kPerStage * (w.hi - w.lo), (keys - w.lo * kKeys + kBlock - 1) / kBlock));
+  };
+  w.blocks[0] = blocks(most0);
+  w.blocks[1] = blocks(most);
   w.edge = least / kKeys;
   return true;
 }
@@ -515,7 +520,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
       const bool lead = elect_lane();
       const int t = __shfl_sync(0xFFFFFFFFu, warp - H::kProductWarp, 0);
       const int stages = __shfl_sync(0xFFFFFFFFu, n, 0);
-      const int blocks = stages > 0 ? __shfl_sync(0xFFFFFFFFu, w.blocks, 0) : 0;
+      const int blocks = stages > 0 ? __shfl_sync(0xFFFFFFFFu, w.blocks[t], 0) : 0;
       const int edge = __shfl_sync(0xFFFFFFFFu, w.edge - w.lo, 0);  // the first stage to be scanned
       const bool here = __shfl_sync(0xFFFFFFFFu, t == 0 || w.two, 0);
       const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
@@ -534,7 +539,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
       bool ok = true;
       int first = min(H::kAhead, stages);  // K stages of the first two blocks
       for (int k = 0; k < first && ok; ++k) ok = mbar_wait_warp(bars, &bars.kv_full[k], 0);
-      if (here && blocks > 0) {
+      if (here && blocks > 0) {  // a tile may see less than the other, or nothing
         ok = ok && mbar_wait_warp(bars, &bars.q_full[t], 0);
         if (ok && lead) {
           product_s(sp, qd, kd, H::kStageBytes / 2);
@@ -633,7 +638,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
       const int head = w.hkv * a.G + r % a.G;
       const bool row = r < a.tile_tokens * a.G && tok < w.lq;
       const int seen = row ? clampi(tok + w.lk - w.lq + 1, 0, w.lk) : w.lk;  // keys of this row
-      const int from = w.lo * H::kKeys, blocks = w.blocks;
+      const int from = w.lo * H::kKeys, blocks = w.blocks[t];
       const int masked = H::kPerStage * (w.edge - w.lo);  // the first block that some row does not see in full
       const float c = a.scale * kLog2e;
       float m = -INFINITY, l = 0.f;
@@ -693,6 +698,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         }
         // ---- output ----
         if (blocks > 0 && ok) ok = mbar_wait_warp(bars, &bars.s_full[t][(blocks + 1) & 1], ((blocks + 1) >> 1) & 1);
+        if (blocks == 0 && n > 0) ok = mbar_wait_warp(bars, &bars.q_full[t], 0);  // Q's place is used below
         if (ok) {
           tc_fence_after();
           const bool bad = *(volatile uint32_t*)&bars.bad != 0u;

@@ -53,9 +53,11 @@ def test_one_sequence(lq, lk, Hq, Hkv):
     check(o, lse, q, k, v)
 
 
-@pytest.mark.parametrize("lq,lk", [(1, 0), (7, 0), (9, 4), (300, 130), (140, 1), (1300, 1100)])
-def test_rows_that_see_nothing(lq, lk):
-    q, k, v, o, lse = run_one(lq, lk, 4, 2)
+@pytest.mark.parametrize("lq,lk,G", [(1, 0, 2), (7, 0, 2), (9, 4, 2), (300, 130, 2), (140, 1, 2), (1300, 1100, 2),
+                                     (256, 100, 1), (256, 128, 1), (300, 290, 1), (600, 345, 1), (200, 72, 1)])
+def test_rows_that_see_nothing(lq, lk, G):
+    """Also whole tiles of such rows beside one that sees something."""
+    q, k, v, o, lse = run_one(lq, lk, 2 * G, 2)
     check(o, lse, q, k, v)
     empty = lq - lk
     assert bool((o[:empty] == 0).all()) and bool((lse[:empty] == -math.inf).all())
