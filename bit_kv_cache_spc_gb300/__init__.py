@@ -61,12 +61,13 @@ def Dims(B, Hq, Hkv, N, R, bits, q_groups_cap=None, resid_cap=None, scale=None, 
     residual rows that spc_num_quantized reports for the shape."""
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    probe = spc_dims(B, Hq, Hkv, D, bits, group, N, R, max(N, 0) // 32 + 1, max(N, 0), scale)
-    nq = max(int(_lib.spc_num_quantized(C.byref(probe))), 0)  # -1: an invalid shape, which every call refuses
-    if q_groups_cap is None:
-        q_groups_cap = nq // 32
-    if resid_cap is None:
-        resid_cap = N - nq
+    if q_groups_cap is None or resid_cap is None:
+        probe = spc_dims(B, Hq, Hkv, D, bits, group, N, R, max(N, 0) // 32 + 1, max(N, 0), scale)
+        nq = max(int(_lib.spc_num_quantized(C.byref(probe))), 0)  # -1: an invalid shape, which every call refuses
+        if q_groups_cap is None:
+            q_groups_cap = nq // 32
+        if resid_cap is None:
+            resid_cap = N - nq
     return spc_dims(B, Hq, Hkv, D, bits, group, N, R, q_groups_cap, resid_cap, scale)
 
 
