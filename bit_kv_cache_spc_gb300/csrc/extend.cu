@@ -225,36 +225,77 @@ __device__ __forceinline__ void code_tokens(ExtendSmem<BITS, GROUP>& sm, uint8_t
   for (int i = tid; i < (int)sizeof(sm.rec) / 16; i += 128) dst[i] = src[i];
 }
 
-// A group at a time: load, code, write; the other CTAs of the SM (seven at
+// Codes group g of (b, hkv): its rows into shared memory, its record out.
+template <int BITS, int GROUP>
+__device__ __forceinline__ void extend_group(const ExtendArgs& a, ExtendSmem<BITS, GROUP>& sm, int64_t bh, int g) {
+  const int tid = threadIdx.x, q = tid & 31, t0 = a.nq + g * GROUP;
+  uint16_t* tile = (q < 16 ? sm.k : sm.v) + 8 * (q & 15);
+  if (t0 >= a.N) {  // none of the window's rows
+    const int64_t b = bh / a.Hkv, h = bh % a.Hkv, step = q < 16 ? a.lk.t : a.lv.t;
+    const uint16_t* src = (q < 16 ? a.k_new + b * a.lk.b + h * a.lk.h : a.v_new + b * a.lv.b + h * a.lv.h) +
+                          8 * (q & 15) + (t0 - a.N + (tid >> 5)) * step;
+#pragma unroll 8
+    for (int row = tid >> 5; row < GROUP; row += 4, src += 4 * step) cp_async16(tile + row * kPitch, src);
+  } else {
+    for (int row = tid >> 5; row < GROUP; row += 4) cp_async16(tile + row * kPitch, extend_source(a, bh, t0 + row, q));
+  }
+  cp_async_commit();
+  cp_async_wait<0>();
+  __syncthreads();
+  code_tokens<BITS, GROUP>(sm, a.records + (bh * a.units_cap + a.nq / GROUP + g) * record_bytes(BITS, GROUP));
+  __syncthreads();  // the tiles and the record are reused
+}
+
+// A group at a time: load, code, write; the other CTAs of the SM (ten at
 // g = 32) fill the waits.  A second tile pair per CTA, with the next group's
 // copies in flight, measured the same (104.9 against 105.7 us below).
-// 1 bit, g = 32, four 32768-token prompts over 8 KV heads (606 MB): 105.5 us,
-// 5.7 TB/s, 85% of the measured copy bandwidth.
+// 1 bit, g = 32, four 32768-token prompts over 8 KV heads (606 MB): 104 us,
+// 5.8 TB/s, 86% of the measured copy bandwidth; g = 64 96 us; 2 bits 169 and
+// 138 us, bound by the thresholds' and comparisons' issue.
 template <int BITS, int GROUP>
 __global__ void __launch_bounds__(128, GROUP == 32 ? 8 : 5) extend_groups_kernel(const __grid_constant__ ExtendArgs a) {
   extern __shared__ __align__(16) uint8_t extend_smem[];
   ExtendSmem<BITS, GROUP>& sm = *reinterpret_cast<ExtendSmem<BITS, GROUP>*>(extend_smem);
-  const int tid = threadIdx.x, q = tid & 31;
   const int per = (a.nq1 - a.nq) / GROUP;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");  // the window's kernel may be set up meanwhile
-  for (int64_t gi = blockIdx.x; gi < a.total_groups; gi += gridDim.x) {
-    const int64_t bh = gi / per, b = bh / a.Hkv, h = bh % a.Hkv;
-    const int g = (int)(gi % per), t0 = a.nq + g * GROUP;
-    uint16_t* tile = (q < 16 ? sm.k : sm.v) + 8 * (q & 15);
-    if (t0 >= a.N) {  // none of the window's rows
-      const int64_t step = q < 16 ? a.lk.t : a.lv.t;
-      const uint16_t* src = (q < 16 ? a.k_new + b * a.lk.b + h * a.lk.h : a.v_new + b * a.lv.b + h * a.lv.h) +
-                            8 * (q & 15) + (t0 - a.N + (tid >> 5)) * step;
-#pragma unroll 8
-      for (int row = tid >> 5; row < GROUP; row += 4, src += 4 * step) cp_async16(tile + row * kPitch, src);
-    } else {
-      for (int row = tid >> 5; row < GROUP; row += 4) cp_async16(tile + row * kPitch, extend_source(a, bh, t0 + row, q));
-    }
-    cp_async_commit();
-    cp_async_wait<0>();
-    __syncthreads();
-    code_tokens<BITS, GROUP>(sm, a.records + (bh * a.units_cap + a.nq / GROUP + g) * record_bytes(BITS, GROUP));
-    __syncthreads();  // the tiles and the record are reused
+  for (int64_t gi = blockIdx.x; gi < a.total_groups; gi += gridDim.x)
+    extend_group<BITS, GROUP>(a, sm, gi / per, (int)(gi % per));
+}
+
+// The same and the window's rows in one launch, for turns of few groups: a
+// cluster of eight CTAs takes a (b, hkv).  They code its groups, a group each,
+// and hold the window's next rows in registers; once every CTA has read what
+// it needs of the old window (a cluster barrier), they write the new one.
+// A 77-token turn of eight conversations (8 KV heads, R = 128): one launch of
+// 5.0 us against two of 9.4.
+constexpr int kTurnCtas = 8, kTurnPieces = 8;
+constexpr int kTurnRows = kTurnCtas * kTurnPieces * 128 / 32;  // of the window
+
+template <int BITS, int GROUP>
+__global__ void __launch_bounds__(128) __cluster_dims__(kTurnCtas, 1, 1)
+extend_turn_kernel(const __grid_constant__ ExtendArgs a) {
+  extern __shared__ __align__(16) uint8_t extend_smem[];
+  ExtendSmem<BITS, GROUP>& sm = *reinterpret_cast<ExtendSmem<BITS, GROUP>*>(extend_smem);
+  const int rank = blockIdx.x % kTurnCtas, id = rank * 128 + threadIdx.x;
+  const int64_t bh = blockIdx.x / kTurnCtas;
+  const int pieces = (a.N + a.n - a.nq1) * 32;  // of 16 bytes
+  uint4 next[kTurnPieces];
+#pragma unroll
+  for (int i = 0; i < kTurnPieces; ++i) {
+    const int p = id + i * kTurnCtas * 128;
+    if (p < pieces) next[i] = *extend_source(a, bh, a.nq1 + (p >> 5), p & 31);
+  }
+  for (int g = rank; g < (a.nq1 - a.nq) / GROUP; g += kTurnCtas) extend_group<BITS, GROUP>(a, sm, bh, g);
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+  uint4* win = reinterpret_cast<uint4*>(a.resid + bh * a.resid_cap * 2 * kD);
+#pragma unroll
+  for (int i = 0; i < kTurnPieces; ++i) {
+    const int p = id + i * kTurnCtas * 128;
+    if (p < pieces) win[p] = next[i];
+  }
+  if (a.host != nullptr) {
+    uint4* host = reinterpret_cast<uint4*>(a.host + (bh * a.n_cap + a.N) * 2 * kD);
+    for (int p = id; p < a.n * 32; p += kTurnCtas * 128) host[p] = *extend_source(a, bh, a.N + (p >> 5), p & 31);
   }
 }
 
@@ -303,8 +344,15 @@ __global__ void __launch_bounds__(256) extend_window_kernel(const __grid_constan
 }
 
 template <int BITS, int GROUP>
-cudaError_t launch_extend_k(const ExtendArgs& a, cudaStream_t stream) {
+cudaError_t launch_extend_k(const ExtendArgs& a, int64_t BH, bool turn, cudaStream_t stream) {
   const int smem = (int)sizeof(ExtendSmem<BITS, GROUP>);
+  if (turn) {
+    static unsigned long long turn_configured = 0ull;
+    const cudaError_t e = spc_host::ensure_smem_limit(turn_configured, extend_turn_kernel<BITS, GROUP>, smem);
+    if (e != cudaSuccess) return e;
+    extend_turn_kernel<BITS, GROUP><<<(unsigned)(BH * kTurnCtas), 128, smem, stream>>>(a);
+    return cudaGetLastError();
+  }
   static unsigned long long configured = 0ull;
   const cudaError_t e = spc_host::ensure_smem_limit(configured, extend_groups_kernel<BITS, GROUP>, smem);
   if (e != cudaSuccess) return e;
@@ -337,14 +385,18 @@ spc_status launch_extend(const spc_dims* d, int32_t n, const uint16_t* k_new, co
   a.units_cap = records_cap(d->group, d->q_groups_cap);
   const int64_t BH = (int64_t)d->B * d->Hkv;
   a.total_groups = BH * ((a.nq1 - a.nq) / d->group);
+  // One launch where a cluster's CTAs have a group each at most and hold the
+  // window; else the groups first, over all SMs, then the window.
+  const bool turn = a.total_groups > 0 && a.total_groups <= BH * kTurnCtas && a.N + n - a.nq1 <= kTurnRows &&
+                    BH <= 0x0FFFFFFF;
   cudaError_t e = cudaSuccess;
   if (a.total_groups > 0) {
     if (d->bits == 1)
-      e = d->group == 64 ? launch_extend_k<1, 64>(a, stream) : launch_extend_k<1, 32>(a, stream);
+      e = d->group == 64 ? launch_extend_k<1, 64>(a, BH, turn, stream) : launch_extend_k<1, 32>(a, BH, turn, stream);
     else
-      e = d->group == 64 ? launch_extend_k<2, 64>(a, stream) : launch_extend_k<2, 32>(a, stream);
+      e = d->group == 64 ? launch_extend_k<2, 64>(a, BH, turn, stream) : launch_extend_k<2, 32>(a, BH, turn, stream);
   }
-  if (e == cudaSuccess) {
+  if (e == cudaSuccess && !turn) {
     const bool moves = a.nq1 > a.nq && a.N > a.nq1;
     const int32_t rows = a.N + n - std::max(a.N, a.nq1);
     a.window_parts = moves ? 1 : (int32_t)std::min<int64_t>(64, (rows + 31) / 32);

@@ -86,6 +86,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 // of two): weights then stay below 2^8, and O is rescaled a few times per row
 // instead of at every tile.
 constexpr float kSlack = 8.0f;
+constexpr int kDense = 256;  // sequences whose actual lengths number the items
 
 struct PromptArgs {
   const uint16_t* v;
@@ -102,6 +103,7 @@ struct PromptArgs {
   int64_t v_b, v_t, v_h, o_b, o_t, o_h;
   int32_t S, Hq, Hkv, G, tile_tokens, pair_tokens, pairs, splits;
   int32_t q_tokens, k_tokens, q_max, k_max;
+  int32_t dense;                 // items are numbered over the pairs that exist
   int32_t q_batched, k_batched;  // sequence s lies at s * stride (else on one token axis)
   float scale;
 };
@@ -300,45 +302,48 @@ __device__ __forceinline__ void sequence(const PromptArgs& a, int s, int& lq, in
 }
 
 // CTAs that a sequence's query rows take ("pairs", of one or two tiles).
-__device__ __forceinline__ int pairs_of(const PromptArgs& a, int lq) { return (lq + a.pair_tokens - 1) / a.pair_tokens; }
 __device__ __forceinline__ int sequence_pairs(const PromptArgs& a, int s) {
   int lq, lk, qb, kb;
   sequence(a, s, lq, lk, qb, kb);
-  return pairs_of(a, lq);
+  return (lq + a.pair_tokens - 1) / a.pair_tokens;
 }
 
-// Sum over the sequences of the pairs from pair p on (a whole warp; `mine` the
-// pairs of the lane's sequence among the first 32).
-__device__ __forceinline__ int pairs_from(const PromptArgs& a, int p, int mine) {
-  int n = max(0, mine - p);
-  for (int s = 32 + (threadIdx.x & 31); s < a.S; s += 32) n += max(0, sequence_pairs(a, s) - p);
+// Sum over the sequences of the pairs from pair p on (a whole warp; lane l has
+// sequences l, l + 32, ... in mine).
+__device__ __forceinline__ int pairs_from(int p, const int* mine) {
+  int n = 0;
+#pragma unroll
+  for (int u = 0; u < kDense / 32; ++u) n += max(0, mine[u] - p);
   return __reduce_add_sync(0xFFFFFFFFu, n);
 }
 
 // Item i of all (a whole warp): split fastest, then KV head, then sequence,
-// then pair, later pairs (more keys) first, over the pairs that exist.  CTAs
-// that run together then read different heads' keys at the same depth, and
-// several pairs of a head share them in L2.  False behind the last one.
+// then pair, later pairs (more keys) first.  CTAs that run together then read
+// different heads' keys at the same depth, and several pairs of a head share
+// them in L2.  Up to kDense sequences of different lengths are numbered over
+// the pairs that exist, so that long and short prompts packed together leave
+// no empty CTAs; more, or equal ones, over all pairs.  False for none.
 template <int TILES>
 __device__ __forceinline__ bool prompt_item(const PromptArgs& a, uint32_t i, PromptItem& w) {
   constexpr int kKeys = Shape<TILES>::kKeys;
   const int lane = threadIdx.x & 31;
-  int lq = 0, lk = 0, qb = 0, kb = 0;  // of sequence `lane`
-  if (lane < a.S) sequence(a, lane, lq, lk, qb, kb);
   w.split = (int)(i % a.splits);
   i /= a.splits;
   w.hkv = (int)(i % a.Hkv);
   i /= a.Hkv;
-  if (a.q_len == nullptr && a.q_begin == nullptr) {  // equal sequences
+  if (!a.dense) {
     w.s = (int)(i % a.S);
     w.pair = a.pairs - 1 - (int)(i / a.S);
     if (w.pair < 0) return false;
   } else {
-    const int mine = pairs_of(a, lq), k0 = (int)i;
+    int mine[kDense / 32];
+#pragma unroll
+    for (int u = 0; u < kDense / 32; ++u) mine[u] = 32 * u + lane < a.S ? sequence_pairs(a, 32 * u + lane) : 0;
+    const int k0 = (int)i;
     int lo = 0, hi = a.pairs, behind = 0;  // pairs_from(lo) > k0 >= pairs_from(hi) = behind
-    if (pairs_from(a, 0, mine) <= k0) return false;
+    if (pairs_from(0, mine) <= k0) return false;
     while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2, n = pairs_from(a, mid, mine);
+      const int mid = (lo + hi) / 2, n = pairs_from(mid, mine);
       if (n > k0) {
         lo = mid;
       } else {
@@ -348,27 +353,18 @@ __device__ __forceinline__ bool prompt_item(const PromptArgs& a, uint32_t i, Pro
     }
     w.pair = lo;
     int k = k0 - behind;  // the k-th sequence that has this pair
-    for (int s0 = 0;; s0 += 32) {
-      const bool has = s0 + lane < a.S && (s0 == 0 ? mine : sequence_pairs(a, s0 + lane)) > lo;
+    w.s = 0;
+#pragma unroll
+    for (int u = 0; u < kDense / 32; ++u) {
+      const bool has = mine[u] > lo;
       const uint32_t who = __ballot_sync(0xFFFFFFFFu, has);
-      const int n = __popc(who);
-      if (k < n) {
-        const bool it = has && __popc(who & ((1u << lane) - 1u)) == k;
-        w.s = s0 + __ffs((int)__ballot_sync(0xFFFFFFFFu, it)) - 1;
-        break;
-      }
-      k -= n;
-      if (s0 + 32 >= a.S) return false;  // the lengths changed under the call
+      const uint32_t it = __ballot_sync(0xFFFFFFFFu, has && __popc(who & ((1u << lane) - 1u)) == k);
+      if (it != 0u) w.s = 32 * u + __ffs((int)it) - 1;
+      k -= __popc(who);  // negative once found
     }
   }
-  if (w.s < 32) {
-    w.lq = __shfl_sync(0xFFFFFFFFu, lq, w.s);
-    w.lk = __shfl_sync(0xFFFFFFFFu, lk, w.s);
-    w.qb = __shfl_sync(0xFFFFFFFFu, qb, w.s);
-    w.kb = __shfl_sync(0xFFFFFFFFu, kb, w.s);
-  } else {
-    sequence(a, w.s, w.lq, w.lk, w.qb, w.kb);
-  }
+  sequence(a, w.s, w.lq, w.lk, w.qb, w.kb);
+  if (w.pair * a.pair_tokens >= w.lq) return false;
   w.tok0 = w.pair * a.pair_tokens;
   w.two = TILES == 2 && w.tok0 + a.tile_tokens < w.lq;
   const int last = min(w.tok0 + a.pair_tokens, w.lq) - 1;  // last query token
@@ -899,7 +895,7 @@ PromptGrid prompt_grid(const spc_prompt_dims* d) {
   g.pair_tokens = g.tiles * g.tile_tokens;
   g.pairs = (d->q_max + g.pair_tokens - 1) / g.pair_tokens;
   int64_t all = (int64_t)d->S * g.pairs;
-  if (d->q.b == 0) all = std::min(all, d->S + (int64_t)d->q_tokens / g.pair_tokens);
+  if (d->q.b == 0 && d->S <= kDense) all = std::min(all, d->S + (int64_t)d->q_tokens / g.pair_tokens);
   g.items = all * d->Hkv;
   g.splits = 1;
   const int64_t places = spc_host::sm_count() * (g.tiles == 1 ? 2 : 1);
@@ -975,6 +971,8 @@ spc_status launch_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const
   a.tile_tokens = g.tile_tokens;
   a.pair_tokens = g.pair_tokens;
   a.pairs = g.pairs;
+  // one pair each is numbered as it is: an empty sequence costs no more than looking for the others would
+  a.dense = (q_len != nullptr || q_begin != nullptr) && d->S > 1 && d->S <= kDense && g.pairs > 1;
   a.splits = g.splits;
   a.fault = static_cast<uint32_t*>(ws);
   a.part_rows = (int64_t)d->S * d->q_max * d->Hq;

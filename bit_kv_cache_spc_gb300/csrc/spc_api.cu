@@ -680,6 +680,7 @@ spc_status spc_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const ui
   spc_status st = check_prompt_dims(d);
   if (st != SPC_OK) return st;
   if (d->q_max == 0) return SPC_OK;
+  if (d->S > 1 && d->q.b == 0 && q_begin == nullptr) return SPC_ERR_INVALID;  // all on the same query rows
   if (q == nullptr || o == nullptr || (d->k_max > 0 && (k == nullptr || v == nullptr))) return SPC_ERR_INVALID;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return SPC_ERR_INVALID;
   const size_t need = spc::prompt_workspace_bytes(d);

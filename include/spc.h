@@ -467,7 +467,8 @@ size_t spc_prompt_attn_workspace_bytes(const spc_prompt_dims* d);
  *   q_begin, q_len, k_begin, k_len : int32 [S] (device) or NULL: each
  *            sequence's first token on its token axis (NULL: 0) and its
  *            length (NULL: q_max, k_max).  Values are held to the tensors
- *            (0 .. q_tokens and so on) and to q_max, k_max.
+ *            (0 .. q_tokens and so on) and to q_max, k_max.  Packed queries
+ *            of several sequences need q_begin; sequences may share keys.
  *   o       : bf16, rows of no sequence are left as they were; sequences'
  *            rows must not overlap, nor share bytes with an input.
  *   lse     : fp32 [q_tokens][Hq] (packed) or [S][q_tokens][Hq], or NULL.

@@ -163,6 +163,38 @@ def test_visible_infinities_and_nan():
     assert torch.equal(o[:, :, kept], o2[:, :, kept])
 
 
+@pytest.mark.parametrize("S,most", [(40, 700), (256, 300), (300, 300)])
+def test_many_packed_sequences(S, most):
+    """Dozens and hundreds of sequences of very different lengths, empty ones among them: every one is done, once."""
+    import bit_kv_cache_spc_gb300 as spc
+    lens = [(s * 97) % 41 if s % 13 else (most if s == 0 else most // (1 + s % 7)) for s in range(S)]
+    begin = [sum(lens[:s]) for s in range(S)]
+    T, Hq, Hkv = sum(lens), 2, 1
+    q, k, v = rnd(1, T, Hq, D), rnd(2, T, Hkv, D), rnd(3, T, Hkv, D)
+    o, lse = torch.full_like(q, 7.0), torch.full((T, Hq), 7.0, device="cuda")
+    spc.spc_prompt_attn(q, k, v, o, lse, q_begin=i32(begin), q_len=i32(lens), k_begin=i32(begin), k_len=i32(lens),
+                        q_max=most, k_max=most)
+    assert not bool((lse == 7).any())
+    for s in list(range(0, S, 13)) + [1, 2, S - 1]:
+        b, n = begin[s], lens[s]
+        if n:
+            check(o[b:b + n], lse[b:b + n], q[b:b + n], k[b:b + n], v[b:b + n])
+
+
+def test_a_large_batch_of_single_tokens():
+    """600 sequences of one new token each, packed, over keys that some of them share."""
+    import bit_kv_cache_spc_gb300 as spc
+    S, T, Hq, Hkv = 600, 900, 4, 1
+    q, k, v = rnd(1, S, Hq, D), rnd(2, T, Hkv, D), rnd(3, T, Hkv, D)
+    lk = [1 + (s * 53) % 300 for s in range(S)]
+    kb = [(s * 31) % 600 for s in range(S)]
+    o, lse = torch.zeros_like(q), torch.zeros((S, Hq), device="cuda")
+    spc.spc_prompt_attn(q, k, v, o, lse, q_begin=torch.arange(S, dtype=torch.int32, device="cuda"),
+                        k_begin=i32(kb), k_len=i32(lk), q_max=1, k_max=300)
+    for s in range(0, S, 7):
+        check(o[s:s + 1], lse[s:s + 1], q[s:s + 1], k[kb[s]:kb[s] + lk[s]], v[kb[s]:kb[s] + lk[s]])
+
+
 def test_other_strides_and_scale():
     """Head-major queries and outputs inside wider buffers, and a scale of the caller's."""
     import bit_kv_cache_spc_gb300 as spc

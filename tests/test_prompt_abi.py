@@ -132,6 +132,11 @@ def test_prompt_attn_refuses_arguments(kw, status):
     assert prompt_call(prompt_dims(), **kw) == status
 
 
+def test_prompt_attn_refuses_sequences_on_the_same_rows():
+    """Packed queries of two sequences without their first tokens."""
+    assert prompt_call(prompt_dims(q=lay(0, 1024, 128), o=lay(0, 1024, 128))) == INVALID
+
+
 def test_prompt_attn_of_no_queries_is_nothing():
     assert prompt_call(prompt_dims(q_max=0)) == 0
 
