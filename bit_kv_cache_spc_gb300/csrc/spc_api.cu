@@ -574,6 +574,11 @@ size_t layout_bytes(const spc_layout& l, int64_t nb, int64_t nt, int64_t nh) {
   return 2 * (size_t)((nb - 1) * l.b + (nt - 1) * l.t + (nh - 1) * l.h + spc::kD);
 }
 
+// The first rows of two views share bytes: the views are one, or nearly.
+bool same_rows(const void* a, const void* b) {
+  return a != nullptr && b != nullptr && overlap(a, 2 * spc::kD, b, 2 * spc::kD);
+}
+
 bool same_layout(const spc_layout& x, const spc_layout& y) { return x.b == y.b && x.t == y.t && x.h == y.h; }
 
 }  // namespace
@@ -648,6 +653,7 @@ spc_status spc_rope(const spc_rope_dims* d, const int32_t* pos, const uint64_t* 
         overlap(r.in, layout_bytes(*r.li, d->B, d->T, r.heads), r.out, layout_bytes(*r.lo, d->B, d->T, r.heads)))
       return SPC_ERR_INVALID;
   }
+  if (same_rows(q_out, k_out) || same_rows(q_out, v_out) || same_rows(k_out, v_out)) return SPC_ERR_INVALID;
   return spc::launch_rope(d, pos, turns, q, k, v, q_out, k_out, v_out, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -686,6 +692,12 @@ spc_status spc_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const ui
   const size_t need = spc::prompt_workspace_bytes(d);
   if ((ws == nullptr && (need > 256 || ws_bytes != 0)) || !aligned16(ws)) return SPC_ERR_INVALID;
   if (ws != nullptr && ws_bytes < need) return SPC_ERR_WORKSPACE;
+  const int64_t qb = d->q.b ? d->S : 1, kb = d->k.b ? d->S : 1;
+  const size_t ob = layout_bytes(d->o, qb, d->q_tokens, d->Hq);
+  if (overlap(q, layout_bytes(d->q, qb, d->q_tokens, d->Hq), o, ob) ||
+      (k != nullptr && overlap(k, layout_bytes(d->k, kb, d->k_tokens, d->Hkv), o, ob)) ||
+      (v != nullptr && overlap(v, layout_bytes(d->v, kb, d->k_tokens, d->Hkv), o, ob)))
+    return SPC_ERR_INVALID;
   return spc::launch_prompt_attn(d, q, k, v, q_begin, q_len, k_begin, k_len, o, lse, ws,
                                  reinterpret_cast<cudaStream_t>(stream));
 }
@@ -754,7 +766,7 @@ spc_status spc_dequantize_kv(const spc_dims* d, const void* records, const uint1
   const size_t res = spc_resid_bytes(d), rec = spc_records_bytes(d);
   const size_t kb = layout_bytes(*k_layout, d->B, n, d->Hkv), vb = layout_bytes(*v_layout, d->B, n, d->Hkv);
   if (overlap(k, kb, resid, res) || overlap(v, vb, resid, res) || overlap(k, kb, records, rec) ||
-      overlap(v, vb, records, rec))
+      overlap(v, vb, records, rec) || same_rows(k, v))
     return SPC_ERR_INVALID;
   return spc::launch_dequantize(d, records, resid, first, n, k, v, k_layout, v_layout,
                                 reinterpret_cast<cudaStream_t>(stream));

@@ -470,7 +470,8 @@ size_t spc_prompt_attn_workspace_bytes(const spc_prompt_dims* d);
  *            (0 .. q_tokens and so on) and to q_max, k_max.  Packed queries
  *            of several sequences need q_begin; sequences may share keys.
  *   o       : bf16, rows of no sequence are left as they were; sequences'
- *            rows must not overlap, nor share bytes with an input.
+ *            rows must not overlap, and the view shares no byte range with an
+ *            input (SPC_ERR_INVALID).
  *   lse     : fp32 [q_tokens][Hq] (packed) or [S][q_tokens][Hq], or NULL.
  *   ws      : at least spc_prompt_attn_workspace_bytes(d) bytes, or NULL with
  *            ws_bytes 0 where that is 256.
@@ -510,7 +511,8 @@ spc_status spc_extend_kv(const spc_dims* d, int32_t n, const uint16_t* k_new, co
  * are fl(z + fl(s * code)) in binary32 (z and s from the group's min and max
  * as under spc_records_bytes), rounded once to bf16; a residual token's are
  * its 16-bit rows.
- *   k, v: bf16 views [B][n][Hkv][D] (device); other rows are left as they were.
+ *   k, v: bf16 views [B][n][Hkv][D] (device) that share no row; other rows are left as
+ *         they were.
  * first >= 0, n >= 0, first + n <= N.
  */
 spc_status spc_dequantize_kv(const spc_dims* d, const void* records, const uint16_t* resid, int32_t first, int32_t n,

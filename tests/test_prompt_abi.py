@@ -83,6 +83,7 @@ def rope_call(q=1 << 16, k=1 << 20, v=None, q_out=-1, k_out=-1, v_out=None, pos=
     (dict(q_out=None), INVALID), (dict(v=1 << 24), INVALID), (dict(v_out=1 << 24), INVALID), (dict(Hkv=0), INVALID),
     (dict(q_out=(1 << 16) + 256), INVALID), (dict(q_out=(1 << 16) - 16384 + 16), INVALID),  # reach into their own input
     (dict(v=1 << 24, v_out=(1 << 24) + 512), INVALID),
+    (dict(q_out=1 << 30, k_out=1 << 30), INVALID), (dict(k_out=1 << 30, v=1 << 24, v_out=(1 << 30) - 128), INVALID),
     (dict(q_out=1 << 30, ql=lay(4096, 512, 64)), INVALID),      # heads overlap
     (dict(q_out=1 << 30, ql=lay(4096, 512, 0)), INVALID),       # a broadcast axis
     (dict(q_out=1 << 30, ql=lay(4096, 384, 128)), INVALID),     # tokens overlap
@@ -135,6 +136,12 @@ def test_prompt_attn_refuses_arguments(kw, status):
 def test_prompt_attn_refuses_sequences_on_the_same_rows():
     """Packed queries of two sequences without their first tokens."""
     assert prompt_call(prompt_dims(q=lay(0, 1024, 128), o=lay(0, 1024, 128))) == INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(q=1 << 30, k=1 << 31), dict(q=1 << 30, v=1 << 31),
+                                dict(k=1 << 30, v=1 << 31, q=4096 + 64 * 8 * 256 * 2 - 256)])
+def test_prompt_attn_refuses_an_output_that_reaches_into_an_input(kw):
+    assert prompt_call(prompt_dims(), **kw) == INVALID
 
 
 def test_prompt_attn_of_no_queries_is_nothing():
@@ -197,6 +204,11 @@ def test_read_refuses_tokens_that_are_not_there():
     assert cache_call("read", first=91, n=10) == INVALID
     assert cache_call("read", first=2 ** 31 - 1, n=10) == INVALID
     assert cache_call("read", first=100, n=0) == 0
+
+
+def test_read_refuses_keys_and_values_on_the_same_rows():
+    assert cache_call("read", k=1 << 32, v=1 << 32) == INVALID
+    assert cache_call("read", k=1 << 32, v=(1 << 32) + 128) == INVALID
 
 
 # ------------------------------------------------------------------------------------------------ tensors
