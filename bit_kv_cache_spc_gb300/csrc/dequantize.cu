@@ -229,7 +229,7 @@ spc_status launch_dequantize(const spc_dims* d, const void* records, const uint1
   a.tile0 = tile_of(first);
   a.tiles_per = tile_of(a.end - 1) - a.tile0 + 1;
   const int64_t tiles = (int64_t)d->B * d->Hkv * a.tiles_per;
-    if (tiles > 0x7FFFFFFF) return SPC_ERR_UNSUPPORTED;
+  if (tiles > 0x7FFFFFFF) return SPC_ERR_UNSUPPORTED;
   const unsigned grid = (unsigned)tiles;
   if (d->group == 64) {
     if (d->bits == 1)

@@ -17,8 +17,8 @@
 //   - keys: a pass over channel pairs for the extremes, a thread per channel
 //     for the thresholds, then thread (token mod 8, channel pair mod 8, four
 //     chunks of channels) builds one word.
-// The 2-bit code is the number of thresholds reached: the high bit is the
-// second comparison, the low bit the parity of the three.
+// The high bit of a 2-bit code is the comparison with the second threshold,
+// the low bit one with the third or the first as the high bit says.
 // Bound by HBM: 512 bytes read and 48 to 96 written per token and KV head.
 #include <algorithm>
 
@@ -91,9 +91,9 @@ __device__ __forceinline__ void code_pair(uint32_t x, const uint32_t* thr, uint3
   if (BITS == 1) {
     acc[0] |= ge_bf16x2(x, thr[0]) & bit;
   } else {
-    const uint32_t m1 = ge_bf16x2(x, thr[0]), m2 = ge_bf16x2(x, thr[1]), m3 = ge_bf16x2(x, thr[2]);
-    acc[0] |= (m1 ^ m2 ^ m3) & bit;
-    acc[BITS - 1] |= m2 & bit;
+    const uint32_t high = ge_bf16x2(x, thr[1]);
+    acc[0] |= ge_bf16x2(x, (thr[2] & high) | (thr[0] & ~high)) & bit;
+    acc[BITS - 1] |= high & bit;
   }
 }
 
@@ -243,23 +243,27 @@ __device__ __forceinline__ void extend_group(const ExtendArgs& a, ExtendSmem<BIT
   cp_async_wait<0>();
   __syncthreads();
   code_tokens<BITS, GROUP>(sm, a.records + (bh * a.units_cap + a.nq / GROUP + g) * record_bytes(BITS, GROUP));
-  __syncthreads();  // the tiles and the record are reused
 }
 
-// A group at a time: load, code, write; the other CTAs of the SM (ten at
-// g = 32) fill the waits.  A second tile pair per CTA, with the next group's
-// copies in flight, measured the same (104.9 against 105.7 us below).
-// 1 bit, g = 32, four 32768-token prompts over 8 KV heads (606 MB): 104 us,
-// 5.8 TB/s, 86% of the measured copy bandwidth; g = 64 96 us; 2 bits 169 and
-// 138 us, bound by the thresholds' and comparisons' issue.
+// CTAs that an SM holds: 10 (1 bit) and 9 (2 bits) at g = 32, 5 at g = 64.
 template <int BITS, int GROUP>
-__global__ void __launch_bounds__(128, GROUP == 32 ? 8 : 5) extend_groups_kernel(const __grid_constant__ ExtendArgs a) {
+constexpr int kResident = 232448 / (sizeof(ExtendSmem<BITS, GROUP>) + 1024);
+
+// A group per CTA; the other CTAs of the SM fill its waits.  CTAs that stay
+// and take group after group end 10% apart (105 us against 93 below), two
+// groups per CTA are slower where groups are few (300 tokens into eight caches
+// 8.3 us against 6.9), and neighbours that take the KV heads of the same
+// tokens instead of a head's groups in turn are too (98).
+// 1 bit, g = 32, four 32768-token prompts over 8 KV heads (606 MB): 93 us,
+// 6.5 TB/s, 96% of the measured copy bandwidth; g = 64 91 us; 2 bits 128 and
+// 113 us, bound by the thresholds' and comparisons' issue.
+template <int BITS, int GROUP>
+__global__ void __launch_bounds__(128, kResident<BITS, GROUP>) extend_groups_kernel(const __grid_constant__ ExtendArgs a) {
   extern __shared__ __align__(16) uint8_t extend_smem[];
   ExtendSmem<BITS, GROUP>& sm = *reinterpret_cast<ExtendSmem<BITS, GROUP>*>(extend_smem);
-  const int per = (a.nq1 - a.nq) / GROUP;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");  // the window's kernel may be set up meanwhile
-  for (int64_t gi = blockIdx.x; gi < a.total_groups; gi += gridDim.x)
-    extend_group<BITS, GROUP>(a, sm, gi / per, (int)(gi % per));
+  const uint32_t per = (a.nq1 - a.nq) / GROUP, bh = blockIdx.x / per;
+  extend_group<BITS, GROUP>(a, sm, bh, (int)(blockIdx.x - bh * per));
 }
 
 // The same and the window's rows in one launch, for turns of few groups: a
@@ -285,7 +289,7 @@ extend_turn_kernel(const __grid_constant__ ExtendArgs a) {
     const int p = id + i * kTurnCtas * 128;
     if (p < pieces) next[i] = *extend_source(a, bh, a.nq1 + (p >> 5), p & 31);
   }
-  for (int g = rank; g < (a.nq1 - a.nq) / GROUP; g += kTurnCtas) extend_group<BITS, GROUP>(a, sm, bh, g);
+  if (rank < (a.nq1 - a.nq) / GROUP) extend_group<BITS, GROUP>(a, sm, bh, rank);
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
   uint4* win = reinterpret_cast<uint4*>(a.resid + bh * a.resid_cap * 2 * kD);
 #pragma unroll
@@ -356,9 +360,7 @@ cudaError_t launch_extend_k(const ExtendArgs& a, int64_t BH, bool turn, cudaStre
   static unsigned long long configured = 0ull;
   const cudaError_t e = spc_host::ensure_smem_limit(configured, extend_groups_kernel<BITS, GROUP>, smem);
   if (e != cudaSuccess) return e;
-  // as many CTAs as are resident at once, each with several groups to code
-  const int64_t grid = std::min<int64_t>(a.total_groups, (int64_t)spc_host::sm_count() * (232448 / (smem + 1024)));
-  extend_groups_kernel<BITS, GROUP><<<(unsigned)grid, 128, smem, stream>>>(a);
+  extend_groups_kernel<BITS, GROUP><<<(unsigned)a.total_groups, 128, smem, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -385,6 +387,7 @@ spc_status launch_extend(const spc_dims* d, int32_t n, const uint16_t* k_new, co
   a.units_cap = records_cap(d->group, d->q_groups_cap);
   const int64_t BH = (int64_t)d->B * d->Hkv;
   a.total_groups = BH * ((a.nq1 - a.nq) / d->group);
+  if (a.total_groups > 0x7FFFFFFF) return SPC_ERR_UNSUPPORTED;
   // One launch where a cluster's CTAs have a group each at most and hold the
   // window; else the groups first, over all SMs, then the window.
   const bool turn = a.total_groups > 0 && a.total_groups <= BH * kTurnCtas && a.N + n - a.nq1 <= kTurnRows &&

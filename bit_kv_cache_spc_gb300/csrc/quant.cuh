@@ -100,9 +100,9 @@ __device__ __forceinline__ float code_threshold(float lo, float hi, float z, flo
 }
 
 // Whether an x with d = fl(x - z) has a code of at least `level`, for s in
-// [2^-100, 2^100], without the quotient.  fl(d / s) is above 1/2 exactly when 2 d > s; at least 3/2 when d / s >= 3/2 - 2^-24 and above 5/2 when
-// d / s > 5/2 + 2^-23 (the ties at those half steps round to the even 3/2 and
-// 5/2).  Both sides of those comparisons are multiples of half an ulp of s
+// [2^-100, 2^100], without the quotient.  fl(d / s) is above 1/2 exactly when
+// 2 d > s; at least 3/2 when d / s >= 3/2 - 2^-24 and above 5/2 when d / s >
+// 5/2 + 2^-23 (the ties at those half steps round to the even 3/2 and 5/2).  Both sides of those comparisons are multiples of half an ulp of s
 // and, where they are close, a few of them, so one rounding decides them
 // exactly.
 template <int BITS>
@@ -135,12 +135,11 @@ __device__ __forceinline__ void code_thresholds(float lo, float hi, float z, flo
     }
     uint16_t b;
     asm("cvt.rn.bf16.f32 %0, %1;\n" : "=h"(b) : "f"(guess));
-    const uint32_t o = bf16_ord(b), down = bf16_unord(o - 1u), up = bf16_unord(o + 1u);
     const bool at = code_reaches<BITS>(__fsub_rn(bf16_to_f32(b), z), s, l);
-    const bool below = code_reaches<BITS>(__fsub_rn(bf16_to_f32(down), z), s, l);
-    const bool above = code_reaches<BITS>(__fsub_rn(bf16_to_f32(up), z), s, l);
-    thr[l - 1] = at ? b : up;
-    found = found && !below && above;
+    // x - z and what it reaches do not decrease with x: one neighbour settles it
+    const uint32_t next = bf16_unord(bf16_ord(b) + (at ? ~0u : 1u));
+    thr[l - 1] = at ? b : next;
+    found = found && code_reaches<BITS>(__fsub_rn(bf16_to_f32(next), z), s, l) != at;
   }
   if (found) return;
   const float rs = quant_recip(s);
