@@ -8,12 +8,15 @@
 // Eight lanes hold a head's row, 16 elements each: lane l < rot/16 the eight
 // pairs 8l .. 8l+7 (the half layout: elements 8l .. and rot/2 + 8l ..;
 // interleaved: 16l .. 16l+15), the other lanes the elements that stay as they
-// are.  So a lane needs eight angles of its token, computes them once and
-// walks over heads with them in registers.  Bound by HBM: every row is read
-// and written once.  Two heads' loads are in flight before the first store: a
-// 32768-token prompt of 32 + 8 + 8 heads (805 MB) takes 129 us, 92% of the
-// measured copy rate, against 143 with one head and 146 with four (fewer
-// resident warps).
+// are.  A CTA forms the angles of its tokens once, in shared memory, and each
+// lane walks over a few heads with its eight in registers (a lane that formed
+// them itself took most of the time where it had few heads: 4096 tokens 23 us
+// against 19).
+// Bound by HBM: every row is read and written once.  Two heads' loads are in
+// flight before the first store, the first ones before the angles: a
+// 32768-token prompt of 32 + 8 + 8 heads (805 MB) takes 122 us, 97% of the
+// measured copy rate, against 138 with one head in flight and 123 to 135 with
+// four (fewer resident warps).
 #include <algorithm>
 
 #include "common.cuh"
@@ -27,7 +30,7 @@ struct RopeArgs {
   const int32_t* pos;
   const uint64_t* turns;
   spc_layout lq, lk, lv, oq, ok, ov;
-  int64_t tokens;                       // B * T
+  uint32_t tokens;                      // B * T
   int32_t T, Hq, Hkv, heads, rot, per;  // heads of all three; heads a group of lanes walks over
   int32_t slices;                       // groups of `per` heads
   float mscale;
@@ -65,28 +68,19 @@ constexpr int kBatch = 2;
 
 template <bool INTERLEAVED>
 __global__ void __launch_bounds__(256, 4) rope_kernel(const __grid_constant__ RopeArgs a) {
-  const int64_t g = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
+  // (cos, sin) of the CTA's tokens (32 at most), two pairs a chunk: lane l's chunk i of a token lies at 4l + (i ^ l/2),
+  // so that the eight lanes of a token read from different banks.
+  __shared__ float4 turned_by[32][kD / 4];
+  const uint32_t g0 = blockIdx.x * 32u, token0 = g0 / (uint32_t)a.slices, rest = g0 - token0 * a.slices;
+  const uint32_t local = rest + (threadIdx.x >> 3), at = local / (uint32_t)a.slices, token = token0 + at;
   const int l = threadIdx.x & 7;
-  const int64_t token = g / a.slices;
-  if (token >= a.tokens) return;
-  const int64_t b = token / a.T, t = token % a.T;
-  const int h0 = (int)(g % a.slices) * a.per, h1 = min(h0 + a.per, a.heads);
+  const uint32_t b = token / (uint32_t)a.T, t = token - b * a.T;
+  const int h0 = (int)(local - at * a.slices) * a.per, h1 = token < a.tokens ? min(h0 + a.per, a.heads) : 0;
   const bool turned = l < a.rot / 16;
-  float c[8], s[8];
-  if (turned && h0 < a.Hq + a.Hkv) {
-    const uint64_t p = (uint64_t)(int64_t)a.pos[token];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int32_t turn = (int32_t)((p * a.turns[8 * l + i]) >> 32);
-      sincospif((float)turn * 4.656612873077393e-10f, &s[i], &c[i]);  // 2^-31: half turns
-      s[i] *= a.mscale;
-      c[i] *= a.mscale;
-    }
-  }
   // kBatch heads' loads in flight before the first store (which the compiler cannot move them across)
-  for (int hb = h0; hb < h1; hb += kBatch) {
-    uint4 u[kBatch], w[kBatch];
-    uint16_t* dst[kBatch];
+  uint4 u[kBatch], w[kBatch];
+  uint16_t* dst[kBatch];
+  const auto load = [&](int hb) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int h = hb + i;
@@ -106,6 +100,31 @@ __global__ void __launch_bounds__(256, 4) rope_kernel(const __grid_constant__ Ro
       u[i] = *reinterpret_cast<const uint4*>(src + (!INTERLEAVED && rot ? 8 * l : 16 * l));
       w[i] = *reinterpret_cast<const uint4*>(src + (!INTERLEAVED && rot ? 8 * l + a.rot / 2 : 16 * l + 8));
     }
+  };
+  load(h0);  // on its way while the angles are formed
+  const uint32_t here = min((rest + 31u) / (uint32_t)a.slices + 1u, a.tokens - token0);  // tokens of the CTA
+  for (uint32_t i = threadIdx.x; i < here * (kD / 2); i += 256) {
+    const uint32_t n = i / (kD / 2), pair = i % (kD / 2);
+    if (pair >= (uint32_t)a.rot / 2) continue;
+    const uint64_t p = (uint64_t)(int64_t)a.pos[token0 + n];
+    const int32_t turn = (int32_t)((p * a.turns[pair]) >> 32);
+    float c, s;
+    sincospif((float)turn * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
+    reinterpret_cast<float2*>(&turned_by[n][(pair >> 1) ^ (pair >> 4)])[pair & 1] = make_float2(c * a.mscale, s * a.mscale);
+  }
+  __syncthreads();
+  float c[8], s[8];
+  if (turned && h0 < min(h1, a.Hq + a.Hkv)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 x = turned_by[at][(4 * l + i) ^ (l >> 1)];
+      c[2 * i] = x.x;
+      s[2 * i] = x.y;
+      c[2 * i + 1] = x.z;
+      s[2 * i + 1] = x.w;
+    }
+  }
+  for (int hb = h0; hb < h1;) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int h = hb + i;
@@ -115,6 +134,8 @@ __global__ void __launch_bounds__(256, 4) rope_kernel(const __grid_constant__ Ro
       *reinterpret_cast<uint4*>(dst[i] + (!INTERLEAVED && rot ? 8 * l : 16 * l)) = u[i];
       *reinterpret_cast<uint4*>(dst[i] + (!INTERLEAVED && rot ? 8 * l + a.rot / 2 : 16 * l + 8)) = w[i];
     }
+    hb += kBatch;
+    load(hb);
   }
 }
 
@@ -124,21 +145,22 @@ spc_status launch_rope(const spc_rope_dims* d, const int32_t* pos, const uint64_
                        const uint16_t* k, const uint16_t* v, uint16_t* q_out, uint16_t* k_out, uint16_t* v_out,
                        cudaStream_t stream) {
   RopeArgs a = {q, k, v, q_out, k_out, v_out, pos, turns, d->q, d->k, d->v, d->q_out, d->k_out, d->v_out};
-  a.tokens = (int64_t)d->B * d->T;
+  const int64_t tokens = (int64_t)d->B * d->T;
   a.T = d->T;
   a.Hq = d->Hq;
   a.Hkv = d->Hkv;
   a.heads = d->Hq + (v != nullptr ? 2 : 1) * d->Hkv;
   a.rot = d->rot;
   a.mscale = d->mscale;
-  // Few tokens: a head per group of lanes, for latency; many: up to eight
-  // heads share a token's angles once that leaves 128 groups for each SM (512:
-  // 30 us for three 1031-token prompts of 32 + 32 + 32 heads, 128: 26).
-  const int64_t rows = a.tokens * a.heads, fill = (int64_t)spc_host::sm_count() * 128;
-  a.per = (int32_t)std::max<int64_t>(1, std::min<int64_t>(8, rows / fill));
+  // Few tokens: a head per group of lanes, for latency; many: up to four heads
+  // once that leaves 128 groups for each SM (1024 tokens of 48 heads 5.5 us,
+  // with 256 7.0; 32768 tokens 122 us, 127 with two heads and 124 with eight).
+  const int64_t rows = tokens * a.heads, fill = (int64_t)spc_host::sm_count() * 128;
+  a.per = (int32_t)std::max<int64_t>(1, std::min<int64_t>(4, rows / fill));
   a.slices = (a.heads + a.per - 1) / a.per;
-  const int64_t blocks = (a.tokens * a.slices + 31) / 32;
-  if (blocks > 0x7FFFFFFF) return SPC_ERR_UNSUPPORTED;
+  if (tokens * a.slices > 0x7FFFFFFF) return SPC_ERR_UNSUPPORTED;
+  a.tokens = (uint32_t)tokens;
+  const int64_t blocks = (tokens * a.slices + 31) / 32;
   if (d->interleaved)
     rope_kernel<true><<<(unsigned)blocks, 256, 0, stream>>>(a);
   else
