@@ -13,11 +13,14 @@
 //   - values: a word holds two tokens' bits of one channel (mod 8) 16 apart,
 //     so a lane takes a token pair and eight channels from eight words.
 // Bound by HBM: 512 bytes written per token and KV head against 48 to 96 read.
-// Eight 32768-token caches of 8 KV heads at 1 bit (1.21 GB) take 181 us, the
-// measured copy rate; at 2 bits (1.28 GB) 240, bound by the selects' issue
-// (levels per thread instead of per group: 24 us against 18 for two 2-bit
-// caches of 32 heads and 2003 tokens).  CTAs that walk over tiles, 16 per SM,
-// wait for each tile's words with nothing else to do (219 us).
+// Eight 32768-token caches of 8 KV heads at 1 bit (1.21 GB) take 176 us, the
+// measured copy rate (g = 64 171); at 2 bits (1.28 GB) 212, 89% of it, bound
+// by the selects' issue.  The code words come through shared memory, so that a
+// thread holds few of them and eight CTAs fit on an SM (words straight into
+// registers, five CTAs: 240 us, and 179 at 1 bit with six).  Levels per thread
+// instead of per group: 24 us against 18 for two 2-bit caches of 32 heads and
+// 2003 tokens, then.  CTAs that walk over tiles, 16 per SM, wait for each
+// tile's words with nothing else to do (219 us against 181, then).
 #include "common.cuh"
 
 namespace spc {
@@ -65,7 +68,7 @@ __device__ __forceinline__ uint32_t top_bits(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t pick(uint32_t mask, uint32_t yes, uint32_t no) { return (yes & mask) | (no & ~mask); }
 
 template <int BITS, int GROUP>
-__global__ void __launch_bounds__(256, BITS == 1 ? 6 : 5) dequantize_kernel(const __grid_constant__ ReadArgs a) {
+__global__ void __launch_bounds__(256, 8) dequantize_kernel(const __grid_constant__ ReadArgs a) {
   constexpr int kWords = GROUP == 32 ? 256 * (BITS + 1) : 512 * BITS + 256;  // of a record
   constexpr int kCodes = 128 * BITS;                                        // words of 32 tokens' codes
   constexpr int L = 1 << BITS;
@@ -93,17 +96,15 @@ __global__ void __launch_bounds__(256, BITS == 1 ? 6 : 5) dequantize_kernel(cons
   const uint32_t* rec = reinterpret_cast<const uint32_t*>(a.records) + (bh * (int64_t)a.units_cap + unit) * kWords;
   constexpr int kKeyMeta = GROUP / 32 * kCodes, kValueCodes = kKeyMeta + 128, kValueMeta = kValueCodes + kKeyMeta;
 
-  // ---- the levels, a group per thread, into shared memory; the code words are on their way meanwhile ----
+  // ---- the levels, a group per thread, into shared memory; the code words are copied there meanwhile ----
   __shared__ __align__(16) uint16_t klev[L][kD];  // of a channel
   __shared__ uint32_t vlev[L][128];               // of a token's group, twice in a word
   constexpr int kVGroups = kD / GROUP;            // groups of a token
-  uint32_t w[BITS][16];  // keys: words 4t + j of row a; values: eight words of each of two token pairs
+  __shared__ __align__(16) uint32_t codes[2][kCodes];  // keys', values'
+  if (tid < kCodes / 4)
+    cp_async16(codes[keys ? 0 : 1] + 4 * tid, rec + (keys ? 0 : kValueCodes) + half * kCodes + 4 * tid);
+  cp_async_commit();
   if (keys) {
-    const uint32_t* kc = rec + half * kCodes + 16 * row + (chunk >> 2);
-#pragma unroll
-    for (int p = 0; p < BITS; ++p)
-#pragma unroll
-      for (int t = 0; t < 4; ++t) w[p][t] = kc[128 * p + 4 * t];
     const int t = tid >> 5, m = tid & 31;  // word 32 t + m
     float lv[L];
     levels<BITS>(rec[kKeyMeta + tid], lv);
@@ -111,14 +112,6 @@ __global__ void __launch_bounds__(256, BITS == 1 ? 6 : 5) dequantize_kernel(cons
     for (int c = 0; c < L; ++c)
       klev[c][16 * (m >> 2) + 2 * t + 8 * ((m >> 1) & 1) + (m & 1)] = (uint16_t)read_pack(lv[c], lv[c]);
   } else {
-    // pair 8 r + row, tokens 8 j + 2 t + {0, 1} with t = row % 4, j = 2 r + row / 4
-    const uint32_t* vc = rec + kValueCodes + half * kCodes + 4 * (row & 3) + (row >> 2);
-#pragma unroll
-    for (int p = 0; p < BITS; ++p)
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int u = 0; u < 8; ++u) w[p][8 * r + u] = vc[128 * p + 16 * u + 2 * r];
     if (tid < 32 * kVGroups) {
       int token, group;
       if (GROUP == 32) {
@@ -136,6 +129,7 @@ __global__ void __launch_bounds__(256, BITS == 1 ? 6 : 5) dequantize_kernel(cons
       for (int c = 0; c < L; ++c) vlev[c][kVGroups * token + group] = read_pack(lv[c], lv[c]);
     }
   }
+  cp_async_wait<0>();
   __syncthreads();
 
   if (keys) {
@@ -149,11 +143,14 @@ __global__ void __launch_bounds__(256, BITS == 1 ? 6 : 5) dequantize_kernel(cons
       lev[c][2] = x.z;
       lev[c][3] = x.w;
     }
+    uint32_t w[BITS][4];  // words 4t + j of row a
 #pragma unroll
     for (int p = 0; p < BITS; ++p)
 #pragma unroll
-      for (int t = 0; t < 4; ++t)  // row 8n + a's two bits to n and 16 + n
-        w[p][t] = __funnelshift_l(w[p][t], w[p][t], 4 * (chunk & 3) + 21);
+      for (int t = 0; t < 4; ++t) {  // row 8n + a's two bits to n and 16 + n
+        const uint32_t x = codes[0][128 * p + 16 * row + 4 * t + (chunk >> 2)];
+        w[p][t] = __funnelshift_l(x, x, 4 * (chunk & 3) + 21);
+      }
     to += row * step;
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
@@ -176,7 +173,9 @@ __global__ void __launch_bounds__(256, BITS == 1 ? 6 : 5) dequantize_kernel(cons
     to += 2 * row * step;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
+      // tokens 8 j + 2 t + {0, 1} with t = row % 4, j = 2 r + row / 4
       const int first = 2 * (8 * r + row);  // the pair's first token
+      const uint32_t* vc = codes[1] + 4 * (row & 3) + (row >> 2) + 2 * r;
       uint32_t lev[2][L];
 #pragma unroll
       for (int x = 0; x < 2; ++x)
@@ -188,7 +187,7 @@ __global__ void __launch_bounds__(256, BITS == 1 ? 6 : 5) dequantize_kernel(cons
         uint32_t m[2][BITS];
 #pragma unroll
         for (int q = 0; q < BITS; ++q) {
-          const uint32_t x = w[q][8 * r + 2 * u] << (15 - chunk), y = w[q][8 * r + 2 * u + 1] << (15 - chunk);
+          const uint32_t x = vc[128 * q + 32 * u] << (15 - chunk), y = vc[128 * q + 32 * u + 16] << (15 - chunk);
           m[0][q] = top_bits<0xDD99>(x, y);  // the first token: bits chunk
           m[1][q] = top_bits<0xFFBB>(x, y);  // the second: bits 16 + chunk
         }
