@@ -479,13 +479,13 @@ def spc_prompt_attn(q, k, v, o, lse=None, q_begin=None, q_len=None, k_begin=None
     kb, kl = _words(fn, "k_begin", k_begin, i32, S, dev), _words(fn, "k_len", k_len, i32, S, dev)
     lse_ptr = None if lse is None else _words(fn, "lse", lse, torch.float32, q.numel() // max(q.shape[-1], 1), dev)
     s = _raw_stream(stream, dev)
+    own = None
     if ws is None:
         if stream is not None and s != _raw_stream(None, dev):
             raise ValueError(f"{fn}: a call on another stream than the current one needs ws")
         w, ws_bytes = None, _lib.spc_prompt_attn_workspace_bytes(d)
         if ws_bytes > 256:  # the keys are split; else the call needs none
-            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-            w = ws.data_ptr()
+            w = own = torch._C._cuda_cudaCachingAllocator_raw_alloc(ws_bytes, s)  # a tensor's allocation takes 3 us more
         else:
             ws_bytes = 0
     else:
@@ -494,8 +494,12 @@ def spc_prompt_attn(q, k, v, o, lse=None, q_begin=None, q_len=None, k_begin=None
         w = _ptr(ws)
         if ws_bytes is None:
             ws_bytes = ws.numel() * ws.element_size()
-    st = _lib.spc_prompt_attn(d, q.data_ptr(), k.data_ptr(), v.data_ptr(), qb, ql, kb, kl, o.data_ptr(), lse_ptr, w,
-                              ws_bytes, s)
+    try:
+        st = _lib.spc_prompt_attn(d, q.data_ptr(), k.data_ptr(), v.data_ptr(), qb, ql, kb, kl, o.data_ptr(), lse_ptr, w,
+                                  ws_bytes, s)
+    finally:
+        if own is not None:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(own)
     if st:
         raise SpcError(fn, st)
 

@@ -103,6 +103,8 @@ struct PromptArgs {
   int64_t v_b, v_t, v_h, o_b, o_t, o_h;
   int32_t S, Hq, Hkv, G, tile_tokens, pair_tokens, pairs, splits;
   int32_t q_tokens, k_tokens, q_max, k_max;
+  int32_t rounds, gap;           // of the last split's CTAs, and the stages that these cost more
+  uint32_t items;                // without splits
   int32_t dense;                 // items are numbered over the pairs that exist
   int32_t q_batched, k_batched;  // sequence s lies at s * stride (else on one token axis)
   float scale;
@@ -317,7 +319,8 @@ __device__ __forceinline__ int pairs_from(int p, const int* mine) {
   return __reduce_add_sync(0xFFFFFFFFu, n);
 }
 
-// Item i of all (a whole warp): split fastest, then KV head, then sequence,
+// Item i of all (a whole warp): split fastest (slowest where the last one is
+// shorter than the others, and so taken last), then KV head, then sequence,
 // then pair, later pairs (more keys) first.  CTAs that run together then read
 // different heads' keys at the same depth, and several pairs of a head share
 // them in L2.  Up to kDense sequences of different lengths are numbered over
@@ -327,8 +330,14 @@ template <int TILES>
 __device__ __forceinline__ bool prompt_item(const PromptArgs& a, uint32_t i, PromptItem& w) {
   constexpr int kKeys = Shape<TILES>::kKeys;
   const int lane = threadIdx.x & 31;
-  w.split = (int)(i % a.splits);
-  i /= a.splits;
+  w.split = 0;
+  if (a.rounds > 1) {
+    w.split = (int)(i / a.items);
+    i -= w.split * a.items;
+  } else if (a.splits > 1) {
+    w.split = (int)(i % a.splits);
+    i /= a.splits;
+  }
   w.hkv = (int)(i % a.Hkv);
   i /= a.Hkv;
   if (!a.dense) {
@@ -371,7 +380,12 @@ __device__ __forceinline__ bool prompt_item(const PromptArgs& a, uint32_t i, Pro
   const int most = w.tok0 < w.lq ? clampi(last + w.lk - w.lq + 1, 0, w.lk) : 0;
   const int least = clampi(w.tok0 + w.lk - w.lq + 1, 0, w.lk);
   const int n = (most + kKeys - 1) / kKeys;
-  const int per = (n + a.splits - 1) / a.splits;
+  int per = n;
+  if (a.splits > 1) per = (n + a.splits - 1) / a.splits;
+  if (a.rounds > 1) {  // `rounds` of the last split take the time of one of the others
+    const int large = a.splits - 1, small = max(0, n - large * a.gap) / (large * a.rounds + 1);
+    per = (n - small + large - 1) / large;
+  }
   w.lo = min(w.split * per, n);
   w.hi = min(w.lo + per, n);
   const int last0 = min(w.tok0 + a.tile_tokens, w.lq) - 1, most0 = min(most, clampi(last0 + w.lk - w.lq + 1, 0, w.lk));
@@ -873,17 +887,24 @@ bool encode_map(CUtensorMap* map, const uint16_t* p, int64_t batch, int64_t toke
 // measurements): an item costs its start and output and its 64-key blocks; a
 // block takes what its products take, or its 32 KB at the rate of HBM where
 // one tile streams them.  Items of one sequence within the CTAs' places end
-// together; others are taken as they come (sequences may be shorter than
-// k_max, so rounds are not counted on), and the last one ends alone.  A split's partial results are written and read back,
-// and joined in a launch of their own.  Measured against it: one token over
+// together; where one split more would not fit, it is made so short that the
+// places left over take all items' in a few rounds by the time the others end.
+// Items of several sequences are taken as they come (these may be shorter than
+// k_max, so rounds are not counted on), and the last one ends alone.  A
+// split's partial results are written and read back, and joined in a launch of
+// their own.  Measured against it: one token over
 // 32768 keys 391 us in one piece, 106 in 4, 43 in 14, 38 in 28 and 41 in 38;
 // eight over up to 32768 keys 206 in 2, 135 in 4, 108 in 7 and in 14, 120 in
-// 28; 500 tokens over 32768 keys 373 in one, 205 in 2, 277 in 3, 213 in 7 and
-// 267 in 14; a 1024-token prompt 23 in one and 43 in 2.
+// 28; 500 tokens over 32768 keys 373 in one, 202 in 2, 277 in 3 equal ones, 181
+// in 3 of which the last takes a third of the others' time, 213 in 7 and 267
+// in 14; 800 over 16384 191 in one and 163 in 2 so; a 1024-token prompt 23 in
+// one and 43 in 2.
 constexpr int kMaxSplits = 64;
 
+int64_t ceil_div(int64_t x, int64_t y) { return (x + y - 1) / y; }
+
 struct PromptGrid {
-  int tiles, tile_tokens, pair_tokens, pairs, splits;
+  int tiles, tile_tokens, pair_tokens, pairs, splits, rounds, gap;
   int64_t items;
 };
 
@@ -897,7 +918,8 @@ PromptGrid prompt_grid(const spc_prompt_dims* d) {
   int64_t all = (int64_t)d->S * g.pairs;
   if (d->q.b == 0 && d->S <= kDense) all = std::min(all, d->S + (int64_t)d->q_tokens / g.pair_tokens);
   g.items = all * d->Hkv;
-  g.splits = 1;
+  g.splits = g.rounds = 1;
+  g.gap = 0;
   const int64_t places = spc_host::sm_count() * (g.tiles == 1 ? 2 : 1);
   const int64_t blocks = ((int64_t)d->k_max + kBlock - 1) / kBlock;
   const int64_t rows = (int64_t)d->S * d->q_max * d->Hq;
@@ -906,12 +928,23 @@ PromptGrid prompt_grid(const spc_prompt_dims* d) {
   for (int64_t z = 1; z <= std::max<int64_t>(1, std::min<int64_t>(blocks / 4, kMaxSplits)); ++z) {
     const int64_t busy = std::min(g.items * z, places), share = (blocks + z - 1) / z, start = 4000;
     const int64_t alone = g.tiles == 2 ? 690 : 760, block = g.tiles == 2 ? 690 : std::max<int64_t>(760, busy * 5);
-    int64_t cost = d->S == 1 && g.items * z <= places ? share * block + start
-                                                      : g.items * (blocks * block + z * start) / places + share * alone;
+    int64_t cost = g.items * (blocks * block + z * start) / places + share * alone, rounds = 1;
+    if (d->S == 1 && g.items * z <= places) {
+      cost = share * block + start;
+    } else if (d->S == 1 && g.items * (z - 1) < places) {
+      const int64_t r = ceil_div(g.items, places - g.items * (z - 1));
+      const int64_t small = (blocks - (z - 1) * (r - 1) * (start / block)) / ((z - 1) * r + 1);
+      if (small >= 4) {
+        cost = ceil_div(blocks - small, z - 1) * block + start;
+        rounds = r;
+      }
+    }
     if (z > 1) cost += 3000 + z * rows / 5;
     if (z == 1 || cost < best) {
       best = cost;
       g.splits = (int)z;
+      g.rounds = (int)rounds;
+      g.gap = (int)((rounds - 1) * (start / block) * kBlock / (g.tiles == 2 ? Shape<2>::kKeys : Shape<1>::kKeys));
     }
   }
   return g;
@@ -974,6 +1007,9 @@ spc_status launch_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const
   // one pair each is numbered as it is: an empty sequence costs no more than looking for the others would
   a.dense = (q_len != nullptr || q_begin != nullptr) && d->S > 1 && d->S <= kDense && g.pairs > 1;
   a.splits = g.splits;
+  a.rounds = g.rounds;
+  a.items = (uint32_t)g.items;
+  a.gap = g.gap;
   a.fault = static_cast<uint32_t*>(ws);
   a.part_rows = (int64_t)d->S * d->q_max * d->Hq;
   if (a.splits > 1) {

@@ -53,6 +53,20 @@ def test_one_sequence(lq, lk, Hq, Hkv):
     check(o, lse, q, k, v)
 
 
+@pytest.mark.parametrize("lq,lk,most,Hq,Hkv", [(1300, 4096, 4096, 16, 16), (1300, 4031, 4096, 16, 16),
+                                               (1300, 1700, 4096, 16, 16), (1300, 900, 4096, 16, 16),
+                                               (1300, 0, 4096, 16, 16), (333, 12000, 12000, 28, 4)])
+def test_a_last_split_shorter_than_the_others(lq, lk, most, Hq, Hkv):
+    """More items than half of the SMs: on 152, two to four splits of which the last ones run in turn."""
+    import bit_kv_cache_spc_gb300 as spc
+    q, k, v = rnd(1, lq, Hq, D), rnd(2, most, Hkv, D), rnd(3, most, Hkv, D)
+    k[lk:], v[lk:] = math.nan, math.nan
+    o = torch.full((lq, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((lq, Hq), 7.0, device="cuda")
+    spc.spc_prompt_attn(q, k, v, o, lse, k_len=i32([lk]))
+    check(o, lse, q, k[:lk], v[:lk])
+
+
 @pytest.mark.parametrize("lq,lk,G", [(1, 0, 2), (7, 0, 2), (9, 4, 2), (300, 130, 2), (140, 1, 2), (1300, 1100, 2),
                                      (256, 100, 1), (256, 128, 1), (300, 290, 1), (600, 345, 1), (200, 72, 1)])
 def test_rows_that_see_nothing(lq, lk, G):
