@@ -16,9 +16,9 @@
 // values in masked places (below).
 // Two tiles (256 rows) share every K and V stage, 128 keys each: prompts,
 // bound by the tensor cores.  One tile, where a sequence's rows fit into it
-// (single tokens, short turns: bound by the bytes of K and V): half the TMEM
-// and shared memory, 64 keys a stage, so that two CTAs share an SM and one's
-// start and output overlap the other's copies.
+// (single tokens, short turns: bound by the bytes of K and V) and for short
+// prompts: half the TMEM and shared memory, 64 keys a stage, so that two CTAs
+// share an SM and one's start and output overlap the other's copies.
 // Why two S blocks per tile: with one block of 128 keys the softmax of a tile
 // and its products alternate, and each turn pays the barriers' and the
 // loads' latencies (3860 cycles for 2 x 128 keys, of which the tensor cores
@@ -879,9 +879,11 @@ bool encode_map(CUtensorMap* map, const uint16_t* p, int64_t batch, int64_t toke
 }
 
 // Grid of a call.  One query tile per CTA where every sequence's rows fit into
-// it, else two; the items without splits that there can be (packed sequences
-// share the tokens of one axis); and splits of the keys where these do not
-// fill the GPU.
+// it, or where the keys are few and the tiles not more than the SMs (a 50-token
+// prompt of 32 and 8 heads 6.8 us, two tiles 7.8; 300 tokens 10.0 and 10.4, 600
+// the same; 300 after a history of 1700 27.9 and 23.0), else two; the items
+// without splits that there can be (packed sequences share the tokens of one
+// axis); and splits of the keys where these do not fill the GPU.
 //
 // The number of splits is the one for which this estimate is least (in ns, of
 // measurements): an item costs its start and output and its 64-key blocks; a
@@ -912,12 +914,16 @@ PromptGrid prompt_grid(const spc_prompt_dims* d) {
   PromptGrid g;
   const int G = d->Hq / d->Hkv;
   g.tile_tokens = kTile / G;
-  g.tiles = d->q_max <= g.tile_tokens ? 1 : 2;
-  g.pair_tokens = g.tiles * g.tile_tokens;
-  g.pairs = (d->q_max + g.pair_tokens - 1) / g.pair_tokens;
-  int64_t all = (int64_t)d->S * g.pairs;
-  if (d->q.b == 0 && d->S <= kDense) all = std::min(all, d->S + (int64_t)d->q_tokens / g.pair_tokens);
-  g.items = all * d->Hkv;
+  const auto count = [&](int tiles) {
+    g.tiles = tiles;
+    g.pair_tokens = tiles * g.tile_tokens;
+    g.pairs = (d->q_max + g.pair_tokens - 1) / g.pair_tokens;
+    int64_t all = (int64_t)d->S * g.pairs;
+    if (d->q.b == 0 && d->S <= kDense) all = std::min(all, d->S + (int64_t)d->q_tokens / g.pair_tokens);
+    g.items = all * d->Hkv;
+  };
+  count(1);
+  if (g.pairs > 1 && (d->k_max > 512 || g.items > spc_host::sm_count())) count(2);
   g.splits = g.rounds = 1;
   g.gap = 0;
   const int64_t places = spc_host::sm_count() * (g.tiles == 1 ? 2 : 1);
