@@ -303,20 +303,56 @@ __device__ __forceinline__ void sequence(const PromptArgs& a, int s, int& lq, in
   lk = clampi(a.k_len ? a.k_len[s] : a.k_max, 0, min(a.k_max, a.k_tokens - kb));
 }
 
-// CTAs that a sequence's query rows take ("pairs", of one or two tiles).
-__device__ __forceinline__ int sequence_pairs(const PromptArgs& a, int s) {
-  int lq, lk, qb, kb;
-  sequence(a, s, lq, lk, qb, kb);
-  return (lq + a.pair_tokens - 1) / a.pair_tokens;
-}
-
-// Sum over the sequences of the pairs from pair p on (a whole warp; lane l has
-// sequences l, l + 32, ... in mine).
-__device__ __forceinline__ int pairs_from(int p, const int* mine) {
-  int n = 0;
+// Item k of those that exist, numbered over the pairs of up to 32 * N
+// sequences (a whole warp; lane l looks after sequences l, l + 32, ...): later
+// pairs first, then the sequences that have the pair.  False for none.
+template <int N>
+__device__ __forceinline__ bool dense_item(const PromptArgs& a, int k, PromptItem& w) {
+  const int lane = threadIdx.x & 31;
+  int lq, lk, qb, kb, mine[N];
 #pragma unroll
-  for (int u = 0; u < kDense / 32; ++u) n += max(0, mine[u] - p);
-  return __reduce_add_sync(0xFFFFFFFFu, n);
+  for (int u = 0; u < N; ++u) {
+    lq = 0;
+    if (32 * u + lane < a.S) sequence(a, 32 * u + lane, lq, lk, qb, kb);
+    mine[u] = (lq + a.pair_tokens - 1) / a.pair_tokens;
+  }
+  const auto pairs_from = [&](int p) {  // sum over the sequences of the pairs from pair p on
+    int n = 0;
+#pragma unroll
+    for (int u = 0; u < N; ++u) n += max(0, mine[u] - p);
+    return __reduce_add_sync(0xFFFFFFFFu, n);
+  };
+  if (pairs_from(0) <= k) return false;
+  int lo = 0, hi = a.pairs, behind = 0;  // pairs_from(lo) > k >= pairs_from(hi) = behind
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2, n = pairs_from(mid);
+    if (n > k) {
+      lo = mid;
+    } else {
+      hi = mid;
+      behind = n;
+    }
+  }
+  w.pair = lo;
+  w.s = 0;
+  k -= behind;  // the k-th sequence that has this pair
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    const bool has = mine[u] > lo;
+    const uint32_t who = __ballot_sync(0xFFFFFFFFu, has);
+    const uint32_t it = __ballot_sync(0xFFFFFFFFu, has && __popc(who & ((1u << lane) - 1u)) == k);
+    if (it != 0u) w.s = 32 * u + __ffs((int)it) - 1;
+    k -= __popc(who);  // negative once found
+  }
+  if (N == 1) {  // the lane has them
+    w.lq = __shfl_sync(0xFFFFFFFFu, lq, w.s);
+    w.lk = __shfl_sync(0xFFFFFFFFu, lk, w.s);
+    w.qb = __shfl_sync(0xFFFFFFFFu, qb, w.s);
+    w.kb = __shfl_sync(0xFFFFFFFFu, kb, w.s);
+  } else {
+    sequence(a, w.s, w.lq, w.lk, w.qb, w.kb);
+  }
+  return true;
 }
 
 // Item i of all (a whole warp): split fastest (slowest where the last one is
@@ -329,7 +365,6 @@ __device__ __forceinline__ int pairs_from(int p, const int* mine) {
 template <int TILES>
 __device__ __forceinline__ bool prompt_item(const PromptArgs& a, uint32_t i, PromptItem& w) {
   constexpr int kKeys = Shape<TILES>::kKeys;
-  const int lane = threadIdx.x & 31;
   w.split = 0;
   if (a.rounds > 1) {
     w.split = (int)(i / a.items);
@@ -344,35 +379,10 @@ __device__ __forceinline__ bool prompt_item(const PromptArgs& a, uint32_t i, Pro
     w.s = (int)(i % a.S);
     w.pair = a.pairs - 1 - (int)(i / a.S);
     if (w.pair < 0) return false;
-  } else {
-    int mine[kDense / 32];
-#pragma unroll
-    for (int u = 0; u < kDense / 32; ++u) mine[u] = 32 * u + lane < a.S ? sequence_pairs(a, 32 * u + lane) : 0;
-    const int k0 = (int)i;
-    int lo = 0, hi = a.pairs, behind = 0;  // pairs_from(lo) > k0 >= pairs_from(hi) = behind
-    if (pairs_from(0, mine) <= k0) return false;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2, n = pairs_from(mid, mine);
-      if (n > k0) {
-        lo = mid;
-      } else {
-        hi = mid;
-        behind = n;
-      }
-    }
-    w.pair = lo;
-    int k = k0 - behind;  // the k-th sequence that has this pair
-    w.s = 0;
-#pragma unroll
-    for (int u = 0; u < kDense / 32; ++u) {
-      const bool has = mine[u] > lo;
-      const uint32_t who = __ballot_sync(0xFFFFFFFFu, has);
-      const uint32_t it = __ballot_sync(0xFFFFFFFFu, has && __popc(who & ((1u << lane) - 1u)) == k);
-      if (it != 0u) w.s = 32 * u + __ffs((int)it) - 1;
-      k -= __popc(who);  // negative once found
-    }
+    sequence(a, w.s, w.lq, w.lk, w.qb, w.kb);
+  } else if (!(a.S <= 32 ? dense_item<1>(a, (int)i, w) : dense_item<kDense / 32>(a, (int)i, w))) {
+    return false;
   }
-  sequence(a, w.s, w.lq, w.lk, w.qb, w.kb);
   if (w.pair * a.pair_tokens >= w.lq) return false;
   w.tok0 = w.pair * a.pair_tokens;
   w.two = TILES == 2 && w.tok0 + a.tile_tokens < w.lq;
