@@ -389,9 +389,12 @@ spc_status launch_extend(const spc_dims* d, int32_t n, const uint16_t* k_new, co
   a.total_groups = BH * ((a.nq1 - a.nq) / d->group);
   if (a.total_groups > 0x7FFFFFFF) return SPC_ERR_UNSUPPORTED;
   // One launch where a cluster's CTAs have a group each at most and hold the
-  // window; else the groups first, over all SMs, then the window.
+  // window, and the clusters are on the SMs together (5 CTAs each); else the
+  // groups first, over all SMs, then the window.  200 tokens into 8 caches of
+  // 8 KV heads: 6.9 us and 6.8, 16: 11.2 and 8.9, 64: 32.8 and 27.0; 77 tokens
+  // 5.3 and 8.5, 7.6 and 8.9, 24.2 and 24.5.
   const bool turn = a.total_groups > 0 && a.total_groups <= BH * kTurnCtas && a.N + n - a.nq1 <= kTurnRows &&
-                    BH <= 0x0FFFFFFF;
+                    BH * kTurnCtas <= (int64_t)spc_host::sm_count() * 5;
   cudaError_t e = cudaSuccess;
   if (a.total_groups > 0) {
     if (d->bits == 1)

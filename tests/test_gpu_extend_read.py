@@ -106,6 +106,21 @@ def test_runs_match_the_oracle(R, group, runs, bits):
         c.check(K[:, :, :at], V[:, :, :at])
 
 
+@pytest.mark.parametrize("bits,group", [(1, 32), (2, 64)])
+def test_runs_of_many_heads_match_the_oracle(bits, group):
+    """More (b, KV head) pairs than a single launch takes: old rows move after the groups' own launch."""
+    B, Hkv, runs = 13, 8, [150, 20, 70, 1, 200]
+    K, V = synth.kv_layer(6, bits, B, Hkv, sum(runs))
+    c = Cache(B, Hkv, sum(runs), 70, bits, group, host=True)
+    at = 0
+    for n in runs:
+        k, v = (dev16(np.ascontiguousarray(x[:, :, at:at + n])).transpose(1, 2) for x in (K, V))
+        c.extend(k, v)
+        torch.cuda.synchronize()
+        at += n
+    c.check(K, V)
+
+
 @pytest.mark.parametrize("bits", [1, 2])
 @pytest.mark.parametrize("group", [32, 64])
 def test_edge_values(bits, group):
