@@ -809,10 +809,18 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
 }
 
 // Joins the splits of a row: o = sum_z 2^(m_z - m) o_z / sum_z 2^(m_z - m) l_z,
-// in the order of the splits.  One warp per row (sequence in blockIdx.y), four
-// channels a lane; lane z holds split z's maximum and sum (two each past 32).
+// in a fixed order.  WARPS warps per row (sequence in blockIdx.y), each with
+// eight splits at a time, four channels a lane; lane z holds split z's maximum
+// and sum (two each past 32).  Four warps where there are more than eight
+// splits, whose loads then take one or two turns, and the rows' CTAs fit on
+// the SMs (7 each) at once: one token over 32768 keys 33.4 us against 34.9,
+// over 8000 14.0 and 16.2, 16 over 4000 12.3 and 12.8; but 64 over 32768 40.4
+// and 38.4.
+template <int WARPS>
 __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant__ PromptArgs a) {
-  const int row = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31, s = blockIdx.y;
+  __shared__ float4 parts[WARPS][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, s = blockIdx.y;
+  const int row = WARPS == 1 ? blockIdx.x * 4 + warp : blockIdx.x, part = WARPS == 1 ? 0 : warp;
   const int tok = row / a.Hq, head = row - tok * a.Hq;
   int lq, lk, qb, kb;
   sequence(a, s, lq, lk, qb, kb);
@@ -825,27 +833,44 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant_
     const int z = lane + 32 * u;
     ml[u] = z < a.splits ? a.part_ml[part_place(a, z, s, tok, head)] : make_float2(-INFINITY, 0.f);
   }
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f), x[8];
+  const auto load = [&](int z0) {  // eight splits' loads in flight
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (z0 + u < a.splits)
+        x[u] = reinterpret_cast<const float4*>(a.part_o + part_place(a, z0 + u, s, tok, head) * kD)[lane];
+  };
+  load(8 * part);
   float m = fmaxf(ml[0].x, ml[1].x);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
   float f[2], l = 0.f;
 #pragma unroll
-  for (int u = 0; u < 2; ++u) f[u] = ml[u].y == 0.f ? 0.f : exp2f(ml[u].x - m);  // a sum of 0: nothing visible there
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int z0 = 0; z0 < a.splits; z0 += 8) {  // eight splits' loads in flight
-    float4 x[8];
+  for (int u = 0; u < 2; ++u) {
+    f[u] = ml[u].y == 0.f ? 0.f : exp2f(ml[u].x - m);  // a sum of 0: nothing visible there
+    l += f[u] * ml[u].y;
+  }
 #pragma unroll
-    for (int u = 0; u < 8; ++u)
-      if (z0 + u < a.splits)
-        x[u] = reinterpret_cast<const float4*>(a.part_o + part_place(a, z0 + u, s, tok, head) * kD)[lane];
+  for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, off);
+  for (int z0 = 8 * part; z0 < a.splits; z0 += 8 * WARPS) {
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int z = z0 + u;
       const float g = __shfl_sync(0xFFFFFFFFu, z < 32 ? f[0] : f[1], z & 31);
       const float sum = __shfl_sync(0xFFFFFFFFu, z < 32 ? ml[0].y : ml[1].y, z & 31);
       if (z >= a.splits || sum == 0.f) continue;
-      l += g * sum;
       o = make_float4(o.x + g * x[u].x, o.y + g * x[u].y, o.z + g * x[u].z, o.w + g * x[u].w);
+    }
+    load(z0 + 8 * WARPS);
+  }
+  if (WARPS > 1) {
+    parts[warp][lane] = o;
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int u = 1; u < WARPS; ++u) {
+      const float4 p = parts[u][lane];
+      o = make_float4(o.x + p.x, o.y + p.y, o.z + p.z, o.w + p.w);
     }
   }
   const float inv = any ? 1.f / l : 0.f;
@@ -1049,12 +1074,14 @@ spc_status launch_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(((int64_t)d->q_max * d->Hq + 3) / 4), (unsigned)d->S);
+    const int64_t rows = (int64_t)d->q_max * d->Hq;
+    const bool wide = a.splits > 8 && rows * d->S <= (int64_t)spc_host::sm_count() * 7;
+    cfg.gridDim = dim3((unsigned)(wide ? rows : (rows + 3) / 4), (unsigned)d->S);
     cfg.blockDim = dim3(128);
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, prompt_join_kernel, a);
+    e = cudaLaunchKernelEx(&cfg, wide ? prompt_join_kernel<4> : prompt_join_kernel<1>, a);
   }
   if (e != cudaSuccess) {
     spc_host::set_cuda_error(e);
