@@ -926,13 +926,14 @@ bool encode_map(CUtensorMap* map, const uint16_t* p, int64_t batch, int64_t toke
 // one tile streams them.  Items of one sequence within the CTAs' places end
 // together; where one split more would not fit, it is made so short that the
 // places left over take all items' in a few rounds by the time the others end.
-// Items of several sequences are taken as they come (these may be shorter than
-// k_max, so rounds are not counted on), and the last one ends alone.  A
-// split's partial results are written and read back, and joined in a launch of
-// their own.  Measured against it: one token over
-// 32768 keys 391 us in one piece, 106 in 4, 43 in 14, 38 in 28 and 41 in 38;
-// eight over up to 32768 keys 206 in 2, 135 in 4, 108 in 7 and in 14, 120 in
-// 28; 500 tokens over 32768 keys 373 in one, 202 in 2, 277 in 3 equal ones, 181
+// Items of several sequences are taken as they come (these are taken to be a
+// little more than half as long as k_max, so rounds are not counted on), and
+// the last one ends alone.  A split's partial results are written and read
+// back, and joined in a launch of their own.  Measured against it: one token
+// over 32768 keys 391 us in one piece, 106 in 4, 43 in 14, 38 in 28 and 41 in
+// 38, over 500 keys 11.7 in one, 9.3 in 4 and 8.7 in 8; eight over up to 32768
+// keys 206 in 2, 135 in 4, 108 in 7 and in 14, 120 in 28; 64 over up to 8000
+// 209 in one, 184 in 3 and 200 in 8; 500 tokens over 32768 keys 373 in one, 202 in 2, 277 in 3 equal ones, 181
 // in 3 of which the last takes a third of the others' time, 213 in 7 and 267
 // in 14; 800 over 16384 191 in one and 163 in 2 so; a 1024-token prompt 23 in
 // one and 43 in 2.
@@ -964,12 +965,14 @@ PromptGrid prompt_grid(const spc_prompt_dims* d) {
   const int64_t places = spc_host::sm_count() * (g.tiles == 1 ? 2 : 1);
   const int64_t blocks = ((int64_t)d->k_max + kBlock - 1) / kBlock;
   const int64_t rows = (int64_t)d->S * d->q_max * d->Hq;
-  if (g.items >= places) return g;
+  if (g.items >= places && (g.tiles == 2 || d->S == 1)) return g;
   int64_t best = 0;
-  for (int64_t z = 1; z <= std::max<int64_t>(1, std::min<int64_t>(blocks / 4, kMaxSplits)); ++z) {
+  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(blocks / g.tiles, kMaxSplits));
+  for (int64_t z = 1; z <= most; ++z) {
     const int64_t busy = std::min(g.items * z, places), share = (blocks + z - 1) / z, start = 4000;
     const int64_t alone = g.tiles == 2 ? 690 : 760, block = g.tiles == 2 ? 690 : std::max<int64_t>(760, busy * 5);
-    int64_t cost = g.items * (blocks * block + z * start) / places + share * alone, rounds = 1;
+    const int64_t whole = d->S == 1 ? blocks * block : blocks * block * 11 / 20;
+    int64_t cost = g.items * (whole + z * start) / places + share * alone, rounds = 1;
     if (d->S == 1 && g.items * z <= places) {
       cost = share * block + start;
     } else if (d->S == 1 && g.items * (z - 1) < places) {
