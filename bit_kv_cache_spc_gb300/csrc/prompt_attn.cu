@@ -965,25 +965,27 @@ PromptGrid prompt_grid(const spc_prompt_dims* d) {
   const int64_t places = spc_host::sm_count() * (g.tiles == 1 ? 2 : 1);
   const int64_t blocks = ((int64_t)d->k_max + kBlock - 1) / kBlock;
   const int64_t rows = (int64_t)d->S * d->q_max * d->Hq;
-  if (g.items >= places && (g.tiles == 2 || d->S == 1)) return g;
-  int64_t best = 0;
+  // (the join numbers sequences in the grid's second dimension)
+  if (g.items >= places && (g.tiles == 2 || d->S == 1 || d->S > 65535)) return g;
+  double best = 0.0;
   const int64_t most = std::max<int64_t>(1, std::min<int64_t>(blocks / g.tiles, kMaxSplits));
   for (int64_t z = 1; z <= most; ++z) {
     const int64_t busy = std::min(g.items * z, places), share = (blocks + z - 1) / z, start = 4000;
     const int64_t alone = g.tiles == 2 ? 690 : 760, block = g.tiles == 2 ? 690 : std::max<int64_t>(760, busy * 5);
     const int64_t whole = d->S == 1 ? blocks * block : blocks * block * 11 / 20;
-    int64_t cost = g.items * (whole + z * start) / places + share * alone, rounds = 1;
+    double cost = (double)g.items * (double)(whole + z * start) / (double)places + (double)(share * alone);
+    int64_t rounds = 1;
     if (d->S == 1 && g.items * z <= places) {
-      cost = share * block + start;
+      cost = (double)(share * block + start);
     } else if (d->S == 1 && g.items * (z - 1) < places) {
       const int64_t r = ceil_div(g.items, places - g.items * (z - 1));
       const int64_t small = (blocks - (z - 1) * (r - 1) * (start / block)) / ((z - 1) * r + 1);
       if (small >= 4) {
-        cost = ceil_div(blocks - small, z - 1) * block + start;
+        cost = (double)(ceil_div(blocks - small, z - 1) * block + start);
         rounds = r;
       }
     }
-    if (z > 1) cost += 3000 + z * rows / 5;
+    if (z > 1) cost += 3000.0 + (double)(z * rows) / 5.0;
     if (z == 1 || cost < best) {
       best = cost;
       g.splits = (int)z;

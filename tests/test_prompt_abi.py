@@ -164,6 +164,14 @@ def test_prompt_attn_workspace_grows_where_the_keys_are_split():
     assert _lib.spc_prompt_attn_workspace_bytes(C.byref(one)) > 256
 
 
+def test_prompt_attn_splits_no_more_sequences_than_a_grid_numbers():
+    """Single tokens over one shared, very long row of keys: 65535 sequences may be split, 65536 are not."""
+    for S, split in ((65535, True), (65536, False)):
+        d = prompt_dims(S=S, Hq=1, Hkv=1, q_tokens=S, q_max=1, k_tokens=1 << 29, k_max=1 << 29, q=lay(0, 128, 128),
+                        o=lay(0, 128, 128), k=lay(0, 128, 128), v=lay(0, 128, 128))
+        assert (_lib.spc_prompt_attn_workspace_bytes(C.byref(d)) > 256) == split
+
+
 # ------------------------------------------------------------------------------------------------ the cache
 def cache_call(fn, d=None, n=10, k=1 << 32, v=1 << 33, lk=None, lv=None, records=4096, resid=1 << 24, first=0, host=None,
                n_cap=0):
