@@ -100,11 +100,11 @@ __device__ __forceinline__ float code_threshold(float lo, float hi, float z, flo
 }
 
 // Whether an x with d = fl(x - z) has a code of at least `level`, for s in
-// [2^-100, 2^100], without the quotient.  fl(d / s) is above 1/2 exactly when
-// 2 d > s; at least 3/2 when d / s >= 3/2 - 2^-24 and above 5/2 when d / s >
-// 5/2 + 2^-23 (the ties at those half steps round to the even 3/2 and 5/2).  Both sides of those comparisons are multiples of half an ulp of s
-// and, where they are close, a few of them, so one rounding decides them
-// exactly.
+// [2^-100, 2^100], without the quotient.  fl(d / s) is above 1/2 exactly when 2
+// d > s; at least 3/2 when d / s >= 3/2 - 2^-24 and above 5/2 when d / s > 5/2
+// + 2^-23 (the ties at those half steps round to the even 3/2 and 5/2).  Both
+// sides of those comparisons are multiples of half an ulp of s and, where they
+// are close, a few of them, so one rounding decides them exactly.
 template <int BITS>
 __device__ __forceinline__ bool code_reaches(float d, float s, int level) {
   if (BITS == 1 || level == 1) return __fadd_rn(d, d) > s;
