@@ -24,8 +24,8 @@ __all__ = [
     "spc_host_gather", "spc_merged_attn_noalloc", "spc_merged_attn_fetch", "spc_attn_kernel_count",
     "spc_decode_step_kernel_count", "spc_decode_step_on_chip", "spc_decode_step", "spc_step_workspace_bytes",
     "spc_read_device_status", "spc_append_kv", "spc_offload_kv", "spc_rope_frequencies", "spc_rope",
-    "spc_prompt_attn", "spc_prompt_attn_workspace_bytes", "spc_prompt_attn_status", "spc_extend_kv",
-    "spc_dequantize_kv", "lib_path",
+    "spc_prompt_attn", "spc_prompt_attn_workspace_bytes", "spc_prompt_attn_status",
+    "spc_prompt_attn_wait_limit", "spc_extend_kv", "spc_dequantize_kv", "lib_path",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -130,6 +130,7 @@ _sig = {
     "spc_prompt_attn_workspace_bytes": (C.c_size_t, [_P]),
     "spc_prompt_attn": (C.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, C.c_size_t, _P]),
     "spc_prompt_attn_status": (C.c_int, [_P, _P]),
+    "spc_prompt_attn_wait_limit": (C.c_int64, [C.c_int64]),
     "spc_extend_kv": (C.c_int, [_D, C.c_int32, _P, _P, _P, _P, _P, _P, _P, C.c_int64, _P]),
     "spc_dequantize_kv": (C.c_int, [_D, _P, _P, C.c_int32, C.c_int32, _P, _P, _P, _P, _P]),
 }
@@ -507,6 +508,11 @@ def spc_prompt_attn(q, k, v, o, lse=None, q_begin=None, q_len=None, k_begin=None
 def spc_prompt_attn_status(ws, stream=None) -> int:
     """0, or SPC_ERR_TIMEOUT (6) if a bounded wait in spc_prompt_attn ran out (the word is cleared)."""
     return int(_lib.spc_prompt_attn_status(_ptr(ws), _stream(stream)))
+
+
+def spc_prompt_attn_wait_limit(ns=0) -> int:
+    """The limit in ns of a wait in spc_prompt_attn's kernels before this call; ns > 0 sets it for the calls to come."""
+    return int(_lib.spc_prompt_attn_wait_limit(int(ns)))
 
 
 def _cache_call(fn, d, names, k, v, records, resid):

@@ -50,6 +50,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 
 #include "common.cuh"
@@ -100,6 +101,7 @@ struct PromptArgs {
   float2* part_ml;  // and their (maximum, sum)
   int64_t part_rows;
   uint32_t* fault;
+  uint64_t limit;   // of a wait, in ns
   int64_t v_b, v_t, v_h, o_b, o_t, o_h;
   int32_t S, Hq, Hkv, G, tile_tokens, pair_tokens, pairs, splits;
   int32_t q_tokens, k_tokens, q_max, k_max;
@@ -131,6 +133,10 @@ struct __align__(16) PromptBars {
   // per query tile and S buffer: block i's scores are there, and so is the product of block i - 2's weights
   uint64_t s_full[2][2];
   uint64_t p_full[2][2];  // its weights are
+  uint64_t drained[2];    // after a wait that ran out: the tile's products have ended
+  uint64_t limit;         // of a wait, in ns
+  uint32_t* fault;        // where one that runs out is reported, or null
+  int filled;             // stages copied in all
   uint32_t tmem;
   uint32_t bad;            // a masked stage held a non-finite value
   volatile uint32_t stop;  // a wait ran out
@@ -156,9 +162,9 @@ __device__ __forceinline__ bool mbar_try(uint64_t* b, uint32_t parity) {
   return ok != 0;
 }
 // Waits for the phase; false once this or another wait of the CTA has run out
-// (two seconds; the longest regular wait is far below a millisecond).
-// The timer is read only after many tries: reading it takes longer than a
-// regular wait.
+// (two seconds unless the caller sets another limit).  The thread whose wait
+// runs out reports it: no other has to be there still to see it.  The timer is
+// read only after many tries: reading it takes longer than a regular wait.
 __device__ __forceinline__ bool mbar_wait(PromptBars& bars, uint64_t* b, uint32_t parity) {
   for (int i = 0; i < 64; ++i)
     if (mbar_try(b, parity)) return true;
@@ -169,11 +175,22 @@ __device__ __forceinline__ bool mbar_wait(PromptBars& bars, uint64_t* b, uint32_
       if (mbar_try(b, parity)) return true;
     if (bars.stop) return false;
     asm volatile("mov.u64 %0, %%globaltimer;\n" : "=l"(now));
-    if (now - start > 2000000000ull) {
+    if (now - start > bars.limit) {
+      if (bars.fault != nullptr) *(volatile uint32_t*)bars.fault = 1u;
       bars.stop = 1u;
       return false;
     }
   }
+}
+
+// After a wait that ran out: waits, for a second at most, for a phase that work in flight completes by itself.
+__device__ __forceinline__ void mbar_drain(uint64_t* b, uint32_t parity) {
+  uint64_t start, now;
+  asm volatile("mov.u64 %0, %%globaltimer;\n" : "=l"(start));
+  do {
+    if (mbar_try(b, parity)) return;
+    asm volatile("mov.u64 %0, %%globaltimer;\n" : "=l"(now));
+  } while (now - start < 1000000000ull);
 }
 
 // For a whole warp: one outcome for all lanes.
@@ -473,9 +490,14 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         mbar_init(&bars.kv_free[i], TILES);
         mbar_init(&bars.v_clean[i], H::kThreads / 32 - H::kScanWarp);
       }
-      for (int i = 0; i < 2; ++i) mbar_init(&bars.v_scan[i], 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&bars.v_scan[i], 1);
+        mbar_init(&bars.drained[i], 1);
+      }
       bars.bad = 0;
       bars.stop = 0;
+      bars.limit = a.limit;
+      bars.fault = a.fault;
       asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
     }
@@ -533,6 +555,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
           ok = load_kv(w, &vmap, j);
           if (ok && j + H::kAhead < n) ok = load_kv(w, &kmap, j + H::kAhead);
         }
+        bars.filled = x;
       }
     } else if (warp >= H::kProductWarp && warp < H::kProductWarp + TILES) {
       // ---- products of a tile: the whole warp walks the blocks, converged, so that operands are formed in uniform
@@ -795,13 +818,22 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
       }
     }
   }
-  if (bars.stop) {  // a wait ran out: report it, and let copies in flight land
-    if (tid == 0 && a.fault != nullptr) *a.fault = 1u;
-    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
-  }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (bars.stop) {  // a wait ran out (none is left): what is in flight ends before its memory goes
+    tc_fence_after();
+    if (warp == H::kCopyWarp && lane == 0) {
+      for (int f = max(bars.filled - kStages, 0); f < bars.filled; ++f) mbar_drain(&bars.kv_full[f % kStages], (f / kStages) & 1);
+      for (int t = 0; t < (n == 0 ? 0 : w.two ? 2 : 1); ++t) mbar_drain(&bars.q_full[t], 0);
+    } else if (warp >= H::kProductWarp && warp < H::kProductWarp + TILES && elect_lane()) {
+      tc_commit(&bars.drained[warp - H::kProductWarp]);  // of the products that this lane issued
+      mbar_drain(&bars.drained[warp - H::kProductWarp], 0);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+  }
   if (warp == H::kProductWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(H::kTmemCols) : "memory");
@@ -998,6 +1030,8 @@ PromptGrid prompt_grid(const spc_prompt_dims* d) {
 
 constexpr size_t kPromptHead = 256;  // the fault word
 
+std::atomic<int64_t> prompt_limit{2000000000};  // of a wait in the kernels launched from now on, in ns
+
 template <int TILES>
 cudaError_t launch_prompt_k(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const PromptArgs& a,
                             int64_t grid, cudaStream_t stream) {
@@ -1010,6 +1044,8 @@ cudaError_t launch_prompt_k(const CUtensorMap& qm, const CUtensorMap& km, const 
 }
 
 }  // namespace
+
+int64_t prompt_wait_limit(int64_t ns) { return ns > 0 ? prompt_limit.exchange(ns) : prompt_limit.load(); }
 
 size_t prompt_workspace_bytes(const spc_prompt_dims* d) {
   const PromptGrid g = prompt_grid(d);
@@ -1057,6 +1093,7 @@ spc_status launch_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const
   a.items = (uint32_t)g.items;
   a.gap = g.gap;
   a.fault = static_cast<uint32_t*>(ws);
+  a.limit = (uint64_t)prompt_limit.load(std::memory_order_relaxed);
   a.part_rows = (int64_t)d->S * d->q_max * d->Hq;
   if (a.splits > 1) {
     a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kPromptHead);

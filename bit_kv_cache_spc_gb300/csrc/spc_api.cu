@@ -26,6 +26,7 @@ spc_status launch_append(const spc_dims*, const uint16_t*, const uint16_t*, void
 spc_status launch_rope(const spc_rope_dims*, const int32_t*, const uint64_t*, const uint16_t*, const uint16_t*,
                        const uint16_t*, uint16_t*, uint16_t*, uint16_t*, cudaStream_t);
 size_t prompt_workspace_bytes(const spc_prompt_dims*);
+int64_t prompt_wait_limit(int64_t);
 spc_status launch_prompt_attn(const spc_prompt_dims*, const uint16_t*, const uint16_t*, const uint16_t*,
                               const int32_t*, const int32_t*, const int32_t*, const int32_t*, uint16_t*, float*,
                               void*, cudaStream_t);
@@ -716,6 +717,8 @@ spc_status spc_prompt_attn_status(void* ws, spc_stream stream) {
   }
   return v != 0u ? SPC_ERR_TIMEOUT : SPC_OK;
 }
+
+int64_t spc_prompt_attn_wait_limit(int64_t ns) { return spc::prompt_wait_limit(ns); }
 
 spc_status spc_extend_kv(const spc_dims* d, int32_t n, const uint16_t* k_new, const uint16_t* v_new,
                          const spc_layout* k_layout, const spc_layout* v_layout, void* records, uint16_t* resid,

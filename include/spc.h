@@ -487,6 +487,14 @@ spc_status spc_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const ui
  * `stream`. */
 spc_status spc_prompt_attn_status(void* ws, spc_stream stream);
 
+/* The limit of a wait in spc_prompt_attn's kernels, in ns (2 * 10^9 unless set;
+ * the longest regular wait of a common call is far below a millisecond).  ns >
+ * 0 sets it for the calls of the process from now on (a captured call keeps
+ * the one it was captured with), any other value changes nothing.  Returns the
+ * limit before the call.  A wait that runs out ends its CTA early, whose rows
+ * of o and lse then hold no result. */
+int64_t spc_prompt_attn_wait_limit(int64_t ns);
+
 /*
  * A run of n new tokens joins the cache (SpeCache page, Algorithm 1 for a
  * prompt: d->N = 0; a follow-up prompt of a conversation: d->N > 0).  The
