@@ -470,7 +470,8 @@ def spc_prompt_attn(q, k, v, o, lse=None, q_begin=None, q_len=None, k_begin=None
     on the device, or None.  q_max, k_max bound the lengths (default: the
     token axis).  lse: fp32 of o's shape without D, contiguous.  Without ws a
     workspace, where one is needed, is taken from torch's allocator for the
-    call, which needs the call to be on the current stream."""
+    call, which needs the call to be on the current stream; a wait that ran
+    out is then found by spc_prompt_attn_status() of the device."""
     fn = "spc_prompt_attn"
     dev = _device(fn, q)
     S = _sequences(q, k, q_len, k_len, q_begin, k_begin)
@@ -505,8 +506,9 @@ def spc_prompt_attn(q, k, v, o, lse=None, q_begin=None, q_len=None, k_begin=None
         raise SpcError(fn, st)
 
 
-def spc_prompt_attn_status(ws, stream=None) -> int:
-    """0, or SPC_ERR_TIMEOUT (6) if a bounded wait in spc_prompt_attn ran out (the word is cleared)."""
+def spc_prompt_attn_status(ws=None, stream=None) -> int:
+    """0, or SPC_ERR_TIMEOUT (6) if a bounded wait in spc_prompt_attn ran out (the word is cleared): in a call with this
+    workspace, or, without one, in any call on the current device."""
     return int(_lib.spc_prompt_attn_status(_ptr(ws), _stream(stream)))
 
 

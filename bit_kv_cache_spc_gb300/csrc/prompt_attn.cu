@@ -89,6 +89,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.0f;
 constexpr int kDense = 256;  // sequences whose actual lengths number the items
 
+__device__ uint32_t prompt_device_fault;  // a wait of some call on the device ran out
+
 struct PromptArgs {
   const uint16_t* v;
   uint16_t* o;
@@ -135,7 +137,7 @@ struct __align__(16) PromptBars {
   uint64_t p_full[2][2];  // its weights are
   uint64_t drained[2];    // after a wait that ran out: the tile's products have ended
   uint64_t limit;         // of a wait, in ns
-  uint32_t* fault;        // where one that runs out is reported, or null
+  uint32_t* fault;        // the workspace's word, or null
   int filled;             // stages copied in all
   uint32_t tmem;
   uint32_t bad;            // a masked stage held a non-finite value
@@ -176,6 +178,7 @@ __device__ __forceinline__ bool mbar_wait(PromptBars& bars, uint64_t* b, uint32_
     if (bars.stop) return false;
     asm volatile("mov.u64 %0, %%globaltimer;\n" : "=l"(now));
     if (now - start > bars.limit) {
+      *(volatile uint32_t*)&prompt_device_fault = 1u;
       if (bars.fault != nullptr) *(volatile uint32_t*)bars.fault = 1u;
       bars.stop = 1u;
       return false;
@@ -1046,6 +1049,8 @@ cudaError_t launch_prompt_k(const CUtensorMap& qm, const CUtensorMap& km, const 
 }  // namespace
 
 int64_t prompt_wait_limit(int64_t ns) { return ns > 0 ? prompt_limit.exchange(ns) : prompt_limit.load(); }
+
+cudaError_t prompt_fault_word(void** word) { return cudaGetSymbolAddress(word, prompt_device_fault); }
 
 size_t prompt_workspace_bytes(const spc_prompt_dims* d) {
   const PromptGrid g = prompt_grid(d);

@@ -27,6 +27,7 @@ spc_status launch_rope(const spc_rope_dims*, const int32_t*, const uint64_t*, co
                        const uint16_t*, uint16_t*, uint16_t*, uint16_t*, cudaStream_t);
 size_t prompt_workspace_bytes(const spc_prompt_dims*);
 int64_t prompt_wait_limit(int64_t);
+cudaError_t prompt_fault_word(void**);
 spc_status launch_prompt_attn(const spc_prompt_dims*, const uint16_t*, const uint16_t*, const uint16_t*,
                               const int32_t*, const int32_t*, const int32_t*, const int32_t*, uint16_t*, float*,
                               void*, cudaStream_t);
@@ -704,10 +705,10 @@ spc_status spc_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const ui
 }
 
 spc_status spc_prompt_attn_status(void* ws, spc_stream stream) {
-  if (ws == nullptr) return SPC_ERR_INVALID;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint32_t v = 0;
-  cudaError_t e = cudaMemcpyAsync(&v, ws, sizeof(v), cudaMemcpyDeviceToHost, s);
+  cudaError_t e = ws == nullptr ? spc::prompt_fault_word(&ws) : cudaSuccess;
+  if (e == cudaSuccess) e = cudaMemcpyAsync(&v, ws, sizeof(v), cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e == cudaSuccess && v != 0u) e = cudaMemsetAsync(ws, 0, sizeof(v), s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);

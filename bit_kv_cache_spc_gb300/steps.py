@@ -59,7 +59,8 @@ def prompt_layer(d, q, k, v, pos, turns, o, records, resid, host_kv=None, n_cap=
     new tokens' behind them; they may be shared by layers that run in turn.
     The new tokens join records and resid, and host_kv if given; d.N is
     advanced by n.  Without ws the attention takes its workspace from torch's
-    allocator."""
+    allocator; spc_prompt_attn_status(), after the layers, says whether a
+    bounded wait of the attention ran out."""
     n, N = k.shape[1], d.N
     if N > 0:
         if history is None or any(b.shape[2] < N + n for b in history):

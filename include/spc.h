@@ -458,7 +458,7 @@ typedef struct spc_prompt_dims {
  * word (256 bytes; zero-filled once by the caller for
  * spc_prompt_attn_status) and, where few queries leave SMs idle and the keys
  * are split, the splits' partial results.  256 says that there is no split:
- * the call then also takes ws = NULL (and reports no status).  Calls that
+ * the call then also takes ws = NULL.  Calls that
  * share a workspace must not overlap on the GPU.  0 for an invalid shape. */
 size_t spc_prompt_attn_workspace_bytes(const spc_prompt_dims* d);
 
@@ -482,9 +482,10 @@ spc_status spc_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const ui
                            const int32_t* k_len, uint16_t* o, float* lse, void* ws, size_t ws_bytes,
                            spc_stream stream);
 
-/* Reads and clears the status word of a workspace of spc_prompt_attn:
- * SPC_ERR_TIMEOUT if a bounded wait ran out since, else SPC_OK.  Synchronises
- * `stream`. */
+/* Reads and clears the status word of a workspace of spc_prompt_attn, or, with
+ * ws = NULL, the current device's, which every call on the device reports to
+ * as well: SPC_ERR_TIMEOUT if a bounded wait ran out since, else SPC_OK.
+ * Synchronises `stream`. */
 spc_status spc_prompt_attn_status(void* ws, spc_stream stream);
 
 /* The limit of a wait in spc_prompt_attn's kernels, in ns (2 * 10^9 unless set;

@@ -31,6 +31,7 @@ def limit():
     before = spc.spc_prompt_attn_wait_limit()
     yield spc.spc_prompt_attn_wait_limit
     spc.spc_prompt_attn_wait_limit(before)
+    spc.spc_prompt_attn_status()  # cleared
 
 
 @pytest.mark.parametrize("tiles,lk", [(2, 1 << 19), (1, 1 << 15)])
@@ -46,9 +47,29 @@ def test_a_wait_that_runs_out_is_reported(limit, tiles, lk):
     assert limit(before) == 1
     assert spc.spc_prompt_attn_status(ws) == TIMEOUT
     assert spc.spc_prompt_attn_status(ws) == 0
+    assert spc.spc_prompt_attn_status() == TIMEOUT  # the device's word
     o.fill_(7.0)
     spc.spc_prompt_attn(q, k, v, o, ws=ws)
     assert bool((o == 1).all()) and spc.spc_prompt_attn_status(ws) == 0
+
+
+@pytest.mark.parametrize("split", [False, True])
+def test_calls_without_a_workspace_report_to_the_device(limit, split):
+    """Also where the call takes its own workspace for the splits: one token, a few heads, a few million keys."""
+    import bit_kv_cache_spc_gb300 as spc
+    q, k, v, o = long_call(2, 1 << 19)
+    if split:
+        k, v = (torch.full((1 << 22, 1, D), float(i), dtype=torch.bfloat16, device="cuda") for i in range(2))
+        q, o = q[:1, :4].contiguous(), o[:1, :4].contiguous()
+        assert spc.spc_prompt_attn_workspace_bytes(q, k, v, o) > 256
+    assert spc.spc_prompt_attn_status() == 0
+    before = limit(1)
+    spc.spc_prompt_attn(q, k, v, o)
+    limit(before)
+    assert spc.spc_prompt_attn_status() == TIMEOUT
+    assert spc.spc_prompt_attn_status() == 0
+    spc.spc_prompt_attn(q, k, v, o)
+    assert bool((o == 1).all()) and spc.spc_prompt_attn_status() == 0
 
 
 def test_small_calls_after_one_that_ran_out(limit):
