@@ -167,7 +167,9 @@ __device__ __forceinline__ bool mbar_try(uint64_t* b, uint32_t parity) {
 // (two seconds unless the caller sets another limit).  The thread whose wait
 // runs out reports it: no other has to be there still to see it.  The timer is
 // read only after many tries: reading it takes longer than a regular wait.
-__device__ __forceinline__ bool mbar_wait(PromptBars& bars, uint64_t* b, uint32_t parity) {
+// A wait for something that regularly comes after `stages` stages of keys has a
+// 65536th of the limit more for each (30 us at two seconds; a stage takes 1.4).
+__device__ __forceinline__ bool mbar_wait(PromptBars& bars, uint64_t* b, uint32_t parity, uint32_t stages = 0) {
   for (int i = 0; i < 64; ++i)
     if (mbar_try(b, parity)) return true;
   uint64_t start, now;
@@ -177,7 +179,7 @@ __device__ __forceinline__ bool mbar_wait(PromptBars& bars, uint64_t* b, uint32_
       if (mbar_try(b, parity)) return true;
     if (bars.stop) return false;
     asm volatile("mov.u64 %0, %%globaltimer;\n" : "=l"(now));
-    if (now - start > bars.limit) {
+    if (now - start > bars.limit + (bars.limit >> 16) * stages) {
       *(volatile uint32_t*)&prompt_device_fault = 1u;
       if (bars.fault != nullptr) *(volatile uint32_t*)bars.fault = 1u;
       bars.stop = 1u;
@@ -197,8 +199,8 @@ __device__ __forceinline__ void mbar_drain(uint64_t* b, uint32_t parity) {
 }
 
 // For a whole warp: one outcome for all lanes.
-__device__ __forceinline__ bool mbar_wait_warp(PromptBars& bars, uint64_t* b, uint32_t parity) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait(bars, b, parity));
+__device__ __forceinline__ bool mbar_wait_warp(PromptBars& bars, uint64_t* b, uint32_t parity, uint32_t stages = 0) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bars, b, parity, stages));
 }
 
 __device__ __forceinline__ void tma_load4(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
@@ -652,7 +654,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
       const int first = min(H::kAhead, n);
       for (int j = max(w.edge - w.lo, 0); j < n; ++j, ++scans) {
         const int xv = first + j + min(j, n - first), sv = xv % kStages;
-        if (!mbar_wait_warp(bars, &bars.v_scan[scans & 1u], (scans >> 1) & 1u)) break;
+        // (the first one comes after all stages that need no scan)
+        if (!mbar_wait_warp(bars, &bars.v_scan[scans & 1u], (scans >> 1) & 1u, n)) break;
         if (!mbar_wait_warp(bars, &bars.kv_full[sv], (xv / kStages) & 1)) break;
         uint4* tile = reinterpret_cast<uint4*>(ring + sv * H::kStageBytes);
         bool touched = false;

@@ -489,7 +489,8 @@ spc_status spc_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const ui
 spc_status spc_prompt_attn_status(void* ws, spc_stream stream);
 
 /* The limit of a wait in spc_prompt_attn's kernels, in ns (2 * 10^9 unless set;
- * the longest regular wait of a common call is far below a millisecond).  ns >
+ * regular waits last microseconds, but for one that lasts as long as a CTA
+ * walks over keys that its rows see in full: its limit grows with them).  ns >
  * 0 sets it for the calls of the process from now on (a captured call keeps
  * the one it was captured with), any other value changes nothing.  Returns the
  * limit before the call.  A wait that runs out ends its CTA early, whose rows

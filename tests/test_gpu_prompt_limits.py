@@ -53,6 +53,29 @@ def test_a_wait_that_runs_out_is_reported(limit, tiles, lk):
     assert bool((o == 1).all()) and spc.spc_prompt_attn_status(ws) == 0
 
 
+def test_a_long_walk_over_keys_is_no_wait_that_ran_out(limit):
+    """65536 stages of 128 keys: the warps that look after masked places wait for nearly all of the call.  A limit of
+    three quarters of its time (with the stages' part, one and a half of it) does not end it."""
+    import bit_kv_cache_spc_gb300 as spc
+    q, k, v, o = long_call(2, 1 << 23)
+    lse = torch.zeros(q.shape[:2], device="cuda")
+    spc.spc_prompt_attn(q, k, v, o, lse)
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record()
+    spc.spc_prompt_attn(q, k, v, o, lse)
+    b.record()
+    b.synchronize()
+    o.fill_(7.0)
+    before = limit(int(0.75e6 * a.elapsed_time(b)))
+    spc.spc_prompt_attn(q, k, v, o, lse)
+    limit(before)
+    assert spc.spc_prompt_attn_status() == 0
+    assert bool((o == 1).all())
+    seen = (1 << 23) - torch.arange(2 * sms() - 1, -1, -1, device="cuda", dtype=torch.float64)
+    # log(l) in binary32: within two units of its 15.9
+    assert bool(((lse.double() - seen.log()[:, None]).abs() <= 2 * 2.0 ** -20).all())
+
+
 @pytest.mark.parametrize("split", [False, True])
 def test_calls_without_a_workspace_report_to_the_device(limit, split):
     """Also where the call takes its own workspace for the splits: one token, a few heads, a few million keys."""
