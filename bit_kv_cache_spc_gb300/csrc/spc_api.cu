@@ -622,9 +622,12 @@ spc_status spc_rope_frequencies(const spc_rope_scaling* s, int32_t rot, uint64_t
   return SPC_OK;
 }
 
-spc_status spc_rope(const spc_rope_dims* d, const int32_t* pos, const uint64_t* turns, const uint16_t* q,
-                    const uint16_t* k, const uint16_t* v, uint16_t* q_out, uint16_t* k_out, uint16_t* v_out,
-                    spc_stream stream) {
+// The checks of a call's arguments come back with `nothing` set where there is
+// nothing to do.
+static spc_status check_rope(const spc_rope_dims* d, const int32_t* pos, const uint64_t* turns, const uint16_t* q,
+                             const uint16_t* k, const uint16_t* v, const uint16_t* q_out, const uint16_t* k_out,
+                             const uint16_t* v_out, bool& nothing) {
+  nothing = false;
   if (d == nullptr || d->B <= 0 || d->T < 0 || d->Hq < 0 || d->Hkv < 0 || d->D <= 0) return SPC_ERR_INVALID;
   if (d->Hq > (1 << 16) || d->Hkv > (1 << 16)) return SPC_ERR_INVALID;
   if (d->interleaved != 0 && d->interleaved != 1) return SPC_ERR_INVALID;
@@ -633,14 +636,19 @@ spc_status spc_rope(const spc_rope_dims* d, const int32_t* pos, const uint64_t* 
   if ((q == nullptr) != (q_out == nullptr) || (k == nullptr) != (k_out == nullptr) ||
       (v == nullptr) != (v_out == nullptr))
     return SPC_ERR_INVALID;
-  if (d->T == 0) return SPC_OK;
+  if (d->T == 0) {
+    nothing = true;
+    return SPC_OK;
+  }
   if ((q == nullptr) != (d->Hq == 0) || (k == nullptr) != (d->Hkv == 0) || (v != nullptr && d->Hkv == 0))
     return SPC_ERR_INVALID;
-  if (q == nullptr && k == nullptr) return SPC_OK;
+  if (q == nullptr && k == nullptr) {
+    nothing = true;
+    return SPC_OK;
+  }
   if (pos == nullptr || turns == nullptr || (reinterpret_cast<uintptr_t>(turns) & 7u) != 0) return SPC_ERR_INVALID;
   const struct {
-    const uint16_t* in;
-    uint16_t* out;
+    const uint16_t *in, *out;
     const spc_layout *li, *lo;
     int32_t heads;
   } rows[3] = {{q, q_out, &d->q, &d->q_out, d->Hq},
@@ -656,6 +664,22 @@ spc_status spc_rope(const spc_rope_dims* d, const int32_t* pos, const uint64_t* 
       return SPC_ERR_INVALID;
   }
   if (same_rows(q_out, k_out) || same_rows(q_out, v_out) || same_rows(k_out, v_out)) return SPC_ERR_INVALID;
+  return SPC_OK;
+}
+
+spc_status spc_rope_check(const spc_rope_dims* d, const int32_t* pos, const uint64_t* turns, const uint16_t* q,
+                          const uint16_t* k, const uint16_t* v, uint16_t* q_out, uint16_t* k_out, uint16_t* v_out,
+                          spc_stream) {
+  bool nothing;
+  return check_rope(d, pos, turns, q, k, v, q_out, k_out, v_out, nothing);
+}
+
+spc_status spc_rope(const spc_rope_dims* d, const int32_t* pos, const uint64_t* turns, const uint16_t* q,
+                    const uint16_t* k, const uint16_t* v, uint16_t* q_out, uint16_t* k_out, uint16_t* v_out,
+                    spc_stream stream) {
+  bool nothing;
+  const spc_status st = check_rope(d, pos, turns, q, k, v, q_out, k_out, v_out, nothing);
+  if (st != SPC_OK || nothing) return st;
   return spc::launch_rope(d, pos, turns, q, k, v, q_out, k_out, v_out, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -681,13 +705,16 @@ size_t spc_prompt_attn_workspace_bytes(const spc_prompt_dims* d) {
   return check_prompt_dims(d) == SPC_OK ? spc::prompt_workspace_bytes(d) : 0;
 }
 
-spc_status spc_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const uint16_t* k, const uint16_t* v,
-                           const int32_t* q_begin, const int32_t* q_len, const int32_t* k_begin,
-                           const int32_t* k_len, uint16_t* o, float* lse, void* ws, size_t ws_bytes,
-                           spc_stream stream) {
-  spc_status st = check_prompt_dims(d);
+static spc_status check_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                                    const int32_t* q_begin, const uint16_t* o, const void* ws, size_t ws_bytes,
+                                    bool& nothing) {
+  nothing = false;
+  const spc_status st = check_prompt_dims(d);
   if (st != SPC_OK) return st;
-  if (d->q_max == 0) return SPC_OK;
+  if (d->q_max == 0) {
+    nothing = true;
+    return SPC_OK;
+  }
   if (d->S > 1 && d->q.b == 0 && q_begin == nullptr) return SPC_ERR_INVALID;  // all on the same query rows
   if (q == nullptr || o == nullptr || (d->k_max > 0 && (k == nullptr || v == nullptr))) return SPC_ERR_INVALID;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return SPC_ERR_INVALID;
@@ -700,6 +727,23 @@ spc_status spc_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const ui
       (k != nullptr && overlap(k, layout_bytes(d->k, kb, d->k_tokens, d->Hkv), o, ob)) ||
       (v != nullptr && overlap(v, layout_bytes(d->v, kb, d->k_tokens, d->Hkv), o, ob)))
     return SPC_ERR_INVALID;
+  return SPC_OK;
+}
+
+spc_status spc_prompt_attn_check(const spc_prompt_dims* d, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                                 const int32_t* q_begin, const int32_t*, const int32_t*, const int32_t*, uint16_t* o,
+                                 float*, void* ws, size_t ws_bytes, spc_stream) {
+  bool nothing;
+  return check_prompt_attn(d, q, k, v, q_begin, o, ws, ws_bytes, nothing);
+}
+
+spc_status spc_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                           const int32_t* q_begin, const int32_t* q_len, const int32_t* k_begin,
+                           const int32_t* k_len, uint16_t* o, float* lse, void* ws, size_t ws_bytes,
+                           spc_stream stream) {
+  bool nothing;
+  const spc_status st = check_prompt_attn(d, q, k, v, q_begin, o, ws, ws_bytes, nothing);
+  if (st != SPC_OK || nothing) return st;
   return spc::launch_prompt_attn(d, q, k, v, q_begin, q_len, k_begin, k_len, o, lse, ws,
                                  reinterpret_cast<cudaStream_t>(stream));
 }
@@ -721,9 +765,10 @@ spc_status spc_prompt_attn_status(void* ws, spc_stream stream) {
 
 int64_t spc_prompt_attn_wait_limit(int64_t ns) { return spc::prompt_wait_limit(ns); }
 
-spc_status spc_extend_kv(const spc_dims* d, int32_t n, const uint16_t* k_new, const uint16_t* v_new,
-                         const spc_layout* k_layout, const spc_layout* v_layout, void* records, uint16_t* resid,
-                         uint16_t* host_kv, int64_t n_cap, spc_stream stream) {
+// host_dev: the device's address of host_kv.
+static spc_status check_extend(const spc_dims* d, int32_t n, const uint16_t* k_new, const uint16_t* v_new,
+                               const spc_layout* k_layout, const spc_layout* v_layout, const void* records,
+                               const uint16_t* resid, const uint16_t* host_kv, int64_t n_cap, const void** host_dev) {
   spc_status st = check_dims(d);
   if (st != SPC_OK) return st;
   if (n < 0 || (int64_t)d->N + n > (1 << 30)) return SPC_ERR_INVALID;
@@ -744,21 +789,36 @@ spc_status spc_extend_kv(const spc_dims* d, int32_t n, const uint16_t* k_new, co
   if (overlap(k_new, kb, resid, res) || overlap(v_new, vb, resid, res) || overlap(k_new, kb, records, rec) ||
       overlap(v_new, vb, records, rec))
     return SPC_ERR_INVALID;
-  const void* host_dev = nullptr;
   if (host_kv != nullptr) {
     if (n_cap < after.N) return SPC_ERR_INVALID;
-    st = mapped_device_pointer(host_kv, &host_dev);
-    if (st != SPC_OK) return st;
+    return mapped_device_pointer(host_kv, host_dev);
   }
+  return SPC_OK;
+}
+
+spc_status spc_extend_kv_check(const spc_dims* d, int32_t n, const uint16_t* k_new, const uint16_t* v_new,
+                               const spc_layout* k_layout, const spc_layout* v_layout, void* records, uint16_t* resid,
+                               uint16_t* host_kv, int64_t n_cap, spc_stream) {
+  const void* host_dev = nullptr;
+  return check_extend(d, n, k_new, v_new, k_layout, v_layout, records, resid, host_kv, n_cap, &host_dev);
+}
+
+spc_status spc_extend_kv(const spc_dims* d, int32_t n, const uint16_t* k_new, const uint16_t* v_new,
+                         const spc_layout* k_layout, const spc_layout* v_layout, void* records, uint16_t* resid,
+                         uint16_t* host_kv, int64_t n_cap, spc_stream stream) {
+  const void* host_dev = nullptr;
+  const spc_status st =
+      check_extend(d, n, k_new, v_new, k_layout, v_layout, records, resid, host_kv, n_cap, &host_dev);
+  if (st != SPC_OK || n == 0) return st;
   return spc::launch_extend(d, n, k_new, v_new, k_layout, v_layout, records, resid,
                             static_cast<uint16_t*>(const_cast<void*>(host_dev)), n_cap,
                             reinterpret_cast<cudaStream_t>(stream));
 }
 
-spc_status spc_dequantize_kv(const spc_dims* d, const void* records, const uint16_t* resid, int32_t first, int32_t n,
-                             uint16_t* k, uint16_t* v, const spc_layout* k_layout, const spc_layout* v_layout,
-                             spc_stream stream) {
-  spc_status st = check_dims(d);
+static spc_status check_dequantize(const spc_dims* d, const void* records, const uint16_t* resid, int32_t first,
+                                   int32_t n, const uint16_t* k, const uint16_t* v, const spc_layout* k_layout,
+                                   const spc_layout* v_layout) {
+  const spc_status st = check_dims(d);
   if (st != SPC_OK) return st;
   if (first < 0 || n < 0 || (int64_t)first + n > d->N) return SPC_ERR_INVALID;
   if (n == 0) return SPC_OK;
@@ -772,6 +832,20 @@ spc_status spc_dequantize_kv(const spc_dims* d, const void* records, const uint1
   if (overlap(k, kb, resid, res) || overlap(v, vb, resid, res) || overlap(k, kb, records, rec) ||
       overlap(v, vb, records, rec) || same_rows(k, v))
     return SPC_ERR_INVALID;
+  return SPC_OK;
+}
+
+spc_status spc_dequantize_kv_check(const spc_dims* d, const void* records, const uint16_t* resid, int32_t first,
+                                   int32_t n, uint16_t* k, uint16_t* v, const spc_layout* k_layout,
+                                   const spc_layout* v_layout, spc_stream) {
+  return check_dequantize(d, records, resid, first, n, k, v, k_layout, v_layout);
+}
+
+spc_status spc_dequantize_kv(const spc_dims* d, const void* records, const uint16_t* resid, int32_t first, int32_t n,
+                             uint16_t* k, uint16_t* v, const spc_layout* k_layout, const spc_layout* v_layout,
+                             spc_stream stream) {
+  const spc_status st = check_dequantize(d, records, resid, first, n, k, v, k_layout, v_layout);
+  if (st != SPC_OK || n == 0) return st;
   return spc::launch_dequantize(d, records, resid, first, n, k, v, k_layout, v_layout,
                                 reinterpret_cast<cudaStream_t>(stream));
 }

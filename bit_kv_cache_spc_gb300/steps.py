@@ -23,9 +23,9 @@ from __future__ import annotations
 
 import torch
 
-from . import (spc_append_kv, spc_decode_attn2, spc_dequantize_kv, spc_extend_kv, spc_host_gather,
-               spc_host_gather_prev, spc_merged_attn, spc_offload_kv, spc_prompt_attn, spc_quantize_kv, spc_rope,
-               spc_topk_select, spc_topk_select_prev)
+from . import (_all_or_none, _dequantize_args, _extend_args, _free, _prompt_args, _rope_args, spc_append_kv,
+               spc_decode_attn2, spc_host_gather, spc_host_gather_prev, spc_merged_attn, spc_offload_kv,
+               spc_quantize_kv, spc_topk_select, spc_topk_select_prev)
 
 
 def prefill_layer(d, k, v, records, resid, host_kv, n_cap, stream=None, copy_stream=None):
@@ -58,7 +58,9 @@ def prompt_layer(d, q, k, v, pos, turns, o, records, resid, host_kv=None, n_cap=
     values) of cap >= d.N + n rows, which then hold the history's rows and the
     new tokens' behind them; they may be shared by layers that run in turn.
     The new tokens join records and resid, and host_kv if given; d.N is
-    advanced by n.  Without ws the attention takes its workspace from torch's
+    advanced by n.  The calls are checked in whole before the first one: one
+    that is refused leaves q, k, history and the cache as they were, and may be
+    made again.  Without ws the attention takes its workspace from torch's
     allocator; spc_prompt_attn_status(), after the layers, says whether a
     bounded wait of the attention ran out."""
     n, N = k.shape[1], d.N
@@ -67,15 +69,24 @@ def prompt_layer(d, q, k, v, pos, turns, o, records, resid, host_kv=None, n_cap=
             raise ValueError(f"prompt_layer: a follow-up prompt needs history buffers of {N + n} rows")
         kk, vv = (b[:, :, :N + n].transpose(1, 2) for b in history)
     stream = torch.cuda.current_stream() if stream is None else stream
+    own = None
     with torch.cuda.stream(stream):
-        if N == 0:
-            kk, vv = k, v
-            spc_rope(q, k, pos, turns, rot, interleaved, mscale)
-        else:
-            spc_dequantize_kv(d, records, resid, 0, kk[:, :N], vv[:, :N])
-            spc_rope(q, k, pos, turns, rot, interleaved, mscale, v=v, k_out=kk[:, N:], v_out=vv[:, N:])
-        spc_prompt_attn(q, kk, vv, o, lse, scale=d.scale, ws=ws)
-        spc_extend_kv(d, kk[:, N:], vv[:, N:], records, resid, host_kv, n_cap)
+        try:
+            calls = []
+            if N == 0:
+                kk, vv = k, v
+                rope = _rope_args(q, k, pos, turns, rot, interleaved, mscale, None, None, None, None, None)
+            else:
+                calls.append(("spc_dequantize_kv", _dequantize_args(d, records, resid, 0, kk[:, :N], vv[:, :N], None)))
+                rope = _rope_args(q, k, pos, turns, rot, interleaved, mscale, v, None, kk[:, N:], vv[:, N:], None)
+            if rope is not None:
+                calls.append(("spc_rope", rope))
+            attn, own = _prompt_args(q, kk, vv, o, lse, None, None, None, None, None, None, d.scale, ws, None, None)
+            calls.append(("spc_prompt_attn", attn))
+            calls.append(("spc_extend_kv", _extend_args(d, kk[:, N:], vv[:, N:], records, resid, host_kv, n_cap, None)))
+            _all_or_none(calls)
+        finally:
+            _free(own)
     d.N += n
 
 

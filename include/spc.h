@@ -530,6 +530,27 @@ spc_status spc_dequantize_kv(const spc_dims* d, const void* records, const uint1
                              spc_stream stream);
 
 /*
+ * What spc_rope, spc_prompt_attn, spc_extend_kv and spc_dequantize_kv would
+ * refuse, without a launch: the same arguments, and the status that the call
+ * would return before it enqueues anything.  For a sequence of calls of which
+ * either all are to be made or none (a prompt is rotated in place before its
+ * attention and its way into the cache).
+ */
+spc_status spc_rope_check(const spc_rope_dims* d, const int32_t* pos, const uint64_t* turns, const uint16_t* q,
+                          const uint16_t* k, const uint16_t* v, uint16_t* q_out, uint16_t* k_out, uint16_t* v_out,
+                          spc_stream stream);
+spc_status spc_prompt_attn_check(const spc_prompt_dims* d, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                                 const int32_t* q_begin, const int32_t* q_len, const int32_t* k_begin,
+                                 const int32_t* k_len, uint16_t* o, float* lse, void* ws, size_t ws_bytes,
+                                 spc_stream stream);
+spc_status spc_extend_kv_check(const spc_dims* d, int32_t n, const uint16_t* k_new, const uint16_t* v_new,
+                               const spc_layout* k_layout, const spc_layout* v_layout, void* records, uint16_t* resid,
+                               uint16_t* host_kv, int64_t n_cap, spc_stream stream);
+spc_status spc_dequantize_kv_check(const spc_dims* d, const void* records, const uint16_t* resid, int32_t first,
+                                   int32_t n, uint16_t* k, uint16_t* v, const spc_layout* k_layout,
+                                   const spc_layout* v_layout, spc_stream stream);
+
+/*
  * Decode-time append (SpeCache page, section 3 "Decoding", Algorithm 3: the
  * new token's K/V joins the cache; section 3: the full-precision cache is
  * offloaded to CPU memory).  d describes the cache BEFORE the call: N tokens
