@@ -576,9 +576,38 @@ size_t layout_bytes(const spc_layout& l, int64_t nb, int64_t nt, int64_t nh) {
   return 2 * (size_t)((nb - 1) * l.b + (nt - 1) * l.t + (nh - 1) * l.h + spc::kD);
 }
 
-// The first rows of two views share bytes: the views are one, or nearly.
-bool same_rows(const void* a, const void* b) {
-  return a != nullptr && b != nullptr && overlap(a, 2 * spc::kD, b, 2 * spc::kD);
+// Whether a row of one view of [nb][nt][heads][128] shares a byte with a row of
+// the other.  Told exactly where an axis that both step along has one stride
+// (views of one buffer; heads may differ): the distance of two rows is then the
+// views' distance less some steps along the axes, and as each stride clears
+// what the smaller ones span, only the two whole numbers of steps next to the
+// distance that is left can come within a row of it, largest stride first.
+// Views of other strides that reach into one another: by their first rows.
+bool rows_meet(const uint16_t* a, const spc_layout& la, int64_t ha, const uint16_t* b, const spc_layout& lb, int64_t hb,
+               int64_t nb, int64_t nt) {
+  if (!overlap(a, layout_bytes(la, nb, nt, ha), b, layout_bytes(lb, nb, nt, hb))) return false;
+  const spc_layout l = {la.b, la.t, ha > 1 ? la.h : lb.h};
+  if ((nb > 1 && la.b != lb.b) || (nt > 1 && la.t != lb.t) || (ha > 1 && hb > 1 && la.h != lb.h) ||
+      !layout_ok(l, nb, nt, std::max(ha, hb)))
+    return overlap(a, 2 * spc::kD, b, 2 * spc::kD);
+  struct Axis {
+    int64_t step, least, most;  // bytes; the difference of two rows' indices
+  } ax[3] = {{2 * l.b, 1 - nb, nb - 1}, {2 * l.t, 1 - nt, nt - 1}, {2 * l.h, 1 - hb, ha - 1}};
+  for (Axis& x : ax)
+    if (x.least == 0 && x.most == 0) x.step = 0;
+  std::sort(ax, ax + 3, [](const Axis& x, const Axis& y) { return x.step > y.step; });
+  const int64_t apart = (int64_t)(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+  for (int pick = 0; pick < 8; ++pick) {
+    int64_t left = apart;
+    bool inside = true;
+    for (int i = 0; i < 3 && ax[i].step > 0; ++i) {
+      int64_t n = left / ax[i].step - (left % ax[i].step < 0) + ((pick >> i) & 1);
+      inside = inside && n >= ax[i].least && n <= ax[i].most;
+      left -= n * ax[i].step;
+    }
+    if (inside && left < 2 * spc::kD && left > -2 * spc::kD) return true;
+  }
+  return false;
 }
 
 bool same_layout(const spc_layout& x, const spc_layout& y) { return x.b == y.b && x.t == y.t && x.h == y.h; }
@@ -663,7 +692,11 @@ static spc_status check_rope(const spc_rope_dims* d, const int32_t* pos, const u
         overlap(r.in, layout_bytes(*r.li, d->B, d->T, r.heads), r.out, layout_bytes(*r.lo, d->B, d->T, r.heads)))
       return SPC_ERR_INVALID;
   }
-  if (same_rows(q_out, k_out) || same_rows(q_out, v_out) || same_rows(k_out, v_out)) return SPC_ERR_INVALID;
+  for (const auto& r : rows)  // nor may an output's rows lie on another tensor's
+    for (const auto& x : rows)
+      if (&r != &x && (rows_meet(r.out, *r.lo, r.heads, x.in, *x.li, x.heads, d->B, d->T) ||
+                       rows_meet(r.out, *r.lo, r.heads, x.out, *x.lo, x.heads, d->B, d->T)))
+        return SPC_ERR_INVALID;
   return SPC_OK;
 }
 
@@ -830,7 +863,8 @@ static spc_status check_dequantize(const spc_dims* d, const void* records, const
   const size_t res = spc_resid_bytes(d), rec = spc_records_bytes(d);
   const size_t kb = layout_bytes(*k_layout, d->B, n, d->Hkv), vb = layout_bytes(*v_layout, d->B, n, d->Hkv);
   if (overlap(k, kb, resid, res) || overlap(v, vb, resid, res) || overlap(k, kb, records, rec) ||
-      overlap(v, vb, records, rec) || same_rows(k, v))
+      overlap(v, vb, records, rec) ||
+      rows_meet(k, *k_layout, d->Hkv, v, *v_layout, d->Hkv, d->B, n))
     return SPC_ERR_INVALID;
   return SPC_OK;
 }

@@ -427,7 +427,9 @@ typedef struct spc_rope_dims {
  *            Hkv 0 (v needs Hkv).
  *   *_out  : where the rows go; in place when pointer and layout equal the
  *            input's, else sharing no byte range with it.  No output row may
- *            share a byte with another tensor's rows.
+ *            share a byte with another tensor's rows (SPC_ERR_INVALID; views of
+ *            different strides that reach into one another are only compared
+ *            by their first rows).
  * Products and sums are binary32 (fused), rounded once to bf16.
  */
 spc_status spc_rope(const spc_rope_dims* d, const int32_t* pos, const uint64_t* turns, const uint16_t* q,
@@ -521,8 +523,9 @@ spc_status spc_extend_kv(const spc_dims* d, int32_t n, const uint16_t* k_new, co
  * are fl(z + fl(s * code)) in binary32 (z and s from the group's min and max
  * as under spc_records_bytes), rounded once to bf16; a residual token's are
  * its 16-bit rows.
- *   k, v: bf16 views [B][n][Hkv][D] (device) that share no row; other rows are left as
- *         they were.
+ *   k, v: bf16 views [B][n][Hkv][D] (device) that share no row (SPC_ERR_INVALID; views of
+ *         different strides that reach into one another are only compared by
+ *         their first rows); other rows are left as they were.
  * first >= 0, n >= 0, first + n <= N.
  */
 spc_status spc_dequantize_kv(const spc_dims* d, const void* records, const uint16_t* resid, int32_t first, int32_t n,

@@ -1,5 +1,6 @@
 """More of the prompt path's host side: settings, and calls that are refused before anything reaches the GPU."""
 import ctypes as C
+import random
 
 import pytest
 
@@ -70,3 +71,64 @@ def test_checks_alone_say_what_the_call_would(fn, args, over, status):
     assert getattr(_lib, fn + "_check")(*args(**over)) == status
     if status:  # (a call that would be made is not: there is no memory behind it)
         assert getattr(_lib, fn)(*args(**over)) == status
+
+
+# ------------------------------------------------------------------------------------------------ outputs on other rows
+def fused(heads, T=8, all_heads=8):
+    """A view of some heads of a fused projection [2][8][8][128]."""
+    return lay(T * all_heads * 128, all_heads * 128, 128)
+
+
+HEAD, TOKEN = 256, 8 * 256  # bytes, of that projection
+
+
+@pytest.mark.parametrize("over", [
+    dict(q=1 << 20, k=(1 << 20) + 4 * HEAD, v=(1 << 20) + 6 * HEAD, v_out=1 << 30),  # q and k rotated in place, side by side
+    dict(q=1 << 20, k=(1 << 20) + 4 * HEAD, v=(1 << 20) + 6 * HEAD, q_out=1 << 30, k_out=1 << 31, v_out=1 << 32),
+    dict(q=1 << 20, k=(1 << 30) + 4 * HEAD, q_out=1 << 30, k_out=1 << 31)])  # q's rows go beside k's
+def test_rope_takes_views_that_lie_between_one_another(over):
+    assert fused_rope(over) == 0
+
+
+@pytest.mark.parametrize("over", [
+    dict(q=1 << 20, k=(1 << 20) + 3 * HEAD),                               # k starts on q's last head
+    dict(q=1 << 20, k=(1 << 20) + 6 * HEAD + 128),                         # ends half a row on the next token's q
+    dict(q=1 << 20, k=1 << 24, q_out=1 << 30, k_out=(1 << 30) + HEAD),     # one head on
+    dict(q=1 << 20, k=1 << 24, q_out=1 << 30, k_out=(1 << 30) + TOKEN),    # one token on
+    dict(q=1 << 20, k=1 << 24, q_out=1 << 30, k_out=(1 << 30) - TOKEN),    # one token before
+    dict(q=1 << 20, k=1 << 24, q_out=1 << 30, k_out=(1 << 30) + 8 * TOKEN + HEAD),  # one sequence and a head on
+    dict(q=1 << 20, k=1 << 24, q_out=1 << 30, k_out=1 << 31, v=1 << 28, v_out=(1 << 30) + 3 * TOKEN + 2 * HEAD),
+    dict(q=1 << 20, k=1 << 24, q_out=(1 << 24) + TOKEN, k_out=1 << 31),    # q's rows go where k's are read
+    dict(q=1 << 20, k=1 << 24, k_out=(1 << 20) + 2 * TOKEN)])              # k's where q's are turned in place
+def test_rope_refuses_outputs_on_other_rows(over):
+    assert fused_rope(over) == INVALID
+
+
+def fused_rope(over):
+    d = spc_rope_dims(2, 8, 4, 2, 128, 128, 0, 1.0, *[fused(h) for h in (4, 2, 2, 4, 2, 2)])
+    a = dict(v=None, v_out=None, q_out=over["q"], k_out=over["k"])
+    a.update(over)
+    return _lib.spc_rope_check(*rope_args(d=d, **a))
+
+
+def test_reading_back_refuses_exactly_the_views_that_share_rows():
+    """Keys and values in one buffer of any order of axes, at any distance: refused where one row of each share a byte,
+    by all pairs of rows."""
+    rng = random.Random(5)
+    seen = set()
+    for _ in range(3000):
+        n = [2, rng.randint(1, 5), 2]  # batch, tokens, heads
+        order, strides, span = rng.sample(range(3), 3), [0, 0, 0], 128
+        for i in order:
+            strides[i] = span + 8 * rng.choice([0, 0, 1, 16, 40])
+            span = strides[i] * n[i] if rng.random() < 0.5 else strides[i] * (n[i] - 1) + span
+        far = 2 * (sum(s * (m - 1) for s, m in zip(strides, n)) + 256)
+        by = rng.choice([16 * rng.randint(-far // 16, far // 16),
+                         2 * sum(s * rng.randint(-m, m) for s, m in zip(strides, n)) + rng.choice([0, 0, 240, 256, -256])])
+        starts = [2 * (strides[0] * b + strides[1] * t + strides[2] * h) for b in range(n[0]) for t in range(n[1])
+                  for h in range(n[2])]
+        want = any(abs(x - y - by) < 256 for x in starts for y in starts)
+        got = _lib.spc_dequantize_kv_check(*read_args(n=n[1], k=1 << 32, v=(1 << 32) + by, lk=lay(*strides), lv=lay(*strides)))
+        assert got == (INVALID if want else 0), (n, strides, by)
+        seen.add((want, abs(by) < far))
+    assert seen == {(True, True), (False, True), (False, False)}
