@@ -10,6 +10,7 @@ library has not been built the import fails: build it with
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import math
 import os
@@ -134,12 +135,13 @@ _sig = {
     "spc_extend_kv": (C.c_int, [_D, C.c_int32, _P, _P, _P, _P, _P, _P, _P, C.c_int64, _P]),
     "spc_dequantize_kv": (C.c_int, [_D, _P, _P, C.c_int32, C.c_int32, _P, _P, _P, _P, _P]),
 }
-_sig.update({f"{_name}_check": _sig[_name]
-             for _name in ("spc_rope", "spc_prompt_attn", "spc_extend_kv", "spc_dequantize_kv")})
+_CHECKED = ("spc_rope", "spc_prompt_attn", "spc_extend_kv", "spc_dequantize_kv")
+_sig.update({f"{_name}_check": _sig[_name] for _name in _CHECKED})
 for _name, (_res, _args) in _sig.items():
     _f = getattr(_lib, _name)
     _f.restype = _res
     _f.argtypes = _args
+_CHECKS = {_name: getattr(_lib, f"{_name}_check") for _name in _CHECKED}
 
 
 def _ptr(t):
@@ -323,8 +325,8 @@ def spc_host_gather_prev(d, host_kv, n_cap, idx, k, staging, src, prev_staging, 
 # what a pointer cannot say: rank, shapes, 16-bit elements, the last axis
 # contiguous, and that every tensor is on the current CUDA device.  The dims
 # structs are packed in one go: short calls are bound by this marshalling.
-# Each call's marshalling stands apart (_rope_args and so on), so that a
-# sequence of calls can be checked in whole before its first one.
+# With _later, a list, a call is marshalled and added to it instead of made, so
+# that a sequence of calls is checked in whole before its first one (_all_or_none).
 
 ROPE_KINDS = {"plain": 0, "linear": 1, "bands": 2, "ramp": 3}
 
@@ -394,17 +396,9 @@ def spc_rope_frequencies(rot=128, theta=10000.0, kind="plain", factor=1.0, low=1
 
 
 def spc_rope(q, k, pos, turns, rot=128, interleaved=False, mscale=1.0, v=None, q_out=None, k_out=None, v_out=None,
-             stream=None):
+             stream=None, _later=None):
     """q [B][T][Hq][D], k (and v) [B][T][Hkv][D], q or k None; the outputs of q
     and k default to in place (v is copied, so it needs v_out)."""
-    args = _rope_args(q, k, pos, turns, rot, interleaved, mscale, v, q_out, k_out, v_out, stream)
-    st = _lib.spc_rope(*args) if args else 0
-    if st:
-        raise SpcError("spc_rope", st)
-
-
-def _rope_args(q, k, pos, turns, rot, interleaved, mscale, v, q_out, k_out, v_out, stream):
-    """The C call's arguments, or None where there are no tokens."""
     fn = "spc_rope"
     x = k if q is None else q
     if x is None:
@@ -442,9 +436,14 @@ def _rope_args(q, k, pos, turns, rot, interleaved, mscale, v, q_out, k_out, v_ou
     pos = _words(fn, "pos", pos, torch.int32, B * T, dev)
     turns = _words(fn, "turns", turns, torch.int64, rot // 2, dev)
     if T == 0:
-        return None
+        return
     d = _ROPE.pack(B, T, Hq, Hkv, D, rot, 1 if interleaved else 0, mscale, *ql, *kl, *vl, *qo, *ko, *vo)
-    return d, pos, turns, qp, kp, vp, qop, kop, vop, _raw_stream(stream, dev)
+    if _later is not None:
+        _later.append((fn, (d, pos, turns, qp, kp, vp, qop, kop, vop, _raw_stream(stream, dev)), None))
+        return
+    st = _lib.spc_rope(d, pos, turns, qp, kp, vp, qop, kop, vop, _raw_stream(stream, dev))
+    if st:
+        raise SpcError(fn, st)
 
 
 def _prompt_dims(fn, q, k, v, o, S, q_max, k_max, scale, dev):
@@ -474,7 +473,7 @@ def spc_prompt_attn_workspace_bytes(q, k, v, o, S=None, q_max=None, k_max=None) 
 
 
 def spc_prompt_attn(q, k, v, o, lse=None, q_begin=None, q_len=None, k_begin=None, k_len=None, q_max=None, k_max=None,
-                    scale=None, ws=None, ws_bytes=None, stream=None):
+                    scale=None, ws=None, ws_bytes=None, stream=None, _later=None):
     """q and o: [T][Hq][D] (packed sequences) or [S][T][Hq][D]; k and v
     [T][Hkv][D] or [S][T][Hkv][D].  q_begin, q_len, k_begin, k_len: int32 [S]
     on the device, or None.  q_max, k_max bound the lengths (default: the
@@ -482,22 +481,6 @@ def spc_prompt_attn(q, k, v, o, lse=None, q_begin=None, q_len=None, k_begin=None
     workspace, where one is needed, is taken from torch's allocator for the
     call, which needs the call to be on the current stream; a wait that ran
     out is then found by spc_prompt_attn_status() of the device."""
-    args, own = _prompt_args(q, k, v, o, lse, q_begin, q_len, k_begin, k_len, q_max, k_max, scale, ws, ws_bytes, stream)
-    try:
-        st = _lib.spc_prompt_attn(*args)
-    finally:
-        _free(own)
-    if st:
-        raise SpcError("spc_prompt_attn", st)
-
-
-def _free(own):
-    if own is not None:
-        torch._C._cuda_cudaCachingAllocator_raw_delete(own)
-
-
-def _prompt_args(q, k, v, o, lse, q_begin, q_len, k_begin, k_len, q_max, k_max, scale, ws, ws_bytes, stream):
-    """The C call's arguments, and the workspace taken for it (to be freed after the call) or None."""
     fn = "spc_prompt_attn"
     dev = _device(fn, q)
     S = _sequences(q, k, q_len, k_len, q_begin, k_begin)
@@ -522,7 +505,18 @@ def _prompt_args(q, k, v, o, lse, q_begin, q_len, k_begin, k_len, q_max, k_max, 
         w = _ptr(ws)
         if ws_bytes is None:
             ws_bytes = ws.numel() * ws.element_size()
-    return (d, q.data_ptr(), k.data_ptr(), v.data_ptr(), qb, ql, kb, kl, o.data_ptr(), lse_ptr, w, ws_bytes, s), own
+    if _later is not None:
+        _later.append((fn, (d, q.data_ptr(), k.data_ptr(), v.data_ptr(), qb, ql, kb, kl, o.data_ptr(), lse_ptr, w,
+                            ws_bytes, s), own))
+        return
+    try:
+        st = _lib.spc_prompt_attn(d, q.data_ptr(), k.data_ptr(), v.data_ptr(), qb, ql, kb, kl, o.data_ptr(), lse_ptr, w,
+                                  ws_bytes, s)
+    finally:
+        if own is not None:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(own)
+    if st:
+        raise SpcError(fn, st)
 
 
 def spc_prompt_attn_status(ws=None, stream=None) -> int:
@@ -554,35 +548,45 @@ def _cache_call(fn, d, names, k, v, records, resid):
     return n, _LAYOUT.pack(*kl), _LAYOUT.pack(*vl), ptr, dev
 
 
-def spc_extend_kv(d, k_new, v_new, records, resid, host_kv=None, n_cap=0, stream=None):
+def spc_extend_kv(d, k_new, v_new, records, resid, host_kv=None, n_cap=0, stream=None, _later=None):
     """k_new, v_new: 16-bit [B][n][Hkv][D] of any strides; the caller advances d.N by n."""
-    st = _lib.spc_extend_kv(*_extend_args(d, k_new, v_new, records, resid, host_kv, n_cap, stream))
-    if st:
-        raise SpcError("spc_extend_kv", st)
-
-
-def _extend_args(d, k_new, v_new, records, resid, host_kv, n_cap, stream):
-    n, lk, lv, (rec, res), dev = _cache_call("spc_extend_kv", d, ("k_new", "v_new"), k_new, v_new, records, resid)
-    return (C.byref(d), n, k_new.data_ptr(), v_new.data_ptr(), lk, lv, rec, res, _ptr(host_kv), n_cap,
+    fn = "spc_extend_kv"
+    n, lk, lv, (rec, res), dev = _cache_call(fn, d, ("k_new", "v_new"), k_new, v_new, records, resid)
+    args = (C.byref(d), n, k_new.data_ptr(), v_new.data_ptr(), lk, lv, rec, res, _ptr(host_kv), n_cap,
             _raw_stream(stream, dev))
-
-
-def spc_dequantize_kv(d, records, resid, first, k, v, stream=None):
-    """k, v: 16-bit [B][n][Hkv][D] of any strides, for the tokens first .. first+n-1."""
-    st = _lib.spc_dequantize_kv(*_dequantize_args(d, records, resid, first, k, v, stream))
+    if _later is not None:
+        _later.append((fn, args, None))
+        return
+    st = _lib.spc_extend_kv(*args)
     if st:
-        raise SpcError("spc_dequantize_kv", st)
+        raise SpcError(fn, st)
 
 
-def _dequantize_args(d, records, resid, first, k, v, stream):
-    n, lk, lv, (rec, res), dev = _cache_call("spc_dequantize_kv", d, ("k", "v"), k, v, records, resid)
-    return C.byref(d), rec, res, first, n, k.data_ptr(), v.data_ptr(), lk, lv, _raw_stream(stream, dev)
+def spc_dequantize_kv(d, records, resid, first, k, v, stream=None, _later=None):
+    """k, v: 16-bit [B][n][Hkv][D] of any strides, for the tokens first .. first+n-1."""
+    fn = "spc_dequantize_kv"
+    n, lk, lv, (rec, res), dev = _cache_call(fn, d, ("k", "v"), k, v, records, resid)
+    args = (C.byref(d), rec, res, first, n, k.data_ptr(), v.data_ptr(), lk, lv, _raw_stream(stream, dev))
+    if _later is not None:
+        _later.append((fn, args, None))
+        return
+    st = _lib.spc_dequantize_kv(*args)
+    if st:
+        raise SpcError(fn, st)
 
 
-def _all_or_none(calls):
-    """Makes the calls, pairs of a name and its arguments, in order, unless one of them would be refused: then raises
-    before the first one."""
-    for fn, args in calls:
-        _check(fn, getattr(_lib, fn + "_check")(*args))
-    for fn, args in calls:
-        _check(fn, getattr(_lib, fn)(*args))
+@contextlib.contextmanager
+def _all_or_none():
+    """A list for calls' _later: they are made in order at the end of the block, unless one of them is refused, there or
+    by its check; then none is.  Workspaces that they took are freed in any case."""
+    calls = []
+    try:
+        yield calls
+        for fn, args, _ in calls:
+            _check(fn, _CHECKS[fn](*args))
+        for fn, args, _ in calls:
+            _check(fn, getattr(_lib, fn)(*args))
+    finally:
+        for _, _, own in calls:
+            if own is not None:
+                torch._C._cuda_cudaCachingAllocator_raw_delete(own)

@@ -23,9 +23,9 @@ from __future__ import annotations
 
 import torch
 
-from . import (_all_or_none, _dequantize_args, _extend_args, _free, _prompt_args, _rope_args, spc_append_kv,
-               spc_decode_attn2, spc_host_gather, spc_host_gather_prev, spc_merged_attn, spc_offload_kv,
-               spc_quantize_kv, spc_topk_select, spc_topk_select_prev)
+from . import (_all_or_none, spc_append_kv, spc_decode_attn2, spc_dequantize_kv, spc_extend_kv, spc_host_gather,
+               spc_host_gather_prev, spc_merged_attn, spc_offload_kv, spc_prompt_attn, spc_quantize_kv, spc_rope,
+               spc_topk_select, spc_topk_select_prev)
 
 
 def prefill_layer(d, k, v, records, resid, host_kv, n_cap, stream=None, copy_stream=None):
@@ -69,24 +69,16 @@ def prompt_layer(d, q, k, v, pos, turns, o, records, resid, host_kv=None, n_cap=
             raise ValueError(f"prompt_layer: a follow-up prompt needs history buffers of {N + n} rows")
         kk, vv = (b[:, :, :N + n].transpose(1, 2) for b in history)
     stream = torch.cuda.current_stream() if stream is None else stream
-    own = None
-    with torch.cuda.stream(stream):
-        try:
-            calls = []
-            if N == 0:
-                kk, vv = k, v
-                rope = _rope_args(q, k, pos, turns, rot, interleaved, mscale, None, None, None, None, None)
-            else:
-                calls.append(("spc_dequantize_kv", _dequantize_args(d, records, resid, 0, kk[:, :N], vv[:, :N], None)))
-                rope = _rope_args(q, k, pos, turns, rot, interleaved, mscale, v, None, kk[:, N:], vv[:, N:], None)
-            if rope is not None:
-                calls.append(("spc_rope", rope))
-            attn, own = _prompt_args(q, kk, vv, o, lse, None, None, None, None, None, None, d.scale, ws, None, None)
-            calls.append(("spc_prompt_attn", attn))
-            calls.append(("spc_extend_kv", _extend_args(d, kk[:, N:], vv[:, N:], records, resid, host_kv, n_cap, None)))
-            _all_or_none(calls)
-        finally:
-            _free(own)
+    with torch.cuda.stream(stream), _all_or_none() as calls:
+        if N == 0:
+            kk, vv = kn, vn = k, v
+            spc_rope(q, k, pos, turns, rot, interleaved, mscale, _later=calls)
+        else:
+            kn, vn = kk[:, N:], vv[:, N:]
+            spc_dequantize_kv(d, records, resid, 0, kk[:, :N], vv[:, :N], _later=calls)
+            spc_rope(q, k, pos, turns, rot, interleaved, mscale, v=v, k_out=kn, v_out=vn, _later=calls)
+        spc_prompt_attn(q, kk, vv, o, lse, scale=d.scale, ws=ws, _later=calls)
+        spc_extend_kv(d, kn, vn, records, resid, host_kv, n_cap, _later=calls)
     d.N += n
 
 
