@@ -739,8 +739,8 @@ size_t spc_prompt_attn_workspace_bytes(const spc_prompt_dims* d) {
 }
 
 static spc_status check_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const uint16_t* k, const uint16_t* v,
-                                    const int32_t* q_begin, const uint16_t* o, const void* ws, size_t ws_bytes,
-                                    bool& nothing) {
+                                    const int32_t* q_begin, const uint16_t* o, const float* lse, const void* ws,
+                                    size_t ws_bytes, bool& nothing) {
   nothing = false;
   const spc_status st = check_prompt_dims(d);
   if (st != SPC_OK) return st;
@@ -755,19 +755,27 @@ static spc_status check_prompt_attn(const spc_prompt_dims* d, const uint16_t* q,
   if ((ws == nullptr && (need > 256 || ws_bytes != 0)) || !aligned16(ws)) return SPC_ERR_INVALID;
   if (ws != nullptr && ws_bytes < need) return SPC_ERR_WORKSPACE;
   const int64_t qb = d->q.b ? d->S : 1, kb = d->k.b ? d->S : 1;
-  const size_t ob = layout_bytes(d->o, qb, d->q_tokens, d->Hq);
-  if (overlap(q, layout_bytes(d->q, qb, d->q_tokens, d->Hq), o, ob) ||
-      (k != nullptr && overlap(k, layout_bytes(d->k, kb, d->k_tokens, d->Hkv), o, ob)) ||
-      (v != nullptr && overlap(v, layout_bytes(d->v, kb, d->k_tokens, d->Hkv), o, ob)))
-    return SPC_ERR_INVALID;
+  // what the call writes shares no byte range with what it reads or writes besides
+  const struct {
+    const void* p;
+    size_t bytes;
+  } part[6] = {{q, layout_bytes(d->q, qb, d->q_tokens, d->Hq)},
+               {k, layout_bytes(d->k, kb, d->k_tokens, d->Hkv)},
+               {v, layout_bytes(d->v, kb, d->k_tokens, d->Hkv)},
+               {o, layout_bytes(d->o, qb, d->q_tokens, d->Hq)},
+               {lse, (size_t)qb * d->q_tokens * d->Hq * sizeof(float)},
+               {ws, need}};
+  for (int i = 3; i < 6; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlap(part[i].p, part[i].bytes, part[j].p, part[j].bytes)) return SPC_ERR_INVALID;
   return SPC_OK;
 }
 
 spc_status spc_prompt_attn_check(const spc_prompt_dims* d, const uint16_t* q, const uint16_t* k, const uint16_t* v,
                                  const int32_t* q_begin, const int32_t*, const int32_t*, const int32_t*, uint16_t* o,
-                                 float*, void* ws, size_t ws_bytes, spc_stream) {
+                                 float* lse, void* ws, size_t ws_bytes, spc_stream) {
   bool nothing;
-  return check_prompt_attn(d, q, k, v, q_begin, o, ws, ws_bytes, nothing);
+  return check_prompt_attn(d, q, k, v, q_begin, o, lse, ws, ws_bytes, nothing);
 }
 
 spc_status spc_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const uint16_t* k, const uint16_t* v,
@@ -775,7 +783,7 @@ spc_status spc_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const ui
                            const int32_t* k_len, uint16_t* o, float* lse, void* ws, size_t ws_bytes,
                            spc_stream stream) {
   bool nothing;
-  const spc_status st = check_prompt_attn(d, q, k, v, q_begin, o, ws, ws_bytes, nothing);
+  const spc_status st = check_prompt_attn(d, q, k, v, q_begin, o, lse, ws, ws_bytes, nothing);
   if (st != SPC_OK || nothing) return st;
   return spc::launch_prompt_attn(d, q, k, v, q_begin, q_len, k_begin, k_len, o, lse, ws,
                                  reinterpret_cast<cudaStream_t>(stream));

@@ -477,6 +477,8 @@ size_t spc_prompt_attn_workspace_bytes(const spc_prompt_dims* d);
  *   lse     : fp32 [q_tokens][Hq] (packed) or [S][q_tokens][Hq], or NULL.
  *   ws      : at least spc_prompt_attn_workspace_bytes(d) bytes, or NULL with
  *            ws_bytes 0 where that is 256.
+ * Neither lse nor those bytes of ws share a byte range with another tensor
+ * (SPC_ERR_INVALID).
  * One launch, and a second, small one where the keys are split.
  */
 spc_status spc_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const uint16_t* k, const uint16_t* v,

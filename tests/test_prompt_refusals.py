@@ -132,3 +132,24 @@ def test_reading_back_refuses_exactly_the_views_that_share_rows():
         assert got == (INVALID if want else 0), (n, strides, by)
         seen.add((want, abs(by) < far))
     assert seen == {(True, True), (False, True), (False, False)}
+
+
+# ------------------------------------------------------------------------------------------------ lse and workspace
+Q_BYTES, K_BYTES, LSE_BYTES = 2 * 64 * 1024 * 2, 2 * 96 * 256 * 2, 2 * 64 * 8 * 4  # of attn_args' call
+
+
+@pytest.mark.parametrize("over", [
+    dict(lse=(1 << 30) + 64), dict(lse=(1 << 30) - LSE_BYTES + 4), dict(lse=(1 << 31) + K_BYTES - 4), dict(lse=1 << 32),
+    dict(lse=(1 << 33) + Q_BYTES - 4), dict(ws=1 << 30, ws_bytes=256), dict(ws=(1 << 31) - 240, ws_bytes=256),
+    dict(ws=(1 << 32) + K_BYTES - 16, ws_bytes=256), dict(ws=1 << 33, ws_bytes=256),
+    dict(lse=1 << 34, ws=(1 << 34) + LSE_BYTES - 16, ws_bytes=256), dict(lse=1 << 34, ws=(1 << 34) - 240, ws_bytes=256)])
+def test_attention_refuses_an_lse_or_workspace_on_other_rows(over):
+    assert _lib.spc_prompt_attn_check(*attn_args(**over)) == INVALID
+
+
+@pytest.mark.parametrize("over", [
+    dict(lse=(1 << 30) - LSE_BYTES), dict(lse=(1 << 31) + K_BYTES), dict(lse=(1 << 33) + Q_BYTES),
+    dict(ws=(1 << 30) - 256, ws_bytes=1 << 20), dict(lse=1 << 34, ws=(1 << 34) + LSE_BYTES, ws_bytes=256)])
+def test_attention_takes_an_lse_or_workspace_beside_other_rows(over):
+    """Of a workspace, the bytes that the call needs count."""
+    assert _lib.spc_prompt_attn_check(*attn_args(**over)) == 0
