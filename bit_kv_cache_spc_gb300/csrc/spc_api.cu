@@ -546,6 +546,9 @@ spc_status spc_host_gather_prev(const spc_dims* d, const uint16_t* host_kv, int6
 // ---------------------------------------------------------------- the prompt path
 namespace {
 
+// On the boundary of a 4-byte element, as an int32 or binary32 array has to be.
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 // A view of [b][t][h][128] whose rows lie on 16-byte boundaries and apart from
 // one another: each stride, smallest first, clears what the smaller ones span
 // (an axis of one element is never stepped along).
@@ -675,7 +678,8 @@ static spc_status check_rope(const spc_rope_dims* d, const int32_t* pos, const u
     nothing = true;
     return SPC_OK;
   }
-  if (pos == nullptr || turns == nullptr || (reinterpret_cast<uintptr_t>(turns) & 7u) != 0) return SPC_ERR_INVALID;
+  if (pos == nullptr || turns == nullptr || !aligned4(pos) || (reinterpret_cast<uintptr_t>(turns) & 7u) != 0)
+    return SPC_ERR_INVALID;
   const struct {
     const uint16_t *in, *out;
     const spc_layout *li, *lo;
@@ -739,7 +743,8 @@ size_t spc_prompt_attn_workspace_bytes(const spc_prompt_dims* d) {
 }
 
 static spc_status check_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const uint16_t* k, const uint16_t* v,
-                                    const int32_t* q_begin, const uint16_t* o, const float* lse, const void* ws,
+                                    const int32_t* q_begin, const int32_t* q_len, const int32_t* k_begin,
+                                    const int32_t* k_len, const uint16_t* o, const float* lse, const void* ws,
                                     size_t ws_bytes, bool& nothing) {
   nothing = false;
   const spc_status st = check_prompt_dims(d);
@@ -751,6 +756,8 @@ static spc_status check_prompt_attn(const spc_prompt_dims* d, const uint16_t* q,
   if (d->S > 1 && d->q.b == 0 && q_begin == nullptr) return SPC_ERR_INVALID;  // all on the same query rows
   if (q == nullptr || o == nullptr || (d->k_max > 0 && (k == nullptr || v == nullptr))) return SPC_ERR_INVALID;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return SPC_ERR_INVALID;
+  if (!aligned4(q_begin) || !aligned4(q_len) || !aligned4(k_begin) || !aligned4(k_len) || !aligned4(lse))
+    return SPC_ERR_INVALID;
   const size_t need = spc::prompt_workspace_bytes(d);
   if ((ws == nullptr && (need > 256 || ws_bytes != 0)) || !aligned16(ws)) return SPC_ERR_INVALID;
   if (ws != nullptr && ws_bytes < need) return SPC_ERR_WORKSPACE;
@@ -772,10 +779,10 @@ static spc_status check_prompt_attn(const spc_prompt_dims* d, const uint16_t* q,
 }
 
 spc_status spc_prompt_attn_check(const spc_prompt_dims* d, const uint16_t* q, const uint16_t* k, const uint16_t* v,
-                                 const int32_t* q_begin, const int32_t*, const int32_t*, const int32_t*, uint16_t* o,
-                                 float* lse, void* ws, size_t ws_bytes, spc_stream) {
+                                 const int32_t* q_begin, const int32_t* q_len, const int32_t* k_begin,
+                                 const int32_t* k_len, uint16_t* o, float* lse, void* ws, size_t ws_bytes, spc_stream) {
   bool nothing;
-  return check_prompt_attn(d, q, k, v, q_begin, o, lse, ws, ws_bytes, nothing);
+  return check_prompt_attn(d, q, k, v, q_begin, q_len, k_begin, k_len, o, lse, ws, ws_bytes, nothing);
 }
 
 spc_status spc_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const uint16_t* k, const uint16_t* v,
@@ -783,7 +790,7 @@ spc_status spc_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const ui
                            const int32_t* k_len, uint16_t* o, float* lse, void* ws, size_t ws_bytes,
                            spc_stream stream) {
   bool nothing;
-  const spc_status st = check_prompt_attn(d, q, k, v, q_begin, o, lse, ws, ws_bytes, nothing);
+  const spc_status st = check_prompt_attn(d, q, k, v, q_begin, q_len, k_begin, k_len, o, lse, ws, ws_bytes, nothing);
   if (st != SPC_OK || nothing) return st;
   return spc::launch_prompt_attn(d, q, k, v, q_begin, q_len, k_begin, k_len, o, lse, ws,
                                  reinterpret_cast<cudaStream_t>(stream));

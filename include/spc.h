@@ -371,7 +371,8 @@ spc_status spc_offload_kv(const spc_dims* d, const uint16_t* k, const uint16_t* 
  * negative, and no two rows share a byte.  The calls below take such views, so
  * that projections are used where they are: a fused projection
  * [B][T][Hq + 2 Hkv][D] is three views of it, and a cache buffer
- * [B][Hkv][cap][D] is the view {Hkv*cap*D, D, cap*D}.
+ * [B][Hkv][cap][D] is the view {Hkv*cap*D, D, cap*D}.  Their int32 and fp32
+ * arrays lie on 4-byte boundaries (SPC_ERR_INVALID otherwise).
  */
 typedef struct spc_layout {
   int64_t b, t, h;

@@ -153,3 +153,16 @@ def test_attention_refuses_an_lse_or_workspace_on_other_rows(over):
 def test_attention_takes_an_lse_or_workspace_beside_other_rows(over):
     """Of a workspace, the bytes that the call needs count."""
     assert _lib.spc_prompt_attn_check(*attn_args(**over)) == 0
+
+
+# ------------------------------------------------------------------------------------------------ arrays off their elements
+@pytest.mark.parametrize("name", ["q_begin", "q_len", "k_begin", "k_len", "lse"])
+@pytest.mark.parametrize("by", [1, 2, 3])
+def test_attention_refuses_arrays_off_their_elements(name, by):
+    assert _lib.spc_prompt_attn_check(*attn_args(**{name: (1 << 34) + by})) == INVALID
+    assert _lib.spc_prompt_attn_check(*attn_args(**{name: (1 << 34) + 4})) == 0
+
+
+def test_rope_refuses_positions_off_their_elements():
+    assert _lib.spc_rope_check(*rope_args(pos=18)) == INVALID
+    assert _lib.spc_rope_check(*rope_args(pos=20)) == 0
