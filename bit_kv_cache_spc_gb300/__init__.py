@@ -450,7 +450,7 @@ def _prompt_dims(fn, q, k, v, o, S, q_max, k_max, scale, dev):
     qs, qt, Hq, D, ql = _view(fn, "q", q, dev)
     ks, kt, Hkv, Dk, kl = _view(fn, "k", k, dev)
     vl, ol = _like(fn, "v", v, dev, k), _like(fn, "o", o, dev, q)
-    if Dk != D:
+    if Dk != D or D == 0:
         raise ValueError(f"{fn}: q has rows of {D} elements, k of {Dk}")
     if (qs != S and q.dim() == 4) or (ks != S and k.dim() == 4):
         raise ValueError(f"{fn}: batches of {qs} and {ks}, and there are {S} sequences")
@@ -500,11 +500,14 @@ def spc_prompt_attn(q, k, v, o, lse=None, q_begin=None, q_len=None, k_begin=None
         else:
             ws_bytes = 0
     else:
-        if not isinstance(ws, int) and ws.get_device() != dev:
-            raise ValueError(f"{fn}: ws must be on the current CUDA device")
         w = _ptr(ws)
-        if ws_bytes is None:
-            ws_bytes = ws.numel() * ws.element_size()
+        if not isinstance(ws, int):
+            if ws.get_device() != dev or not ws.is_contiguous():
+                raise ValueError(f"{fn}: ws must be contiguous on the current CUDA device")
+            if ws_bytes is None:
+                ws_bytes = ws.numel() * ws.element_size()
+        elif ws_bytes is None:
+            raise ValueError(f"{fn}: a workspace given by its address needs ws_bytes")
     if _later is not None:
         _later.append((fn, (d, q.data_ptr(), k.data_ptr(), v.data_ptr(), qb, ql, kb, kl, o.data_ptr(), lse_ptr, w,
                             ws_bytes, s), own))
