@@ -962,8 +962,7 @@ def measure_config(cfg, peak_gbs, oracle_on=True, reps=10, rig=None):
             secs = [ref.run() for _ in range(2 if cfg["N"] >= 65536 else 3)]
             dt = statistics.median(secs)
             pt["oracle_ms_per_layer"] = ref.layer_ms(dt)
-            pt["oracle_sample"] = (f"merged attention + top-k + gather of {ref.P} of {ref.pairs_per_layer} "
-                                   f"(b, kv-head) pairs, {ref.threads} threads, scaled to the layer")
+            pt["oracle_pairs"], pt["layer_pairs"], pt["oracle_threads"] = ref.P, ref.pairs_per_layer, ref.threads
         out.append(pt)
     return out
 
@@ -997,6 +996,29 @@ def measure_configs(peak_gbs, oracle_on=True, log=None):
     res["c5"] = dict(workload="LLaMA-3-8B layer (32 query / 8 KV heads), B in {1, 4}, N in {4096, 16384, 65536, "
                               "131072}, 1 and 2 bits, k = 0.5 / 1 / 4 % of N", points=pts)
     return res
+
+
+def configs_table(res):
+    """The points of measure_configs as rows of one table, numbers to five significant digits: the names stand once
+    (spelled out for each point the JSON line was 45 KB, too long for what reads it)."""
+    if res is None:
+        return None
+    columns = []
+    for cfg in res.values():
+        for pt in cfg.get("points", []):
+            columns += [name for name in pt if name not in columns]
+
+    def short(x):
+        return float(f"{x:.5g}") if isinstance(x, float) else x
+
+    out = {"columns": columns,
+           "oracle": "merged attention + top-k + gather of oracle_pairs of the layer_pairs (b, kv-head) pairs, scaled "
+                     "to the layer"}
+    for name, cfg in res.items():
+        out[name] = dict(cfg)
+        if "points" in cfg:
+            out[name]["points"] = [[short(pt.get(c)) for c in columns] for pt in cfg["points"]]
+    return out
 
 
 # ------------------------------------------------------------------ ranks
@@ -1321,7 +1343,7 @@ def main():
                                      "microseconds longer than in the timed step)"},
             "append": append,
             "nonspeculative_baseline": serial,
-            "prefill": prefill, "configs": configs, "clocks": clk.summary(), "e2e": e2e,
+            "prefill": prefill, "configs": configs_table(configs), "clocks": clk.summary(), "e2e": e2e,
             "gpu_launches": launches_per_step * args.steps}
     if rank == 0 and not args.no_cpu_baseline:
         pairs = args.cpu_pairs or min(W["B"] * W["Hkv"], max(16, host_cores()))

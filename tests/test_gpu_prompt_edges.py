@@ -114,3 +114,30 @@ def test_rows_of_no_elements_are_refused():
     x = torch.zeros((4, 2, 0), dtype=torch.bfloat16, device="cuda")
     with pytest.raises(ValueError):
         spc.spc_prompt_attn(x, x, x, torch.zeros_like(x))
+
+
+def test_captured_without_a_workspace_of_its_own():
+    """Two split calls captured in one graph, each with the workspace it takes: replayed, between other allocations of
+    the same sizes, they give the eager calls' bits."""
+    import bit_kv_cache_spc_gb300 as spc
+    calls = []
+    for seed, n in ((1, 4000), (5, 7000)):
+        q, k, v = rnd(seed, 1, 8, D), rnd(seed + 1, n, 2, D), rnd(seed + 2, n, 2, D)
+        calls.append((q, k, v, torch.zeros_like(q), torch.zeros_like(q)))
+    for q, k, v, o, want in calls:
+        assert spc.spc_prompt_attn_workspace_bytes(q, k, v, o) > 256
+        spc.spc_prompt_attn(q, k, v, want)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for q, k, v, o, _ in calls:
+            spc.spc_prompt_attn(q, k, v, o)
+    for _ in range(3):
+        for *_, o, _ in calls:
+            o.fill_(7.0)
+        other = [torch.full((1 << 18,), math.nan, device="cuda") for _ in range(4)]
+        g.replay()
+        more = [torch.full((1 << 18,), math.nan, device="cuda") for _ in range(4)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, want) for *_, o, want in calls)
+        del other, more
