@@ -15,7 +15,8 @@
 // Bound by HBM: 512 bytes written per token and KV head against 48 to 96 read.
 // Eight 32768-token caches of 8 KV heads at 1 bit (1.21 GB) take 176 us, the
 // measured copy rate (g = 64 171); at 2 bits (1.28 GB) 212, 89% of it, bound
-// by the selects' issue.  The code words come through shared memory, so that a
+// by the selects' issue (74% of the cycles issue; eight CTAs an SM leave 32
+// registers, and 32 bytes spill).  The code words come through shared memory, so that a
 // thread holds few of them and eight CTAs fit on an SM (words straight into
 // registers, five CTAs: 240 us, and 179 at 1 bit with six).  Levels per thread
 // instead of per group: 24 us against 18 for two 2-bit caches of 32 heads and

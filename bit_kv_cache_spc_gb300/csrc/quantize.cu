@@ -78,7 +78,7 @@ __device__ __forceinline__ void code_group(QuantSmem& sm, const uint16_t* ks, co
     const float rs = quant_recip(s);
     if (BITS == 1) {
       sm.kt[0][c] = code_threshold<1>(lo, hi, z, s, rs, 1u);
-    } else {  // three thresholds of the dearer 2-bit code cost more than the codes they replace
+    } else {  // three searches by the dearer 2-bit code cost more than the codes they replace
       sm.kt[0][c] = z;
       sm.kt[1][c] = s;
       sm.kt[2][c] = rs;
@@ -90,8 +90,10 @@ __device__ __forceinline__ void code_group(QuantSmem& sm, const uint16_t* ks, co
   // ---- key codes: warp per token, one ballot per code word.  At 1 bit a
   // code is one comparison with the channel's threshold, found once per
   // channel for the group's tokens (a value group's 32 elements are spread
-  // over 4 lanes, 8 each, and the 2-bit code needs three thresholds: there the
-  // per-element quotient costs less) ----
+  // over 4 lanes, 8 each, and the 2-bit code needs three searches of
+  // code_threshold: there the per-element quotient costs less.  extend.cu, whose
+  // threads hold a value group each, finds all thresholds without a quotient,
+  // code_thresholds, and writes the same bytes at twice the rate) ----
   {
     float T[4][3];  // 1 bit: the channel's threshold; 2 bits: its z, s, 1/s
 #pragma unroll

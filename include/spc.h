@@ -446,7 +446,9 @@ spc_status spc_rope(const spc_rope_dims* d, const int32_t* pos, const uint64_t* 
  * normaliser.  Query head h uses KV head h / G, G = Hq / Hkv (1 .. 128).  A
  * query that sees no key (lk < lq) gets o = 0 and lse = -infinity.
  * What keys and values hold in places that a query does not see does not
- * change its output, infinities and NaN included.
+ * change its output, infinities and NaN included.  The weighted sum of values
+ * is formed before it is divided by the sum of weights, with weights of up to
+ * 2^8, in binary32: values beyond 2^119 / (number of keys) may overflow in it.
  */
 typedef struct spc_prompt_dims {
   int32_t S, Hq, Hkv, D;      /* D = 128 */
