@@ -1051,7 +1051,10 @@ cudaError_t launch_prompt_k(const CUtensorMap& qm, const CUtensorMap& km, const 
 
 }  // namespace
 
-int64_t prompt_wait_limit(int64_t ns) { return ns > 0 ? prompt_limit.exchange(ns) : prompt_limit.load(); }
+// (held to 1000 s, so that no sum of times overflows: mbar_wait)
+int64_t prompt_wait_limit(int64_t ns) {
+  return ns > 0 ? prompt_limit.exchange(std::min<int64_t>(ns, 1000000000000)) : prompt_limit.load();
+}
 
 cudaError_t prompt_fault_word(void** word) { return cudaGetSymbolAddress(word, prompt_device_fault); }
 

@@ -498,8 +498,8 @@ spc_status spc_prompt_attn_status(void* ws, spc_stream stream);
 /* The limit of a wait in spc_prompt_attn's kernels, in ns (2 * 10^9 unless set;
  * regular waits last microseconds, but for one that lasts as long as a CTA
  * walks over keys that its rows see in full: its limit grows with them).  ns >
- * 0 sets it for the calls of the process from now on (a captured call keeps
- * the one it was captured with), any other value changes nothing.  Returns the
+ * 0 sets it, to 10^12 at most, for the calls of the process from now on (a
+ * captured call keeps the one it was captured with), any other value changes nothing.  Returns the
  * limit before the call.  A wait that runs out ends its CTA early, whose rows
  * of o and lse then hold no result. */
 int64_t spc_prompt_attn_wait_limit(int64_t ns);

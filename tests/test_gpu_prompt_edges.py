@@ -141,3 +141,47 @@ def test_captured_without_a_workspace_of_its_own():
         torch.cuda.synchronize()
         assert all(torch.equal(o, want) for *_, o, want in calls)
         del other, more
+
+
+@pytest.mark.parametrize("before", [0, 300])
+def test_a_captured_prompt_layer(before):
+    """A prompt's calls captured together (the cache's length is that of the capture): replayed on other projections,
+    the bits of the eager call."""
+    import bit_kv_cache_spc_gb300 as spc
+    from bit_kv_cache_spc_gb300.steps import prompt_layer
+    B, n, Hq, Hkv, total = 2, 90, 8, 2, 390
+    turns = spc.spc_rope_frequencies(128)[0].cuda()
+    made = []
+    for captured in (False, True):
+        d = spc.Dims(B, Hq, Hkv, 0, 16, 1, q_groups_cap=total // 32 + 1, resid_cap=48)
+        rec = torch.zeros(spc.spc_records_bytes(d), dtype=torch.uint8, device="cuda")
+        res = torch.zeros(spc.spc_resid_bytes(d) // 2, dtype=torch.int16, device="cuda")
+        history = torch.zeros((2, B, Hkv, total, D), dtype=torch.bfloat16, device="cuda")
+        o = torch.zeros((B, n, Hq, D), dtype=torch.bfloat16, device="cuda")
+
+        def prompt(x, out):
+            at = d.N + torch.arange(x.shape[1], device="cuda", dtype=torch.int32)
+            q, k, v = x.split([Hq, Hkv, Hkv], dim=2)
+            return lambda: prompt_layer(d, q, k, v, at.expand(B, -1).contiguous(), turns, out, rec, res, history=history)
+
+        if before:
+            prompt(rnd(1, B, before, Hq + 2 * Hkv, D), torch.zeros((B, before, Hq, D), dtype=torch.bfloat16, device="cuda"))()
+        x = rnd(2, B, n, Hq + 2 * Hkv, D)
+        if captured:
+            start, empty = (rec.clone(), res.clone()), torch.zeros_like(x)
+            call = prompt(empty, o)
+            torch.cuda.synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                call()
+            rec.copy_(start[0])
+            res.copy_(start[1])
+            empty.copy_(x)
+            g.replay()
+        else:
+            prompt(x, o)()
+        torch.cuda.synchronize()
+        assert d.N == before + n
+        made.append((o, rec, res, history))
+    assert all(torch.equal(x, y) for x, y in zip(*made))
+    assert bool((made[0][0] != 0).any()) and spc.spc_prompt_attn_status() == 0

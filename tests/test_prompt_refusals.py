@@ -166,3 +166,11 @@ def test_attention_refuses_arrays_off_their_elements(name, by):
 def test_rope_refuses_positions_off_their_elements():
     assert _lib.spc_rope_check(*rope_args(pos=18)) == INVALID
     assert _lib.spc_rope_check(*rope_args(pos=20)) == 0
+
+
+def test_the_wait_limit_is_held_to_a_thousand_seconds():
+    try:
+        spc.spc_prompt_attn_wait_limit(2 ** 63 - 1)
+        assert spc.spc_prompt_attn_wait_limit() == 10 ** 12
+    finally:
+        spc.spc_prompt_attn_wait_limit(2_000_000_000)
