@@ -254,8 +254,8 @@ constexpr int kResident = 232448 / (sizeof(ExtendSmem<BITS, GROUP>) + 1024);
 // groups per CTA are slower where groups are few (300 tokens into eight caches
 // 8.3 us against 6.9), and neighbours that take the KV heads of the same
 // tokens instead of a head's groups in turn are too (98).
-// 1 bit, g = 32, four 32768-token prompts over 8 KV heads (606 MB): 93 to 100
-// us from call to call, 6.1 to 6.5 TB/s, 90 to 96% of the measured copy
+// 1 bit, g = 32, four 32768-token prompts over 8 KV heads (606 MB): 93 to 102
+// us from process to process, 5.9 to 6.5 TB/s, 87 to 96% of the measured copy
 // bandwidth; g = 64 91 us; 2 bits 128 and 113 us, 74% of it at g = 32, bound by
 // the thresholds' and comparisons' issue (68% of the cycles issue, and of the
 // waiting warps more are ready or wait for the arithmetic pipes than for
