@@ -25,6 +25,7 @@ __all__ = [
     "spc_host_gather", "spc_merged_attn_noalloc", "spc_merged_attn_fetch", "spc_attn_kernel_count",
     "spc_decode_step_kernel_count", "spc_decode_step_on_chip", "spc_decode_step", "spc_step_workspace_bytes",
     "spc_read_device_status", "spc_append_kv", "spc_offload_kv", "spc_rope_frequencies", "spc_rope",
+    "spc_rope_axes", "spc_norm_rope",
     "spc_prompt_attn", "spc_prompt_attn_workspace_bytes", "spc_prompt_attn_status",
     "spc_prompt_attn_wait_limit", "spc_extend_kv", "spc_dequantize_kv", "lib_path",
 ]
@@ -87,6 +88,10 @@ class spc_rope_dims(C.Structure):
                     (n, spc_layout) for n in ("q", "k", "v", "q_out", "k_out", "v_out")]
 
 
+class spc_norm_rope_dims(C.Structure):
+    _fields_ = [("rope", spc_rope_dims), ("axes", C.c_int32), ("eps", C.c_float), ("axis", C.c_uint8 * 64)]
+
+
 class spc_prompt_dims(C.Structure):
     _fields_ = [(n, C.c_int32) for n in ("S", "Hq", "Hkv", "D", "q_tokens", "k_tokens", "q_max", "k_max")] + [
         ("scale", C.c_float)] + [(n, spc_layout) for n in ("q", "k", "v", "o")]
@@ -128,6 +133,8 @@ _sig = {
     "spc_read_device_status": (C.c_int, [_P, _D, _P]),
     "spc_rope_frequencies": (C.c_int, [C.POINTER(spc_rope_scaling), C.c_int32, _P, C.POINTER(C.c_float)]),
     "spc_rope": (C.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "spc_rope_axes": (C.c_int, [_P, C.c_int32, C.c_int32, C.c_int32, _P]),
+    "spc_norm_rope": (C.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     "spc_prompt_attn_workspace_bytes": (C.c_size_t, [_P]),
     "spc_prompt_attn": (C.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, C.c_size_t, _P]),
     "spc_prompt_attn_status": (C.c_int, [_P, _P]),
@@ -135,7 +142,7 @@ _sig = {
     "spc_extend_kv": (C.c_int, [_D, C.c_int32, _P, _P, _P, _P, _P, _P, _P, C.c_int64, _P]),
     "spc_dequantize_kv": (C.c_int, [_D, _P, _P, C.c_int32, C.c_int32, _P, _P, _P, _P, _P]),
 }
-_CHECKED = ("spc_rope", "spc_prompt_attn", "spc_extend_kv", "spc_dequantize_kv")
+_CHECKED = ("spc_rope", "spc_norm_rope", "spc_prompt_attn", "spc_extend_kv", "spc_dequantize_kv")
 _sig.update({f"{_name}_check": _sig[_name] for _name in _CHECKED})
 for _name, (_res, _args) in _sig.items():
     _f = getattr(_lib, _name)
@@ -329,12 +336,15 @@ def spc_host_gather_prev(d, host_kv, n_cap, idx, k, staging, src, prev_staging, 
 # that a sequence of calls is checked in whole before its first one (_all_or_none).
 
 ROPE_KINDS = {"plain": 0, "linear": 1, "bands": 2, "ramp": 3}
+AXIS_ORDERS = {"sections": 0, "turns": 1}
 
 _ROWS = frozenset((torch.bfloat16, torch.int16, torch.uint16))  # bf16 values or their bit patterns
 _ROPE = struct.Struct("=7if18q")
+_NORM_ROPE = struct.Struct("=7if18qif64s")
 _PROMPT = struct.Struct("=8if4x12q")
 _LAYOUT = struct.Struct("=3q")
-assert _ROPE.size == C.sizeof(spc_rope_dims) and _PROMPT.size == C.sizeof(spc_prompt_dims)
+assert _ROPE.size == C.sizeof(spc_rope_dims) and _NORM_ROPE.size == C.sizeof(spc_norm_rope_dims)
+assert _PROMPT.size == C.sizeof(spc_prompt_dims)
 
 
 def _device(fn, t):
@@ -395,11 +405,8 @@ def spc_rope_frequencies(rot=128, theta=10000.0, kind="plain", factor=1.0, low=1
     return torch.tensor(buf[:int(rot) // 2], dtype=torch.int64), mscale.value  # below 2^62: positive as int64 too
 
 
-def spc_rope(q, k, pos, turns, rot=128, interleaved=False, mscale=1.0, v=None, q_out=None, k_out=None, v_out=None,
-             stream=None, _later=None):
-    """q [B][T][Hq][D], k (and v) [B][T][Hkv][D], q or k None; the outputs of q
-    and k default to in place (v is copied, so it needs v_out)."""
-    fn = "spc_rope"
+def _rope_rows(fn, q, k, v, q_out, k_out, v_out):
+    """(device, sizes and layouts, pointers) of the rows that a rotation reads and writes."""
     x = k if q is None else q
     if x is None:
         raise ValueError(f"{fn}: neither q nor k")
@@ -433,15 +440,65 @@ def spc_rope(q, k, pos, turns, rot=128, interleaved=False, mscale=1.0, v=None, q
     if v is not None:
         vl, vo = _like(fn, "v", v, dev, k), _like(fn, "v_out", v_out, dev, k)
         vp, vop = v.data_ptr(), v_out.data_ptr()
+    return dev, (B, T, Hq, Hkv, D), (*ql, *kl, *vl, *qo, *ko, *vo), (qp, kp, vp, qop, kop, vop)
+
+
+def spc_rope(q, k, pos, turns, rot=128, interleaved=False, mscale=1.0, v=None, q_out=None, k_out=None, v_out=None,
+             stream=None, _later=None):
+    """q [B][T][Hq][D], k (and v) [B][T][Hkv][D], q or k None; the outputs of q
+    and k default to in place (v is copied, so it needs v_out)."""
+    fn = "spc_rope"
+    dev, (B, T, Hq, Hkv, D), layouts, rows = _rope_rows(fn, q, k, v, q_out, k_out, v_out)
     pos = _words(fn, "pos", pos, torch.int32, B * T, dev)
     turns = _words(fn, "turns", turns, torch.int64, rot // 2, dev)
     if T == 0:
         return
-    d = _ROPE.pack(B, T, Hq, Hkv, D, rot, 1 if interleaved else 0, mscale, *ql, *kl, *vl, *qo, *ko, *vo)
+    d = _ROPE.pack(B, T, Hq, Hkv, D, rot, 1 if interleaved else 0, mscale, *layouts)
+    args = (d, pos, turns, *rows, _raw_stream(stream, dev))
     if _later is not None:
-        _later.append((fn, (d, pos, turns, qp, kp, vp, qop, kop, vop, _raw_stream(stream, dev)), None))
+        _later.append((fn, args, None))
         return
-    st = _lib.spc_rope(d, pos, turns, qp, kp, vp, qop, kop, vop, _raw_stream(stream, dev))
+    st = _lib.spc_rope(*args)
+    if st:
+        raise SpcError(fn, st)
+
+
+def spc_rope_axes(sections, rot=128, order="sections"):
+    """The axis of positions that turns each of the rot/2 pairs (a list, for spc_norm_rope): sections[a] pairs axis a,
+    "sections" behind one another or by "turns" (see spc_axis_order in include/spc.h)."""
+    if order not in AXIS_ORDERS:
+        raise ValueError(f"spc_rope_axes: order is one of {', '.join(AXIS_ORDERS)}, got {order!r}")
+    buf = (C.c_uint8 * 64)()
+    sizes = (C.c_int32 * max(len(sections), 1))(*sections)
+    _check("spc_rope_axes", _lib.spc_rope_axes(sizes, len(sections), AXIS_ORDERS[order], int(rot), buf))
+    return list(buf[:int(rot) // 2])
+
+
+def spc_norm_rope(q, k, pos, turns, q_weight=None, k_weight=None, eps=1e-6, axis=None, rot=128, interleaved=False,
+                  mscale=1.0, v=None, q_out=None, k_out=None, v_out=None, stream=None, _later=None):
+    """spc_rope with a norm of each query and key row before it.  q_weight, k_weight: fp32 [D] on the device, or None
+    (rows not normed).  pos: int32 [B][T], or [axes][B][T] with axis, the axis that turns each of the rot/2 pairs (a
+    sequence of rot/2 numbers; see spc_rope_axes)."""
+    fn = "spc_norm_rope"
+    dev, (B, T, Hq, Hkv, D), layouts, rows = _rope_rows(fn, q, k, v, q_out, k_out, v_out)
+    axes = pos.shape[0] if pos.dim() == 3 else 1
+    if axis is None:
+        if axes != 1:
+            raise ValueError(f"{fn}: positions of {axes} axes need axis")
+        axis = b""
+    elif len(axis) != rot // 2 or not all(0 <= a < axes for a in axis):
+        raise ValueError(f"{fn}: axis must be {rot // 2} numbers from 0 to {axes - 1}")
+    pos = _words(fn, "pos", pos, torch.int32, axes * B * T, dev)
+    turns = _words(fn, "turns", turns, torch.int64, rot // 2, dev)
+    wq, wk = _words(fn, "q_weight", q_weight, torch.float32, D, dev), _words(fn, "k_weight", k_weight, torch.float32, D, dev)
+    if T == 0:
+        return
+    d = _NORM_ROPE.pack(B, T, Hq, Hkv, D, rot, 1 if interleaved else 0, mscale, *layouts, axes, eps, bytes(axis))
+    args = (d, pos, turns, wq, wk, *rows, _raw_stream(stream, dev))
+    if _later is not None:
+        _later.append((fn, args, None))
+        return
+    st = _lib.spc_norm_rope(*args)
     if st:
         raise SpcError(fn, st)
 

@@ -25,6 +25,9 @@ spc_status launch_append(const spc_dims*, const uint16_t*, const uint16_t*, void
                          cudaStream_t);
 spc_status launch_rope(const spc_rope_dims*, const int32_t*, const uint64_t*, const uint16_t*, const uint16_t*,
                        const uint16_t*, uint16_t*, uint16_t*, uint16_t*, cudaStream_t);
+spc_status launch_norm_rope(const spc_norm_rope_dims*, const int32_t*, const uint64_t*, const float*, const float*,
+                            const uint16_t*, const uint16_t*, const uint16_t*, uint16_t*, uint16_t*, uint16_t*,
+                            cudaStream_t);
 size_t prompt_workspace_bytes(const spc_prompt_dims*);
 int64_t prompt_wait_limit(int64_t);
 cudaError_t prompt_fault_word(void**);
@@ -718,6 +721,71 @@ spc_status spc_rope(const spc_rope_dims* d, const int32_t* pos, const uint64_t* 
   const spc_status st = check_rope(d, pos, turns, q, k, v, q_out, k_out, v_out, nothing);
   if (st != SPC_OK || nothing) return st;
   return spc::launch_rope(d, pos, turns, q, k, v, q_out, k_out, v_out, reinterpret_cast<cudaStream_t>(stream));
+}
+
+spc_status spc_rope_axes(const int32_t* sections, int32_t axes, int32_t order, int32_t rot, uint8_t* axis) {
+  if (sections == nullptr || axis == nullptr || axes < 1 || axes > 4) return SPC_ERR_INVALID;
+  if (order != SPC_AXIS_SECTIONS && order != SPC_AXIS_TURNS) return SPC_ERR_INVALID;
+  if (rot < 16 || rot > spc::kD || rot % 16 != 0) return SPC_ERR_UNSUPPORTED;
+  int64_t sum = 0;
+  for (int32_t a = 0; a < axes; ++a) {
+    if (sections[a] < 0) return SPC_ERR_INVALID;
+    sum += sections[a];
+  }
+  if (sum != rot / 2) return SPC_ERR_INVALID;
+  uint8_t of[spc::kD / 2];
+  int32_t count[4] = {0, 0, 0, 0}, section = 0, left = sections[0];
+  for (int32_t i = 0; i < rot / 2; ++i) {
+    if (order == SPC_AXIS_SECTIONS) {
+      while (left == 0) left = sections[++section];
+      --left;
+      of[i] = (uint8_t)section;
+    } else {
+      of[i] = (uint8_t)(i < axes * sections[i % axes] ? i % axes : 0);
+    }
+    ++count[of[i]];
+  }
+  for (int32_t a = 0; a < axes; ++a)
+    if (count[a] != sections[a]) return SPC_ERR_INVALID;
+  std::copy(of, of + rot / 2, axis);
+  return SPC_OK;
+}
+
+static spc_status check_norm_rope(const spc_norm_rope_dims* d, const int32_t* pos, const uint64_t* turns,
+                                  const float* q_weight, const float* k_weight, const uint16_t* q, const uint16_t* k,
+                                  const uint16_t* v, const uint16_t* q_out, const uint16_t* k_out,
+                                  const uint16_t* v_out, bool& nothing) {
+  nothing = false;
+  if (d == nullptr) return SPC_ERR_INVALID;
+  const spc_status st = check_rope(&d->rope, pos, turns, q, k, v, q_out, k_out, v_out, nothing);
+  if (st != SPC_OK) return st;
+  if (d->axes < 1 || d->axes > 4) return SPC_ERR_INVALID;
+  for (int32_t i = 0; i < d->rope.rot / 2; ++i)
+    if (d->axis[i] >= d->axes) return SPC_ERR_INVALID;
+  if ((q_weight != nullptr || k_weight != nullptr) && !(std::isfinite(d->eps) && d->eps >= 1e-30f))
+    return SPC_ERR_INVALID;
+  if (nothing) return SPC_OK;
+  if ((q_weight != nullptr && q == nullptr) || (k_weight != nullptr && k == nullptr)) return SPC_ERR_INVALID;
+  if (!aligned4(q_weight) || !aligned4(k_weight)) return SPC_ERR_INVALID;
+  return SPC_OK;
+}
+
+spc_status spc_norm_rope_check(const spc_norm_rope_dims* d, const int32_t* pos, const uint64_t* turns,
+                               const float* q_weight, const float* k_weight, const uint16_t* q, const uint16_t* k,
+                               const uint16_t* v, uint16_t* q_out, uint16_t* k_out, uint16_t* v_out, spc_stream) {
+  bool nothing;
+  return check_norm_rope(d, pos, turns, q_weight, k_weight, q, k, v, q_out, k_out, v_out, nothing);
+}
+
+spc_status spc_norm_rope(const spc_norm_rope_dims* d, const int32_t* pos, const uint64_t* turns, const float* q_weight,
+                         const float* k_weight, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                         uint16_t* q_out, uint16_t* k_out, uint16_t* v_out, spc_stream stream) {
+  bool nothing;
+  const spc_status st =
+      check_norm_rope(d, pos, turns, q_weight, k_weight, q, k, v, q_out, k_out, v_out, nothing);
+  if (st != SPC_OK || nothing) return st;
+  return spc::launch_norm_rope(d, pos, turns, q_weight, k_weight, q, k, v, q_out, k_out, v_out,
+                               reinterpret_cast<cudaStream_t>(stream));
 }
 
 static spc_status check_prompt_dims(const spc_prompt_dims* d) {

@@ -438,6 +438,45 @@ spc_status spc_rope(const spc_rope_dims* d, const int32_t* pos, const uint64_t* 
                     spc_stream stream);
 
 /*
+ * Which axis of the positions turns each pair, for positions of several axes
+ * (time, height and width of a video's tokens, say).  sections (HOST, `axes`
+ * numbers >= 0, in sum rot/2): how many pairs each axis turns.  Fills axis
+ * (HOST, rot/2 bytes).
+ */
+typedef enum spc_axis_order {
+  SPC_AXIS_SECTIONS = 0, /* the first sections[0] pairs axis 0, the next sections[1] axis 1, and so on */
+  SPC_AXIS_TURNS = 1     /* pair i axis a = i % axes where i < axes * sections[a], else axis 0 (SPC_ERR_INVALID where an
+                            axis then turns another number of pairs than its section says) */
+} spc_axis_order;
+
+spc_status spc_rope_axes(const int32_t* sections, int32_t axes, int32_t order, int32_t rot, uint8_t* axis);
+
+typedef struct spc_norm_rope_dims {
+  spc_rope_dims rope;
+  int32_t axes;     /* of the positions: 1 .. 4 */
+  float eps;        /* finite, at least 1e-30 (read where there is a weight) */
+  uint8_t axis[64]; /* of each pair i < rot/2: below axes */
+} spc_norm_rope_dims;
+
+/*
+ * spc_rope with a norm of each query and key head before the rotation, in the
+ * same pass, and with positions of up to four axes: a row x of 128 elements
+ * becomes
+ *   x_j * w_j / sqrt(mean(x^2) + eps),
+ * and pair i of that is turned by pos[axis[i]] * f_i.  Elements rot .. 127 are
+ * normed and not turned.
+ *   pos      : int32 [axes][B][T] (device).
+ *   q_weight : fp32 [128] (device), or NULL: query rows are not normed.
+ *   k_weight : the same of the key rows.
+ * The values' rows are copied as they are.  Everything else as spc_rope.  The
+ * mean, the norm and the rotation are binary32, rounded once to bf16; squares
+ * that overflow binary32 are formed of scaled elements.
+ */
+spc_status spc_norm_rope(const spc_norm_rope_dims* d, const int32_t* pos, const uint64_t* turns, const float* q_weight,
+                         const float* k_weight, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                         uint16_t* q_out, uint16_t* k_out, uint16_t* v_out, spc_stream stream);
+
+/*
  * Causal attention of prompts over 16-bit keys and values (SpeCache page,
  * section 3 "Prefilling": the attention that Quant and Offload follow).
  * S sequences; sequence s has lq query tokens, the last of its lk tokens, and
@@ -538,8 +577,8 @@ spc_status spc_dequantize_kv(const spc_dims* d, const void* records, const uint1
                              spc_stream stream);
 
 /*
- * What spc_rope, spc_prompt_attn, spc_extend_kv and spc_dequantize_kv would
- * refuse, without a launch: the same arguments, and the status that the call
+ * What spc_rope, spc_norm_rope, spc_prompt_attn, spc_extend_kv and
+ * spc_dequantize_kv would refuse, without a launch: the same arguments, and the status that the call
  * would return before it enqueues anything.  For a sequence of calls of which
  * either all are to be made or none (a prompt is rotated in place before its
  * attention and its way into the cache).
@@ -547,6 +586,9 @@ spc_status spc_dequantize_kv(const spc_dims* d, const void* records, const uint1
 spc_status spc_rope_check(const spc_rope_dims* d, const int32_t* pos, const uint64_t* turns, const uint16_t* q,
                           const uint16_t* k, const uint16_t* v, uint16_t* q_out, uint16_t* k_out, uint16_t* v_out,
                           spc_stream stream);
+spc_status spc_norm_rope_check(const spc_norm_rope_dims* d, const int32_t* pos, const uint64_t* turns,
+                               const float* q_weight, const float* k_weight, const uint16_t* q, const uint16_t* k,
+                               const uint16_t* v, uint16_t* q_out, uint16_t* k_out, uint16_t* v_out, spc_stream stream);
 spc_status spc_prompt_attn_check(const spc_prompt_dims* d, const uint16_t* q, const uint16_t* k, const uint16_t* v,
                                  const int32_t* q_begin, const int32_t* q_len, const int32_t* k_begin,
                                  const int32_t* k_len, uint16_t* o, float* lse, void* ws, size_t ws_bytes,
