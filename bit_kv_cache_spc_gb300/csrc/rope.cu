@@ -17,12 +17,7 @@
 // 32768-token prompt of 32 + 8 + 8 heads (805 MB) takes 122 us, 97% of the
 // measured copy rate, against 138 with one head in flight and 123 to 135 with
 // four (fewer resident warps).
-//
-// With norms (spc_norm_rope): the eight lanes of a row add up their squares
-// (three shuffles), x becomes x * w / sqrt(mean + eps) in binary32 on its way
-// into the rotation, and is rounded once, behind it.
 #include <algorithm>
-#include <cstring>
 
 #include "common.cuh"
 
@@ -39,10 +34,6 @@ struct RopeArgs {
   int32_t T, Hq, Hkv, heads, rot, per;  // heads of all three; heads a group of lanes walks over
   int32_t slices;                       // groups of `per` heads
   float mscale;
-  // spc_norm_rope's:
-  const float *wq, *wk;  // null: no norm
-  float eps;
-  uint8_t axis[kD / 2];  // of positions, of each pair
 };
 
 __device__ __forceinline__ uint32_t rope_pack(float lo, float hi) {
@@ -73,70 +64,13 @@ __device__ __forceinline__ void turn_pairs(uint4& u, uint4& w, const float* c, c
   w = make_uint4(y[0], y[1], y[2], y[3]);
 }
 
-// A lane's 16 elements of a row: normed where `weight` says so (its own 16
-// weights: wu of u's elements, ww of w's), then turned where `rot`.
-template <bool INTERLEAVED>
-__device__ __forceinline__ void norm_turn(uint4& u, uint4& w, bool norm, const float4* wu, const float4* ww, float eps,
-                                          bool rot, const float* c, const float* s) {
-  if (!norm && !rot) return;
-  uint32_t bits[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
-  float x[16];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[2 * i] = __uint_as_float(bits[i] << 16);
-    x[2 * i + 1] = __uint_as_float(bits[i] & 0xFFFF0000u);
-  }
-  if (norm) {  // alike for the row's lanes
-    const uint32_t row = 0xFFu << (threadIdx.x & 24u);
-    const auto squares = [&]() {
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) sum = fmaf(x[i], x[i], sum);
-#pragma unroll
-      for (int off = 4; off > 0; off >>= 1) sum += __shfl_xor_sync(row, sum, off);
-      return sum;
-    };
-    float sum = squares();
-    if (sum == INFINITY) {  // elements from 2^60 on: their squares overflow, those of 2^-70 of them do not
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] *= 8.470329472543003e-22f;
-      sum = squares();
-      eps = 0.f;
-    }
-    const float r = rsqrtf(fmaf(sum, 1.f / kD, eps));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 f = i < 2 ? wu[i] : ww[i - 2];
-      x[4 * i] *= r * f.x;
-      x[4 * i + 1] *= r * f.y;
-      x[4 * i + 2] *= r * f.z;
-      x[4 * i + 3] *= r * f.w;
-    }
-  }
-  if (rot) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float& a = x[INTERLEAVED ? 2 * i : i];
-      float& b = x[INTERLEAVED ? 2 * i + 1 : 8 + i];
-      const float y = a * c[i] - b * s[i];
-      b = a * s[i] + b * c[i];
-      a = y;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) bits[i] = rope_pack(x[2 * i], x[2 * i + 1]);
-  u = make_uint4(bits[0], bits[1], bits[2], bits[3]);
-  w = make_uint4(bits[4], bits[5], bits[6], bits[7]);
-}
-
 constexpr int kBatch = 2;
 
-template <bool INTERLEAVED, bool NORM>
+template <bool INTERLEAVED>
 __global__ void __launch_bounds__(256, 4) rope_kernel(const __grid_constant__ RopeArgs a) {
   // (cos, sin) of the CTA's tokens (32 at most), two pairs a chunk: lane l's chunk i of a token lies at 4l + (i ^ l/2),
   // so that the eight lanes of a token read from different banks.
   __shared__ float4 turned_by[32][kD / 4];
-  __shared__ float4 weights[2][NORM ? kD / 4 : 1];
   const uint32_t g0 = blockIdx.x * 32u, token0 = g0 / (uint32_t)a.slices, rest = g0 - token0 * a.slices;
   const uint32_t local = rest + (threadIdx.x >> 3), at = local / (uint32_t)a.slices, token = token0 + at;
   const int l = threadIdx.x & 7;
@@ -168,15 +102,11 @@ __global__ void __launch_bounds__(256, 4) rope_kernel(const __grid_constant__ Ro
     }
   };
   load(h0);  // on its way while the angles are formed
-  if (NORM) {
-    const float* from = threadIdx.x < kD ? a.wq : a.wk;
-    if (from != nullptr) reinterpret_cast<float*>(weights)[threadIdx.x] = from[threadIdx.x % kD];
-  }
   const uint32_t here = min((rest + 31u) / (uint32_t)a.slices + 1u, a.tokens - token0);  // tokens of the CTA
   for (uint32_t i = threadIdx.x; i < here * (kD / 2); i += 256) {
     const uint32_t n = i / (kD / 2), pair = i % (kD / 2);
     if (pair >= (uint32_t)a.rot / 2) continue;
-    const uint64_t p = (uint64_t)(int64_t)a.pos[(NORM ? (int64_t)a.axis[pair] * a.tokens : 0) + token0 + n];
+    const uint64_t p = (uint64_t)(int64_t)a.pos[token0 + n];
     const int32_t turn = (int32_t)((p * a.turns[pair]) >> 32);
     float c, s;
     sincospif((float)turn * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
@@ -200,16 +130,9 @@ __global__ void __launch_bounds__(256, 4) rope_kernel(const __grid_constant__ Ro
       const int h = hb + i;
       if (h >= h1) break;
       const bool rot = turned && h < a.Hq + a.Hkv;
-      const int at_u = !INTERLEAVED && rot ? 8 * l : 16 * l, at_w = !INTERLEAVED && rot ? 8 * l + a.rot / 2 : 16 * l + 8;
-      if (!NORM) {
-        if (rot) turn_pairs<INTERLEAVED>(u[i], w[i], c, s);
-      } else if (h < a.Hq + a.Hkv) {
-        const float4* own = weights[h < a.Hq ? 0 : 1];
-        norm_turn<INTERLEAVED>(u[i], w[i], (h < a.Hq ? a.wq : a.wk) != nullptr, own + at_u / 4, own + at_w / 4, a.eps,
-                               rot, c, s);
-      }
-      *reinterpret_cast<uint4*>(dst[i] + at_u) = u[i];
-      *reinterpret_cast<uint4*>(dst[i] + at_w) = w[i];
+      if (rot) turn_pairs<INTERLEAVED>(u[i], w[i], c, s);
+      *reinterpret_cast<uint4*>(dst[i] + (!INTERLEAVED && rot ? 8 * l : 16 * l)) = u[i];
+      *reinterpret_cast<uint4*>(dst[i] + (!INTERLEAVED && rot ? 8 * l + a.rot / 2 : 16 * l + 8)) = w[i];
     }
     hb += kBatch;
     load(hb);
@@ -218,10 +141,9 @@ __global__ void __launch_bounds__(256, 4) rope_kernel(const __grid_constant__ Ro
 
 }  // namespace
 
-static spc_status launch_rope_k(const spc_rope_dims* d, const spc_norm_rope_dims* norm, const float* q_weight,
-                                const float* k_weight, const int32_t* pos, const uint64_t* turns, const uint16_t* q,
-                                const uint16_t* k, const uint16_t* v, uint16_t* q_out, uint16_t* k_out, uint16_t* v_out,
-                                cudaStream_t stream) {
+spc_status launch_rope(const spc_rope_dims* d, const int32_t* pos, const uint64_t* turns, const uint16_t* q,
+                       const uint16_t* k, const uint16_t* v, uint16_t* q_out, uint16_t* k_out, uint16_t* v_out,
+                       cudaStream_t stream) {
   RopeArgs a = {q, k, v, q_out, k_out, v_out, pos, turns, d->q, d->k, d->v, d->q_out, d->k_out, d->v_out};
   const int64_t tokens = (int64_t)d->B * d->T;
   a.T = d->T;
@@ -239,38 +161,16 @@ static spc_status launch_rope_k(const spc_rope_dims* d, const spc_norm_rope_dims
   if (tokens * a.slices > 0x7FFFFFFF) return SPC_ERR_UNSUPPORTED;
   a.tokens = (uint32_t)tokens;
   const int64_t blocks = (tokens * a.slices + 31) / 32;
-  if (norm != nullptr) {
-    a.wq = q_weight;
-    a.wk = k_weight;
-    a.eps = norm->eps;
-    std::memcpy(a.axis, norm->axis, sizeof(a.axis));
-    if (d->interleaved)
-      rope_kernel<true, true><<<(unsigned)blocks, 256, 0, stream>>>(a);
-    else
-      rope_kernel<false, true><<<(unsigned)blocks, 256, 0, stream>>>(a);
-  } else if (d->interleaved) {
-    rope_kernel<true, false><<<(unsigned)blocks, 256, 0, stream>>>(a);
-  } else {
-    rope_kernel<false, false><<<(unsigned)blocks, 256, 0, stream>>>(a);
-  }
+  if (d->interleaved)
+    rope_kernel<true><<<(unsigned)blocks, 256, 0, stream>>>(a);
+  else
+    rope_kernel<false><<<(unsigned)blocks, 256, 0, stream>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
     spc_host::set_cuda_error(e);
     return SPC_ERR_CUDA;
   }
   return SPC_OK;
-}
-
-spc_status launch_rope(const spc_rope_dims* d, const int32_t* pos, const uint64_t* turns, const uint16_t* q,
-                       const uint16_t* k, const uint16_t* v, uint16_t* q_out, uint16_t* k_out, uint16_t* v_out,
-                       cudaStream_t stream) {
-  return launch_rope_k(d, nullptr, nullptr, nullptr, pos, turns, q, k, v, q_out, k_out, v_out, stream);
-}
-
-spc_status launch_norm_rope(const spc_norm_rope_dims* d, const int32_t* pos, const uint64_t* turns,
-                            const float* q_weight, const float* k_weight, const uint16_t* q, const uint16_t* k,
-                            const uint16_t* v, uint16_t* q_out, uint16_t* k_out, uint16_t* v_out, cudaStream_t stream) {
-  return launch_rope_k(&d->rope, d, q_weight, k_weight, pos, turns, q, k, v, q_out, k_out, v_out, stream);
 }
 
 }  // namespace spc
