@@ -27,7 +27,8 @@ __all__ = [
     "spc_read_device_status", "spc_append_kv", "spc_offload_kv", "spc_rope_frequencies", "spc_rope",
     "spc_rope_axes", "spc_norm_rope",
     "spc_prompt_attn", "spc_prompt_attn_workspace_bytes", "spc_prompt_attn_status",
-    "spc_prompt_attn_wait_limit", "spc_extend_kv", "spc_dequantize_kv", "lib_path",
+    "spc_prompt_attn_wait_limit", "spc_window_attn", "spc_window_attn_workspace_bytes", "spc_prefix_attn",
+    "spc_prefix_attn_workspace_bytes", "spc_extend_kv", "spc_dequantize_kv", "lib_path",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -97,6 +98,10 @@ class spc_prompt_dims(C.Structure):
         ("scale", C.c_float)] + [(n, spc_layout) for n in ("q", "k", "v", "o")]
 
 
+class spc_prefix(C.Structure):
+    _fields_ = [("tokens", C.c_int32), ("k", spc_layout), ("v", spc_layout)]
+
+
 _P = C.c_void_p
 _D = C.POINTER(spc_dims)
 _sig = {
@@ -139,10 +144,15 @@ _sig = {
     "spc_prompt_attn": (C.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, C.c_size_t, _P]),
     "spc_prompt_attn_status": (C.c_int, [_P, _P]),
     "spc_prompt_attn_wait_limit": (C.c_int64, [C.c_int64]),
+    "spc_window_attn_workspace_bytes": (C.c_size_t, [_P, C.c_int32, C.c_int32]),
+    "spc_window_attn": (C.c_int, [_P, C.c_int32, C.c_int32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, C.c_size_t, _P]),
+    "spc_prefix_attn_workspace_bytes": (C.c_size_t, [_P, _P]),
+    "spc_prefix_attn": (C.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, C.c_size_t, _P]),
     "spc_extend_kv": (C.c_int, [_D, C.c_int32, _P, _P, _P, _P, _P, _P, _P, C.c_int64, _P]),
     "spc_dequantize_kv": (C.c_int, [_D, _P, _P, C.c_int32, C.c_int32, _P, _P, _P, _P, _P]),
 }
-_CHECKED = ("spc_rope", "spc_norm_rope", "spc_prompt_attn", "spc_extend_kv", "spc_dequantize_kv")
+_CHECKED = ("spc_rope", "spc_norm_rope", "spc_prompt_attn", "spc_window_attn", "spc_prefix_attn", "spc_extend_kv",
+            "spc_dequantize_kv")
 _sig.update({f"{_name}_check": _sig[_name] for _name in _CHECKED})
 for _name, (_res, _args) in _sig.items():
     _f = getattr(_lib, _name)
@@ -343,8 +353,9 @@ _ROPE = struct.Struct("=7if18q")
 _NORM_ROPE = struct.Struct("=7if18qif64s")
 _PROMPT = struct.Struct("=8if4x12q")
 _LAYOUT = struct.Struct("=3q")
+_PREFIX = struct.Struct("=i4x6q")
 assert _ROPE.size == C.sizeof(spc_rope_dims) and _NORM_ROPE.size == C.sizeof(spc_norm_rope_dims)
-assert _PROMPT.size == C.sizeof(spc_prompt_dims)
+assert _PROMPT.size == C.sizeof(spc_prompt_dims) and _PREFIX.size == C.sizeof(spc_prefix)
 
 
 def _device(fn, t):
@@ -529,16 +540,10 @@ def spc_prompt_attn_workspace_bytes(q, k, v, o, S=None, q_max=None, k_max=None) 
     return int(_lib.spc_prompt_attn_workspace_bytes(d))
 
 
-def spc_prompt_attn(q, k, v, o, lse=None, q_begin=None, q_len=None, k_begin=None, k_len=None, q_max=None, k_max=None,
-                    scale=None, ws=None, ws_bytes=None, stream=None, _later=None):
-    """q and o: [T][Hq][D] (packed sequences) or [S][T][Hq][D]; k and v
-    [T][Hkv][D] or [S][T][Hkv][D].  q_begin, q_len, k_begin, k_len: int32 [S]
-    on the device, or None.  q_max, k_max bound the lengths (default: the
-    token axis).  lse: fp32 of o's shape without D, contiguous.  Without ws a
-    workspace, where one is needed, is taken from torch's allocator for the
-    call, which needs the call to be on the current stream; a wait that ran
-    out is then found by spc_prompt_attn_status() of the device."""
-    fn = "spc_prompt_attn"
+def _attend(fn, rule, prefix, q, k, v, o, lse, q_begin, q_len, k_begin, k_len, q_max, k_max, scale, ws, ws_bytes, stream,
+            later):
+    """A call of spc_prompt_attn or one of its siblings: rule, its arguments behind the dims, and prefix, those between
+    the queries and the keys."""
     dev = _device(fn, q)
     S = _sequences(q, k, q_len, k_len, q_begin, k_begin)
     d = _prompt_dims(fn, q, k, v, o, S, q_max, k_max, scale, dev)
@@ -551,7 +556,7 @@ def spc_prompt_attn(q, k, v, o, lse=None, q_begin=None, q_len=None, k_begin=None
     if ws is None:
         if stream is not None and s != _raw_stream(None, dev):
             raise ValueError(f"{fn}: a call on another stream than the current one needs ws")
-        w, ws_bytes = None, _lib.spc_prompt_attn_workspace_bytes(d)
+        w, ws_bytes = None, getattr(_lib, fn + "_workspace_bytes")(d, *rule)
         if ws_bytes > 256:  # the keys are split; else the call needs none
             w = own = torch._C._cuda_cudaCachingAllocator_raw_alloc(ws_bytes, s)  # a tensor's allocation takes 3 us more
         else:
@@ -565,18 +570,83 @@ def spc_prompt_attn(q, k, v, o, lse=None, q_begin=None, q_len=None, k_begin=None
                 ws_bytes = ws.numel() * ws.element_size()
         elif ws_bytes is None:
             raise ValueError(f"{fn}: a workspace given by its address needs ws_bytes")
-    if _later is not None:
-        _later.append((fn, (d, q.data_ptr(), k.data_ptr(), v.data_ptr(), qb, ql, kb, kl, o.data_ptr(), lse_ptr, w,
-                            ws_bytes, s), own))
+    args = (d, *rule, q.data_ptr(), *prefix, k.data_ptr(), v.data_ptr(), qb, ql, kb, kl, o.data_ptr(), lse_ptr, w, ws_bytes, s)
+    if later is not None:
+        later.append((fn, args, own))
         return
     try:
-        st = _lib.spc_prompt_attn(d, q.data_ptr(), k.data_ptr(), v.data_ptr(), qb, ql, kb, kl, o.data_ptr(), lse_ptr, w,
-                                  ws_bytes, s)
+        st = getattr(_lib, fn)(*args)
     finally:
         if own is not None:
             torch._C._cuda_cudaCachingAllocator_raw_delete(own)
     if st:
         raise SpcError(fn, st)
+
+
+def spc_prompt_attn(q, k, v, o, lse=None, q_begin=None, q_len=None, k_begin=None, k_len=None, q_max=None, k_max=None,
+                    scale=None, ws=None, ws_bytes=None, stream=None, _later=None):
+    """q and o: [T][Hq][D] (packed sequences) or [S][T][Hq][D]; k and v
+    [T][Hkv][D] or [S][T][Hkv][D].  q_begin, q_len, k_begin, k_len: int32 [S]
+    on the device, or None.  q_max, k_max bound the lengths (default: the
+    token axis).  lse: fp32 of o's shape without D, contiguous.  Without ws a
+    workspace, where one is needed, is taken from torch's allocator for the
+    call, which needs the call to be on the current stream; a wait that ran
+    out is then found by spc_prompt_attn_status() of the device."""
+    _attend("spc_prompt_attn", (), (), q, k, v, o, lse, q_begin, q_len, k_begin, k_len, q_max, k_max, scale, ws, ws_bytes,
+            stream, _later)
+
+
+def _window(fn, window, sinks):
+    if not 1 <= window or sinks < 0:
+        raise ValueError(f"{fn}: a window of at least 1 and no negative number of first tokens, got {window} and {sinks}")
+    return min(window, 2 ** 31 - 1), min(sinks, 2 ** 31 - 1)
+
+
+def spc_window_attn_workspace_bytes(q, k, v, o, window, sinks=0, S=None, q_max=None, k_max=None) -> int:
+    """Bytes of workspace of spc_window_attn over these tensors (S sequences; default: the batch)."""
+    fn = "spc_window_attn_workspace_bytes"
+    d = _prompt_dims(fn, q, k, v, o, _sequences(q, k) if S is None else S, q_max, k_max, None, _device(fn, q))
+    return int(_lib.spc_window_attn_workspace_bytes(d, *_window(fn, window, sinks)))
+
+
+def spc_window_attn(q, k, v, o, window, sinks=0, lse=None, q_begin=None, q_len=None, k_begin=None, k_len=None, q_max=None,
+                    k_max=None, scale=None, ws=None, ws_bytes=None, stream=None, _later=None):
+    """spc_prompt_attn where a query sees the last `window` keys up to its own
+    and the first `sinks` keys of its sequence; the other arguments are
+    spc_prompt_attn's."""
+    fn = "spc_window_attn"
+    _attend(fn, _window(fn, window, sinks), (), q, k, v, o, lse, q_begin, q_len, k_begin, k_len, q_max, k_max, scale, ws,
+            ws_bytes, stream, _later)
+
+
+def _prefix(fn, pk, pv, k, dev):
+    """The packed spc_prefix of a call's shared rows."""
+    _, P, Hkv, D, lk = _view(fn, "pk", pk, dev)
+    if pk.dim() != 3 or (Hkv, D) != (k.shape[-2], k.shape[-1]):
+        raise ValueError(f"{fn}: pk has shape {tuple(pk.shape)}, expected [P][{k.shape[-2]}][{k.shape[-1]}]")
+    return _PREFIX.pack(P, *lk, *_like(fn, "pv", pv, dev, pk))
+
+
+def spc_prefix_attn_workspace_bytes(q, pk, pv, k, v, o, S=None, q_max=None, k_max=None) -> int:
+    """Bytes of workspace of spc_prefix_attn over these tensors (S sequences; default: the batch)."""
+    fn = "spc_prefix_attn_workspace_bytes"
+    dev = _device(fn, q)
+    d = _prompt_dims(fn, q, k, v, o, _sequences(q, k) if S is None else S, q_max, k_max, None, dev)
+    return int(_lib.spc_prefix_attn_workspace_bytes(d, _prefix(fn, pk, pv, k, dev)))
+
+
+def spc_prefix_attn(q, pk, pv, k, v, o, lse=None, p_len=None, q_begin=None, q_len=None, k_begin=None, k_len=None,
+                    q_max=None, k_max=None, scale=None, ws=None, ws_bytes=None, stream=None, _later=None):
+    """spc_prompt_attn of sequences that share a prefix: pk, pv [P][Hkv][D],
+    which every query sees in whole; k and v are the sequences' own keys behind
+    it.  p_len: int32 [1] on the device (how many of the P tokens there are), or
+    None.  The other arguments are spc_prompt_attn's."""
+    fn = "spc_prefix_attn"
+    dev = _device(fn, q)
+    p = _prefix(fn, pk, pv, k, dev)
+    n = _words(fn, "p_len", p_len, torch.int32, 1, dev)
+    _attend(fn, (p,), (pk.data_ptr(), pv.data_ptr(), n), q, k, v, o, lse, q_begin, q_len, k_begin, k_len, q_max, k_max,
+            scale, ws, ws_bytes, stream, _later)
 
 
 def spc_prompt_attn_status(ws=None, stream=None) -> int:

@@ -1,0 +1,26 @@
+// The attention of sequences that share a prefix: every query sees all of the
+// prefix, whose keys and values are stored once, and of its own sequence's keys
+// those that are not behind it.  The kernel of prompt_attn.cuh, walking over the
+// prefix's blocks and then over the sequence's.
+#include "prompt_attn.cuh"
+
+namespace spc {
+
+cudaError_t prefix_fault_word(void** word) { return cudaGetSymbolAddress(word, prompt_device_fault); }
+
+size_t prefix_workspace_bytes(const spc_prompt_dims* d, const spc_prefix* p) {
+  PromptRule rule;
+  rule.prefix = p->tokens;
+  return prompt_bytes(d, rule);
+}
+
+spc_status launch_prefix_attn(const spc_prompt_dims* d, const spc_prefix* p, const uint16_t* q, const uint16_t* pk,
+                              const uint16_t* pv, const int32_t* p_len, const uint16_t* k, const uint16_t* v,
+                              const int32_t* q_begin, const int32_t* q_len, const int32_t* k_begin,
+                              const int32_t* k_len, uint16_t* o, float* lse, void* ws, cudaStream_t stream) {
+  PromptRule rule;
+  rule.prefix = p->tokens;
+  return launch_prompt<kPrefix>(d, rule, {q, k, v, q_begin, q_len, k_begin, k_len, o, lse, ws, pk, pv, p_len, p}, stream);
+}
+
+}  // namespace spc

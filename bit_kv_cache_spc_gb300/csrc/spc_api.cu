@@ -29,6 +29,16 @@ spc_status launch_norm_rope(const spc_norm_rope_dims*, const int32_t*, const uin
                             const uint16_t*, const uint16_t*, const uint16_t*, uint16_t*, uint16_t*, uint16_t*,
                             cudaStream_t);
 size_t prompt_workspace_bytes(const spc_prompt_dims*);
+size_t window_workspace_bytes(const spc_prompt_dims*, int32_t, int32_t);
+size_t prefix_workspace_bytes(const spc_prompt_dims*, const spc_prefix*);
+cudaError_t window_fault_word(void**);
+cudaError_t prefix_fault_word(void**);
+spc_status launch_window_attn(const spc_prompt_dims*, int32_t, int32_t, const uint16_t*, const uint16_t*,
+                              const uint16_t*, const int32_t*, const int32_t*, const int32_t*, const int32_t*,
+                              uint16_t*, float*, void*, cudaStream_t);
+spc_status launch_prefix_attn(const spc_prompt_dims*, const spc_prefix*, const uint16_t*, const uint16_t*,
+                              const uint16_t*, const int32_t*, const uint16_t*, const uint16_t*, const int32_t*,
+                              const int32_t*, const int32_t*, const int32_t*, uint16_t*, float*, void*, cudaStream_t);
 int64_t prompt_wait_limit(int64_t);
 cudaError_t prompt_fault_word(void**);
 spc_status launch_prompt_attn(const spc_prompt_dims*, const uint16_t*, const uint16_t*, const uint16_t*,
@@ -810,13 +820,18 @@ size_t spc_prompt_attn_workspace_bytes(const spc_prompt_dims* d) {
   return check_prompt_dims(d) == SPC_OK ? spc::prompt_workspace_bytes(d) : 0;
 }
 
-static spc_status check_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const uint16_t* k, const uint16_t* v,
-                                    const int32_t* q_begin, const int32_t* q_len, const int32_t* k_begin,
-                                    const int32_t* k_len, const uint16_t* o, const float* lse, const void* ws,
-                                    size_t ws_bytes, bool& nothing) {
+// A range of bytes that a call reads.
+struct Bytes {
+  const void* p;
+  size_t n;
+};
+
+// need: workspace of the call (a valid shape's); more: what it reads besides.
+static spc_status check_attn(const spc_prompt_dims* d, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                             const int32_t* q_begin, const int32_t* q_len, const int32_t* k_begin,
+                             const int32_t* k_len, const uint16_t* o, const float* lse, const void* ws,
+                             size_t ws_bytes, size_t need, const Bytes (&more)[2], bool& nothing) {
   nothing = false;
-  const spc_status st = check_prompt_dims(d);
-  if (st != SPC_OK) return st;
   if (d->q_max == 0) {
     nothing = true;
     return SPC_OK;
@@ -826,24 +841,33 @@ static spc_status check_prompt_attn(const spc_prompt_dims* d, const uint16_t* q,
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return SPC_ERR_INVALID;
   if (!aligned4(q_begin) || !aligned4(q_len) || !aligned4(k_begin) || !aligned4(k_len) || !aligned4(lse))
     return SPC_ERR_INVALID;
-  const size_t need = spc::prompt_workspace_bytes(d);
   if ((ws == nullptr && (need > 256 || ws_bytes != 0)) || !aligned16(ws)) return SPC_ERR_INVALID;
   if (ws != nullptr && ws_bytes < need) return SPC_ERR_WORKSPACE;
   const int64_t qb = d->q.b ? d->S : 1, kb = d->k.b ? d->S : 1;
   // what the call writes shares no byte range with what it reads or writes besides
-  const struct {
-    const void* p;
-    size_t bytes;
-  } part[6] = {{q, layout_bytes(d->q, qb, d->q_tokens, d->Hq)},
-               {k, layout_bytes(d->k, kb, d->k_tokens, d->Hkv)},
-               {v, layout_bytes(d->v, kb, d->k_tokens, d->Hkv)},
-               {o, layout_bytes(d->o, qb, d->q_tokens, d->Hq)},
-               {lse, (size_t)qb * d->q_tokens * d->Hq * sizeof(float)},
-               {ws, need}};
-  for (int i = 3; i < 6; ++i)
+  const Bytes part[8] = {{q, layout_bytes(d->q, qb, d->q_tokens, d->Hq)},
+                         {k, layout_bytes(d->k, kb, d->k_tokens, d->Hkv)},
+                         {v, layout_bytes(d->v, kb, d->k_tokens, d->Hkv)},
+                         more[0],
+                         more[1],
+                         {o, layout_bytes(d->o, qb, d->q_tokens, d->Hq)},
+                         {lse, (size_t)qb * d->q_tokens * d->Hq * sizeof(float)},
+                         {ws, need}};
+  for (int i = 5; i < 8; ++i)
     for (int j = 0; j < i; ++j)
-      if (overlap(part[i].p, part[i].bytes, part[j].p, part[j].bytes)) return SPC_ERR_INVALID;
+      if (overlap(part[i].p, part[i].n, part[j].p, part[j].n)) return SPC_ERR_INVALID;
   return SPC_OK;
+}
+
+static spc_status check_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                                    const int32_t* q_begin, const int32_t* q_len, const int32_t* k_begin,
+                                    const int32_t* k_len, const uint16_t* o, const float* lse, const void* ws,
+                                    size_t ws_bytes, bool& nothing) {
+  nothing = false;
+  const spc_status st = check_prompt_dims(d);
+  if (st != SPC_OK) return st;
+  return check_attn(d, q, k, v, q_begin, q_len, k_begin, k_len, o, lse, ws, ws_bytes, spc::prompt_workspace_bytes(d),
+                    {{nullptr, 0}, {nullptr, 0}}, nothing);
 }
 
 spc_status spc_prompt_attn_check(const spc_prompt_dims* d, const uint16_t* q, const uint16_t* k, const uint16_t* v,
@@ -866,20 +890,124 @@ spc_status spc_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const ui
 
 spc_status spc_prompt_attn_status(void* ws, spc_stream stream) {
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  uint32_t v = 0;
-  cudaError_t e = ws == nullptr ? spc::prompt_fault_word(&ws) : cudaSuccess;
-  if (e == cudaSuccess) e = cudaMemcpyAsync(&v, ws, sizeof(v), cudaMemcpyDeviceToHost, s);
+  void* word[3] = {ws, nullptr, nullptr};
+  cudaError_t e = cudaSuccess;
+  if (ws == nullptr) {  // the device's words, one of each kind of call
+    e = spc::prompt_fault_word(&word[0]);
+    if (e == cudaSuccess) e = spc::window_fault_word(&word[1]);
+    if (e == cudaSuccess) e = spc::prefix_fault_word(&word[2]);
+  }
+  uint32_t v[3] = {0, 0, 0};
+  for (int i = 0; i < 3 && e == cudaSuccess; ++i)
+    if (word[i] != nullptr) e = cudaMemcpyAsync(&v[i], word[i], sizeof(v[i]), cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e == cudaSuccess && v != 0u) e = cudaMemsetAsync(ws, 0, sizeof(v), s);
+  for (int i = 0; i < 3 && e == cudaSuccess; ++i)
+    if (v[i] != 0u) e = cudaMemsetAsync(word[i], 0, sizeof(v[i]), s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) {
     spc_host::set_cuda_error(e);
     return SPC_ERR_CUDA;
   }
-  return v != 0u ? SPC_ERR_TIMEOUT : SPC_OK;
+  return (v[0] | v[1] | v[2]) != 0u ? SPC_ERR_TIMEOUT : SPC_OK;
 }
 
 int64_t spc_prompt_attn_wait_limit(int64_t ns) { return spc::prompt_wait_limit(ns); }
+
+static spc_status check_window(const spc_prompt_dims* d, int32_t window, int32_t sinks) {
+  const spc_status st = check_prompt_dims(d);
+  if (st != SPC_OK) return st;
+  return window < 1 || sinks < 0 ? SPC_ERR_INVALID : SPC_OK;
+}
+
+size_t spc_window_attn_workspace_bytes(const spc_prompt_dims* d, int32_t window, int32_t sinks) {
+  if (check_window(d, window, sinks) != SPC_OK) return 0;
+  return window >= d->k_max ? spc::prompt_workspace_bytes(d) : spc::window_workspace_bytes(d, window, sinks);
+}
+
+static spc_status check_window_attn(const spc_prompt_dims* d, int32_t window, int32_t sinks, const uint16_t* q,
+                                    const uint16_t* k, const uint16_t* v, const int32_t* q_begin,
+                                    const int32_t* q_len, const int32_t* k_begin, const int32_t* k_len,
+                                    const uint16_t* o, const float* lse, const void* ws, size_t ws_bytes,
+                                    bool& nothing) {
+  nothing = false;
+  const spc_status st = check_window(d, window, sinks);
+  if (st != SPC_OK) return st;
+  return check_attn(d, q, k, v, q_begin, q_len, k_begin, k_len, o, lse, ws, ws_bytes,
+                    spc_window_attn_workspace_bytes(d, window, sinks), {{nullptr, 0}, {nullptr, 0}}, nothing);
+}
+
+spc_status spc_window_attn_check(const spc_prompt_dims* d, int32_t window, int32_t sinks, const uint16_t* q,
+                                 const uint16_t* k, const uint16_t* v, const int32_t* q_begin, const int32_t* q_len,
+                                 const int32_t* k_begin, const int32_t* k_len, uint16_t* o, float* lse, void* ws,
+                                 size_t ws_bytes, spc_stream) {
+  bool nothing;
+  return check_window_attn(d, window, sinks, q, k, v, q_begin, q_len, k_begin, k_len, o, lse, ws, ws_bytes, nothing);
+}
+
+spc_status spc_window_attn(const spc_prompt_dims* d, int32_t window, int32_t sinks, const uint16_t* q,
+                           const uint16_t* k, const uint16_t* v, const int32_t* q_begin, const int32_t* q_len,
+                           const int32_t* k_begin, const int32_t* k_len, uint16_t* o, float* lse, void* ws,
+                           size_t ws_bytes, spc_stream stream) {
+  bool nothing;
+  const spc_status st =
+      check_window_attn(d, window, sinks, q, k, v, q_begin, q_len, k_begin, k_len, o, lse, ws, ws_bytes, nothing);
+  if (st != SPC_OK || nothing) return st;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (window >= d->k_max) return spc::launch_prompt_attn(d, q, k, v, q_begin, q_len, k_begin, k_len, o, lse, ws, s);
+  return spc::launch_window_attn(d, window, sinks, q, k, v, q_begin, q_len, k_begin, k_len, o, lse, ws, s);
+}
+
+static spc_status check_prefix(const spc_prompt_dims* d, const spc_prefix* p) {
+  const spc_status st = check_prompt_dims(d);
+  if (st != SPC_OK) return st;
+  if (p == nullptr || p->tokens < 0) return SPC_ERR_INVALID;
+  if (p->tokens >= (1 << 30)) return SPC_ERR_UNSUPPORTED;
+  if (!layout_ok(p->k, 1, p->tokens, d->Hkv) || !layout_ok(p->v, 1, p->tokens, d->Hkv)) return SPC_ERR_INVALID;
+  return SPC_OK;
+}
+
+size_t spc_prefix_attn_workspace_bytes(const spc_prompt_dims* d, const spc_prefix* p) {
+  if (check_prefix(d, p) != SPC_OK) return 0;
+  return p->tokens == 0 ? spc::prompt_workspace_bytes(d) : spc::prefix_workspace_bytes(d, p);
+}
+
+static spc_status check_prefix_attn(const spc_prompt_dims* d, const spc_prefix* p, const uint16_t* q,
+                                    const uint16_t* pk, const uint16_t* pv, const int32_t* p_len, const uint16_t* k,
+                                    const uint16_t* v, const int32_t* q_begin, const int32_t* q_len,
+                                    const int32_t* k_begin, const int32_t* k_len, const uint16_t* o, const float* lse,
+                                    const void* ws, size_t ws_bytes, bool& nothing) {
+  nothing = false;
+  spc_status st = check_prefix(d, p);
+  if (st != SPC_OK) return st;
+  st = check_attn(d, q, k, v, q_begin, q_len, k_begin, k_len, o, lse, ws, ws_bytes, spc_prefix_attn_workspace_bytes(d, p),
+                  {{pk, layout_bytes(p->k, 1, p->tokens, d->Hkv)}, {pv, layout_bytes(p->v, 1, p->tokens, d->Hkv)}},
+                  nothing);
+  if (st != SPC_OK || nothing) return st;
+  if (p->tokens > 0 && (pk == nullptr || pv == nullptr)) return SPC_ERR_INVALID;
+  return !aligned16(pk) || !aligned16(pv) || !aligned4(p_len) ? SPC_ERR_INVALID : SPC_OK;
+}
+
+spc_status spc_prefix_attn_check(const spc_prompt_dims* d, const spc_prefix* p, const uint16_t* q, const uint16_t* pk,
+                                 const uint16_t* pv, const int32_t* p_len, const uint16_t* k, const uint16_t* v,
+                                 const int32_t* q_begin, const int32_t* q_len, const int32_t* k_begin,
+                                 const int32_t* k_len, uint16_t* o, float* lse, void* ws, size_t ws_bytes, spc_stream) {
+  bool nothing;
+  return check_prefix_attn(d, p, q, pk, pv, p_len, k, v, q_begin, q_len, k_begin, k_len, o, lse, ws, ws_bytes, nothing);
+}
+
+spc_status spc_prefix_attn(const spc_prompt_dims* d, const spc_prefix* p, const uint16_t* q, const uint16_t* pk,
+                           const uint16_t* pv, const int32_t* p_len, const uint16_t* k, const uint16_t* v,
+                           const int32_t* q_begin, const int32_t* q_len, const int32_t* k_begin,
+                           const int32_t* k_len, uint16_t* o, float* lse, void* ws, size_t ws_bytes,
+                           spc_stream stream) {
+  bool nothing;
+  const spc_status st =
+      check_prefix_attn(d, p, q, pk, pv, p_len, k, v, q_begin, q_len, k_begin, k_len, o, lse, ws, ws_bytes, nothing);
+  if (st != SPC_OK || nothing) return st;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (p->tokens == 0) return spc::launch_prompt_attn(d, q, k, v, q_begin, q_len, k_begin, k_len, o, lse, ws, s);
+  return spc::launch_prefix_attn(d, p, q, pk, pv, p_len, k, v, q_begin, q_len, k_begin, k_len, o, lse, ws, s);
+}
 
 // host_dev: the device's address of host_kv.
 static spc_status check_extend(const spc_dims* d, int32_t n, const uint16_t* k_new, const uint16_t* v_new,

@@ -528,13 +528,14 @@ spc_status spc_prompt_attn(const spc_prompt_dims* d, const uint16_t* q, const ui
                            const int32_t* k_len, uint16_t* o, float* lse, void* ws, size_t ws_bytes,
                            spc_stream stream);
 
-/* Reads and clears the status word of a workspace of spc_prompt_attn, or, with
- * ws = NULL, the current device's, which every call on the device reports to
- * as well: SPC_ERR_TIMEOUT if a bounded wait ran out since, else SPC_OK.
+/* Reads and clears the status word of a workspace of spc_prompt_attn (or
+ * spc_window_attn or spc_prefix_attn), or, with ws = NULL, the current device's,
+ * which every call on the device reports to as well: SPC_ERR_TIMEOUT if a bounded wait ran out since, else SPC_OK.
  * Synchronises `stream`. */
 spc_status spc_prompt_attn_status(void* ws, spc_stream stream);
 
-/* The limit of a wait in spc_prompt_attn's kernels, in ns (2 * 10^9 unless set;
+/* The limit of a wait in the kernels of spc_prompt_attn, spc_window_attn and
+ * spc_prefix_attn, in ns (2 * 10^9 unless set;
  * regular waits last microseconds, but for one that lasts as long as a CTA
  * walks over keys that its rows see in full: its limit grows with them).  ns >
  * 0 sets it, to 10^12 at most, for the calls of the process from now on (a
@@ -542,6 +543,49 @@ spc_status spc_prompt_attn_status(void* ws, spc_stream stream);
  * limit before the call.  A wait that runs out ends its CTA early, whose rows
  * of o and lse then hold no result. */
 int64_t spc_prompt_attn_wait_limit(int64_t ns);
+
+/*
+ * spc_prompt_attn with a sliding window and first tokens that stay visible
+ * ("attention sinks"): the query at place p = i + lk - lq of its sequence sees
+ * the keys j <= p with j > p - window (its own and the window - 1 before it) or
+ * j < sinks.  window >= 1, sinks >= 0; a window of k_max or more leaves
+ * spc_prompt_attn, and makes its call.  Keys and values that no query of a call
+ * sees are not used (and mostly not read).  Arguments, results, refusals and
+ * the workspace's rules are spc_prompt_attn's; spc_prompt_attn_status and
+ * spc_prompt_attn_wait_limit cover its waits.
+ */
+size_t spc_window_attn_workspace_bytes(const spc_prompt_dims* d, int32_t window, int32_t sinks);
+
+spc_status spc_window_attn(const spc_prompt_dims* d, int32_t window, int32_t sinks, const uint16_t* q,
+                           const uint16_t* k, const uint16_t* v, const int32_t* q_begin, const int32_t* q_len,
+                           const int32_t* k_begin, const int32_t* k_len, uint16_t* o, float* lse, void* ws,
+                           size_t ws_bytes, spc_stream stream);
+
+/* A prefix that all sequences of a call share: [tokens][Hkv][D] rows of keys and of values. */
+typedef struct spc_prefix {
+  int32_t tokens;  /* that the views hold: 0 .. 2^30 - 1 */
+  spc_layout k, v; /* (b is not used) */
+} spc_prefix;
+
+/*
+ * spc_prompt_attn of sequences that share a prefix, stored once: every query
+ * sees all P tokens of the prefix, and of its own sequence's lk keys those
+ * j <= i + lk - lq.
+ *   pk, pv : bf16 views of the prefix's rows; may be NULL when p->tokens = 0,
+ *            which leaves spc_prompt_attn, and makes its call.
+ *   p_len  : int32 [1] (device) or NULL: P (NULL: p->tokens), held to 0 ..
+ *            p->tokens.
+ * A query that sees no key of its own sequence has the prefix; k_max may be 0.
+ * Everything else as spc_prompt_attn (neither o, lse nor the workspace shares a
+ * byte range with the prefix).
+ */
+size_t spc_prefix_attn_workspace_bytes(const spc_prompt_dims* d, const spc_prefix* p);
+
+spc_status spc_prefix_attn(const spc_prompt_dims* d, const spc_prefix* p, const uint16_t* q, const uint16_t* pk,
+                           const uint16_t* pv, const int32_t* p_len, const uint16_t* k, const uint16_t* v,
+                           const int32_t* q_begin, const int32_t* q_len, const int32_t* k_begin,
+                           const int32_t* k_len, uint16_t* o, float* lse, void* ws, size_t ws_bytes,
+                           spc_stream stream);
 
 /*
  * A run of n new tokens joins the cache (SpeCache page, Algorithm 1 for a
@@ -577,8 +621,9 @@ spc_status spc_dequantize_kv(const spc_dims* d, const void* records, const uint1
                              spc_stream stream);
 
 /*
- * What spc_rope, spc_norm_rope, spc_prompt_attn, spc_extend_kv and
- * spc_dequantize_kv would refuse, without a launch: the same arguments, and the status that the call
+ * What spc_rope, spc_norm_rope, spc_prompt_attn, spc_window_attn,
+ * spc_prefix_attn, spc_extend_kv and spc_dequantize_kv would refuse, without a
+ * launch: the same arguments, and the status that the call
  * would return before it enqueues anything.  For a sequence of calls of which
  * either all are to be made or none (a prompt is rotated in place before its
  * attention and its way into the cache).
@@ -590,6 +635,15 @@ spc_status spc_norm_rope_check(const spc_norm_rope_dims* d, const int32_t* pos, 
                                const float* q_weight, const float* k_weight, const uint16_t* q, const uint16_t* k,
                                const uint16_t* v, uint16_t* q_out, uint16_t* k_out, uint16_t* v_out, spc_stream stream);
 spc_status spc_prompt_attn_check(const spc_prompt_dims* d, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                                 const int32_t* q_begin, const int32_t* q_len, const int32_t* k_begin,
+                                 const int32_t* k_len, uint16_t* o, float* lse, void* ws, size_t ws_bytes,
+                                 spc_stream stream);
+spc_status spc_window_attn_check(const spc_prompt_dims* d, int32_t window, int32_t sinks, const uint16_t* q,
+                                 const uint16_t* k, const uint16_t* v, const int32_t* q_begin, const int32_t* q_len,
+                                 const int32_t* k_begin, const int32_t* k_len, uint16_t* o, float* lse, void* ws,
+                                 size_t ws_bytes, spc_stream stream);
+spc_status spc_prefix_attn_check(const spc_prompt_dims* d, const spc_prefix* p, const uint16_t* q, const uint16_t* pk,
+                                 const uint16_t* pv, const int32_t* p_len, const uint16_t* k, const uint16_t* v,
                                  const int32_t* q_begin, const int32_t* q_len, const int32_t* k_begin,
                                  const int32_t* k_len, uint16_t* o, float* lse, void* ws, size_t ws_bytes,
                                  spc_stream stream);
