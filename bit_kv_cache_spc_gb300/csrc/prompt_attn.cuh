@@ -132,6 +132,11 @@ struct PromptArgs {
   const int32_t* p_len;
   int64_t pv_t, pv_h;
   int32_t p_tokens;
+  // kPrefix with rows of all sequences together in the prefix's tiles:
+  int32_t together;
+  int32_t p_items, p_tiles, p_splits;  // items of the prefix (they come first); tiles of rows; splits
+  int32_t p_bt, p_bs;                  // a tile of batched queries: p_bt tokens of p_bs sequences each (packed: 0)
+  int64_t p_rows;                      // rows of the prefix's partial results, per split; the sequences' own come behind
 };
 
 template <int KIND>
@@ -140,7 +145,7 @@ struct PromptMaps {
 };
 template <>
 struct PromptMaps<kPrefix> {
-  CUtensorMap q, k, v, pk, pv;
+  CUtensorMap q, k, v, pk, pv, qs;  // qs: of tiles with several sequences' rows
 };
 
 // What a CTA works on.
@@ -157,10 +162,17 @@ struct PromptItem {
   int nb0, key1, nb;  // nb: blocks in all
   int ma, mb, mc;  // blocks that some row does not see in full: [ma, mb) and from mc on
   int prefix;      // tokens of the shared prefix
+  int shared;      // rows of several sequences, the prefix's keys alone (tok0: the first token on the axis of packed
+                   // queries; s: the first sequence of batched ones)
 };
 
 __device__ __forceinline__ int block_key(const PromptItem& w, int g) {
   return kBlock * (g < w.nb0 ? g : g - w.nb0) + (g < w.nb0 ? 0 : w.key1);
+}
+// Whether partial results are written, to be joined.
+template <int KIND>
+__device__ __forceinline__ bool in_parts(const PromptArgs& a) {
+  return a.splits > 1 || (KIND == kPrefix && a.together);
 }
 __device__ __forceinline__ bool block_masked(const PromptItem& w, int g) { return (g >= w.ma && g < w.mb) || g >= w.mc; }
 
@@ -423,10 +435,61 @@ __device__ __forceinline__ bool dense_item(const PromptArgs& a, int k, PromptIte
 // them in L2.  Up to kDense sequences of different lengths are numbered over
 // the pairs that exist, so that long and short prompts packed together leave
 // no empty CTAs; more, or equal ones, over all pairs.  False for none.
+// Item i of the prefix's, rows of all sequences together: tile of rows fastest, so that CTAs that run together share
+// keys, then KV head, then split.  False where no sequence has a row in the tile.
+template <int TILES>
+__device__ __forceinline__ bool shared_item(const PromptArgs& a, uint32_t i, PromptItem& w) {
+  constexpr int kPerStage = Shape<TILES>::kPerStage;
+  const int lane = threadIdx.x & 31, tile = (int)(i % a.p_tiles);
+  i /= a.p_tiles;
+  w = PromptItem();
+  w.shared = 1;
+  w.hkv = (int)(i % a.Hkv);
+  w.split = (int)(i / a.Hkv);
+  const int per_tile = a.p_bt > 0 ? a.p_bs : a.tile_tokens;  // sequences or tokens
+  const int first = tile * TILES * per_tile, end = first + TILES * per_tile;
+  w.s = a.p_bt > 0 ? first : 0;
+  w.tok0 = a.p_bt > 0 ? 0 : first;
+  w.two = TILES == 2 && first + per_tile < (a.p_bt > 0 ? a.S : a.q_tokens);
+  bool live = false;
+  if (a.p_bt > 0) {
+    for (int s = first + lane; s < min(end, a.S); s += 32) live |= (a.q_len ? a.q_len[s] : a.q_max) > 0;
+    live = __any_sync(0xFFFFFFFFu, live);
+  } else {  // from where the sequence is likely to stand on, 256 sequences at a time
+    const int chunks = (a.S + 255) / 256, start = (int)((int64_t)first * a.S / a.q_tokens) / 256;
+    for (int c = 0; c < chunks && !live; ++c) {
+      const int base = (start + c) % chunks * 256 + lane;
+      bool here = false;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        int lq = 0, lk, qb = 0, kb;
+        if (base + 32 * u < a.S) sequence(a, base + 32 * u, lq, lk, qb, kb);
+        here |= lq > 0 && qb < end && qb + lq > first;
+      }
+      live = __any_sync(0xFFFFFFFFu, here);
+    }
+  }
+  if (!live) return false;
+  w.prefix = a.p_len ? clampi(a.p_len[0], 0, a.p_tokens) : a.p_tokens;
+  w.nb = w.nb0 = w.mc = (w.prefix + kBlock - 1) / kBlock;
+  w.mb = w.prefix % kBlock != 0 ? w.nb0 : 0;
+  w.ma = max(w.mb - 1, 0);
+  const int n = (w.nb + kPerStage - 1) / kPerStage, per = (n + a.p_splits - 1) / a.p_splits;
+  w.lo = min(w.split * per, n);
+  w.hi = min(w.lo + per, n);
+  w.blocks[0] = w.blocks[1] = max(0, min(kPerStage * (w.hi - w.lo), w.nb - w.lo * kPerStage));
+  return true;
+}
+
 template <int TILES, int KIND>
 __device__ __forceinline__ bool prompt_item(const PromptArgs& a, uint32_t i, PromptItem& w) {
   constexpr int kKeys = Shape<TILES>::kKeys;
   constexpr int kPerStage = Shape<TILES>::kPerStage;
+  if constexpr (KIND == kPrefix) {
+    if (i < (uint32_t)a.p_items) return shared_item<TILES>(a, i, w);
+    i -= a.p_items;
+    w.shared = 0;
+  }
   w.split = 0;
   if (a.rounds > 1) {
     w.split = (int)(i / a.items);
@@ -465,7 +528,7 @@ __device__ __forceinline__ bool prompt_item(const PromptArgs& a, uint32_t i, Pro
     w.nb = most == 0 ? 0 : w.nb0 + (most - w.key1 + kBlock - 1) / kBlock;
     n = (w.nb + kPerStage - 1) / kPerStage;
   } else if constexpr (KIND == kPrefix) {
-    w.prefix = a.p_len ? clampi(a.p_len[0], 0, a.p_tokens) : a.p_tokens;
+    w.prefix = a.together ? 0 : a.p_len ? clampi(a.p_len[0], 0, a.p_tokens) : a.p_tokens;
     w.nb0 = (w.prefix + kBlock - 1) / kBlock;
     w.key1 = 0;
     w.mb = w.prefix % kBlock != 0 ? w.nb0 : 0;
@@ -501,6 +564,11 @@ __device__ __forceinline__ int64_t lse_place(const PromptArgs& a, int s, int tok
 }
 __device__ __forceinline__ int64_t part_place(const PromptArgs& a, int split, int s, int tok, int head) {
   return split * a.part_rows + ((int64_t)s * a.q_max + tok) * a.Hq + head;
+}
+// The same with the prefix's splits before the sequences' own: qb is the sequence's first query token.
+__device__ __forceinline__ int64_t joined_place(const PromptArgs& a, int z, int s, int qb, int tok, int head) {
+  if (z >= a.p_splits) return a.p_splits * a.p_rows + part_place(a, z - a.p_splits, s, tok, head);
+  return z * a.p_rows + ((a.p_bt > 0 ? (int64_t)s * a.q_max : qb) + tok) * a.Hq + head;
 }
 
 // exp2(x c - m c) of a row's 64 scores, as bf16 pairs into P, and their sum.
@@ -616,6 +684,15 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
       if (w.hi > w.lo) {
         load_kv(w, false, 0);
         for (int t = 0; t < (w.two ? 2 : 1); ++t) {
+          if constexpr (KIND == kPrefix) {
+            if (w.shared && a.p_bt > 0) {
+              mbar_expect(&bars.q_full[t], a.p_bt * a.p_bs * a.G * kD * 2);
+              for (int h = 0; h < 2; ++h)
+                tma_load4(base + t * kTileBytes + h * (kTileBytes / 2), &maps.qs, &bars.q_full[t], 64 * h, w.hkv * a.G, 0,
+                          w.s + t * a.p_bs);
+              continue;
+            }
+          }
           mbar_expect(&bars.q_full[t], a.tile_tokens * a.G * kD * 2);
           for (int h = 0; h < 2; ++h)
             tma_load4(base + t * kTileBytes + h * (kTileBytes / 2), &maps.q, &bars.q_full[t], 64 * h, w.hkv * a.G,
@@ -786,9 +863,19 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
       const int t = warp >> 2, r = tid & 127;
       const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // TMEM lane 32 * (warp % 4)
       const uint32_t s_addr = tmem + lanes + 2 * kBlock * t, o_addr = tmem + lanes + 2 * kBlock * TILES + kD * t;
-      const int tok = w.tok0 + t * a.tile_tokens + r / a.G;
+      int tok = w.tok0 + t * a.tile_tokens + r / a.G, seq = w.s;
       const int head = w.hkv * a.G + r % a.G;
-      const bool row = r < a.tile_tokens * a.G && tok < w.lq;
+      bool row = r < a.tile_tokens * a.G && tok < w.lq;
+      if constexpr (KIND == kPrefix) {
+        if (w.shared && a.p_bt > 0) {
+          const int u = r / a.G;
+          seq = w.s + t * a.p_bs + u / a.p_bt;
+          tok = u % a.p_bt;
+          row = u < a.p_bt * a.p_bs && seq < a.S;
+        } else if (w.shared) {
+          row = r < a.tile_tokens * a.G && tok < a.q_tokens;
+        }
+      }
       const int seen = row ? clampi(tok + w.lk - w.lq + 1, 0, w.lk) : w.lk;  // keys of this row
       const int from = w.lo * H::kKeys, blocks = w.blocks[t];
       const int masked = H::kPerStage * (w.edge - w.lo);  // the first block that some row does not see in full
@@ -873,18 +960,22 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
           const bool bad = *(volatile uint32_t*)&bars.bad != 0u;
           const int first = max(w.edge, w.lo) * H::kKeys, end = min(seen, w.hi * H::kKeys);
           // no visible key: 0; otherwise the sum is positive, or not a number when the scores are not
-          const bool any = KIND == kPlain                ? seen > from
-                           : a.splits > 1 || blocks == 0 ? blocks > 0 && l != 0.f
-                                                         : seen > 0 || (KIND == kPrefix && w.prefix > 0);
-          const float inv = a.splits > 1 ? 1.f : (any ? 1.f / l : 0.f);
-          const int64_t part = part_place(a, w.split, w.s, tok, head);
+          const bool parts = in_parts<KIND>(a);
+          const bool any = KIND == kPlain         ? seen > from
+                           : parts || blocks == 0 ? blocks > 0 && l != 0.f
+                                                  : seen > 0 || (KIND == kPrefix && w.prefix > 0);
+          const float inv = parts ? 1.f : (any ? 1.f / l : 0.f);
+          int64_t part = part_place(a, w.split, w.s, tok, head);
+          if constexpr (KIND == kPrefix) {
+            if (a.together) part = joined_place(a, w.split + (w.shared ? 0 : a.p_splits), seq, 0, tok, head);
+          }
           // Through shared memory (the tile's Q has been used up), 256 bytes of every row at a time, so that a warp
           // stores whole rows: chunk c of row i of the warp lies at chunk c ^ (i % 8).
           uint4* stage = reinterpret_cast<uint4*>(base + t * kTileBytes) + (warp & 3) * 512;
           uint4* mine = stage + lane * 16;
           uint64_t out = 0;  // where the row goes
           if (row)
-            out = a.splits > 1 ? (uint64_t)(a.part_o + part * kD)
+            out = parts ? (uint64_t)(a.part_o + part * kD)
                                : (uint64_t)(a.o + w.s * a.o_b + (int64_t)(w.qb + tok) * a.o_t + head * a.o_h);
           // Rolled loops: this runs once per item, and unrolled it is bound by fetching its instructions.
 #pragma unroll 1
@@ -930,7 +1021,7 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
               }
             }
             bool full;  // 256 bytes of every row are staged
-            if (a.splits > 1) {
+            if (parts) {
 #pragma unroll
               for (int i = 0; i < 8; ++i)
                 mine[(8 * (q & 1) + i) ^ (lane & 7)] =
@@ -953,12 +1044,12 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
               const int rr = 2 * i + (lane >> 4), cc = lane & 15;
               const uint64_t to = __shfl_sync(0xFFFFFFFFu, out, rr);
               const uint4 v = stage[rr * 16 + (cc ^ (rr & 7))];
-              if (to != 0) reinterpret_cast<uint4*>(to)[(a.splits > 1 ? 16 * (q >> 1) : 0) + cc] = v;
+              if (to != 0) reinterpret_cast<uint4*>(to)[(parts ? 16 * (q >> 1) : 0) + cc] = v;
             }
             __syncwarp();
           }
           if (row) {
-            if (a.splits > 1)
+            if (parts)
               a.part_ml[part] = make_float2(any ? m * c : -INFINITY, any ? l : 0.f);
             else if (a.lse)
               a.lse[lse_place(a, w.s, w.qb + tok, head)] = any ? m * a.scale + logf(l) : -INFINITY;
@@ -1009,18 +1100,21 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant_
   if (tok >= lq) return;
   bool any = tok + lk - lq + 1 > 0 && lk > 0;
   if (KIND == kPrefix) any = any || (a.p_len ? clampi(a.p_len[0], 0, a.p_tokens) : a.p_tokens) > 0;
+  const int splits = a.splits + (KIND == kPrefix ? a.p_splits : 0);
+  const auto place = [&](int z) {
+    return KIND == kPrefix ? joined_place(a, z, s, qb, tok, head) : part_place(a, z, s, tok, head);
+  };
   float2 ml[2];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int z = lane + 32 * u;
-    ml[u] = z < a.splits ? a.part_ml[part_place(a, z, s, tok, head)] : make_float2(-INFINITY, 0.f);
+    ml[u] = z < splits ? a.part_ml[place(z)] : make_float2(-INFINITY, 0.f);
   }
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f), x[8];
   const auto load = [&](int z0) {  // eight splits' loads in flight
 #pragma unroll
     for (int u = 0; u < 8; ++u)
-      if (z0 + u < a.splits)
-        x[u] = reinterpret_cast<const float4*>(a.part_o + part_place(a, z0 + u, s, tok, head) * kD)[lane];
+      if (z0 + u < splits) x[u] = reinterpret_cast<const float4*>(a.part_o + place(z0 + u) * kD)[lane];
   };
   load(8 * part);
   float m = fmaxf(ml[0].x, ml[1].x);
@@ -1034,13 +1128,13 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant_
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, off);
-  for (int z0 = 8 * part; z0 < a.splits; z0 += 8 * WARPS) {
+  for (int z0 = 8 * part; z0 < splits; z0 += 8 * WARPS) {
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int z = z0 + u;
       const float g = __shfl_sync(0xFFFFFFFFu, z < 32 ? f[0] : f[1], z & 31);
       const float sum = __shfl_sync(0xFFFFFFFFu, z < 32 ? ml[0].y : ml[1].y, z & 31);
-      if (z >= a.splits || sum == 0.f) continue;
+      if (z >= splits || sum == 0.f) continue;
       o = make_float4(o.x + g * x[u].x, o.y + g * x[u].y, o.z + g * x[u].z, o.w + g * x[u].w);
     }
     load(z0 + 8 * WARPS);
@@ -1079,17 +1173,17 @@ EncodeTiled encode_tiled() {
   return fn;
 }
 
-// Map of [batch][token][head][128] with the given strides: boxes of `heads`
-// heads and `tokens` tokens of half a row (64 channels, 128 bytes, swizzled).
+// Map of [batch][token][head][128] with the given strides: boxes of so many
+// heads, tokens and sequences of half a row (64 channels, 128 bytes, swizzled).
 bool encode_map(CUtensorMap* map, const uint16_t* p, int64_t batch, int64_t tokens, int64_t heads,
-                const spc_layout& st, uint32_t box_heads, uint32_t box_tokens) {
+                const spc_layout& st, uint32_t box_heads, uint32_t box_tokens, uint32_t box_batch = 1) {
   const EncodeTiled fn = encode_tiled();
   if (fn == nullptr) return false;
   // an axis of one element is never stepped along: any valid stride does
   const auto stride = [](int64_t n, int64_t s) { return (cuuint64_t)(n > 1 ? s * 2 : kD * 2); };
   const cuuint64_t dims[4] = {(cuuint64_t)kD, (cuuint64_t)heads, (cuuint64_t)tokens, (cuuint64_t)batch};
   const cuuint64_t strides[3] = {stride(heads, st.h), stride(tokens, st.t), stride(batch, st.b)};
-  const cuuint32_t box[4] = {64, box_heads, box_tokens, 1}, step[4] = {1, 1, 1, 1};
+  const cuuint32_t box[4] = {64, box_heads, box_tokens, box_batch}, step[4] = {1, 1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(p), dims, strides, box, step,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -1143,6 +1237,9 @@ struct PromptRule {
 struct PromptGrid {
   int tiles, tile_tokens, pair_tokens, pairs, splits, rounds, gap;
   int64_t items;
+  // kPrefix with all sequences' rows together:
+  int p_tiles = 0, p_splits = 0, p_bt = 0, p_bs = 0;
+  int64_t p_rows = 0, p_items = 0;
 };
 
 PromptGrid prompt_grid(const spc_prompt_dims* d, const PromptRule& rule) {
@@ -1195,13 +1292,74 @@ PromptGrid prompt_grid(const spc_prompt_dims* d, const PromptRule& rule) {
   return g;
 }
 
+// Grid of a call behind a prefix whose tiles hold the rows of all sequences
+// together, so that the prefix's keys are walked once for them and not once for
+// each; the sequences' own keys are walked by items of their own, and all
+// results are joined.  p_items = 0 where that does not pay: the sequences' own
+// tiles are as few, or the partial results cost more than what is saved.
+// One-tile CTAs, as the own items mostly have a few rows.
+//
+// Of the splits of the prefix, the number with the least estimate: the items
+// taken in turns by the CTAs' places, the own items filling what the last turn
+// leaves.  Own keys are split where their items would take longer than one of
+// the prefix's.
+PromptGrid together_grid(const spc_prompt_dims* d, const PromptRule& rule) {
+  PromptGrid g = {};
+  const int G = d->Hq / d->Hkv;
+  const bool batched = d->q.b != 0 && d->S > 1;
+  g.tiles = 1;
+  g.tile_tokens = g.pair_tokens = kTile / G;
+  if (d->S < 2 || d->S > 65535 || rule.prefix == 0 || (batched && 2 * d->q_max > g.tile_tokens)) return g;
+  g.pairs = (int)ceil_div(d->q_max, g.tile_tokens);
+  int64_t tokens = (int64_t)d->S * d->q_max, own_tiles = (int64_t)d->S * g.pairs;
+  if (batched) {
+    g.p_bt = d->q_max;
+    g.p_bs = g.tile_tokens / d->q_max;
+    g.p_tiles = (int)ceil_div(d->S, g.p_bs);
+  } else {
+    tokens = std::min<int64_t>(tokens, d->q_tokens);
+    g.p_tiles = (int)ceil_div(d->q_tokens, g.tile_tokens);
+    if (d->S <= kDense) own_tiles = std::min(own_tiles, d->S + (int64_t)d->q_tokens / g.tile_tokens);
+  }
+  g.p_rows = (batched ? (int64_t)d->S * d->q_max : d->q_tokens) * d->Hq;
+  g.items = own_tiles * d->Hkv;
+  g.rounds = 1;
+  const int64_t places = std::max(2 * spc_host::sm_count(), 1), blocks = ceil_div(rule.prefix, kBlock), own = ceil_div(d->k_max, kBlock);
+  const int64_t items = (int64_t)g.p_tiles * d->Hkv, start = 4000;
+  if (items > (1 << 24)) return g;
+  double best = 0.0;
+  for (int64_t z = 1; z <= std::min<int64_t>(blocks, kMaxSplits / 2); ++z) {
+    const int64_t share = ceil_div(blocks, z), oz = std::min<int64_t>(std::max<int64_t>(1, ceil_div(own, share)), kMaxSplits / 2);
+    const int64_t block = std::max<int64_t>(760, std::min(items * z, places) * 5 / std::min(g.p_tiles, 2)), one = start + share * block;
+    const double all = (double)(items * z * one) + (double)g.items * (double)(oz * start + (own * 11 / 20) * 760);
+    double cost = std::max((double)(ceil_div(items * z, places) * one), all / (double)places);
+    cost += 3000.0 + ((double)(z * g.p_rows) + (double)(oz * tokens * d->Hq)) / 5.0;
+    if (z == 1 || cost < best) {
+      best = cost;
+      g.p_splits = (int)z;
+      g.splits = (int)oz;
+    }
+  }
+  // against the sequences one by one, whose tiles walk over the prefix each
+  const int64_t apart = own_tiles * d->Hkv * (blocks + own * 11 / 20) * 760 / places;
+  if (best < (double)apart) g.p_items = items * g.p_splits;
+  return g;
+}
+
 constexpr size_t kPromptHead = 256;  // the fault word
 
+int64_t part_rows(const spc_prompt_dims* d, const PromptGrid& g) {
+  return g.p_splits * g.p_rows + (int64_t)d->S * d->q_max * d->Hq * g.splits;
+}
+
 size_t prompt_bytes(const spc_prompt_dims* d, const PromptRule& rule) {
-  const PromptGrid g = prompt_grid(d, rule);
-  if (g.splits == 1) return kPromptHead;
-  const size_t rows = (size_t)d->S * d->q_max * d->Hq * g.splits;
-  return kPromptHead + rows * (kD * sizeof(float) + sizeof(float2));
+  PromptGrid g = prompt_grid(d, rule);
+  int64_t rows = g.splits > 1 ? part_rows(d, g) : 0;
+  if (rule.prefix > 0) {  // (batched queries with first tokens of their own are not taken together)
+    g = together_grid(d, rule);
+    if (g.p_items > 0) rows = d->q.b != 0 ? std::max(rows, part_rows(d, g)) : part_rows(d, g);
+  }
+  return kPromptHead + (size_t)rows * (kD * sizeof(float) + sizeof(float2));
 }
 
 template <int TILES, int KIND>
@@ -1253,7 +1411,18 @@ spc_status launch_prompt(const spc_prompt_dims* d, const PromptRule& rule, const
   a.q_max = d->q_max;
   a.k_max = d->k_max;
   a.scale = d->scale;
-  const PromptGrid g = prompt_grid(d, rule);
+  PromptGrid g = prompt_grid(d, rule);
+  if constexpr (KIND == kPrefix) {
+    const PromptGrid all = together_grid(d, rule);
+    a.together = all.p_items > 0 && !(d->q.b != 0 && x.q_begin != nullptr);
+    if (a.together) g = all;
+    a.p_items = (int32_t)g.p_items;
+    a.p_tiles = g.p_tiles;
+    a.p_splits = g.p_splits;
+    a.p_bt = g.p_bt;
+    a.p_bs = g.p_bs;
+    a.p_rows = g.p_rows;
+  }
   a.tile_tokens = g.tile_tokens;
   a.pair_tokens = g.pair_tokens;
   a.pairs = g.pairs;
@@ -1266,9 +1435,10 @@ spc_status launch_prompt(const spc_prompt_dims* d, const PromptRule& rule, const
   a.fault = static_cast<uint32_t*>(x.ws);
   a.limit = (uint64_t)prompt_wait_limit(0);
   a.part_rows = (int64_t)d->S * d->q_max * d->Hq;
-  if (a.splits > 1) {
+  const bool parts = a.splits > 1 || a.together;
+  if (parts) {
     a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(x.ws) + kPromptHead);
-    a.part_ml = reinterpret_cast<float2*>(a.part_o + a.part_rows * a.splits * kD);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + part_rows(d, g) * kD);
   }
   a.window = rule.window;
   a.sinks = rule.sinks;
@@ -1285,22 +1455,24 @@ spc_status launch_prompt(const spc_prompt_dims* d, const PromptRule& rule, const
     a.p_tokens = x.p->tokens;
     a.p_len = x.p_len;
     ok = ok && encode_map(&maps.pk, x.pk, 1, x.p->tokens, d->Hkv, x.p->k, 1, keys) &&
-         encode_map(&maps.pv, x.pv, 1, x.p->tokens, d->Hkv, x.p->v, 1, keys);
+         encode_map(&maps.pv, x.pv, 1, x.p->tokens, d->Hkv, x.p->v, 1, keys) &&
+         encode_map(&maps.qs, x.q, a.q_batched ? d->S : 1, d->q_tokens, d->Hq, d->q, a.G, std::max(a.p_bt, 1),
+                    std::max(a.p_bs, 1));
   }
   if (!ok) {
     spc_host::set_cuda_error(cudaErrorInvalidValue);
     return SPC_ERR_CUDA;
   }
-  const int64_t grid = g.items * a.splits;
+  const int64_t grid = g.items * a.splits + g.p_items;
   cudaError_t e = g.tiles == 2 ? launch_prompt_k<2, KIND>(maps, a, grid, stream)
                                : launch_prompt_k<1, KIND>(maps, a, grid, stream);
-  if (e == cudaSuccess && a.splits > 1) {
+  if (e == cudaSuccess && parts) {
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     const int64_t rows = (int64_t)d->q_max * d->Hq;
-    const bool wide = a.splits > 8 && rows * d->S <= (int64_t)spc_host::sm_count() * 7;
+    const bool wide = a.splits + a.p_splits > 8 && rows * d->S <= (int64_t)spc_host::sm_count() * 7;
     cfg.gridDim = dim3((unsigned)(wide ? rows : (rows + 3) / 4), (unsigned)d->S);
     cfg.blockDim = dim3(128);
     cfg.stream = stream;
