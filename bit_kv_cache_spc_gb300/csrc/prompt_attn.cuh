@@ -1309,7 +1309,7 @@ PromptGrid together_grid(const spc_prompt_dims* d, const PromptRule& rule) {
   const bool batched = d->q.b != 0 && d->S > 1;
   g.tiles = 1;
   g.tile_tokens = g.pair_tokens = kTile / G;
-  if (d->S < 2 || d->S > 65535 || rule.prefix == 0 || (batched && 2 * d->q_max > g.tile_tokens)) return g;
+  if (d->S < 2 || d->S > 65535 || d->q_max == 0 || rule.prefix == 0 || (batched && 2 * d->q_max > g.tile_tokens)) return g;
   g.pairs = (int)ceil_div(d->q_max, g.tile_tokens);
   int64_t tokens = (int64_t)d->S * d->q_max, own_tiles = (int64_t)d->S * g.pairs;
   if (batched) {
@@ -1324,7 +1324,7 @@ PromptGrid together_grid(const spc_prompt_dims* d, const PromptRule& rule) {
   g.p_rows = (batched ? (int64_t)d->S * d->q_max : d->q_tokens) * d->Hq;
   g.items = own_tiles * d->Hkv;
   g.rounds = 1;
-  const int64_t places = std::max(2 * spc_host::sm_count(), 1), blocks = ceil_div(rule.prefix, kBlock), own = ceil_div(d->k_max, kBlock);
+  const int64_t places = 2 * spc_host::sm_count(), blocks = ceil_div(rule.prefix, kBlock), own = ceil_div(d->k_max, kBlock);
   const int64_t items = (int64_t)g.p_tiles * d->Hkv, start = 4000;
   if (items > (1 << 24)) return g;
   double best = 0.0;
