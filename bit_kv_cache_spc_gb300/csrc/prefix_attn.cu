@@ -1,8 +1,10 @@
 // The attention of sequences that share a prefix: every query sees all of the
 // prefix, whose keys and values are stored once, and of its own sequence's keys
 // those that are not behind it.  The kernel of prompt_attn.cuh, walking over the
-// prefix's blocks and then over the sequence's.
-#include "prompt_attn.cuh"
+// prefix's blocks and then over the sequence's; or, where the sequences have few
+// rows, over the prefix with the rows of all of them together, and then over
+// each one's own keys (single tokens with few_attn.cuh's kernel).
+#include "few_attn.cuh"
 
 namespace spc {
 
@@ -20,7 +22,8 @@ spc_status launch_prefix_attn(const spc_prompt_dims* d, const spc_prefix* p, con
                               const int32_t* k_len, uint16_t* o, float* lse, void* ws, cudaStream_t stream) {
   PromptRule rule;
   rule.prefix = p->tokens;
-  return launch_prompt<kPrefix>(d, rule, {q, k, v, q_begin, q_len, k_begin, k_len, o, lse, ws, pk, pv, p_len, p}, stream);
+  return launch_prompt<kPrefix>(d, rule, {q, k, v, q_begin, q_len, k_begin, k_len, o, lse, ws, pk, pv, p_len, p}, stream,
+                                launch_few<true>);
 }
 
 }  // namespace spc

@@ -134,9 +134,13 @@ struct PromptArgs {
   int32_t p_tokens;
   // kPrefix with rows of all sequences together in the prefix's tiles:
   int32_t together;
-  int32_t p_items, p_tiles, p_splits;  // items of the prefix (they come first); tiles of rows; splits
+  int32_t p_items, p_tiles, p_splits;  // items of the prefix (0 in the launch of the sequences' own); CTAs' rows; splits
   int32_t p_bt, p_bs;                  // a tile of batched queries: p_bt tokens of p_bs sequences each (packed: 0)
   int64_t p_rows;                      // rows of the prefix's partial results, per split; the sequences' own come behind
+  // few_attn.cuh's:
+  const uint16_t *q, *k;
+  int64_t q_b, q_t, q_h, k_b, k_t, k_h;
+  int32_t few_ctas;  // that share a sequence's keys
 };
 
 template <int KIND>
@@ -174,7 +178,6 @@ template <int KIND>
 __device__ __forceinline__ bool in_parts(const PromptArgs& a) {
   return a.splits > 1 || (KIND == kPrefix && a.together);
 }
-__device__ __forceinline__ bool block_masked(const PromptItem& w, int g) { return (g >= w.ma && g < w.mb) || g >= w.mc; }
 
 struct __align__(16) PromptBars {
   PromptItem item;
@@ -717,8 +720,8 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
   // Whether some row does not see stage j of them in full.
   const auto partly = [&](int j) {
     if constexpr (KIND != kPlain) {
-      const int g = (w.lo + j) * H::kPerStage;
-      return block_masked(w, g) || (H::kPerStage == 2 && block_masked(w, g + 1));
+      const int g = (w.lo + j) * H::kPerStage, end = g + H::kPerStage;
+      return (end > w.ma && g < w.mb) || end > w.mc;
     }
     return w.lo + j >= w.edge;
   };
@@ -730,9 +733,17 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
       // ---- copies: V_j and K_j+kAhead by turns, through the ring ----
       if (lane == 0) {
         bool ok = true;
-        for (int j = 0; j < n && ok; ++j) {
-          ok = load_kv(w, true, j);
-          if (ok && j + H::kAhead < n) ok = load_kv(w, false, j + H::kAhead);
+        if constexpr (KIND != kPlain) {
+          const PromptItem here = w;  // in registers
+          for (int j = 0; j < n && ok; ++j) {
+            ok = load_kv(here, true, j);
+            if (ok && j + H::kAhead < n) ok = load_kv(here, false, j + H::kAhead);
+          }
+        } else {
+          for (int j = 0; j < n && ok; ++j) {
+            ok = load_kv(w, true, j);
+            if (ok && j + H::kAhead < n) ok = load_kv(w, false, j + H::kAhead);
+          }
         }
         bars.filled = x;
       }
@@ -744,8 +755,12 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
       const int stages = __shfl_sync(0xFFFFFFFFu, n, 0);
       const int blocks = stages > 0 ? __shfl_sync(0xFFFFFFFFu, w.blocks[t], 0) : 0;
       const int edge = __shfl_sync(0xFFFFFFFFu, w.edge - w.lo, 0);  // the first stage to be scanned
+      // stages with a block of [ma, mb) or from mc on, in uniform registers
+      const int from_a = KIND == kPlain ? 0 : __shfl_sync(0xFFFFFFFFu, w.ma / H::kPerStage - w.lo, 0);
+      const int to_a = KIND == kPlain ? 0 : __shfl_sync(0xFFFFFFFFu, (w.mb + H::kPerStage - 1) / H::kPerStage - w.lo, 0);
+      const int from_c = KIND == kPlain ? 0 : __shfl_sync(0xFFFFFFFFu, w.mc / H::kPerStage - w.lo, 0);
       const auto scanned = [&](int j) {
-        if constexpr (KIND != kPlain) return __shfl_sync(0xFFFFFFFFu, (int)partly(j), 0) != 0;
+        if constexpr (KIND != kPlain) return (j >= from_a && j < to_a) || j >= from_c;
         return j >= edge;
       };
       const bool here = __shfl_sync(0xFFFFFFFFu, t == 0 || w.two, 0);
@@ -880,6 +895,7 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
       const int from = w.lo * H::kKeys, blocks = w.blocks[t];
       const int masked = H::kPerStage * (w.edge - w.lo);  // the first block that some row does not see in full
       const int g0 = H::kPerStage * w.lo;
+      const int from_a = w.ma - g0, to_a = w.mb - g0, from_c = w.mc - g0;  // the same, for the two runs of not kPlain
       const int low = KIND == kWindow ? max(0, seen - a.window) : 0;  // where the row's window begins
       // the keys of block g that the row sees, as bits
       const auto visible = [&](int g) {
@@ -905,7 +921,7 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
           tmem_wait_ld(x);
           tmem_wait_ld(x + 32);
           if constexpr (KIND != kPlain) {
-            if (block_masked(w, g0 + i)) {
+            if ((i >= from_a && i < to_a) || i >= from_c) {
               const uint64_t vis = visible(g0 + i);
               const uint32_t half[2] = {(uint32_t)vis, (uint32_t)(vis >> 32)};
 #pragma unroll
@@ -1239,6 +1255,7 @@ struct PromptGrid {
   int64_t items;
   // kPrefix with all sequences' rows together:
   int p_tiles = 0, p_splits = 0, p_bt = 0, p_bs = 0;
+  bool p_two = false;  // two-tile CTAs
   int64_t p_rows = 0, p_items = 0;
 };
 
@@ -1292,48 +1309,53 @@ PromptGrid prompt_grid(const spc_prompt_dims* d, const PromptRule& rule) {
   return g;
 }
 
+// Whether a call's queries are single tokens of few heads: few_attn.cuh's.
+constexpr int kFewRows = 16;  // of its products
+bool few_rows(const spc_prompt_dims* d) { return d->q_max == 1 && d->Hq / d->Hkv <= kFewRows; }
+
 // Grid of a call behind a prefix whose tiles hold the rows of all sequences
 // together, so that the prefix's keys are walked once for them and not once for
-// each; the sequences' own keys are walked by items of their own, and all
-// results are joined.  p_items = 0 where that does not pay: the sequences' own
-// tiles are as few, or the partial results cost more than what is saved.
-// One-tile CTAs, as the own items mostly have a few rows.
+// each (in a launch of its own, of two-tile CTAs where the rows fill more than
+// one tile); then the sequences' own keys, and all results are joined.
+// p_items = 0 where that does not pay: the sequences' own tiles are as few, or
+// the partial results cost more than what is saved.
 //
 // Of the splits of the prefix, the number with the least estimate: the items
-// taken in turns by the CTAs' places, the own items filling what the last turn
-// leaves.  Own keys are split where their items would take longer than one of
-// the prefix's.
+// taken in turns by the CTAs' places, and the partial results.  Own keys are
+// split where their items would take longer than one of the prefix's.
 PromptGrid together_grid(const spc_prompt_dims* d, const PromptRule& rule) {
   PromptGrid g = {};
   const int G = d->Hq / d->Hkv;
-  const bool batched = d->q.b != 0 && d->S > 1;
+  const bool batched = d->q.b != 0 && d->S > 1, few = few_rows(d);
   g.tiles = 1;
   g.tile_tokens = g.pair_tokens = kTile / G;
   if (d->S < 2 || d->S > 65535 || d->q_max == 0 || rule.prefix == 0 || (batched && 2 * d->q_max > g.tile_tokens)) return g;
   g.pairs = (int)ceil_div(d->q_max, g.tile_tokens);
-  int64_t tokens = (int64_t)d->S * d->q_max, own_tiles = (int64_t)d->S * g.pairs;
+  int64_t tokens = (int64_t)d->S * d->q_max, own_tiles = (int64_t)d->S * g.pairs, tiles;
   if (batched) {
     g.p_bt = d->q_max;
-    g.p_bs = g.tile_tokens / d->q_max;
-    g.p_tiles = (int)ceil_div(d->S, g.p_bs);
+    g.p_bs = std::min(g.tile_tokens / d->q_max, 256);
+    tiles = ceil_div(d->S, g.p_bs);
   } else {
     tokens = std::min<int64_t>(tokens, d->q_tokens);
-    g.p_tiles = (int)ceil_div(d->q_tokens, g.tile_tokens);
+    tiles = ceil_div(d->q_tokens, g.tile_tokens);
     if (d->S <= kDense) own_tiles = std::min(own_tiles, d->S + (int64_t)d->q_tokens / g.tile_tokens);
   }
   g.p_rows = (batched ? (int64_t)d->S * d->q_max : d->q_tokens) * d->Hq;
-  g.items = own_tiles * d->Hkv;
+  g.items = few ? 0 : own_tiles * d->Hkv;
   g.rounds = 1;
-  const int64_t places = 2 * spc_host::sm_count(), blocks = ceil_div(rule.prefix, kBlock), own = ceil_div(d->k_max, kBlock);
-  const int64_t items = (int64_t)g.p_tiles * d->Hkv, start = 4000;
+  g.p_two = tiles > 1;
+  g.p_tiles = (int)ceil_div(tiles, g.p_two ? 2 : 1);
+  const int64_t items = (int64_t)g.p_tiles * d->Hkv, start = 4000, places = spc_host::sm_count() * (g.p_two ? 1 : 2);
   if (items > (1 << 24)) return g;
+  const int64_t blocks = ceil_div(rule.prefix, kBlock), own = ceil_div(d->k_max, kBlock);
   double best = 0.0;
-  for (int64_t z = 1; z <= std::min<int64_t>(blocks, kMaxSplits / 2); ++z) {
-    const int64_t share = ceil_div(blocks, z), oz = std::min<int64_t>(std::max<int64_t>(1, ceil_div(own, share)), kMaxSplits / 2);
-    const int64_t block = std::max<int64_t>(760, std::min(items * z, places) * 5 / std::min(g.p_tiles, 2)), one = start + share * block;
-    const double all = (double)(items * z * one) + (double)g.items * (double)(oz * start + (own * 11 / 20) * 760);
-    double cost = std::max((double)(ceil_div(items * z, places) * one), all / (double)places);
-    cost += 3000.0 + ((double)(z * g.p_rows) + (double)(oz * tokens * d->Hq)) / 5.0;
+  for (int64_t z = 1; z <= std::min<int64_t>(blocks, few ? kMaxSplits : kMaxSplits / 2); ++z) {
+    const int64_t share = ceil_div(blocks, z);
+    const int64_t oz = few ? 0 : std::min<int64_t>(std::max<int64_t>(1, ceil_div(own, share)), kMaxSplits / 2);
+    const int64_t block = std::max<int64_t>(g.p_two ? 690 : 760, std::min(items * z, places) * 5 / std::min(g.p_tiles, 2));
+    const double cost = (double)(ceil_div(items * z, places) * (start + share * block)) +
+                        ((double)(z * g.p_rows) + (double)(oz * tokens * d->Hq)) / 5.0;
     if (z == 1 || cost < best) {
       best = cost;
       g.p_splits = (int)z;
@@ -1341,8 +1363,8 @@ PromptGrid together_grid(const spc_prompt_dims* d, const PromptRule& rule) {
     }
   }
   // against the sequences one by one, whose tiles walk over the prefix each
-  const int64_t apart = own_tiles * d->Hkv * (blocks + own * 11 / 20) * 760 / places;
-  if (best < (double)apart) g.p_items = items * g.p_splits;
+  const double apart = (double)(own_tiles * d->Hkv * blocks * 760) / (2 * spc_host::sm_count());
+  if (best + 6000.0 < apart) g.p_items = items * g.p_splits;
   return g;
 }
 
@@ -1384,9 +1406,16 @@ struct PromptTensors {
   const spc_prefix* p = nullptr;
 };
 
-template <int KIND>
-spc_status launch_prompt(const spc_prompt_dims* d, const PromptRule& rule, const PromptTensors& x, cudaStream_t stream) {
+PromptArgs prompt_args(const spc_prompt_dims* d, const PromptRule& rule, const PromptTensors& x) {
   PromptArgs a = {};
+  a.q = x.q;
+  a.k = x.k;
+  a.q_b = d->q.b;
+  a.q_t = d->q.t;
+  a.q_h = d->q.h;
+  a.k_b = d->k.b;
+  a.k_t = d->k.t;
+  a.k_h = d->k.h;
   a.v = x.v;
   a.o = x.o;
   a.lse = x.lse;
@@ -1411,6 +1440,27 @@ spc_status launch_prompt(const spc_prompt_dims* d, const PromptRule& rule, const
   a.q_max = d->q_max;
   a.k_max = d->k_max;
   a.scale = d->scale;
+  a.window = rule.window;
+  a.sinks = rule.sinks;
+  if (x.p != nullptr) {
+    a.pv = x.pv;
+    a.pv_t = x.p->v.t;
+    a.pv_h = x.p->v.h;
+    a.p_tokens = x.p->tokens;
+    a.p_len = x.p_len;
+  }
+  a.fault = static_cast<uint32_t*>(x.ws);
+  a.limit = (uint64_t)prompt_wait_limit(0);
+  a.part_rows = (int64_t)d->S * d->q_max * d->Hq;
+  a.splits = a.rounds = 1;
+  return a;
+}
+
+// few: the launch of single tokens' own keys, with what joins them with the prefix.
+template <int KIND>
+spc_status launch_prompt(const spc_prompt_dims* d, const PromptRule& rule, const PromptTensors& x, cudaStream_t stream,
+                         spc_status (*few)(PromptArgs&, const spc_prompt_dims*, cudaStream_t) = nullptr) {
+  PromptArgs a = prompt_args(d, rule, x);
   PromptGrid g = prompt_grid(d, rule);
   if constexpr (KIND == kPrefix) {
     const PromptGrid all = together_grid(d, rule);
@@ -1432,16 +1482,11 @@ spc_status launch_prompt(const spc_prompt_dims* d, const PromptRule& rule, const
   a.rounds = g.rounds;
   a.items = (uint32_t)g.items;
   a.gap = g.gap;
-  a.fault = static_cast<uint32_t*>(x.ws);
-  a.limit = (uint64_t)prompt_wait_limit(0);
-  a.part_rows = (int64_t)d->S * d->q_max * d->Hq;
   const bool parts = a.splits > 1 || a.together;
   if (parts) {
     a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(x.ws) + kPromptHead);
     a.part_ml = reinterpret_cast<float2*>(a.part_o + part_rows(d, g) * kD);
   }
-  a.window = rule.window;
-  a.sinks = rule.sinks;
   PromptMaps<KIND> maps;
   const int64_t kt = std::max(d->k_tokens, 1);  // no keys at all: the maps are never read through
   const uint32_t keys = KIND == kPlain && g.tiles == 2 ? Shape<2>::kKeys : kBlock;
@@ -1449,11 +1494,6 @@ spc_status launch_prompt(const spc_prompt_dims* d, const PromptRule& rule, const
             encode_map(&maps.k, x.k ? x.k : x.q, a.k_batched ? d->S : 1, kt, d->Hkv, d->k, 1, keys) &&
             encode_map(&maps.v, x.v ? x.v : x.q, a.k_batched ? d->S : 1, kt, d->Hkv, d->v, 1, keys);
   if constexpr (KIND == kPrefix) {
-    a.pv = x.pv;
-    a.pv_t = x.p->v.t;
-    a.pv_h = x.p->v.h;
-    a.p_tokens = x.p->tokens;
-    a.p_len = x.p_len;
     ok = ok && encode_map(&maps.pk, x.pk, 1, x.p->tokens, d->Hkv, x.p->k, 1, keys) &&
          encode_map(&maps.pv, x.pv, 1, x.p->tokens, d->Hkv, x.p->v, 1, keys) &&
          encode_map(&maps.qs, x.q, a.q_batched ? d->S : 1, d->q_tokens, d->Hq, d->q, a.G, std::max(a.p_bt, 1),
@@ -1463,9 +1503,15 @@ spc_status launch_prompt(const spc_prompt_dims* d, const PromptRule& rule, const
     spc_host::set_cuda_error(cudaErrorInvalidValue);
     return SPC_ERR_CUDA;
   }
-  const int64_t grid = g.items * a.splits + g.p_items;
-  cudaError_t e = g.tiles == 2 ? launch_prompt_k<2, KIND>(maps, a, grid, stream)
-                               : launch_prompt_k<1, KIND>(maps, a, grid, stream);
+  cudaError_t e = cudaSuccess;
+  if (a.together) {
+    e = g.p_two ? launch_prompt_k<2, KIND>(maps, a, g.p_items, stream) : launch_prompt_k<1, KIND>(maps, a, g.p_items, stream);
+    if (e == cudaSuccess && few != nullptr && g.items == 0) return few(a, d, stream);
+    a.p_items = 0;
+  }
+  const int64_t grid = g.items * a.splits;
+  if (e == cudaSuccess)
+    e = g.tiles == 2 ? launch_prompt_k<2, KIND>(maps, a, grid, stream) : launch_prompt_k<1, KIND>(maps, a, grid, stream);
   if (e == cudaSuccess && parts) {
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -29,6 +29,41 @@ def test_one_sequence(lq, lk, Hq, Hkv, window, sinks):
     check(o, lse, q, k, v, window_sight(lq, lk, window, sinks))
 
 
+@pytest.mark.parametrize("G", [1, 2, 3, 4, 5, 8, 9, 16, 17])
+@pytest.mark.parametrize("Hkv", [1, 8])
+@pytest.mark.parametrize("lk,window,sinks", [([1], 1, 0), ([15], 9, 3), ([16, 17, 0, 33], 16, 0), ([700, 64, 65, 1, 0, 5000], 300, 4),
+                                             ([5000], 4000, 900), ([9000, 3], 5000, 1), ([260] * 40, 128, 1)])
+def test_single_tokens(G, Hkv, lk, window, sinks):
+    """One query token per sequence, of any number of heads over a KV head, in batches of one to many."""
+    import bit_kv_cache_spc_gb300 as spc
+    S, Hq, cap = len(lk), G * Hkv, max(lk) + 3
+    q = rnd(1, S, 1, Hq, D)
+    k, v = (rnd(i, S, Hkv, cap, D).transpose(1, 2) for i in (2, 3))
+    o, lse = torch.full_like(q, 7.0), torch.full((S, 1, Hq), 7.0, device="cuda")
+    for s, n in enumerate(lk):
+        k[s, n:], v[s, n:] = math.nan, math.inf
+    spc.spc_window_attn(q, k, v, o, window, sinks, lse, k_len=i32(lk))
+    for s, n in enumerate(lk[:8]):
+        check(o[s], lse[s], q[s], k[s, :n], v[s, :n], window_sight(1, n, window, sinks))
+
+
+def test_single_tokens_of_some_sequences():
+    """Packed single tokens between others' rows, empty sequences among them; keys of a row that a sequence does not have
+    stay unread."""
+    import bit_kv_cache_spc_gb300 as spc
+    S, T, Hq, Hkv = 50, 900, 8, 2
+    q, k, v = rnd(1, 2 * S, Hq, D), rnd(2, T, Hkv, D), rnd(3, T, Hkv, D)
+    lk, kb, lq = [(s * 53) % 300 for s in range(S)], [(s * 31) % 600 for s in range(S)], [int(s % 5 != 2) for s in range(S)]
+    o, lse = torch.full_like(q, 7.0), torch.full((2 * S, Hq), 7.0, device="cuda")
+    spc.spc_window_attn(q, k, v, o, 100, 3, lse, q_begin=2 * torch.arange(S, dtype=torch.int32, device="cuda"), q_len=i32(lq),
+                        k_begin=i32(kb), k_len=i32(lk), q_max=1, k_max=300)
+    for s in range(S):
+        b = 2 * s
+        if lq[s]:
+            check(o[b:b + 1], lse[b:b + 1], q[b:b + 1], k[kb[s]:kb[s] + lk[s]], v[kb[s]:kb[s] + lk[s]], window_sight(1, lk[s], 100, 3))
+        assert bool((o[b + lq[s]:b + 2] == 7).all()) and bool((lse[b + lq[s]:b + 2] == 7).all())
+
+
 @pytest.mark.parametrize("lq,lk,window,sinks", [(1, 0, 5, 2), (9, 4, 2, 1), (300, 130, 64, 10), (140, 1, 1, 0), (1300, 1100, 90, 5),
                                                 (256, 100, 70, 200), (600, 345, 100, 0)])
 def test_rows_that_see_nothing(lq, lk, window, sinks):
@@ -209,14 +244,15 @@ def test_device_lengths_are_held_to_the_tensors():
     assert bool((buf[:150] == 7).all()) and bool((buf[150 + 30:150 + 90] == 7).all()) and bool((buf[150 + T:] == 7).all())
 
 
-def test_graphs_and_streams_repeat_the_same_bits():
+@pytest.mark.parametrize("lq", [1, 2])
+def test_graphs_and_streams_repeat_the_same_bits(lq):
     """Captured and replayed with other lengths, on other streams, two calls at once with their own workspaces."""
     import bit_kv_cache_spc_gb300 as spc
-    q, k, v = rnd(1, 1, 32, D), rnd(2, 9000, 8, D), rnd(3, 9000, 8, D)
-    o, lse, n = torch.zeros_like(q), torch.zeros((1, 32), device="cuda"), i32([9000])
+    q, k, v = rnd(1, lq, 32, D), rnd(2, 9000, 8, D), rnd(3, 9000, 8, D)
+    o, lse, n = torch.zeros_like(q), torch.zeros((lq, 32), device="cuda"), i32([9000])
     need = spc.spc_window_attn_workspace_bytes(q, k, v, o, 4000, 4)
     ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
-    assert need > 256  # one query over a long window: the keys are split
+    assert (need > 256) == (lq == 2)  # two queries over a long window: the keys are split
     spc.spc_window_attn(q, k, v, o, 4000, 4, lse, k_len=n, ws=ws)
     want = (o.clone(), lse.clone())
     torch.cuda.synchronize()
@@ -230,7 +266,7 @@ def test_graphs_and_streams_repeat_the_same_bits():
     n.fill_(5003)
     g.replay()
     torch.cuda.synchronize()
-    check(o, lse, q, k[:5003], v[:5003], window_sight(1, 5003, 4000, 4))
+    check(o, lse, q, k[:5003], v[:5003], window_sight(lq, 5003, 4000, 4))
     n.fill_(9000)
     side = [torch.cuda.Stream() for _ in range(2)]
     outs, wss = [torch.zeros_like(o) for _ in side], [torch.zeros_like(ws) for _ in side]

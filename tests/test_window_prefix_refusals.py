@@ -97,12 +97,14 @@ def test_workspaces():
     one = dims(q_max=1, k_tokens=8192, k_max=8192, k=kl, v=kl)
     plain = _lib.spc_prompt_attn_workspace_bytes(C.byref(one))
     assert plain > 256 and _lib.spc_window_attn_workspace_bytes(C.byref(one), 8192, 3) == plain
-    assert 256 < _lib.spc_window_attn_workspace_bytes(C.byref(one), 4096, 3) <= plain
-    assert _lib.spc_window_attn_workspace_bytes(C.byref(one), 64, 0) == 256  # two blocks of keys: no split
+    assert _lib.spc_window_attn_workspace_bytes(C.byref(one), 4096, 3) == 256  # single tokens join on the chip
+    two = dims(q_max=2, k_tokens=8192, k_max=8192, k=kl, v=kl)
+    assert _lib.spc_window_attn_workspace_bytes(C.byref(two), 4096, 3) > 256
+    assert _lib.spc_window_attn_workspace_bytes(C.byref(two), 64, 0) == 256  # two blocks of keys: no split
     p = spc_prefix(0, lay(0, 256, 128), lay(0, 256, 128))
     assert _lib.spc_prefix_attn_workspace_bytes(C.byref(one), C.byref(p)) == plain
     assert _lib.spc_prefix_attn_workspace_bytes(C.byref(one), None) == 0
-    small = dims(q_max=1)
+    small = dims(q_max=2)
     p.tokens = 30000
     need = _lib.spc_prefix_attn_workspace_bytes(C.byref(small), C.byref(p))
     assert need > 256 and _lib.spc_prefix_attn(*prefix_args(d=small, tokens=30000, ws=None, ws_bytes=0)) == INVALID
