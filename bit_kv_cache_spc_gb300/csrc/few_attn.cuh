@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) few_attn_kernel(const __gri
     if (PREFIX) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
-        if (lane + 32 * u < splits) out[u] = a.part_ml[joined_place(a, lane + 32 * u, s, qb, 0, head)];
+        if (lane + 32 * u < splits) out[u] = a.part_ml[shared_row(a, lane + 32 * u, s, qb, 0, head)];
     }
     float top = fmaxf(in.x, fmaxf(out[0].x, out[1].x));
 #pragma unroll
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) few_attn_kernel(const __gri
 #pragma unroll
         for (int u = 0; u < 8; ++u)
           if (z0 + u < splits)
-            x[u] = reinterpret_cast<const float4*>(a.part_o + joined_place(a, z0 + u, s, qb, 0, head) * kD)[lane];
+            x[u] = shared_part(a, shared_row(a, z0 + u, s, qb, 0, head), lane);
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
           const int z = z0 + u;

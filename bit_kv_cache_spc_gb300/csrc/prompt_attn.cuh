@@ -136,7 +136,8 @@ struct PromptArgs {
   int32_t together;
   int32_t p_items, p_tiles, p_splits;  // items of the prefix (0 in the launch of the sequences' own); CTAs' rows; splits
   int32_t p_bt, p_bs;                  // a tile of batched queries: p_bt tokens of p_bs sequences each (packed: 0)
-  int64_t p_rows;                      // rows of the prefix's partial results, per split; the sequences' own come behind
+  int32_t row_tiles;                   // tiles of rows in all
+  int64_t p_rows;                      // rows of the prefix's partial results; the sequences' own come behind
   // few_attn.cuh's:
   const uint16_t *q, *k;
   int64_t q_b, q_t, q_h, k_b, k_t, k_h;
@@ -568,10 +569,21 @@ __device__ __forceinline__ int64_t lse_place(const PromptArgs& a, int s, int tok
 __device__ __forceinline__ int64_t part_place(const PromptArgs& a, int split, int s, int tok, int head) {
   return split * a.part_rows + ((int64_t)s * a.q_max + tok) * a.Hq + head;
 }
-// The same with the prefix's splits before the sequences' own: qb is the sequence's first query token.
-__device__ __forceinline__ int64_t joined_place(const PromptArgs& a, int z, int s, int qb, int tok, int head) {
-  if (z >= a.p_splits) return a.p_splits * a.p_rows + part_place(a, z - a.p_splits, s, tok, head);
-  return z * a.p_rows + ((a.p_bt > 0 ? (int64_t)s * a.q_max : qb) + tok) * a.Hq + head;
+// Partial results of the prefix's items lie before the sequences' own, tile by tile, as the CTAs' shared memory holds
+// them (so that a warp's 32 rows leave in four copies): 32 rows of 32 floats after 32 rows of the next 32, each 16-byte
+// chunk i of a row at i ^ (row % 8).  Number of row r of a tile, and of a token's and head's row:
+__device__ __forceinline__ int64_t shared_row(const PromptArgs& a, int split, int hkv, int tile, int r) {
+  return ((int64_t)(split * a.Hkv + hkv) * a.row_tiles + tile) * kTile + r;
+}
+__device__ __forceinline__ int64_t shared_row(const PromptArgs& a, int split, int s, int qb, int tok, int head) {
+  const int unit = a.p_bt > 0 ? a.p_bs : a.tile_tokens, at = a.p_bt > 0 ? s : qb + tok, tile = at / unit;
+  const int token = a.p_bt > 0 ? (at - tile * unit) * a.p_bt + tok : at - tile * unit;
+  return shared_row(a, split, head / a.G, tile, token * a.G + head % a.G);
+}
+// Lane `lane`'s four channels of such a row.
+__device__ __forceinline__ float4 shared_part(const PromptArgs& a, int64_t row, int lane) {
+  const int r = (int)(row & 31);
+  return reinterpret_cast<const float4*>(a.part_o)[(row - r) * (kD / 4) + (lane >> 3) * 256 + r * 8 + ((lane & 7) ^ (r & 7))];
 }
 
 // exp2(x c - m c) of a row's 64 scores, as bf16 pairs into P, and their sum.
@@ -605,6 +617,9 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
   PromptBars& bars = *reinterpret_cast<PromptBars*>(ring + kStages * H::kStageBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+  if constexpr (KIND == kPrefix) {  // the launch behind the prefix's waits for its results itself
+    if (a.p_items > 0) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  }
   int x = 0;  // the copy warp: stages filled so far
   // values: of the values' rows (else of the keys')
   const auto load_kv = [&](const PromptItem& w, bool values, int j) {
@@ -983,7 +998,12 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
           const float inv = parts ? 1.f : (any ? 1.f / l : 0.f);
           int64_t part = part_place(a, w.split, w.s, tok, head);
           if constexpr (KIND == kPrefix) {
-            if (a.together) part = joined_place(a, w.split + (w.shared ? 0 : a.p_splits), seq, 0, tok, head);
+            if (w.shared) {
+              const int first = a.p_bt > 0 ? w.s / a.p_bs : w.tok0 / a.tile_tokens;
+              part = shared_row(a, w.split, w.hkv, first + t, r);
+            } else {
+              part += a.p_rows;
+            }
           }
           // Through shared memory (the tile's Q has been used up), 256 bytes of every row at a time, so that a warp
           // stores whole rows: chunk c of row i of the warp lies at chunk c ^ (i % 8).
@@ -993,10 +1013,8 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
           if (row)
             out = parts ? (uint64_t)(a.part_o + part * kD)
                                : (uint64_t)(a.o + w.s * a.o_b + (int64_t)(w.qb + tok) * a.o_t + head * a.o_h);
-          // Rolled loops: this runs once per item, and unrolled it is bound by fetching its instructions.
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            float y[32];
+          // 32 channels of the row's sum
+          const auto sums = [&](int q, float* y) {
             if (blocks > 0) {
               tmem_ld32(o_addr + 32 * q, y);
               tmem_wait_ld(y);
@@ -1036,6 +1054,45 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
                 }
               }
             }
+          };
+          bool stored = false;
+          if constexpr (KIND == kPrefix) {
+            // A whole tile, whatever rows it has: each warp's 8 KB hold its rows' 32 channels twice.
+            if (w.shared) {
+              stored = true;
+              float* to = a.part_o + (part - lane) * kD;
+              const bool some = __any_sync(0xFFFFFFFFu, row);
+#pragma unroll 1
+              for (int q = 0; q < 4 && some; ++q) {
+                float y[32];
+                sums(q, y);
+                if (q >= 2) {
+                  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;\n" ::: "memory");
+                  __syncwarp();
+                }
+                uint4* here = stage + (q & 1) * 256;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  here[lane * 8 + (i ^ (lane & 7))] = make_uint4(__float_as_uint(y[4 * i]), __float_as_uint(y[4 * i + 1]),
+                                                                 __float_as_uint(y[4 * i + 2]), __float_as_uint(y[4 * i + 3]));
+                asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], 4096;\n" ::"l"(to + q * 1024),
+                               "r"(smem_addr(here))
+                               : "memory");
+                  asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+                }
+              }
+              if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
+              __syncwarp();
+            }
+          }
+          // Rolled loops: this runs once per item, and unrolled it is bound by fetching its instructions.
+#pragma unroll 1
+          for (int q = 0; q < 4 && !stored; ++q) {
+            float y[32];
+            sums(q, y);
             bool full;  // 256 bytes of every row are staged
             if (parts) {
 #pragma unroll
@@ -1090,6 +1147,9 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
     tc_fence_before();
     __syncthreads();
   }
+  if constexpr (KIND == kPrefix) {  // the join comes when this launch has ended, and needs both
+    if (a.together && a.p_items == 0) asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  }
   if (warp == H::kProductWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(H::kTmemCols) : "memory");
@@ -1117,8 +1177,10 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant_
   bool any = tok + lk - lq + 1 > 0 && lk > 0;
   if (KIND == kPrefix) any = any || (a.p_len ? clampi(a.p_len[0], 0, a.p_tokens) : a.p_tokens) > 0;
   const int splits = a.splits + (KIND == kPrefix ? a.p_splits : 0);
+  const int shared = KIND == kPrefix ? a.p_splits : 0;  // they come first
   const auto place = [&](int z) {
-    return KIND == kPrefix ? joined_place(a, z, s, qb, tok, head) : part_place(a, z, s, tok, head);
+    if (z < shared) return shared_row(a, z, s, qb, tok, head);
+    return (KIND == kPrefix ? a.p_rows : 0) + part_place(a, z - shared, s, tok, head);
   };
   float2 ml[2];
 #pragma unroll
@@ -1130,7 +1192,10 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant_
   const auto load = [&](int z0) {  // eight splits' loads in flight
 #pragma unroll
     for (int u = 0; u < 8; ++u)
-      if (z0 + u < splits) x[u] = reinterpret_cast<const float4*>(a.part_o + place(z0 + u) * kD)[lane];
+      if (z0 + u < shared)
+        x[u] = shared_part(a, place(z0 + u), lane);
+      else if (z0 + u < splits)
+        x[u] = reinterpret_cast<const float4*>(a.part_o + place(z0 + u) * kD)[lane];
   };
   load(8 * part);
   float m = fmaxf(ml[0].x, ml[1].x);
@@ -1341,11 +1406,11 @@ PromptGrid together_grid(const spc_prompt_dims* d, const PromptRule& rule) {
     tiles = ceil_div(d->q_tokens, g.tile_tokens);
     if (d->S <= kDense) own_tiles = std::min(own_tiles, d->S + (int64_t)d->q_tokens / g.tile_tokens);
   }
-  g.p_rows = (batched ? (int64_t)d->S * d->q_max : d->q_tokens) * d->Hq;
   g.items = few ? 0 : own_tiles * d->Hkv;
   g.rounds = 1;
   g.p_two = tiles > 1;
   g.p_tiles = (int)ceil_div(tiles, g.p_two ? 2 : 1);
+  const int64_t shared = (int64_t)d->Hkv * g.p_tiles * (g.p_two ? 2 : 1) * kTile;  // rows of partial results per split
   const int64_t items = (int64_t)g.p_tiles * d->Hkv, start = 4000, places = spc_host::sm_count() * (g.p_two ? 1 : 2);
   if (items > (1 << 24)) return g;
   const int64_t blocks = ceil_div(rule.prefix, kBlock), own = ceil_div(d->k_max, kBlock);
@@ -1355,15 +1420,19 @@ PromptGrid together_grid(const spc_prompt_dims* d, const PromptRule& rule) {
     const int64_t oz = few ? 0 : std::min<int64_t>(std::max<int64_t>(1, ceil_div(own, share)), kMaxSplits / 2);
     const int64_t block = std::max<int64_t>(g.p_two ? 690 : 760, std::min(items * z, places) * 5 / std::min(g.p_tiles, 2));
     const double cost = (double)(ceil_div(items * z, places) * (start + share * block)) +
-                        ((double)(z * g.p_rows) + (double)(oz * tokens * d->Hq)) / 5.0;
+                        ((double)(z * shared) + (double)(oz * tokens * d->Hq)) / 5.0;
     if (z == 1 || cost < best) {
       best = cost;
       g.p_splits = (int)z;
       g.splits = (int)oz;
     }
   }
+  g.p_rows = shared * g.p_splits;
   // against the sequences one by one, whose tiles walk over the prefix each
-  const double apart = (double)(own_tiles * d->Hkv * blocks * 760) / (2 * spc_host::sm_count());
+  const bool pairs = g.pairs > 1;
+  int64_t own_pairs = (int64_t)d->S * ceil_div(d->q_max, 2 * g.tile_tokens);
+  if (!batched && d->S <= kDense) own_pairs = std::min(own_pairs, d->S + (int64_t)d->q_tokens / (2 * g.tile_tokens));
+  const double apart = (double)((pairs ? own_pairs * 690 * 2 : own_tiles * 760) * d->Hkv * blocks) / (2 * spc_host::sm_count());
   if (best + 6000.0 < apart) g.p_items = items * g.p_splits;
   return g;
 }
@@ -1371,7 +1440,7 @@ PromptGrid together_grid(const spc_prompt_dims* d, const PromptRule& rule) {
 constexpr size_t kPromptHead = 256;  // the fault word
 
 int64_t part_rows(const spc_prompt_dims* d, const PromptGrid& g) {
-  return g.p_splits * g.p_rows + (int64_t)d->S * d->q_max * d->Hq * g.splits;
+  return g.p_rows + (int64_t)d->S * d->q_max * d->Hq * g.splits;
 }
 
 size_t prompt_bytes(const spc_prompt_dims* d, const PromptRule& rule) {
@@ -1384,14 +1453,25 @@ size_t prompt_bytes(const spc_prompt_dims* d, const PromptRule& rule) {
   return kPromptHead + (size_t)rows * (kD * sizeof(float) + sizeof(float2));
 }
 
+// early: may start while the launch before it runs (which says when, and is waited for in the kernel).
 template <int TILES, int KIND>
-cudaError_t launch_prompt_k(const PromptMaps<KIND>& maps, const PromptArgs& a, int64_t grid, cudaStream_t stream) {
+cudaError_t launch_prompt_k(const PromptMaps<KIND>& maps, const PromptArgs& a, int64_t grid, cudaStream_t stream,
+                            bool early = false) {
   static unsigned long long configured = 0ull;
   const cudaError_t e =
       spc_host::ensure_smem_limit(configured, prompt_attn_kernel<TILES, KIND>, Shape<TILES>::kSmemBytes);
   if (e != cudaSuccess) return e;
-  prompt_attn_kernel<TILES, KIND><<<(unsigned)grid, Shape<TILES>::kThreads, Shape<TILES>::kSmemBytes, stream>>>(maps, a);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(Shape<TILES>::kThreads);
+  cfg.dynamicSmemBytes = Shape<TILES>::kSmemBytes;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, prompt_attn_kernel<TILES, KIND>, maps, a);
 }
 
 // What the caller gives besides the shape; pk, pv, p: kPrefix.
@@ -1472,6 +1552,7 @@ spc_status launch_prompt(const spc_prompt_dims* d, const PromptRule& rule, const
     a.p_bt = g.p_bt;
     a.p_bs = g.p_bs;
     a.p_rows = g.p_rows;
+    a.row_tiles = g.p_tiles * (g.p_two ? 2 : 1);
   }
   a.tile_tokens = g.tile_tokens;
   a.pair_tokens = g.pair_tokens;
@@ -1511,7 +1592,8 @@ spc_status launch_prompt(const spc_prompt_dims* d, const PromptRule& rule, const
   }
   const int64_t grid = g.items * a.splits;
   if (e == cudaSuccess)
-    e = g.tiles == 2 ? launch_prompt_k<2, KIND>(maps, a, grid, stream) : launch_prompt_k<1, KIND>(maps, a, grid, stream);
+    e = g.tiles == 2 ? launch_prompt_k<2, KIND>(maps, a, grid, stream)
+                     : launch_prompt_k<1, KIND>(maps, a, grid, stream, a.together);
   if (e == cudaSuccess && parts) {
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
