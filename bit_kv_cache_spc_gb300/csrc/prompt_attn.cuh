@@ -137,6 +137,7 @@ struct PromptArgs {
   int32_t p_items, p_tiles, p_splits;  // items of the prefix (0 in the launch of the sequences' own); CTAs' rows; splits
   int32_t p_bt, p_bs;                  // a tile of batched queries: p_bt tokens of p_bs sequences each (packed: 0)
   int32_t row_tiles;                   // tiles of rows in all
+  int32_t o_boxes;                     // not kPlain: a warp's 32 rows are whole tokens, so that the map of o has them
   int64_t p_rows;                      // rows of the prefix's partial results; the sequences' own come behind
   // few_attn.cuh's:
   const uint16_t *q, *k;
@@ -146,11 +147,15 @@ struct PromptArgs {
 
 template <int KIND>
 struct PromptMaps {
+  CUtensorMap q, k, v, o;  // o: of a warp's 32 rows
+};
+template <>
+struct PromptMaps<kPlain> {
   CUtensorMap q, k, v;
 };
 template <>
 struct PromptMaps<kPrefix> {
-  CUtensorMap q, k, v, pk, pv, qs;  // qs: of tiles with several sequences' rows
+  CUtensorMap q, k, v, o, pk, pv, qs;  // qs: of tiles with several sequences' rows
 };
 
 // What a CTA works on.
@@ -872,13 +877,14 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
   #pragma unroll 4
         for (int i = tid - 32 * H::kScanWarp; i < H::kStageBytes / 16; i += H::kThreads - 32 * H::kScanWarp) {
           const uint4 v = tile[i];
+          // an exponent of all ones carries into the sign's place
+          const auto carry = [](uint32_t x) { return (x & 0x7F807F80u) + 0x00800080u; };
+          if (((carry(v.x) | carry(v.y) | carry(v.z) | carry(v.w)) & 0x80008000u) == 0u) continue;
           // 16-bit halves with an exponent of all ones
           const uint32_t m0 = __vcmpeq2(v.x & 0x7F807F80u, 0x7F807F80u), m1 = __vcmpeq2(v.y & 0x7F807F80u, 0x7F807F80u);
           const uint32_t m2 = __vcmpeq2(v.z & 0x7F807F80u, 0x7F807F80u), m3 = __vcmpeq2(v.w & 0x7F807F80u, 0x7F807F80u);
-          if (m0 | m1 | m2 | m3) {
-            tile[i] = make_uint4(v.x & ~m0, v.y & ~m1, v.z & ~m2, v.w & ~m3);
-            touched = true;
-          }
+          tile[i] = make_uint4(v.x & ~m0, v.y & ~m1, v.z & ~m2, v.w & ~m3);
+          touched = true;
         }
         if (touched) bars.bad = 1u;
         asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
@@ -1085,6 +1091,35 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
                 }
               }
               if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
+              __syncwarp();
+            }
+          }
+          if constexpr (KIND != kPlain) {
+            // Rows of the sequence to the warp's last one: as two boxes of 64 channels, swizzled like Q's.
+            if (!stored && !parts && a.o_boxes && __all_sync(0xFFFFFFFFu, row)) {
+              stored = true;
+#pragma unroll 1
+              for (int q = 0; q < 4; ++q) {
+                float y[32];
+                sums(q, y);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  stage[(q >> 1) * 256 + lane * 8 + ((4 * (q & 1) + i) ^ (lane & 7))] =
+                      make_uint4(pack_bf16x2(y[8 * i] * inv, y[8 * i + 1] * inv), pack_bf16x2(y[8 * i + 2] * inv, y[8 * i + 3] * inv),
+                                 pack_bf16x2(y[8 * i + 4] * inv, y[8 * i + 5] * inv),
+                                 pack_bf16x2(y[8 * i + 6] * inv, y[8 * i + 7] * inv));
+              }
+              asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+              __syncwarp();
+              if (lane == 0) {
+                for (int h = 0; h < 2; ++h)
+                  asm volatile(
+                      "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];\n" ::"l"(&maps.o),
+                      "r"(smem_addr(stage + 256 * h)), "r"(64 * h), "r"(w.hkv * a.G), "r"(w.qb + tok), "r"(a.q_batched ? w.s : 0)
+                      : "memory");
+                asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+                asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
+              }
               __syncwarp();
             }
           }
@@ -1574,6 +1609,11 @@ spc_status launch_prompt(const spc_prompt_dims* d, const PromptRule& rule, const
   bool ok = encode_map(&maps.q, x.q, a.q_batched ? d->S : 1, d->q_tokens, d->Hq, d->q, a.G, a.tile_tokens) &&
             encode_map(&maps.k, x.k ? x.k : x.q, a.k_batched ? d->S : 1, kt, d->Hkv, d->k, 1, keys) &&
             encode_map(&maps.v, x.v ? x.v : x.q, a.k_batched ? d->S : 1, kt, d->Hkv, d->v, 1, keys);
+  if constexpr (KIND != kPlain) {
+    a.o_boxes = a.G <= 32 && 32 % a.G == 0;
+    ok = ok && encode_map(&maps.o, x.o, a.q_batched ? d->S : 1, d->q_tokens, d->Hq, d->o, a.o_boxes ? a.G : 1,
+                          a.o_boxes ? 32 / a.G : 1);
+  }
   if constexpr (KIND == kPrefix) {
     ok = ok && encode_map(&maps.pk, x.pk, 1, x.p->tokens, d->Hkv, x.p->k, 1, keys) &&
          encode_map(&maps.pv, x.pv, 1, x.p->tokens, d->Hkv, x.p->v, 1, keys) &&
