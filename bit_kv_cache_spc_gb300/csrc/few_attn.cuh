@@ -33,12 +33,15 @@ constexpr int kFewWarpBytes = kFewStages * kFewStageBytes;
 constexpr int kFewRowFloats = kD + 4;  // of a warp's result in shared memory: rows start in different banks
 constexpr int kFewSmemBytes = kFewWarps * kFewWarpBytes + kFewWarps * kFewRows * 8;
 constexpr int kFewCluster = 8;   // CTAs at most
+constexpr int kFewLoads = 16;    // of the prefix's splits' results in flight
 static_assert(kFewRows * kFewRowFloats * 4 <= kFewWarpBytes, "a warp's result outgrows its stages");
 static_assert(2 * (kFewSmemBytes + 1024) <= 233472, "more shared memory than two CTAs have");
 
 // Copies 16 bytes, or fills in zeros.
-__device__ __forceinline__ void copy_or_zero(uint32_t to, const void* from, bool copy) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(to), "l"(from), "r"(copy ? 16 : 0) : "memory");
+__device__ __forceinline__ void copy_or_zero(uint32_t to, const void* from, bool copy, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;\n" ::"r"(to), "l"(from), "r"(copy ? 16 : 0),
+               "l"(policy)
+               : "memory");
 }
 __device__ __forceinline__ void load_matrices(uint32_t addr, uint32_t r[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
@@ -102,6 +105,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) few_attn_kernel(const __gri
   // ---- copies: a lane takes chunk lane % 16 of every second row ----
   const uint16_t* kp = a.k + seq_k * a.k_b + (int64_t)kb * a.k_t + hkv * a.k_h + (lane & 15) * 8;
   const uint16_t* vp = a.v + seq_k * a.v_b + (int64_t)kb * a.v_t + hkv * a.v_h + (lane & 15) * 8;
+  const uint64_t policy = l2_policy(true);
   const auto load = [&](int it) {
     const int b = b0 + it * kFewWarps;
     if (b < b1) {
@@ -112,8 +116,8 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) few_attn_kernel(const __gri
         const bool there = x < n;
         const int64_t key = there ? (x < ns ? x : x + (low - ns)) : 0;
         const uint32_t at = to + row * 256 + (((lane & 15) ^ (row & 7)) << 4);  // so that eight rows' chunks lie in all banks
-        copy_or_zero(at, kp + key * a.k_t, there);
-        copy_or_zero(at + kFewStageBytes / 2, vp + key * a.v_t, there);
+        copy_or_zero(at, kp + key * a.k_t, there, policy);
+        copy_or_zero(at + kFewStageBytes / 2, vp + key * a.v_t, there, policy);
       }
     }
     cp_async_commit();
@@ -235,11 +239,23 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) few_attn_kernel(const __gri
   for (int row = rank * kFewWarps + warp; row < a.G; row += parts) {
     const int head = hkv * a.G + row;
     float2 in = make_float2(-INFINITY, 0.f), out[2] = {in, in};
+    float4 x[kFewLoads];
+    int64_t first = 0, step = 0;  // the row among the prefix's partial results, and from one split to the next
+    const auto load_parts = [&](int z0) {
+#pragma unroll
+      for (int u = 0; u < kFewLoads; ++u)
+        if (z0 + u < splits) x[u] = shared_part(a, first + (z0 + u) * step, lane);
+    };
+    if (PREFIX) {
+      first = shared_row(a, 0, s, qb, 0, head);
+      step = (int64_t)a.Hkv * a.row_tiles * kTile;
+      load_parts(0);
+    }
     if (lane < parts) in = cluster_ld2(cluster_addr(ml_at + ((lane & 3) * kFewRows + row) * 8, lane >> 2));
     if (PREFIX) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
-        if (lane + 32 * u < splits) out[u] = a.part_ml[shared_row(a, lane + 32 * u, s, qb, 0, head)];
+        if (lane + 32 * u < splits) out[u] = a.part_ml[first + (lane + 32 * u) * step];
     }
     float top = fmaxf(in.x, fmaxf(out[0].x, out[1].x));
 #pragma unroll
@@ -252,14 +268,10 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) few_attn_kernel(const __gri
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
     const auto add = [&](float w, float4 x) { y = make_float4(y.x + w * x.x, y.y + w * x.y, y.z + w * x.z, y.w + w * x.w); };
     if (PREFIX) {
-      for (int z0 = 0; z0 < splits; z0 += 8) {
-        float4 x[8];
+      for (int z0 = 0; z0 < splits; z0 += kFewLoads) {
+        if (z0 > 0) load_parts(z0);
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-          if (z0 + u < splits)
-            x[u] = shared_part(a, shared_row(a, z0 + u, s, qb, 0, head), lane);
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < kFewLoads; ++u) {
           const int z = z0 + u;
           const float w = __shfl_sync(0xFFFFFFFFu, z < 32 ? g[0] : g[1], z & 31);
           const float total = __shfl_sync(0xFFFFFFFFu, z < 32 ? out[0].y : out[1].y, z & 31);
