@@ -137,6 +137,8 @@ struct PromptArgs {
   int32_t p_items, p_tiles, p_splits;  // items of the prefix (0 in the launch of the sequences' own); CTAs' rows; splits
   int32_t p_bt, p_bs;                  // a tile of batched queries: p_bt tokens of p_bs sequences each (packed: 0)
   int32_t row_tiles;                   // tiles of rows in all
+  int32_t mixed;                       // the prefix's items walk over their sequences' own keys too
+  int32_t parts;                       // partial results are written, to be joined
   int32_t o_boxes;                     // not kPlain: a warp's 32 rows are whole tokens, so that the map of o has them
   int64_t p_rows;                      // rows of the prefix's partial results; the sequences' own come behind
   // few_attn.cuh's:
@@ -174,6 +176,7 @@ struct PromptItem {
   int prefix;      // tokens of the shared prefix
   int shared;      // rows of several sequences, the prefix's keys alone (tok0: the first token on the axis of packed
                    // queries; s: the first sequence of batched ones)
+  int mixed;       // of those, the sequences whose own keys are walked as well
 };
 
 __device__ __forceinline__ int block_key(const PromptItem& w, int g) {
@@ -182,7 +185,25 @@ __device__ __forceinline__ int block_key(const PromptItem& w, int g) {
 // Whether partial results are written, to be joined.
 template <int KIND>
 __device__ __forceinline__ bool in_parts(const PromptArgs& a) {
-  return a.splits > 1 || (KIND == kPrefix && a.together);
+  return KIND == kPrefix ? a.parts != 0 : a.splits > 1;
+}
+
+// The sequences of a mixed item, in shared memory behind the barriers: sequence s has rows in its tiles, and its keys'
+// blocks are those from number g0 of the walk on.
+struct MixedSeq {
+  int s, qb, lq, kb, lk, g0;
+};
+constexpr int kMixed = 64;
+template <int TILES, int KIND>
+constexpr int smem_bytes() {
+  return Shape<TILES>::kSmemBytes + (KIND == kPrefix ? kMixed * (int)sizeof(MixedSeq) : 0);
+}
+static_assert(smem_bytes<2, kPrefix>() <= 232448 && 2 * (smem_bytes<1, kPrefix>() + 1024) <= 233472,
+              "more shared memory than an SM has");
+// Of block g, from entry e on.
+__device__ __forceinline__ int mixed_entry(const MixedSeq* table, int n, int g, int e = 0) {
+  while (e + 1 < n && table[e + 1].g0 <= g) ++e;
+  return e;
 }
 
 struct __align__(16) PromptBars {
@@ -465,7 +486,7 @@ __device__ __forceinline__ bool dense_item(const PromptArgs& a, int k, PromptIte
 // Item i of the prefix's, rows of all sequences together: tile of rows fastest, so that CTAs that run together share
 // keys, then KV head, then split.  False where no sequence has a row in the tile.
 template <int TILES>
-__device__ __forceinline__ bool shared_item(const PromptArgs& a, uint32_t i, PromptItem& w) {
+__device__ __forceinline__ bool shared_item(const PromptArgs& a, uint32_t i, PromptItem& w, MixedSeq* table) {
   constexpr int kPerStage = Shape<TILES>::kPerStage;
   const int lane = threadIdx.x & 31, tile = (int)(i % a.p_tiles);
   i /= a.p_tiles;
@@ -478,8 +499,33 @@ __device__ __forceinline__ bool shared_item(const PromptArgs& a, uint32_t i, Pro
   w.s = a.p_bt > 0 ? first : 0;
   w.tok0 = a.p_bt > 0 ? 0 : first;
   w.two = TILES == 2 && first + per_tile < (a.p_bt > 0 ? a.S : a.q_tokens);
+  w.prefix = a.p_len ? clampi(a.p_len[0], 0, a.p_tokens) : a.p_tokens;
+  w.nb = w.nb0 = w.mc = (w.prefix + kBlock - 1) / kBlock;
   bool live = false;
-  if (a.p_bt > 0) {
+  if (a.mixed) {  // 64 sequences at most, two a lane: those with rows here, one behind the other
+#pragma unroll
+    for (int u = 0; u < kMixed / 32; ++u) {
+      const int s = 32 * u + lane;
+      int lq = 0, lk = 0, qb = 0, kb = 0;
+      if (s < a.S) sequence(a, s, lq, lk, qb, kb);
+      const bool here = lq > 0 && (a.p_bt > 0 ? s >= first && s < end : qb < end && qb + lq > first);
+      // keys that its last row here sees
+      const int rows = a.p_bt > 0 ? lq : min(end - qb, lq);
+      int blocks = here ? (clampi(rows + lk - lq, 0, lk) + kBlock - 1) / kBlock : 0;
+      const uint32_t who = __ballot_sync(0xFFFFFFFFu, here);
+      const int own = blocks;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int other = __shfl_up_sync(0xFFFFFFFFu, blocks, off);
+        if (lane >= off) blocks += other;
+      }
+      if (here) table[w.mixed + __popc(who & ((1u << lane) - 1u))] = {s, qb, lq, kb, lk, w.nb + blocks - own};
+      w.mixed += __popc(who);
+      w.nb += __shfl_sync(0xFFFFFFFFu, blocks, 31);
+    }
+    __syncwarp();
+    live = w.mixed > 0;
+  } else if (a.p_bt > 0) {
     for (int s = first + lane; s < min(end, a.S); s += 32) live |= (a.q_len ? a.q_len[s] : a.q_max) > 0;
     live = __any_sync(0xFFFFFFFFu, live);
   } else {  // from where the sequence is likely to stand on, 256 sequences at a time
@@ -497,8 +543,6 @@ __device__ __forceinline__ bool shared_item(const PromptArgs& a, uint32_t i, Pro
     }
   }
   if (!live) return false;
-  w.prefix = a.p_len ? clampi(a.p_len[0], 0, a.p_tokens) : a.p_tokens;
-  w.nb = w.nb0 = w.mc = (w.prefix + kBlock - 1) / kBlock;
   w.mb = w.prefix % kBlock != 0 ? w.nb0 : 0;
   w.ma = max(w.mb - 1, 0);
   const int n = (w.nb + kPerStage - 1) / kPerStage, per = (n + a.p_splits - 1) / a.p_splits;
@@ -509,13 +553,13 @@ __device__ __forceinline__ bool shared_item(const PromptArgs& a, uint32_t i, Pro
 }
 
 template <int TILES, int KIND>
-__device__ __forceinline__ bool prompt_item(const PromptArgs& a, uint32_t i, PromptItem& w) {
+__device__ __forceinline__ bool prompt_item(const PromptArgs& a, uint32_t i, PromptItem& w, MixedSeq* table) {
   constexpr int kKeys = Shape<TILES>::kKeys;
   constexpr int kPerStage = Shape<TILES>::kPerStage;
   if constexpr (KIND == kPrefix) {
-    if (i < (uint32_t)a.p_items) return shared_item<TILES>(a, i, w);
+    if (i < (uint32_t)a.p_items) return shared_item<TILES>(a, i, w, table);
     i -= a.p_items;
-    w.shared = 0;
+    w.shared = w.mixed = 0;
   }
   w.split = 0;
   if (a.rounds > 1) {
@@ -638,12 +682,14 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
   uint8_t* base = prompt_smem + ((1024u - (smem_addr(prompt_smem) & 1023u)) & 1023u);
   uint8_t* ring = base + TILES * kTileBytes;
   PromptBars& bars = *reinterpret_cast<PromptBars*>(ring + kStages * H::kStageBytes);
+  MixedSeq* table = reinterpret_cast<MixedSeq*>(ring + kStages * H::kStageBytes + 512);  // kPrefix
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if constexpr (KIND == kPrefix) {  // the launch behind the prefix's waits for its results itself
     if (a.p_items > 0) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   }
   int x = 0;  // the copy warp: stages filled so far
+  int at_k = 0, at_v = 0;  // and the sequence of a mixed item whose keys and values it copies
   // values: of the values' rows (else of the keys')
   const auto load_kv = [&](const PromptItem& w, bool values, int j) {
     const int st = x % kStages;
@@ -663,6 +709,12 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
             map = values ? &maps.pv : &maps.pk;
             key = g * kBlock;
             batch = 0;
+          } else if (w.mixed > 0) {
+            int& at = values ? at_v : at_k;
+            at = mixed_entry(table, w.mixed, g, at);
+            const MixedSeq& e = table[at];
+            key = e.kb + (g - e.g0) * kBlock;
+            batch = a.k_batched ? e.s : 0;
           }
         }
         for (int h = 0; h < 2; ++h) {
@@ -720,7 +772,7 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
     }
     __syncwarp();
     PromptItem w;
-    if (!prompt_item<TILES, KIND>(a, blockIdx.x, w)) {
+    if (!prompt_item<TILES, KIND>(a, blockIdx.x, w, table)) {
       w.s = -1;
       w.lo = w.hi = 0;
     }
@@ -925,6 +977,7 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
       int tok = w.tok0 + t * a.tile_tokens + r / a.G, seq = w.s;
       const int head = w.hkv * a.G + r % a.G;
       bool row = r < a.tile_tokens * a.G && tok < w.lq;
+      int entry = -1, own_seen = 0;  // the row's sequence of a mixed item, and how many of its keys it sees
       if constexpr (KIND == kPrefix) {
         if (w.shared && a.p_bt > 0) {
           const int u = r / a.G;
@@ -934,6 +987,15 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
         } else if (w.shared) {
           row = r < a.tile_tokens * a.G && tok < a.q_tokens;
         }
+        if (w.mixed > 0) {
+          for (int e = 0; e < w.mixed && row && entry < 0; ++e) {
+            const int at = a.p_bt > 0 ? tok : tok - table[e].qb;
+            if (at < 0 || at >= table[e].lq || (a.p_bt > 0 && table[e].s != seq)) continue;
+            entry = e;
+            own_seen = clampi(at + table[e].lk - table[e].lq + 1, 0, table[e].lk);
+          }
+          row = entry >= 0;
+        }
       }
       const int seen = row ? clampi(tok + w.lk - w.lq + 1, 0, w.lk) : w.lk;  // keys of this row
       const int from = w.lo * H::kKeys, blocks = w.blocks[t];
@@ -942,15 +1004,20 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
       const int from_a = w.ma - g0, to_a = w.mb - g0, from_c = w.mc - g0;  // the same, for the two runs of not kPlain
       const int low = KIND == kWindow ? max(0, seen - a.window) : 0;  // where the row's window begins
       // the keys of block g that the row sees, as bits
-      const auto visible = [&](int g) {
+      const auto visible = [&](int g, int& at) {  // at: the block's sequence of a mixed item, or one before it
         const auto first = [](int k) { return k <= 0 ? 0ull : k >= 64 ? ~0ull : (1ull << k) - 1ull; };
         const int key = block_key(w, g);
         if (KIND == kPrefix && g < w.nb0) return first(w.prefix - key);
+        if (KIND == kPrefix && w.mixed > 0) {
+          at = mixed_entry(table, w.mixed, g, at);
+          return at == entry ? first(own_seen - (g - table[at].g0) * kBlock) : 0ull;
+        }
         const uint64_t m = first(seen - key);
         return KIND == kWindow ? m & (~first(low - key) | first(a.sinks - key)) : m;
       };
       const float c = a.scale * kLog2e;
       float m = -INFINITY, l = 0.f;
+      int at = 0;
       bool ok = true;
       if (t == 0 || w.two) {
         for (int i = 0; i < blocks; ++i) {
@@ -966,7 +1033,7 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
           tmem_wait_ld(x + 32);
           if constexpr (KIND != kPlain) {
             if ((i >= from_a && i < to_a) || i >= from_c) {
-              const uint64_t vis = visible(g0 + i);
+              const uint64_t vis = visible(g0 + i, at);
               const uint32_t half[2] = {(uint32_t)vis, (uint32_t)(vis >> 32)};
 #pragma unroll
               for (int e = 0; e < kBlock; ++e) x[e] = (half[e / 32] >> (e % 32)) & 1u ? x[e] : -INFINITY;
@@ -1023,14 +1090,14 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
           const bool parts = in_parts<KIND>(a);
           const bool any = KIND == kPlain         ? seen > from
                            : parts || blocks == 0 ? blocks > 0 && l != 0.f
-                                                  : seen > 0 || (KIND == kPrefix && w.prefix > 0);
+                                                  : seen + own_seen > 0 || (KIND == kPrefix && w.prefix > 0);
           const float inv = parts ? 1.f : (any ? 1.f / l : 0.f);
           int64_t part = part_place(a, w.split, w.s, tok, head);
           if constexpr (KIND == kPrefix) {
             if (w.shared) {
               const int first = a.p_bt > 0 ? w.s / a.p_bs : w.tok0 / a.tile_tokens;
               part = shared_row(a, w.split, w.hkv, first + t, r);
-            } else {
+            } else if (parts) {
               part += a.p_rows;
             }
           }
@@ -1041,7 +1108,7 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
           uint64_t out = 0;  // where the row goes
           if (row)
             out = parts ? (uint64_t)(a.part_o + part * kD)
-                               : (uint64_t)(a.o + w.s * a.o_b + (int64_t)(w.qb + tok) * a.o_t + head * a.o_h);
+                               : (uint64_t)(a.o + (KIND == kPrefix ? seq : w.s) * a.o_b + (int64_t)(w.qb + tok) * a.o_t + head * a.o_h);
           // 32 channels of the row's sum
           const auto sums = [&](int q, float* y) {
             if (blocks > 0) {
@@ -1056,12 +1123,16 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
               for (int j = 0; j < n; ++j) {
                 if (!partly(j)) continue;
                 for (int g = g0 + j * H::kPerStage; g < g0 + (j + 1) * H::kPerStage && g < g0 + blocks; ++g) {
-                  const uint64_t vis = visible(g);
+                  int any_at = 0;
+                  const uint64_t vis = visible(g, any_at);
                   const uint16_t* vr = a.v + w.s * a.v_b + (int64_t)(w.kb + block_key(w, g)) * a.v_t + w.hkv * a.v_h;
                   int64_t step = a.v_t;
                   if (KIND == kPrefix && g < w.nb0) {
                     vr = a.pv + (int64_t)(g * kBlock) * a.pv_t + w.hkv * a.pv_h;
                     step = a.pv_t;
+                  } else if (KIND == kPrefix && w.mixed > 0) {
+                    const MixedSeq& e = table[mixed_entry(table, w.mixed, g)];
+                    vr = a.v + (a.k_batched ? e.s : 0) * a.v_b + (int64_t)(e.kb + (g - e.g0) * kBlock) * a.v_t + w.hkv * a.v_h;
                   }
                   for (int e = 0; e < kBlock; ++e) {
                     if (((vis >> e) & 1u) == 0) continue;
@@ -1087,7 +1158,7 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
           bool stored = false;
           if constexpr (KIND == kPrefix) {
             // A whole tile, whatever rows it has: each warp's 8 KB hold its rows' 32 channels twice.
-            if (w.shared) {
+            if (w.shared && parts) {
               stored = true;
               float* to = a.part_o + (part - lane) * kD;
               const bool some = __any_sync(0xFFFFFFFFu, row);
@@ -1119,7 +1190,7 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
           }
           if constexpr (KIND != kPlain) {
             // Rows of the sequence to the warp's last one: as two boxes of 64 channels, swizzled like Q's.
-            if (!stored && !parts && a.o_boxes && __all_sync(0xFFFFFFFFu, row)) {
+            if (!stored && !parts && a.o_boxes && !(KIND == kPrefix && w.shared && a.p_bt > 0) && __all_sync(0xFFFFFFFFu, row)) {
               stored = true;
 #pragma unroll 1
               for (int q = 0; q < 4; ++q) {
@@ -1183,7 +1254,7 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
             if (parts)
               a.part_ml[part] = make_float2(any ? m * c : -INFINITY, any ? l : 0.f);
             else if (a.lse)
-              a.lse[lse_place(a, w.s, w.qb + tok, head)] = any ? m * a.scale + logf(l) : -INFINITY;
+              a.lse[lse_place(a, KIND == kPrefix ? seq : w.s, w.qb + tok, head)] = any ? m * a.scale + logf(l) : -INFINITY;
           }
         }
       }
@@ -1379,6 +1450,7 @@ struct PromptGrid {
   // kPrefix with all sequences' rows together:
   int p_tiles = 0, p_splits = 0, p_bt = 0, p_bs = 0;
   bool p_two = false;  // two-tile CTAs
+  bool mixed = false;  // these walk over the own keys too
   int64_t p_rows = 0, p_items = 0;
 };
 
@@ -1438,17 +1510,20 @@ bool few_rows(const spc_prompt_dims* d) { return d->q_max == 1 && d->Hq / d->Hkv
 
 // Grid of a call behind a prefix whose tiles hold the rows of all sequences
 // together, so that the prefix's keys are walked once for them and not once for
-// each (in a launch of its own, of two-tile CTAs where the rows fill more than
-// one tile); then the sequences' own keys, and all results are joined.
+// each (two-tile CTAs where the rows fill more than one tile).  The sequences'
+// own keys come either in the same walk, masked for the rows of the others
+// (`mixed`: up to 64 sequences, where a tile has rows of a few of them), or in a
+// launch of their own, and are joined with the prefix's results.
 // p_items = 0 where that does not pay: the sequences' own tiles are as few, or
 // the partial results cost more than what is saved.
 //
-// Of the splits of the prefix, the number with the least estimate: the items
-// taken in turns by the CTAs' places, and the partial results.  Own keys are
-// split where their items would take longer than one of the prefix's.
+// Of both ways and of the splits of the walk, those with the least estimate (in
+// ns): the items taken in turns by the CTAs' places, and the partial results.
+// Own keys in a launch of their own are split where their items would take
+// longer than one of the prefix's.
 PromptGrid together_grid(const spc_prompt_dims* d, const PromptRule& rule) {
   PromptGrid g = {};
-  const int G = d->Hq / d->Hkv;
+  const int G = d->Hq / d->Hkv, sms = spc_host::sm_count();
   const bool batched = d->q.b != 0 && d->S > 1, few = few_rows(d);
   g.tiles = 1;
   g.tile_tokens = g.pair_tokens = kTile / G;
@@ -1467,31 +1542,42 @@ PromptGrid together_grid(const spc_prompt_dims* d, const PromptRule& rule) {
   g.items = few ? 0 : own_tiles * d->Hkv;
   g.rounds = 1;
   g.p_two = tiles > 1;
-  g.p_tiles = (int)ceil_div(tiles, g.p_two ? 2 : 1);
-  const int64_t shared = (int64_t)d->Hkv * g.p_tiles * (g.p_two ? 2 : 1) * kTile;  // rows of partial results per split
-  const int64_t items = (int64_t)g.p_tiles * d->Hkv, start = 4000, places = spc_host::sm_count() * (g.p_two ? 1 : 2);
+  const int two = g.p_two ? 2 : 1;
+  g.p_tiles = (int)ceil_div(tiles, two);
+  const int64_t shared = (int64_t)d->Hkv * g.p_tiles * two * kTile;  // rows of partial results per split
+  const int64_t items = (int64_t)g.p_tiles * d->Hkv, start = 4000, places = sms * (g.p_two ? 1 : 2);
   if (items > (1 << 24)) return g;
   const int64_t blocks = ceil_div(rule.prefix, kBlock), own = ceil_div(d->k_max, kBlock);
+  // sequences with rows in a CTA's tiles, and their blocks (lengths are taken to be a little more than half of k_max)
+  const int64_t here = batched ? std::min<int64_t>(d->S, (int64_t)g.p_bs * two)
+                               : std::min<int64_t>(d->S, (int64_t)two * g.tile_tokens * d->S / d->q_tokens + 1);
+  const int64_t inside = here * ceil_div(own * 11, 20);
   double best = 0.0;
-  for (int64_t z = 1; z <= std::min<int64_t>(blocks, few ? kMaxSplits : kMaxSplits / 2); ++z) {
-    const int64_t share = ceil_div(blocks, z);
-    const int64_t oz = few ? 0 : std::min<int64_t>(std::max<int64_t>(1, ceil_div(own, share)), kMaxSplits / 2);
-    const int64_t block = std::max<int64_t>(g.p_two ? 690 : 760, std::min(items * z, places) * 5 / std::min(g.p_tiles, 2));
-    const double cost = (double)(ceil_div(items * z, places) * (start + share * block)) +
-                        ((double)(z * shared) + (double)(oz * tokens * d->Hq)) / 5.0;
-    if (z == 1 || cost < best) {
-      best = cost;
-      g.p_splits = (int)z;
-      g.splits = (int)oz;
+  for (int mixed = 0; mixed < (d->S <= kMixed && !few ? 2 : 1); ++mixed) {
+    const int64_t walk = blocks + (mixed ? inside : 0);
+    for (int64_t z = 1; z <= std::min<int64_t>(walk, few || mixed ? kMaxSplits : kMaxSplits / 2); ++z) {
+      const int64_t share = ceil_div(walk, z);
+      const int64_t oz = few || mixed ? 0 : std::min<int64_t>(std::max<int64_t>(1, ceil_div(own, share)), kMaxSplits / 2);
+      const int64_t block = std::max<int64_t>(g.p_two ? 690 : 760, std::min(items * z, places) * 5 / std::min(g.p_tiles, 2));
+      double cost = (double)(ceil_div(items * z, places) * (start + share * block));
+      if (!mixed || z > 1) cost += 6000.0 + ((double)(z * shared) + (double)(oz * tokens * d->Hq)) / 5.0;
+      if (oz > 0) cost += (double)(g.items * (oz * start + own * 760 * 11 / 20)) / (2 * sms);
+      if (best == 0.0 || cost < best) {
+        best = cost;
+        g.p_splits = (int)z;
+        g.splits = (int)oz;
+        g.mixed = mixed != 0;
+      }
     }
   }
-  g.p_rows = shared * g.p_splits;
+  if (g.mixed) g.items = 0;
+  g.p_rows = g.mixed && g.p_splits == 1 ? 0 : shared * g.p_splits;
   // against the sequences one by one, whose tiles walk over the prefix each
   const bool pairs = g.pairs > 1;
   int64_t own_pairs = (int64_t)d->S * ceil_div(d->q_max, 2 * g.tile_tokens);
   if (!batched && d->S <= kDense) own_pairs = std::min(own_pairs, d->S + (int64_t)d->q_tokens / (2 * g.tile_tokens));
-  const double apart = (double)((pairs ? own_pairs * 690 * 2 : own_tiles * 760) * d->Hkv * blocks) / (2 * spc_host::sm_count());
-  if (best + 6000.0 < apart) g.p_items = items * g.p_splits;
+  const double apart = (double)((pairs ? own_pairs * 690 * 2 : own_tiles * 760) * d->Hkv * (blocks + own * 11 / 20)) / (2 * sms);
+  if (best < apart) g.p_items = items * g.p_splits;
   return g;
 }
 
@@ -1517,7 +1603,7 @@ cudaError_t launch_prompt_k(const PromptMaps<KIND>& maps, const PromptArgs& a, i
                             bool early = false) {
   static unsigned long long configured = 0ull;
   const cudaError_t e =
-      spc_host::ensure_smem_limit(configured, prompt_attn_kernel<TILES, KIND>, Shape<TILES>::kSmemBytes);
+      spc_host::ensure_smem_limit(configured, prompt_attn_kernel<TILES, KIND>, smem_bytes<TILES, KIND>());
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1525,7 +1611,7 @@ cudaError_t launch_prompt_k(const PromptMaps<KIND>& maps, const PromptArgs& a, i
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(Shape<TILES>::kThreads);
-  cfg.dynamicSmemBytes = Shape<TILES>::kSmemBytes;
+  cfg.dynamicSmemBytes = smem_bytes<TILES, KIND>();
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = early ? 1 : 0;
@@ -1610,6 +1696,7 @@ spc_status launch_prompt(const spc_prompt_dims* d, const PromptRule& rule, const
     a.p_bt = g.p_bt;
     a.p_bs = g.p_bs;
     a.p_rows = g.p_rows;
+    a.mixed = a.together && g.mixed;
     a.row_tiles = g.p_tiles * (g.p_two ? 2 : 1);
   }
   a.tile_tokens = g.tile_tokens;
@@ -1621,7 +1708,8 @@ spc_status launch_prompt(const spc_prompt_dims* d, const PromptRule& rule, const
   a.rounds = g.rounds;
   a.items = (uint32_t)g.items;
   a.gap = g.gap;
-  const bool parts = a.splits > 1 || a.together;
+  const bool parts = a.splits > 1 || (a.together && !(a.mixed && a.p_splits == 1));
+  a.parts = parts;
   if (parts) {
     a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(x.ws) + kPromptHead);
     a.part_ml = reinterpret_cast<float2*>(a.part_o + part_rows(d, g) * kD);
@@ -1650,11 +1738,11 @@ spc_status launch_prompt(const spc_prompt_dims* d, const PromptRule& rule, const
   cudaError_t e = cudaSuccess;
   if (a.together) {
     e = g.p_two ? launch_prompt_k<2, KIND>(maps, a, g.p_items, stream) : launch_prompt_k<1, KIND>(maps, a, g.p_items, stream);
-    if (e == cudaSuccess && few != nullptr && g.items == 0) return few(a, d, stream);
+    if (e == cudaSuccess && g.items == 0 && !a.mixed) return few(a, d, stream);
     a.p_items = 0;
   }
   const int64_t grid = g.items * a.splits;
-  if (e == cudaSuccess)
+  if (e == cudaSuccess && grid > 0)
     e = g.tiles == 2 ? launch_prompt_k<2, KIND>(maps, a, grid, stream)
                      : launch_prompt_k<1, KIND>(maps, a, grid, stream, a.together);
   if (e == cudaSuccess && parts) {

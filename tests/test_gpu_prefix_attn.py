@@ -263,3 +263,63 @@ def test_a_wait_that_runs_out_is_reported():
     finally:
         spc.spc_prompt_attn_wait_limit(before)
         spc.spc_prompt_attn_status()
+
+
+@pytest.mark.parametrize("P", [64, 1000, 8001])
+@pytest.mark.parametrize("Hq,Hkv", [(4, 4), (8, 2), (6, 2), (32, 1)])
+@pytest.mark.parametrize("S,most,own", [(2, 20, 90), (17, 77, 0), (40, 9, 300), (64, 30, 33), (65, 30, 33), (64, 3, 0)])
+def test_few_rows_each_of_many_sequences(P, Hq, Hkv, S, most, own):
+    """Tiles with rows of several sequences, whose own keys lie anywhere, are shared, or do not reach all of their rows."""
+    import bit_kv_cache_spc_gb300 as spc
+    lq = [(s * 37) % (most + 1) if s else most for s in range(S)]
+    lk = [(s * 53) % (own + 1) if own else lq[s] for s in range(S)]
+    T, N = sum(lq) + 5, 700
+    q, k, v, pk, pv = rnd(1, T, Hq, D), rnd(2, N, Hkv, D), rnd(3, N, Hkv, D), rnd(4, P, Hkv, D), rnd(5, P, Hkv, D)
+    qb = [sum(lq[:s]) + 3 * (s > S // 2) for s in range(S)]  # a gap within
+    kb = [(s * 131) % (N - max(lk) + 1) for s in range(S)]
+    o, lse = torch.full_like(q, 7.0), torch.full((T, Hq), 7.0, device="cuda")
+    spc.spc_prefix_attn(q, pk, pv, k, v, o, lse, q_begin=i32(qb), q_len=i32(lq), k_begin=i32(kb), k_len=i32(lk), q_max=most,
+                        k_max=max(max(lk), 1))
+    rest = torch.ones(T, dtype=torch.bool, device="cuda")
+    for s in range(S):
+        rest[qb[s]:qb[s] + lq[s]] = False
+        if lq[s] and (s % 5 == 0 or S < 20):
+            at, own_k = slice(qb[s], qb[s] + lq[s]), slice(kb[s], kb[s] + lk[s])
+            check(o[at], lse[at], q[at], both(pk, k[own_k]), both(pv, v[own_k]), prefix_sight(lq[s], lk[s], P))
+    assert bool((o[rest] == 7).all()) and bool((lse[rest] == 7).all()) and not bool((lse[~rest] == 7).any())
+
+
+@pytest.mark.parametrize("what", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("S,n", [(6, 20), (40, 7)])
+def test_other_sequences_keys_do_not_matter(S, n, what):
+    """One sequence's own keys and values are poisoned: the others, in the same tiles, keep their bits; so do its own rows
+    before the poisoned place."""
+    import bit_kv_cache_spc_gb300 as spc
+    P, Hq, Hkv = 500, 4, 2
+    q, k, v, pk, pv = rnd(1, S * n, Hq, D), rnd(2, S * n, Hkv, D), rnd(3, S * n, Hkv, D), rnd(4, P, Hkv, D), rnd(5, P, Hkv, D)
+    at = i32([s * n for s in range(S)])
+    outs = []
+    for x in (0.0, what):
+        kk, vv = k.clone(), v.clone()
+        kk[2 * n + 4:3 * n], vv[2 * n + 4:3 * n] = x, x
+        o, lse = torch.zeros_like(q), torch.zeros((S * n, Hq), device="cuda")
+        spc.spc_prefix_attn(q, pk, pv, kk, vv, o, lse, q_begin=at, q_len=i32([n] * S), k_begin=at, k_len=i32([n] * S), q_max=n, k_max=n)
+        outs.append((o, lse))
+    clean = torch.ones(S * n, dtype=torch.bool, device="cuda")
+    clean[2 * n + 4:3 * n] = False
+    assert torch.equal(outs[0][0][clean], outs[1][0][clean]) and torch.equal(outs[0][1][clean], outs[1][1][clean])
+
+
+def test_visible_infinities_and_nan_of_one_sequence_among_others():
+    import bit_kv_cache_spc_gb300 as spc
+    S, n, P, Hq, Hkv = 9, 13, 200, 2, 1
+    q, k, v = rnd(1, S * n, Hq, D, mul=0.1), rnd(2, S * n, Hkv, D, mul=0.1), rnd(3, S * n, Hkv, D)
+    pk, pv = rnd(4, P, Hkv, D, mul=0.1), rnd(5, P, Hkv, D)
+    v[3 * n + 5, 0, 3], v[7 * n, 0, 9], pv[198, 0, 20] = math.inf, math.nan, -math.inf
+    at, o = i32([s * n for s in range(S)]), torch.zeros_like(q)
+    spc.spc_prefix_attn(q, pk, pv, k, v, o, q_begin=at, q_len=i32([n] * S), k_begin=at, k_len=i32([n] * S), q_max=n, k_max=n)
+    three, seven = slice(3 * n + 5, 4 * n), slice(7 * n, 8 * n)
+    rest = torch.ones(S * n, dtype=torch.bool, device="cuda")
+    rest[three], rest[seven] = False, False
+    assert bool((o[three, :, 3] == math.inf).all()) and bool(torch.isnan(o[seven, :, 9]).all()) and bool((o[..., 20] == -math.inf).all())
+    assert bool(torch.isfinite(o[rest][:, :, [c for c in range(D) if c != 20]]).all())
