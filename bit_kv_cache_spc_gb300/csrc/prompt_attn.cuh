@@ -137,6 +137,7 @@ struct PromptArgs {
   int32_t p_items, p_tiles, p_splits;  // items of the prefix (0 in the launch of the sequences' own); CTAs' rows; splits
   int32_t p_bt, p_bs;                  // a tile of batched queries: p_bt tokens of p_bs sequences each (packed: 0)
   int32_t row_tiles;                   // tiles of rows in all
+  int32_t p_rounds, p_gap;             // as rounds and gap, of the prefix's splits
   int32_t mixed;                       // the prefix's items walk over their sequences' own keys too
   int32_t parts;                       // partial results are written, to be joined
   int32_t o_boxes;                     // not kPlain: a warp's 32 rows are whole tokens, so that the map of o has them
@@ -545,7 +546,12 @@ __device__ __forceinline__ bool shared_item(const PromptArgs& a, uint32_t i, Pro
   if (!live) return false;
   w.mb = w.prefix % kBlock != 0 ? w.nb0 : 0;
   w.ma = max(w.mb - 1, 0);
-  const int n = (w.nb + kPerStage - 1) / kPerStage, per = (n + a.p_splits - 1) / a.p_splits;
+  const int n = (w.nb + kPerStage - 1) / kPerStage;
+  int per = (n + a.p_splits - 1) / a.p_splits;
+  if (a.p_rounds > 1) {  // the last split is shorter, as in prompt_item
+    const int large = a.p_splits - 1, small = max(0, n - large * a.p_gap) / (large * a.p_rounds + 1);
+    per = (n - small + large - 1) / large;
+  }
   w.lo = min(w.split * per, n);
   w.hi = min(w.lo + per, n);
   w.blocks[0] = w.blocks[1] = max(0, min(kPerStage * (w.hi - w.lo), w.nb - w.lo * kPerStage));
@@ -1448,7 +1454,7 @@ struct PromptGrid {
   int tiles, tile_tokens, pair_tokens, pairs, splits, rounds, gap;
   int64_t items;
   // kPrefix with all sequences' rows together:
-  int p_tiles = 0, p_splits = 0, p_bt = 0, p_bs = 0;
+  int p_tiles = 0, p_splits = 0, p_bt = 0, p_bs = 0, p_rounds = 1, p_gap = 0;
   bool p_two = false;  // two-tile CTAs
   bool mixed = false;  // these walk over the own keys too
   int64_t p_rows = 0, p_items = 0;
@@ -1511,16 +1517,20 @@ bool few_rows(const spc_prompt_dims* d) { return d->q_max == 1 && d->Hq / d->Hkv
 // Grid of a call behind a prefix whose tiles hold the rows of all sequences
 // together, so that the prefix's keys are walked once for them and not once for
 // each (two-tile CTAs where the rows fill more than one tile).  The sequences'
-// own keys come either in the same walk, masked for the rows of the others
-// (`mixed`: up to 64 sequences, where a tile has rows of a few of them), or in a
-// launch of their own, and are joined with the prefix's results.
+// own keys come in the same walk, masked for the rows of the others (`mixed`,
+// up to 64 sequences: 17 prompts of up to 77 tokens behind 8011 keys 109 us, in
+// a launch of their own and joined 118; 40 of 20 tokens 88 and 102), or for
+// more sequences, and for single tokens, in a launch of their own.
 // p_items = 0 where that does not pay: the sequences' own tiles are as few, or
 // the partial results cost more than what is saved.
 //
-// Of both ways and of the splits of the walk, those with the least estimate (in
-// ns): the items taken in turns by the CTAs' places, and the partial results.
-// Own keys in a launch of their own are split where their items would take
-// longer than one of the prefix's.
+// Of the splits of the walk, the number with the least estimate (in ns): the
+// items taken in turns by the CTAs' places, or the last split shorter as in
+// prompt_grid, and the partial results.  Own keys in a launch of their own are
+// split where their items would take longer than one of the prefix's.  Measured
+// against it: the 17 prompts 111 us in one piece, 129 in 2, 109 in 3, 122 in 4;
+// the 40 127, 88, 111 and 98; 64 single tokens behind 32768 keys 126 in 4, 76
+// in 9, 62 in 18.
 PromptGrid together_grid(const spc_prompt_dims* d, const PromptRule& rule) {
   PromptGrid g = {};
   const int G = d->Hq / d->Hkv, sms = spc_host::sm_count();
@@ -1545,29 +1555,44 @@ PromptGrid together_grid(const spc_prompt_dims* d, const PromptRule& rule) {
   const int two = g.p_two ? 2 : 1;
   g.p_tiles = (int)ceil_div(tiles, two);
   const int64_t shared = (int64_t)d->Hkv * g.p_tiles * two * kTile;  // rows of partial results per split
-  const int64_t items = (int64_t)g.p_tiles * d->Hkv, start = 4000, places = sms * (g.p_two ? 1 : 2);
+  const int64_t items = (int64_t)g.p_tiles * d->Hkv, start = 8000, places = sms * (g.p_two ? 1 : 2);
   if (items > (1 << 24)) return g;
   const int64_t blocks = ceil_div(rule.prefix, kBlock), own = ceil_div(d->k_max, kBlock);
   // sequences with rows in a CTA's tiles, and their blocks (lengths are taken to be a little more than half of k_max)
   const int64_t here = batched ? std::min<int64_t>(d->S, (int64_t)g.p_bs * two)
                                : std::min<int64_t>(d->S, (int64_t)two * g.tile_tokens * d->S / d->q_tokens + 1);
   const int64_t inside = here * ceil_div(own * 11, 20);
+  // In the walk the own keys' blocks take nearly twice the others' time: masked in every row, their values looked through.
+  // (64 sequences of 4 tokens behind 32768 keys, 16 a CTA with up to 1024 keys each: 188 us so, 149 in a launch of their own.)
+  const double within = (double)(items * inside * 2 * 690) / sms;
+  const double behind = (double)(g.items * (4000 + own * 760 * 11 / 20)) / (2 * sms) + (double)(tokens * d->Hq) / 5.0 + 8000.0;
+  g.mixed = d->S <= kMixed && !few && within <= behind;
+  const int64_t walk = blocks + (g.mixed ? inside : 0);
   double best = 0.0;
-  for (int mixed = 0; mixed < (d->S <= kMixed && !few ? 2 : 1); ++mixed) {
-    const int64_t walk = blocks + (mixed ? inside : 0);
-    for (int64_t z = 1; z <= std::min<int64_t>(walk, few || mixed ? kMaxSplits : kMaxSplits / 2); ++z) {
-      const int64_t share = ceil_div(walk, z);
-      const int64_t oz = few || mixed ? 0 : std::min<int64_t>(std::max<int64_t>(1, ceil_div(own, share)), kMaxSplits / 2);
-      const int64_t block = std::max<int64_t>(g.p_two ? 690 : 760, std::min(items * z, places) * 5 / std::min(g.p_tiles, 2));
-      double cost = (double)(ceil_div(items * z, places) * (start + share * block));
-      if (!mixed || z > 1) cost += 6000.0 + ((double)(z * shared) + (double)(oz * tokens * d->Hq)) / 5.0;
-      if (oz > 0) cost += (double)(g.items * (oz * start + own * 760 * 11 / 20)) / (2 * sms);
-      if (best == 0.0 || cost < best) {
-        best = cost;
-        g.p_splits = (int)z;
-        g.splits = (int)oz;
-        g.mixed = mixed != 0;
+  for (int64_t z = 1; z <= std::min<int64_t>(walk, few || g.mixed ? kMaxSplits : kMaxSplits / 2); ++z) {
+    const int64_t share = ceil_div(walk, z);
+    const int64_t oz = few || g.mixed ? 0 : std::min<int64_t>(std::max<int64_t>(1, ceil_div(own, share)), kMaxSplits / 2);
+    const int64_t block = std::max<int64_t>(g.p_two ? 690 : 760, std::min(items * z, places) * 5 / std::min(g.p_tiles, 2));
+    double cost = (double)(ceil_div(items * z, places) * (start + share * block));
+    int64_t rounds = 1;
+    if (z > 1 && items * z > places && items * (z - 1) < places) {  // the last split shorter, in a few rounds on what is left
+      const int64_t r = ceil_div(items, places - items * (z - 1));
+      const int64_t small = (walk - (z - 1) * (r - 1) * (start / block)) / ((z - 1) * r + 1);
+      const int64_t last = r * (start + (small + (g.mixed ? std::min(inside, small) : 0)) * block);
+      const double one = (double)std::max(start + ceil_div(walk - small, z - 1) * block, last);
+      if (small >= 4 && one < cost) {
+        cost = one;
+        rounds = r;
       }
+    }
+    if (!g.mixed || z > 1) cost += 6000.0 + ((double)(z * shared) + (double)(oz * tokens * d->Hq)) / 5.0;
+    if (oz > 0) cost += (double)(g.items * (oz * 4000 + own * 760 * 11 / 20)) / (2 * sms);
+    if (z == 1 || cost < best) {
+      best = cost;
+      g.p_splits = (int)z;
+      g.splits = (int)oz;
+      g.p_rounds = (int)rounds;
+      g.p_gap = (int)((rounds - 1) * (start / block) / two);  // stages have two blocks where CTAs have two tiles
     }
   }
   if (g.mixed) g.items = 0;
@@ -1576,8 +1601,13 @@ PromptGrid together_grid(const spc_prompt_dims* d, const PromptRule& rule) {
   const bool pairs = g.pairs > 1;
   int64_t own_pairs = (int64_t)d->S * ceil_div(d->q_max, 2 * g.tile_tokens);
   if (!batched && d->S <= kDense) own_pairs = std::min(own_pairs, d->S + (int64_t)d->q_tokens / (2 * g.tile_tokens));
-  const double apart = (double)((pairs ? own_pairs * 690 * 2 : own_tiles * 760) * d->Hkv * (blocks + own * 11 / 20)) / (2 * sms);
-  if (best < apart) g.p_items = items * g.p_splits;
+  const int64_t each = blocks + own * 11 / 20, alone = (pairs ? own_pairs : own_tiles) * d->Hkv;
+  const int64_t one = pairs ? 690 : 760, room = pairs ? sms : 2 * sms;
+  double apart = (double)(ceil_div(alone, room) * (start + each * one));
+  if (alone < room / 2) apart = (double)(alone * each * one) / (double)room + 12000.0;  // its keys split
+  // (pairs of tiles that are nearly as many: four prompts of up to 2048 tokens behind 16384 keys 709 us together, 668 apart)
+  const bool as_many = pairs && 10 * (int64_t)g.p_tiles > 9 * own_pairs;
+  if (1.1 * best < apart && !as_many) g.p_items = items * g.p_splits;
   return g;
 }
 
@@ -1693,6 +1723,8 @@ spc_status launch_prompt(const spc_prompt_dims* d, const PromptRule& rule, const
     a.p_items = (int32_t)g.p_items;
     a.p_tiles = g.p_tiles;
     a.p_splits = g.p_splits;
+    a.p_rounds = g.p_rounds;
+    a.p_gap = g.p_gap;
     a.p_bt = g.p_bt;
     a.p_bs = g.p_bs;
     a.p_rows = g.p_rows;
