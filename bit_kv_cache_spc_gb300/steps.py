@@ -11,7 +11,9 @@ the cache length in the dims struct.
     prompt_layer    Algorithm 1 from the projections on: rotary positions, the
                     prompt's causal attention, its K/V into the low-bit cache
                     and the host cache; also for the follow-up prompts of a
-                    conversation, which attend over the cache read back.
+                    conversation, which attend over the cache read back.  With
+                    norms of the heads, positions of several axes, a sliding
+                    window, or a prefix that the sequences share.
     predecode_layer Algorithm 2: append the first token's K/V, attention of
                     its single query over the cache, ArgTopK over that
                     attention, Pre-fetch of the selected 16-bit rows.
@@ -24,8 +26,8 @@ from __future__ import annotations
 import torch
 
 from . import (_all_or_none, spc_append_kv, spc_decode_attn2, spc_dequantize_kv, spc_extend_kv, spc_host_gather,
-               spc_host_gather_prev, spc_merged_attn, spc_offload_kv, spc_prompt_attn, spc_quantize_kv, spc_rope,
-               spc_topk_select, spc_topk_select_prev)
+               spc_host_gather_prev, spc_merged_attn, spc_norm_rope, spc_offload_kv, spc_prefix_attn, spc_prompt_attn,
+               spc_quantize_kv, spc_rope, spc_topk_select, spc_topk_select_prev, spc_window_attn)
 
 
 def prefill_layer(d, k, v, records, resid, host_kv, n_cap, stream=None, copy_stream=None):
@@ -45,7 +47,8 @@ def prefill_layer(d, k, v, records, resid, host_kv, n_cap, stream=None, copy_str
 
 
 def prompt_layer(d, q, k, v, pos, turns, o, records, resid, host_kv=None, n_cap=0, history=None, lse=None, ws=None,
-                 rot=128, interleaved=False, mscale=1.0, stream=None):
+                 rot=128, interleaved=False, mscale=1.0, stream=None, q_norm=None, k_norm=None, eps=1e-6, axis=None,
+                 window=None, sinks=0, prefix=None):
     """A prompt of n tokens per sequence through one layer's attention, and
     into its cache.  q: 16-bit [B][n][Hq][D], k, v: [B][n][Hkv][D], views of
     the projections (any strides); pos: int32 [B][n], the tokens' positions;
@@ -62,22 +65,55 @@ def prompt_layer(d, q, k, v, pos, turns, o, records, resid, host_kv=None, n_cap=
     that is refused leaves q, k, history and the cache as they were, and may be
     made again.  Without ws the attention takes its workspace from torch's
     allocator; spc_prompt_attn_status(), after the layers, says whether a
-    bounded wait of the attention ran out."""
+    bounded wait of the attention ran out.
+
+    What a layer may have besides (spc_norm_rope, spc_window_attn,
+    spc_prefix_attn):
+    q_norm, k_norm (fp32 [D] weights) and eps: norms of the query and key heads
+    before the rotation.  axis: pos is int32 [axes][B][n], and pair i is turned
+    by the axis axis[i].
+    window (and sinks): a query sees the last `window` keys and the first
+    `sinks`; of a history only what some query sees is read back, and the rows
+    between hold what they held.
+    prefix: a pair of 16-bit [P][Hkv][D] views (keys, values), rotated, of the
+    first P tokens, which all sequences' caches share and hold already (P <=
+    d.N): they are attended to there, and the history is read back from token P
+    on.  Row i of the history buffers is then token P + i, and they need
+    d.N - P + n rows.  Not together with a window."""
     n, N = k.shape[1], d.N
+    P = 0 if prefix is None else prefix[0].shape[0]
+    if prefix is not None and (window is not None or P > N):
+        raise ValueError(f"prompt_layer: a prefix of {P} tokens needs them in the cache, which holds {N}, and no window")
+    own = N - P  # tokens of the cache to be read back
     if N > 0:
-        if history is None or any(b.shape[2] < N + n for b in history):
-            raise ValueError(f"prompt_layer: a follow-up prompt needs history buffers of {N + n} rows")
-        kk, vv = (b[:, :, :N + n].transpose(1, 2) for b in history)
+        if history is None or any(b.shape[2] < own + n for b in history):
+            raise ValueError(f"prompt_layer: a follow-up prompt needs history buffers of {own + n} rows")
+        kk, vv = (b[:, :, :own + n].transpose(1, 2) for b in history)
     stream = torch.cuda.current_stream() if stream is None else stream
     with torch.cuda.stream(stream), _all_or_none() as calls:
+        rows = {}
         if N == 0:
             kk, vv = kn, vn = k, v
-            spc_rope(q, k, pos, turns, rot, interleaved, mscale, _later=calls)
         else:
-            kn, vn = kk[:, N:], vv[:, N:]
-            spc_dequantize_kv(d, records, resid, 0, kk[:, :N], vv[:, :N], _later=calls)
-            spc_rope(q, k, pos, turns, rot, interleaved, mscale, v=v, k_out=kn, v_out=vn, _later=calls)
-        spc_prompt_attn(q, kk, vv, o, lse, scale=d.scale, ws=ws, _later=calls)
+            kn, vn = kk[:, own:], vv[:, own:]
+            rows = dict(v=v, k_out=kn, v_out=vn)
+            read = [(0, own)]
+            if window is not None and window < own + n:  # the first tokens, and from the first query's window on
+                low = max(0, own + 1 - window)
+                read = [(0, min(sinks, low)), (low, own)]
+            for a, b in read:
+                if a < b:
+                    spc_dequantize_kv(d, records, resid, P + a, kk[:, a:b], vv[:, a:b], _later=calls)
+        if q_norm is None and k_norm is None and axis is None:
+            spc_rope(q, k, pos, turns, rot, interleaved, mscale, _later=calls, **rows)
+        else:
+            spc_norm_rope(q, k, pos, turns, q_norm, k_norm, eps, axis, rot, interleaved, mscale, _later=calls, **rows)
+        if window is not None:
+            spc_window_attn(q, kk, vv, o, window, sinks, lse, scale=d.scale, ws=ws, _later=calls)
+        elif prefix is not None:
+            spc_prefix_attn(q, *prefix, kk, vv, o, lse, scale=d.scale, ws=ws, _later=calls)
+        else:
+            spc_prompt_attn(q, kk, vv, o, lse, scale=d.scale, ws=ws, _later=calls)
         spc_extend_kv(d, kn, vn, records, resid, host_kv, n_cap, _later=calls)
     d.N += n
 
