@@ -497,7 +497,7 @@ def spc_norm_rope(q, k, pos, turns, q_weight=None, k_weight=None, eps=1e-6, axis
         if axes != 1:
             raise ValueError(f"{fn}: positions of {axes} axes need axis")
         axis = b""
-    elif len(axis) != rot // 2 or min(axis) < 0 or max(axis) >= axes:
+    elif len(axis) != rot // 2:
         raise ValueError(f"{fn}: axis must be {rot // 2} numbers from 0 to {axes - 1}")
     pos = _words(fn, "pos", pos, torch.int32, axes * B * T, dev)
     turns = _words(fn, "turns", turns, torch.int64, rot // 2, dev)

@@ -1537,7 +1537,8 @@ PromptGrid together_grid(const spc_prompt_dims* d, const PromptRule& rule) {
   const bool batched = d->q.b != 0 && d->S > 1, few = few_rows(d);
   g.tiles = 1;
   g.tile_tokens = g.pair_tokens = kTile / G;
-  if (d->S < 2 || d->S > 65535 || d->q_max == 0 || rule.prefix == 0 || (batched && 2 * d->q_max > g.tile_tokens)) return g;
+  if ((d->S < 2 && !few) || d->S > 65535 || d->q_max == 0 || rule.prefix == 0) return g;
+  if (batched ? 2 * d->q_max > g.tile_tokens : d->q_tokens > 4 * (int64_t)d->S * d->q_max) return g;  // tiles with few rows
   g.pairs = (int)ceil_div(d->q_max, g.tile_tokens);
   int64_t tokens = (int64_t)d->S * d->q_max, own_tiles = (int64_t)d->S * g.pairs, tiles;
   if (batched) {
@@ -1607,7 +1608,8 @@ PromptGrid together_grid(const spc_prompt_dims* d, const PromptRule& rule) {
   if (alone < room / 2) apart = (double)(alone * each * one) / (double)room + 12000.0;  // its keys split
   // (pairs of tiles that are nearly as many: four prompts of up to 2048 tokens behind 16384 keys 709 us together, 668 apart)
   const bool as_many = pairs && 10 * (int64_t)g.p_tiles > 9 * own_pairs;
-  if (1.1 * best < apart && !as_many) g.p_items = items * g.p_splits;
+  // Single tokens: always (one to 16 behind 2003 keys 12.4 to 13.3 us together, 15 to 27 apart).
+  if (few || (1.1 * best < apart && !as_many)) g.p_items = items * g.p_splits;
   return g;
 }
 
