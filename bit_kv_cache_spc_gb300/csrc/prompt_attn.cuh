@@ -134,12 +134,14 @@ struct PromptArgs {
   int32_t p_tokens;
   // kPrefix with rows of all sequences together in the prefix's tiles:
   int32_t together;
-  int32_t p_items, p_tiles, p_splits;  // items of the prefix (0 in the launch of the sequences' own); CTAs' rows; splits
+  int32_t p_items, p_tiles, p_pieces;  // items of the prefix (0 in the launch of the sequences' own); CTAs' rows; splits
+  int32_t p_splits;                    // of these, what is left to be joined behind the clusters
   int32_t p_bt, p_bs;                  // a tile of batched queries: p_bt tokens of p_bs sequences each (packed: 0)
   int32_t row_tiles;                   // tiles of rows in all
   int32_t p_rounds, p_gap;             // as rounds and gap, of the prefix's splits
   int32_t mixed;                       // the prefix's items walk over their sequences' own keys too
-  int32_t parts;                       // partial results are written, to be joined
+  int32_t parts;                       // not kPlain: partial results are written, to be joined
+  int32_t cluster;                     // CTAs that share an item's keys and join their results (1, 2 or 4)
   int32_t o_boxes;                     // not kPlain: a warp's 32 rows are whole tokens, so that the map of o has them
   int64_t p_rows;                      // rows of the prefix's partial results; the sequences' own come behind
   // few_attn.cuh's:
@@ -186,7 +188,7 @@ __device__ __forceinline__ int block_key(const PromptItem& w, int g) {
 // Whether partial results are written, to be joined.
 template <int KIND>
 __device__ __forceinline__ bool in_parts(const PromptArgs& a) {
-  return KIND == kPrefix ? a.parts != 0 : a.splits > 1;
+  return KIND == kPlain ? a.splits > 1 : a.parts != 0;
 }
 
 // The sequences of a mixed item, in shared memory behind the barriers: sequence s has rows in its tiles, and its keys'
@@ -314,6 +316,36 @@ __device__ __forceinline__ uint64_t l2_policy(bool once) {
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];\n" ::"l"(map) : "memory");
+}
+
+// The address of another CTA's shared memory in the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float2 cluster_ld2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];\n" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 cluster_ld4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ void cluster_st2(uint32_t addr, float2 v) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};\n" ::"r"(addr), "f"(v.x), "f"(v.y) : "memory");
+}
+__device__ __forceinline__ void cluster_st4(uint32_t addr, const float* v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3])
+               : "memory");
 }
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
@@ -484,17 +516,19 @@ __device__ __forceinline__ bool dense_item(const PromptArgs& a, int k, PromptIte
 // them in L2.  Up to kDense sequences of different lengths are numbered over
 // the pairs that exist, so that long and short prompts packed together leave
 // no empty CTAs; more, or equal ones, over all pairs.  False for none.
-// Item i of the prefix's, rows of all sequences together: tile of rows fastest, so that CTAs that run together share
-// keys, then KV head, then split.  False where no sequence has a row in the tile.
+// Item i of the prefix's, rows of all sequences together: the cluster's split fastest, then tile of rows, so that CTAs that
+// run together share keys, then KV head, then the other splits.  False where no sequence has a row in the tile.
 template <int TILES>
 __device__ __forceinline__ bool shared_item(const PromptArgs& a, uint32_t i, PromptItem& w, MixedSeq* table) {
   constexpr int kPerStage = Shape<TILES>::kPerStage;
+  const int rank = (int)(i % a.cluster);
+  i /= a.cluster;
   const int lane = threadIdx.x & 31, tile = (int)(i % a.p_tiles);
   i /= a.p_tiles;
   w = PromptItem();
   w.shared = 1;
   w.hkv = (int)(i % a.Hkv);
-  w.split = (int)(i / a.Hkv);
+  w.split = (int)(i / a.Hkv) * a.cluster + rank;
   const int per_tile = a.p_bt > 0 ? a.p_bs : a.tile_tokens;  // sequences or tokens
   const int first = tile * TILES * per_tile, end = first + TILES * per_tile;
   w.s = a.p_bt > 0 ? first : 0;
@@ -547,9 +581,9 @@ __device__ __forceinline__ bool shared_item(const PromptArgs& a, uint32_t i, Pro
   w.mb = w.prefix % kBlock != 0 ? w.nb0 : 0;
   w.ma = max(w.mb - 1, 0);
   const int n = (w.nb + kPerStage - 1) / kPerStage;
-  int per = (n + a.p_splits - 1) / a.p_splits;
+  int per = (n + a.p_pieces - 1) / a.p_pieces;
   if (a.p_rounds > 1) {  // the last split is shorter, as in prompt_item
-    const int large = a.p_splits - 1, small = max(0, n - large * a.p_gap) / (large * a.p_rounds + 1);
+    const int large = a.p_pieces - 1, small = max(0, n - large * a.p_gap) / (large * a.p_rounds + 1);
     per = (n - small + large - 1) / large;
   }
   w.lo = min(w.split * per, n);
@@ -973,8 +1007,16 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
         if (lane == 0) mbar_arrive(&bars.v_clean[sv]);
       }
     }
+    if constexpr (KIND != kPlain) {
+      if (a.cluster > 1) {  // the softmax warps' (below)
+        __syncwarp();
+        cluster_sync();
+        cluster_sync();
+      }
+    }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 168;\n");
+    bool synced = KIND == kPlain || a.cluster == 1;
     if (w.s >= 0) {
       // ---- softmax and output of one tile, a thread per row ----
       const int t = warp >> 2, r = tid & 127;
@@ -1088,21 +1130,22 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
         // ---- output ----
         if (blocks > 0 && ok) ok = mbar_wait_warp(bars, &bars.s_full[t][(blocks + 1) & 1], ((blocks + 1) >> 1) & 1);
         if (blocks == 0 && n > 0) ok = mbar_wait_warp(bars, &bars.q_full[t], 0);  // Q's place is used below
-        if (ok) {
+        if (ok || !synced) {
           tc_fence_after();
           const bool bad = *(volatile uint32_t*)&bars.bad != 0u;
           const int first = max(w.edge, w.lo) * H::kKeys, end = min(seen, w.hi * H::kKeys);
           // no visible key: 0; otherwise the sum is positive, or not a number when the scores are not
           const bool parts = in_parts<KIND>(a);
-          const bool any = KIND == kPlain         ? seen > from
-                           : parts || blocks == 0 ? blocks > 0 && l != 0.f
-                                                  : seen + own_seen > 0 || (KIND == kPrefix && w.prefix > 0);
+          const bool some_key = seen + own_seen > 0 || (KIND == kPrefix && w.prefix > 0);
+          const bool any = KIND == kPlain                    ? seen > from
+                           : parts || !synced || blocks == 0 ? blocks > 0 && l != 0.f
+                                                             : some_key;
           const float inv = parts ? 1.f : (any ? 1.f / l : 0.f);
           int64_t part = part_place(a, w.split, w.s, tok, head);
           if constexpr (KIND == kPrefix) {
             if (w.shared) {
               const int first = a.p_bt > 0 ? w.s / a.p_bs : w.tok0 / a.tile_tokens;
-              part = shared_row(a, w.split, w.hkv, first + t, r);
+              part = shared_row(a, w.split / a.cluster, w.hkv, first + t, r);
             } else if (parts) {
               part += a.p_rows;
             }
@@ -1162,9 +1205,134 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
             }
           };
           bool stored = false;
+          if constexpr (KIND != kPlain) {
+            if (!synced) {
+              // ---- splits of a cluster: each CTA takes its share of the channels (64 or 32) of all rows ----
+              // Once all walks have ended, the ring takes the other CTAs' (maximum, sum) of each row and their sums of these
+              // channels, chunk by chunk of all rows, so that a warp writes 512 bytes in a row.
+              synced = stored = true;
+              constexpr int kRows = TILES * kTile;
+              const int C = a.cluster, me = w.split % C, per = 4 / C, R = t * kTile + r;  // per: quarters of the channels
+              const uint32_t ml_at = smem_addr(ring), o_at = ml_at + C * kRows * 8;
+              const float2 own = make_float2(any ? m * c : -INFINITY, any ? l : 0.f);
+              __syncwarp();
+              cluster_sync();
+              if (ok) {
+                for (int p = 0; p < C; ++p)
+                  if (p != me) cluster_st2(cluster_addr(ml_at + (me * kRows + R) * 8, p), own);
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                  const int p = q / per;
+                  if (p == me) continue;
+                  float y[32];
+                  sums(q, y);
+                  const int slot = (me < p ? me : me - 1) * per + q % per;
+                  const uint32_t to = cluster_addr(o_at + (slot * 8 * kRows + R) * 16, p);
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) cluster_st4(to + i * kRows * 16, y + 4 * i);
+                }
+              }
+              __syncwarp();
+              cluster_sync();
+              if (ok) {
+                const float2* ml = reinterpret_cast<const float2*>(ring) + R;
+                float2 other[3];
+                float top = own.x;
+#pragma unroll
+                for (int u = 0; u < 3; ++u) {
+                  other[u] = u < C - 1 ? ml[(u < me ? u : u + 1) * kRows] : make_float2(-INFINITY, 0.f);
+                  top = fmaxf(top, other[u].x);
+                }
+                const auto weight = [&](float2 x) { return x.y == 0.f ? 0.f : fast_exp2(x.x - top); };  // 0: nothing visible there
+                const float f0 = weight(own);
+                float total = f0 * own.y;
+#pragma unroll
+                for (int u = 0; u < 3; ++u) {
+                  const float f = weight(other[u]);
+                  total += f * other[u].y;
+                  other[u].x = f;
+                }
+                const bool seen_any = parts ? total != 0.f : some_key;
+                const float inv_all = parts ? 1.f : (seen_any ? 1.f / total : 0.f);
+                const bool whole = !parts && C == 2 && a.o_boxes && !(KIND == kPrefix && w.shared && a.p_bt > 0) &&
+                                   __all_sync(0xFFFFFFFFu, row);
+                const bool tile_rows = parts && __any_sync(0xFFFFFFFFu, row);
+#pragma unroll 1
+                for (int k = 0; k < per; ++k) {
+                  const int q = me * per + k;
+                  float y[32];
+                  sums(q, y);
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) y[i] *= f0;
+#pragma unroll
+                  for (int u = 0; u < 3; ++u) {
+                    if (u >= C - 1 || other[u].y == 0.f) continue;
+                    const float4* from = reinterpret_cast<const float4*>(ring + C * kRows * 8) + (u * per + k) * 8 * kRows + R;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                      const float4 v = from[i * kRows];
+                      y[4 * i] = fmaf(other[u].x, v.x, y[4 * i]);
+                      y[4 * i + 1] = fmaf(other[u].x, v.y, y[4 * i + 1]);
+                      y[4 * i + 2] = fmaf(other[u].x, v.z, y[4 * i + 2]);
+                      y[4 * i + 3] = fmaf(other[u].x, v.w, y[4 * i + 3]);
+                    }
+                  }
+                  if (parts) {  // a quarter of the tile's partial results, as below
+                    if (!tile_rows) continue;
+                    uint4* here = stage + k * 256;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                      here[lane * 8 + (i ^ (lane & 7))] = make_uint4(__float_as_uint(y[4 * i]), __float_as_uint(y[4 * i + 1]),
+                                                                     __float_as_uint(y[4 * i + 2]), __float_as_uint(y[4 * i + 3]));
+                    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], 4096;\n" ::"l"(
+                                       a.part_o + (part - lane) * kD + q * 1024),
+                                   "r"(smem_addr(here))
+                                   : "memory");
+                      asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+                    }
+                    continue;
+                  }
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const uint4 v = make_uint4(pack_bf16x2(y[8 * i] * inv_all, y[8 * i + 1] * inv_all),
+                                               pack_bf16x2(y[8 * i + 2] * inv_all, y[8 * i + 3] * inv_all),
+                                               pack_bf16x2(y[8 * i + 4] * inv_all, y[8 * i + 5] * inv_all),
+                                               pack_bf16x2(y[8 * i + 6] * inv_all, y[8 * i + 7] * inv_all));
+                    if (whole)
+                      stage[lane * 8 + ((4 * k + i) ^ (lane & 7))] = v;
+                    else if (row)
+                      reinterpret_cast<uint4*>(out)[4 * q + i] = v;
+                  }
+                }
+                if (whole) {
+                  asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+                  __syncwarp();
+                  if (lane == 0) {
+                    asm volatile(
+                        "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];\n" ::"l"(&maps.o),
+                        "r"(smem_addr(stage)), "r"(64 * me), "r"(w.hkv * a.G), "r"(w.qb + tok), "r"(a.q_batched ? w.s : 0)
+                        : "memory");
+                    asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+                  }
+                }
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
+                if (row && me == 0) {
+                  if (parts)
+                    a.part_ml[part] = make_float2(top, total);
+                  else if (a.lse)
+                    a.lse[lse_place(a, KIND == kPrefix ? seq : w.s, w.qb + tok, head)] =
+                        seen_any ? top * kLn2 + logf(total) : -INFINITY;
+                }
+                __syncwarp();
+              }
+            }
+          }
           if constexpr (KIND == kPrefix) {
             // A whole tile, whatever rows it has: each warp's 8 KB hold its rows' 32 channels twice.
-            if (w.shared && parts) {
+            if (w.shared && parts && !stored) {
               stored = true;
               float* to = a.part_o + (part - lane) * kD;
               const bool some = __any_sync(0xFFFFFFFFu, row);
@@ -1256,13 +1424,20 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
             }
             __syncwarp();
           }
-          if (row) {
+          if (row && !(KIND != kPlain && a.cluster > 1)) {
             if (parts)
               a.part_ml[part] = make_float2(any ? m * c : -INFINITY, any ? l : 0.f);
             else if (a.lse)
               a.lse[lse_place(a, KIND == kPrefix ? seq : w.s, w.qb + tok, head)] = any ? m * a.scale + logf(l) : -INFINITY;
           }
         }
+      }
+    }
+    if constexpr (KIND != kPlain) {
+      if (!synced) {  // a tile without rows, an item without work: the others' walks and results
+        __syncwarp();
+        cluster_sync();
+        cluster_sync();
       }
     }
   }
@@ -1452,9 +1627,10 @@ struct PromptRule {
 
 struct PromptGrid {
   int tiles, tile_tokens, pair_tokens, pairs, splits, rounds, gap;
+  int cluster = 1;  // CTAs that join an item's splits on the chip
   int64_t items;
   // kPrefix with all sequences' rows together:
-  int p_tiles = 0, p_splits = 0, p_bt = 0, p_bs = 0, p_rounds = 1, p_gap = 0;
+  int p_tiles = 0, p_pieces = 0, p_splits = 0, p_bt = 0, p_bs = 0, p_rounds = 1, p_gap = 0;
   bool p_two = false;  // two-tile CTAs
   bool mixed = false;  // these walk over the own keys too
   int64_t p_rows = 0, p_items = 0;
@@ -1499,9 +1675,11 @@ PromptGrid prompt_grid(const spc_prompt_dims* d, const PromptRule& rule) {
         rounds = r;
       }
     }
-    if (z > 1) cost += 3000.0 + (double)(z * rows) / 5.0;
+    const bool cluster = (rule.window > 0 || rule.prefix > 0) && rounds == 1 && (z == 2 || z == 4);
+    if (z > 1) cost += cluster ? 1500.0 : 3000.0 + (double)(z * rows) / 5.0;
     if (z == 1 || cost < best) {
       best = cost;
+      g.cluster = cluster ? (int)z : 1;
       g.splits = (int)z;
       g.rounds = (int)rounds;
       g.gap = (int)((rounds - 1) * (start / block) * kBlock / (g.tiles == 2 ? Shape<2>::kKeys : Shape<1>::kKeys));
@@ -1586,14 +1764,23 @@ PromptGrid together_grid(const spc_prompt_dims* d, const PromptRule& rule) {
         rounds = r;
       }
     }
-    if (!g.mixed || z > 1) cost += 6000.0 + ((double)(z * shared) + (double)(oz * tokens * d->Hq)) / 5.0;
     if (oz > 0) cost += (double)(g.items * (oz * 4000 + own * 760 * 11 / 20)) / (2 * sms);
-    if (z == 1 || cost < best) {
-      best = cost;
-      g.p_splits = (int)z;
-      g.splits = (int)oz;
-      g.p_rounds = (int)rounds;
-      g.p_gap = (int)((rounds - 1) * (start / block) / two);  // stages have two blocks where CTAs have two tiles
+    // Splits that join on the chip, in whole clusters of a GPC's SMs (not single tokens', whose next launch joins what there
+    // is in any case: five behind 2003 keys 12.8 us, 18.0 so).
+    for (int64_t cluster = 1; cluster <= 4; cluster *= 2) {
+      if (z % cluster != 0 || (cluster > 1 && (few || rounds > 1 || items * z > places * (20 - cluster) / 19))) break;
+      const int64_t left = z / cluster;
+      double all = cost + (cluster > 1 ? 1500.0 : 0.0);
+      if (!g.mixed || left > 1) all += 6000.0 + ((double)(left * shared) + (double)(oz * tokens * d->Hq)) / 5.0;
+      if (best == 0.0 || all < best) {
+        best = all;
+        g.cluster = (int)cluster;
+        g.p_pieces = (int)z;
+        g.p_splits = (int)left;
+        g.splits = (int)oz;
+        g.p_rounds = (int)rounds;
+        g.p_gap = (int)((rounds - 1) * (start / block) / two);  // stages have two blocks where CTAs have two tiles
+      }
     }
   }
   if (g.mixed) g.items = 0;
@@ -1609,7 +1796,7 @@ PromptGrid together_grid(const spc_prompt_dims* d, const PromptRule& rule) {
   // (pairs of tiles that are nearly as many: four prompts of up to 2048 tokens behind 16384 keys 709 us together, 668 apart)
   const bool as_many = pairs && 10 * (int64_t)g.p_tiles > 9 * own_pairs;
   // Single tokens: always (one to 16 behind 2003 keys 12.4 to 13.3 us together, 15 to 27 apart).
-  if (few || (1.1 * best < apart && !as_many)) g.p_items = items * g.p_splits;
+  if (few || (1.1 * best < apart && !as_many)) g.p_items = items * g.p_pieces;
   return g;
 }
 
@@ -1621,7 +1808,7 @@ int64_t part_rows(const spc_prompt_dims* d, const PromptGrid& g) {
 
 size_t prompt_bytes(const spc_prompt_dims* d, const PromptRule& rule) {
   PromptGrid g = prompt_grid(d, rule);
-  int64_t rows = g.splits > 1 ? part_rows(d, g) : 0;
+  int64_t rows = g.splits > 1 && g.cluster == 1 ? part_rows(d, g) : 0;
   if (rule.prefix > 0) {  // (batched queries with first tokens of their own are not taken together)
     g = together_grid(d, rule);
     if (g.p_items > 0) rows = d->q.b != 0 ? std::max(rows, part_rows(d, g)) : part_rows(d, g);
@@ -1637,16 +1824,24 @@ cudaError_t launch_prompt_k(const PromptMaps<KIND>& maps, const PromptArgs& a, i
   const cudaError_t e =
       spc_host::ensure_smem_limit(configured, prompt_attn_kernel<TILES, KIND>, smem_bytes<TILES, KIND>());
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2] = {};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(Shape<TILES>::kThreads);
   cfg.dynamicSmemBytes = smem_bytes<TILES, KIND>();
   cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = early ? 1 : 0;
+  cfg.attrs = attr;
+  if (early) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+  }
+  if (a.cluster > 1) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = (unsigned)a.cluster;
+    attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
   return cudaLaunchKernelEx(&cfg, prompt_attn_kernel<TILES, KIND>, maps, a);
 }
 
@@ -1724,6 +1919,7 @@ spc_status launch_prompt(const spc_prompt_dims* d, const PromptRule& rule, const
     if (a.together) g = all;
     a.p_items = (int32_t)g.p_items;
     a.p_tiles = g.p_tiles;
+    a.p_pieces = g.p_pieces;
     a.p_splits = g.p_splits;
     a.p_rounds = g.p_rounds;
     a.p_gap = g.p_gap;
@@ -1742,7 +1938,8 @@ spc_status launch_prompt(const spc_prompt_dims* d, const PromptRule& rule, const
   a.rounds = g.rounds;
   a.items = (uint32_t)g.items;
   a.gap = g.gap;
-  const bool parts = a.splits > 1 || (a.together && !(a.mixed && a.p_splits == 1));
+  a.cluster = KIND == kPlain ? 1 : g.cluster;
+  const bool parts = a.together ? !(a.mixed && a.p_splits == 1) : a.splits > 1 && a.cluster == 1;
   a.parts = parts;
   if (parts) {
     a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(x.ws) + kPromptHead);
@@ -1774,6 +1971,7 @@ spc_status launch_prompt(const spc_prompt_dims* d, const PromptRule& rule, const
     e = g.p_two ? launch_prompt_k<2, KIND>(maps, a, g.p_items, stream) : launch_prompt_k<1, KIND>(maps, a, g.p_items, stream);
     if (e == cudaSuccess && g.items == 0 && !a.mixed) return few(a, d, stream);
     a.p_items = 0;
+    a.cluster = 1;
   }
   const int64_t grid = g.items * a.splits;
   if (e == cudaSuccess && grid > 0)
