@@ -69,9 +69,15 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) few_attn_kernel(const __gri
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)(blockIdx.x % a.few_ctas), hkv = (int)(blockIdx.x / a.few_ctas % a.Hkv);
   const int s = (int)(blockIdx.x / a.few_ctas / a.Hkv);
+  // Launched while the kernel before in the stream ends.  (Behind a prefix's launch, which has waited for the ones before
+  // it, only that launch's results are waited for, below.)
+  if (!PREFIX) asm volatile("griddepcontrol.wait;\n" ::: "memory");
   int lq, lk, qb, kb;
   sequence(a, s, lq, lk, qb, kb);
-  if (lq == 0) return;  // all CTAs of the cluster do
+  if (lq == 0) {  // in all CTAs of the cluster
+    if (PREFIX) asm volatile("griddepcontrol.wait;\n" ::: "memory");  // what comes behind this launch comes behind both
+    return;
+  }
   // Keys that the token sees: the first `ns` and those from `low` on, numbered through.
   const int low = a.window > 0 ? max(0, lk - a.window) : 0, ns = min(a.sinks, low), n = ns + lk - low;
   const int blocks = (n + kFewKeys - 1) / kFewKeys;
@@ -309,7 +315,7 @@ spc_status launch_few(PromptArgs& a, const spc_prompt_dims* d, cudaStream_t stre
     cfg.dynamicSmemBytes = kFewSmemBytes;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = PREFIX ? 2 : 1;
+    cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, few_attn_kernel<PREFIX>, a);
   }
   if (e != cudaSuccess) {

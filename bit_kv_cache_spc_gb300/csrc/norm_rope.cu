@@ -110,6 +110,7 @@ __global__ void __launch_bounds__(256, 3) norm_rope_kernel(const __grid_constant
     }
     cp_async_commit();
   };
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");  // launched while the kernel before in the stream ends
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) load(i);  // on their way while the angles are formed
   {
@@ -242,11 +243,16 @@ spc_status launch_norm_rope(const spc_norm_rope_dims* dn, const int32_t* pos, co
   if (tokens * a.slices > 0x7FFFFFFF) return SPC_ERR_UNSUPPORTED;
   a.tokens = (uint32_t)tokens;
   const int64_t blocks = (tokens * a.slices + 31) / 32;
-  if (d->interleaved)
-    norm_rope_kernel<true><<<(unsigned)blocks, 256, 0, stream>>>(a);
-  else
-    norm_rope_kernel<false><<<(unsigned)blocks, 256, 0, stream>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, d->interleaved ? norm_rope_kernel<true> : norm_rope_kernel<false>, a);
   if (e != cudaSuccess) {
     spc_host::set_cuda_error(e);
     return SPC_ERR_CUDA;
