@@ -1,6 +1,8 @@
 // The attention of prompts' queries, for prompt_attn.cu (causal), window_attn.cu
 // (a sliding window) and prefix_attn.cu (a shared prefix): one kernel, whose
-// walk over the keys the kind of call decides.
+// walk over the keys the kind of call decides.  For the last two the walk's
+// 64-key blocks are two runs (PromptItem), rows and partial results leave by
+// bulk copies, and the splits of an item may join in a cluster.
 //
 // The causal attention of prompts (SpeCache page, section 3 "Prefilling": the
 // attention that Algorithm 1's Quant and Offload follow), over 16-bit keys and
