@@ -255,7 +255,8 @@ __device__ __forceinline__ bool mbar_try(uint64_t* b, uint32_t parity) {
 // read only after many tries: reading it takes longer than a regular wait.
 // A wait for something that regularly comes after `stages` stages of keys has a
 // 65536th of the limit more for each (30 us at two seconds; a stage takes 1.4).
-__device__ __forceinline__ bool mbar_wait(PromptBars& bars, uint64_t* b, uint32_t parity, uint32_t stages = 0) {
+template <class Bars>
+__device__ __forceinline__ bool mbar_wait(Bars& bars, uint64_t* b, uint32_t parity, uint32_t stages = 0) {
   for (int i = 0; i < 64; ++i)
     if (mbar_try(b, parity)) return true;
   uint64_t start, now;
@@ -285,7 +286,8 @@ __device__ __forceinline__ void mbar_drain(uint64_t* b, uint32_t parity) {
 }
 
 // For a whole warp: one outcome for all lanes.
-__device__ __forceinline__ bool mbar_wait_warp(PromptBars& bars, uint64_t* b, uint32_t parity, uint32_t stages = 0) {
+template <class Bars>
+__device__ __forceinline__ bool mbar_wait_warp(Bars& bars, uint64_t* b, uint32_t parity, uint32_t stages = 0) {
   return __all_sync(0xFFFFFFFFu, mbar_wait(bars, b, parity, stages));
 }
 
@@ -449,6 +451,25 @@ __device__ __forceinline__ void product_o(uint32_t d, uint32_t p, uint64_t v, bo
 }
 
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return min(max(x, lo), hi); }
+
+// Replaces the non-finite bf16 elements of the 16-byte words first, first + step, ... of n by zeros; says whether there
+// was one.
+__device__ __forceinline__ bool clear_non_finite(uint4* tile, int first, int n, int step) {
+  bool touched = false;
+#pragma unroll 4
+  for (int i = first; i < n; i += step) {
+    const uint4 v = tile[i];
+    // an exponent of all ones carries into the sign's place
+    const auto carry = [](uint32_t x) { return (x & 0x7F807F80u) + 0x00800080u; };
+    if (((carry(v.x) | carry(v.y) | carry(v.z) | carry(v.w)) & 0x80008000u) == 0u) continue;
+    // 16-bit halves with an exponent of all ones
+    const uint32_t m0 = __vcmpeq2(v.x & 0x7F807F80u, 0x7F807F80u), m1 = __vcmpeq2(v.y & 0x7F807F80u, 0x7F807F80u);
+    const uint32_t m2 = __vcmpeq2(v.z & 0x7F807F80u, 0x7F807F80u), m3 = __vcmpeq2(v.w & 0x7F807F80u, 0x7F807F80u);
+    tile[i] = make_uint4(v.x & ~m0, v.y & ~m1, v.z & ~m2, v.w & ~m3);
+    touched = true;
+  }
+  return touched;
+}
 
 // Lengths and first tokens as the device arrays give them, held to the
 // tensors: no row outside them is read or written whatever the arrays hold.
@@ -990,19 +1011,7 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
         ++scans;
         if (!mbar_wait_warp(bars, &bars.kv_full[sv], (xv / kStages) & 1)) break;
         uint4* tile = reinterpret_cast<uint4*>(ring + sv * H::kStageBytes);
-        bool touched = false;
-  #pragma unroll 4
-        for (int i = tid - 32 * H::kScanWarp; i < H::kStageBytes / 16; i += H::kThreads - 32 * H::kScanWarp) {
-          const uint4 v = tile[i];
-          // an exponent of all ones carries into the sign's place
-          const auto carry = [](uint32_t x) { return (x & 0x7F807F80u) + 0x00800080u; };
-          if (((carry(v.x) | carry(v.y) | carry(v.z) | carry(v.w)) & 0x80008000u) == 0u) continue;
-          // 16-bit halves with an exponent of all ones
-          const uint32_t m0 = __vcmpeq2(v.x & 0x7F807F80u, 0x7F807F80u), m1 = __vcmpeq2(v.y & 0x7F807F80u, 0x7F807F80u);
-          const uint32_t m2 = __vcmpeq2(v.z & 0x7F807F80u, 0x7F807F80u), m3 = __vcmpeq2(v.w & 0x7F807F80u, 0x7F807F80u);
-          tile[i] = make_uint4(v.x & ~m0, v.y & ~m1, v.z & ~m2, v.w & ~m3);
-          touched = true;
-        }
+        const bool touched = clear_non_finite(tile, tid - 32 * H::kScanWarp, H::kStageBytes / 16, H::kThreads - 32 * H::kScanWarp);
         if (touched) bars.bad = 1u;
         asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
         __syncwarp();
@@ -1848,6 +1857,20 @@ cudaError_t launch_prompt_k(const PromptMaps<KIND>& maps, const PromptArgs& a, i
   return cudaLaunchKernelEx(&cfg, prompt_attn_kernel<TILES, KIND>, maps, a);
 }
 
+// Whether two-tile CTAs stay and take item after item (prompt_stay.cuh), or
+// leave and the next one starts wherever there is a place.  Staying saves a part
+// of each item's start and output, but fixes which CTA takes which items: what
+// one CTA has more of than the others counts the less the more items it takes
+// and the shorter they are.  32 and 8 heads, us leaving and staying, by items a
+// CTA: 1.7 (2048 tokens), window 128 24.5 and 21.5, 1024 36 and 39; 3.4, window
+// 512 58 and 54, 1024 70 and 73; 6.7, window 1024 141 and 134, 2048 201 and 203,
+// 4096 296 and 311; 13.5, window 2048 417 and 407, 4096 694 and 701; 27, window
+// 4096 1474 and 1464, 128 274 and 199.
+bool stays(const spc_prompt_dims* d, const PromptRule& rule, const PromptGrid& g) {
+  const int64_t sms = spc_host::sm_count();
+  return g.tiles == 2 && g.splits == 1 && g.items > sms && rule.keys(d, g.pair_tokens) * sms <= 256 * g.items;
+}
+
 // What the caller gives besides the shape; pk, pv, p: kPrefix.
 struct PromptTensors {
   const uint16_t *q, *k, *v;
@@ -1910,10 +1933,11 @@ PromptArgs prompt_args(const spc_prompt_dims* d, const PromptRule& rule, const P
   return a;
 }
 
-// few: the launch of single tokens' own keys, with what joins them with the prefix.
+// few: the launch of single tokens' own keys, with what joins them with the prefix; stay: of CTAs that take item after item.
 template <int KIND>
 spc_status launch_prompt(const spc_prompt_dims* d, const PromptRule& rule, const PromptTensors& x, cudaStream_t stream,
-                         spc_status (*few)(PromptArgs&, const spc_prompt_dims*, cudaStream_t) = nullptr) {
+                         spc_status (*few)(PromptArgs&, const spc_prompt_dims*, cudaStream_t) = nullptr,
+                         cudaError_t (*stay)(const PromptMaps<KIND>&, const PromptArgs&, cudaStream_t) = nullptr) {
   PromptArgs a = prompt_args(d, rule, x);
   PromptGrid g = prompt_grid(d, rule);
   if constexpr (KIND == kPrefix) {
@@ -1977,7 +2001,9 @@ spc_status launch_prompt(const spc_prompt_dims* d, const PromptRule& rule, const
     a.cluster = 1;
   }
   const int64_t grid = g.items * a.splits;
-  if (e == cudaSuccess && grid > 0)
+  if (e == cudaSuccess && stay != nullptr && stays(d, rule, g))
+    e = stay(maps, a, stream);
+  else if (e == cudaSuccess && grid > 0)
     e = g.tiles == 2 ? launch_prompt_k<2, KIND>(maps, a, grid, stream)
                      : launch_prompt_k<1, KIND>(maps, a, grid, stream, a.together);
   if (e == cudaSuccess && parts) {

@@ -8,9 +8,11 @@
 // heads, window 4096, takes 1.45 to 1.48 ms (2.06 TFLOP: 74% of the measured
 // burst rate; 0.73 us per 64 keys and two tiles, where the products take 0.68,
 // and 5 us of start and output for every 66 such blocks).  Short windows by
-// those 5 us: 17216 packed tokens of 32 ungrouped heads, window 128, 178 us
-// (564 MB, 84 us at the copy rate).
+// starts and outputs, of which CTAs that stay hide a part (prompt_stay.cuh):
+// 17216 packed tokens of 32 ungrouped heads, window 128, 160 us (564 MB, 84 us
+// at the copy rate).
 #include "few_attn.cuh"
+#include "prompt_stay.cuh"
 
 namespace spc {
 
@@ -36,7 +38,7 @@ spc_status launch_window_attn(const spc_prompt_dims* d, int32_t window, int32_t 
     PromptArgs a = prompt_args(d, rule, x);
     return launch_few<false>(a, d, stream);
   }
-  return launch_prompt<kWindow>(d, rule, x, stream);
+  return launch_prompt<kWindow>(d, rule, x, stream, nullptr, launch_stay<kWindow>);
 }
 
 }  // namespace spc
