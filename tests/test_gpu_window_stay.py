@@ -144,3 +144,27 @@ def test_graphs_and_streams_repeat_the_same_bits():
     torch.cuda.synchronize()
     assert all(torch.equal(x, want[0]) for x in outs)
     assert spc.spc_prompt_attn_status(ws) == 0 and spc.spc_prompt_attn_status() == 0
+
+
+def test_a_wait_that_runs_out_is_reported():
+    """With a limit of a nanosecond: each item's second tile has no rows, and its warps wait for the walk of the first over
+    16384 keys.  The next call is right."""
+    import bit_kv_cache_spc_gb300 as spc
+    lk = 1 << 14
+    S = torch.cuda.get_device_properties(0).multi_processor_count * (lk // 256 + 1)
+    z = dict(dtype=torch.bfloat16, device="cuda")
+    q, k = torch.zeros((S, 128, D), **z), torch.zeros((lk, 1, D), **z)
+    v, o, ws = torch.ones_like(k), torch.full_like(q, 7.0), torch.zeros(256, dtype=torch.uint8, device="cuda")
+    at = dict(q_begin=torch.arange(S, dtype=torch.int32, device="cuda"), q_len=i32([1] * S), k_begin=i32([0] * S),
+              k_len=i32([lk] * S), q_max=2, k_max=lk)
+    before = spc.spc_prompt_attn_wait_limit(1)
+    try:
+        spc.spc_window_attn(q, k, v, o, lk - 1, ws=ws, **at)
+        spc.spc_prompt_attn_wait_limit(before)
+        assert spc.spc_prompt_attn_status(ws) == 6 and spc.spc_prompt_attn_status(ws) == 0
+        assert spc.spc_prompt_attn_status() == 6 and spc.spc_prompt_attn_status() == 0
+        spc.spc_window_attn(q, k, v, o, lk - 1, ws=ws, **at)
+        assert bool((o == 1).all()) and spc.spc_prompt_attn_status(ws) == 0
+    finally:
+        spc.spc_prompt_attn_wait_limit(before)
+        spc.spc_prompt_attn_status()
