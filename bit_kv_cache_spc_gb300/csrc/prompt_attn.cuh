@@ -255,13 +255,21 @@ __device__ __forceinline__ bool mbar_try(uint64_t* b, uint32_t parity) {
 // read only after many tries: reading it takes longer than a regular wait.
 // A wait for something that regularly comes after `stages` stages of keys has a
 // 65536th of the limit more for each (30 us at two seconds; a stage takes 1.4).
-template <class Bars>
+// The softmax warps take UNROLL = 1: with 64 tries written out at each of their
+// waits, their code and the other warps' come late from the instruction cache
+// (prefix attention of 8192 queries 676 to 665 us, of 17 turns 109.4 to
+// 106.6; 17216 packed tokens, window 128, 164 to 147).  For the warps of the
+// products they are written out: rolled, a 32768-token prompt takes 5.73 ms
+// instead of 5.59.
+template <int UNROLL = 64, class Bars>
 __device__ __forceinline__ bool mbar_wait(Bars& bars, uint64_t* b, uint32_t parity, uint32_t stages = 0) {
+#pragma unroll UNROLL
   for (int i = 0; i < 64; ++i)
     if (mbar_try(b, parity)) return true;
   uint64_t start, now;
   asm volatile("mov.u64 %0, %%globaltimer;\n" : "=l"(start));
   for (;;) {
+#pragma unroll(UNROLL < 16 ? UNROLL : 16)
     for (int i = 0; i < 16; ++i)
       if (mbar_try(b, parity)) return true;
     if (bars.stop) return false;
@@ -286,9 +294,9 @@ __device__ __forceinline__ void mbar_drain(uint64_t* b, uint32_t parity) {
 }
 
 // For a whole warp: one outcome for all lanes.
-template <class Bars>
+template <int UNROLL = 64, class Bars>
 __device__ __forceinline__ bool mbar_wait_warp(Bars& bars, uint64_t* b, uint32_t parity, uint32_t stages = 0) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait(bars, b, parity, stages));
+  return __all_sync(0xFFFFFFFFu, mbar_wait<UNROLL>(bars, b, parity, stages));
 }
 
 __device__ __forceinline__ void tma_load4(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
@@ -1082,7 +1090,7 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
         for (int i = 0; i < blocks; ++i) {
           const int b = i & 1;
           const uint32_t sp = s_addr + kBlock * b;
-          ok = mbar_wait_warp(bars, &bars.s_full[t][b], (i >> 1) & 1);
+          ok = mbar_wait_warp<1>(bars, &bars.s_full[t][b], (i >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
           float x[kBlock];
@@ -1116,7 +1124,7 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
             l *= f;
             if (i > 0) {
               // the product of the block before has to be complete: the next use of the other buffer says so
-              ok = mbar_wait_warp(bars, &bars.s_full[t][b ^ 1], ((i + 1) >> 1) & 1);
+              ok = mbar_wait_warp<1>(bars, &bars.s_full[t][b ^ 1], ((i + 1) >> 1) & 1);
               if (!ok) break;
               tc_fence_after();
   #pragma unroll
@@ -1139,8 +1147,8 @@ prompt_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_c
           if (lane == 0) mbar_arrive(&bars.p_full[t][b]);
         }
         // ---- output ----
-        if (blocks > 0 && ok) ok = mbar_wait_warp(bars, &bars.s_full[t][(blocks + 1) & 1], ((blocks + 1) >> 1) & 1);
-        if (blocks == 0 && n > 0) ok = mbar_wait_warp(bars, &bars.q_full[t], 0);  // Q's place is used below
+        if (blocks > 0 && ok) ok = mbar_wait_warp<1>(bars, &bars.s_full[t][(blocks + 1) & 1], ((blocks + 1) >> 1) & 1);
+        if (blocks == 0 && n > 0) ok = mbar_wait_warp<1>(bars, &bars.q_full[t], 0);  // Q's place is used below
         if (ok || !synced) {
           tc_fence_after();
           const bool bad = *(volatile uint32_t*)&bars.bad != 0u;
@@ -1862,13 +1870,13 @@ cudaError_t launch_prompt_k(const PromptMaps<KIND>& maps, const PromptArgs& a, i
 // of each item's start and output, but fixes which CTA takes which items: what
 // one CTA has more of than the others counts the less the more items it takes
 // and the shorter they are.  32 and 8 heads, us leaving and staying, by items a
-// CTA: 1.7 (2048 tokens), window 128 24.5 and 21.5, 1024 36 and 39; 3.4, window
-// 512 58 and 54, 1024 70 and 73; 6.7, window 1024 141 and 134, 2048 201 and 203,
-// 4096 296 and 311; 13.5, window 2048 417 and 407, 4096 694 and 701; 27, window
-// 4096 1474 and 1464, 128 274 and 199.
+// CTA: 1.7 (2048 tokens), window 128 24.6 and 21.6, 1024 36.6 and 39.5; 3.4,
+// window 512 58 and 53, 1024 71 and 72; 6.7, window 1024 141 and 133, 2048 203
+// and 204; 13.5, window 1024 278 and 259, 2048 423 and 421; 27, window 128 277
+// and 196, 2048 865 and 847, 4096 1490 and 1515.
 bool stays(const spc_prompt_dims* d, const PromptRule& rule, const PromptGrid& g) {
-  const int64_t sms = spc_host::sm_count();
-  return g.tiles == 2 && g.splits == 1 && g.items > sms && rule.keys(d, g.pair_tokens) * sms <= 256 * g.items;
+  const int64_t sms = spc_host::sm_count(), keys = rule.keys(d, g.pair_tokens);
+  return g.tiles == 2 && g.splits == 1 && g.items > sms && keys <= 2560 && keys * sms <= 256 * g.items;
 }
 
 // What the caller gives besides the shape; pk, pv, p: kPrefix.

@@ -13,14 +13,16 @@
 // weights that it takes.
 //
 // 17216 packed tokens of 32 ungrouped heads, window 128: 180 us by CTAs that
-// leave, 160 so (564 MB: 53% of the copy rate); of 8 KV heads 146 and 94; 32768
-// tokens of 32 and 8 heads 274 and 199.  An item of three blocks takes 5.8 us:
-// 1.9 from its first scores to its last but one, 1.9 from the last product until
-// its rows are stored, 2 until the next one's scores, which wait for keys that
-// the ring takes up late.  Measured against it: the next item looked up before
-// the last copies of this one 170 us, the output's 64 channels held in registers
-// until what was staged before has left 159 but of a window of 4096 1.50 ms
-// instead of 1.47, both 172.
+// leave, 147 so (564 MB: 57% of the copy rate); of 8 KV heads 146 and 93; 32768
+// tokens of 32 and 8 heads 274 and 196.  Bound by the chain of an item: where
+// heads are grouped 6 us for four blocks, 3.4 of them the softmax, 1.9 from the
+// last product until the rows are stored, 0.6 until the next item's scores.
+// Measured against it: the next item looked up by a warp of its own 160 us where
+// this took 160.5, and a window of 4096 1.50 ms instead of 1.47; looked up
+// before the last copies of this one 170; the output's 64 channels held in
+// registers until what was staged before has left 159, and the long window
+// 1.50; stages that no row of the second tile sees left out by it, in a kernel
+// of its own, 142 where this took 147, and grouped heads 201 instead of 197.
 #pragma once
 
 #include "prompt_attn.cuh"
@@ -345,7 +347,7 @@ stay_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_con
     int u = 0, walk = 0;
     bool ok = true;
     for (int it = 0; ok; ++it) {
-      ok = mbar_wait_warp(bars, &bars.item_full[it & 1], (it >> 1) & 1, walk + skip);
+      ok = mbar_wait_warp<1>(bars, &bars.item_full[it & 1], (it >> 1) & 1, walk + skip);
       if (!ok) break;
       const PromptItem& w = bars.item[it & 1];
       if (__shfl_sync(0xFFFFFFFFu, w.s, 0) < 0) break;
@@ -370,7 +372,7 @@ stay_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_con
       for (int i = 0; i < blocks; ++i) {
         const int b = (u + i) & 1;
         const uint32_t sp = s_addr + kBlock * b;
-        ok = mbar_wait_warp(bars, &bars.s_full[t][b], ((u + i) >> 1) & 1);
+        ok = mbar_wait_warp<1>(bars, &bars.s_full[t][b], ((u + i) >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
         float x[kBlock];
@@ -398,7 +400,7 @@ stay_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_con
           l *= f;
           if (i > 0) {
             // the product of the block before has to be complete: the next use of the other buffer says so
-            ok = mbar_wait_warp(bars, &bars.s_full[t][b ^ 1], ((u + i + 1) >> 1) & 1);
+            ok = mbar_wait_warp<1>(bars, &bars.s_full[t][b ^ 1], ((u + i + 1) >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
@@ -419,7 +421,7 @@ stay_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_con
         if (lane == 0) mbar_arrive(&bars.p_full[t][b]);
       }
       // ---- output: 64 channels at a time ----
-      if (blocks > 0 && ok) ok = mbar_wait_warp(bars, &bars.s_full[t][(u + blocks + 1) & 1], ((u + blocks + 1) >> 1) & 1);
+      if (blocks > 0 && ok) ok = mbar_wait_warp<1>(bars, &bars.s_full[t][(u + blocks + 1) & 1], ((u + blocks + 1) >> 1) & 1);
       if (!ok) break;
       if (blocks > 0) {
         u += blocks + 2;

@@ -20,7 +20,8 @@ def call(q, k, v, window, sinks, **kw):
 
 @pytest.mark.parametrize("lq,lk,Hq,Hkv,window,sinks", [
     (3000, 3000, 32, 32, 200, 0), (3001, 3100, 32, 8, 130, 5), (2999, 2600, 32, 8, 64, 0), (801, 900, 128, 1, 70, 3),
-    (1900, 1900, 40, 40, 1, 0), (1153, 1153, 96, 48, 128, 1), (2000, 0, 32, 32, 9, 2), (1000, 2100, 120, 24, 300, 70)])
+    (1900, 1900, 40, 40, 1, 0), (1153, 1153, 96, 48, 128, 1), (2000, 0, 32, 32, 9, 2), (1000, 2100, 120, 24, 300, 70),
+    (3000, 3000, 40, 40, 600, 0), (2300, 2200, 48, 24, 384, 0)])
 def test_one_sequence(lq, lk, Hq, Hkv, window, sinks):
     """Also with fewer keys than queries (items without a block), none at all, and a last pair with one tile."""
     q, k, v = rnd(1, lq, Hq, D), rnd(2, lk, Hkv, D), rnd(3, lk, Hkv, D)
@@ -82,10 +83,11 @@ def test_batch_over_head_major_caches():
 
 
 @pytest.mark.parametrize("what", [math.nan, math.inf, -math.inf])
-def test_non_finite_keys_and_values(what):
+@pytest.mark.parametrize("sinks", [0, 2])
+def test_non_finite_keys_and_values(what, sinks):
     """A poisoned stretch of one head leaves the rows that do not see it bit for bit as they were, in every item that a CTA
     takes before and after; values alone reach the rows that see them with their sign."""
-    L, H, window, sinks = 2600, 32, 150, 2
+    L, H, window = 2600, 32, 150
     q, k, v = rnd(1, L, H, D), rnd(2, L, H, D), rnd(3, L, H, D)
     o, lse = call(q, k, v, window, sinks)
     kk, vv = k.clone(), v.clone()
@@ -148,10 +150,9 @@ def test_graphs_and_streams_repeat_the_same_bits():
 
 def test_a_wait_that_runs_out_is_reported():
     """With a limit of a nanosecond: each item's second tile has no rows, and its warps wait for the walk of the first over
-    16384 keys.  The next call is right."""
+    2560 keys.  The next call is right."""
     import bit_kv_cache_spc_gb300 as spc
-    lk = 1 << 14
-    S = torch.cuda.get_device_properties(0).multi_processor_count * (lk // 256 + 1)
+    lk, S = 2560, 40 * torch.cuda.get_device_properties(0).multi_processor_count
     z = dict(dtype=torch.bfloat16, device="cuda")
     q, k = torch.zeros((S, 128, D), **z), torch.zeros((lk, 1, D), **z)
     v, o, ws = torch.ones_like(k), torch.full_like(q, 7.0), torch.zeros(256, dtype=torch.uint8, device="cuda")
