@@ -35,8 +35,8 @@
 // execution, so what one warp spends on waiting and committing between the
 // tiles' products leaves the tensor cores idle (3980 cycles).
 // Items are numbered densely over the sequences' actual lengths, longer rows
-// of keys first.  CTAs that stay and take item after item measured slower
-// (a 32768-token prompt 5.68 ms against 5.43, eight single tokens over up to
+// of keys first.  For long walks CTAs that stay and take item after item (as
+// prompt_stay.cuh's do for short ones) measured slower (a 32768-token prompt 5.68 ms against 5.43, eight single tokens over up to
 // 32768 keys 140 us against 103): the next item's copies wait for Q's place,
 // and its softmax for the last one's output, all the same.
 //
@@ -1715,7 +1715,7 @@ bool few_rows(const spc_prompt_dims* d) { return d->q_max == 1 && d->Hq / d->Hkv
 // together, so that the prefix's keys are walked once for them and not once for
 // each (two-tile CTAs where the rows fill more than one tile).  The sequences'
 // own keys come in the same walk, masked for the rows of the others (`mixed`,
-// up to 64 sequences: 17 prompts of up to 77 tokens behind 8011 keys 109 us, in
+// up to 64 sequences: 17 prompts of up to 77 tokens behind 8011 keys 104 us, in
 // a launch of their own and joined 118; 40 of 20 tokens 88 and 102), or for
 // more sequences, and for single tokens, in a launch of their own.
 // p_items = 0 where that does not pay: the sequences' own tiles are as few, or
@@ -1725,9 +1725,9 @@ bool few_rows(const spc_prompt_dims* d) { return d->q_max == 1 && d->Hq / d->Hkv
 // items taken in turns by the CTAs' places, or the last split shorter as in
 // prompt_grid, and the partial results.  Own keys in a launch of their own are
 // split where their items would take longer than one of the prefix's.  Measured
-// against it: the 17 prompts 111 us in one piece, 129 in 2, 109 in 3, 122 in 4;
-// the 40 127, 88, 111 and 98; 64 single tokens behind 32768 keys 126 in 4, 76
-// in 9, 62 in 18.
+// against it: the 17 prompts 104 us in 2 (129 in equal ones), 106 in 3, 121 in
+// 4; the 40 127 in one piece, 88 in 2, 111 and 98; 64 single tokens behind 32768
+// keys 126 in 4, 76 in 9, 62 in 18.
 PromptGrid together_grid(const spc_prompt_dims* d, const PromptRule& rule) {
   PromptGrid g = {};
   const int G = d->Hq / d->Hkv, sms = spc_host::sm_count();
@@ -1774,14 +1774,17 @@ PromptGrid together_grid(const spc_prompt_dims* d, const PromptRule& rule) {
     const int64_t block = std::max<int64_t>(g.p_two ? 690 : 760, std::min(items * z, places) * 5 / std::min(g.p_tiles, 2));
     double cost = (double)(ceil_div(items * z, places) * (start + share * block));
     int64_t rounds = 1;
+    int64_t gap = 0;
     if (z > 1 && items * z > places && items * (z - 1) < places) {  // the last split shorter, in a few rounds on what is left
-      const int64_t r = ceil_div(items, places - items * (z - 1));
-      const int64_t small = (walk - (z - 1) * (r - 1) * (start / block)) / ((z - 1) * r + 1);
-      const int64_t last = r * (start + (small + (g.mixed ? std::min(inside, small) : 0)) * block);
+      const int64_t r = ceil_div(items, places - items * (z - 1)), behind = g.mixed ? inside : 0;
+      const int64_t less = (r - 1) * (start / block) + r * behind;  // what its starts and own keys take besides
+      const int64_t small = (walk - (z - 1) * less) / ((z - 1) * r + 1);
+      const int64_t last = r * (start + (small + std::min(behind, small)) * block);
       const double one = (double)std::max(start + ceil_div(walk - small, z - 1) * block, last);
       if (small >= 4 && one < cost) {
         cost = one;
         rounds = r;
+        gap = less;
       }
     }
     if (oz > 0) cost += (double)(g.items * (oz * 4000 + own * 760 * 11 / 20)) / (2 * sms);
@@ -1799,7 +1802,7 @@ PromptGrid together_grid(const spc_prompt_dims* d, const PromptRule& rule) {
         g.p_splits = (int)left;
         g.splits = (int)oz;
         g.p_rounds = (int)rounds;
-        g.p_gap = (int)((rounds - 1) * (start / block) / two);  // stages have two blocks where CTAs have two tiles
+        g.p_gap = (int)(gap / two);  // stages have two blocks where CTAs have two tiles
       }
     }
   }
