@@ -13,7 +13,7 @@
 // weights that it takes.
 //
 // 17216 packed tokens of 32 ungrouped heads, window 128: 180 us by CTAs that
-// leave, 147 so (564 MB: 57% of the copy rate); of 8 KV heads 146 and 93; 32768
+// leave, 142 so (564 MB: 59% of the copy rate); of 8 KV heads 146 and 93; 32768
 // tokens of 32 and 8 heads 274 and 196.  Bound by the chain of an item: where
 // heads are grouped 6 us for four blocks, 3.4 of them the softmax, 1.9 from the
 // last product until the rows are stored, 0.6 until the next item's scores.
@@ -21,8 +21,7 @@
 // this took 160.5, and a window of 4096 1.50 ms instead of 1.47; looked up
 // before the last copies of this one 170; the output's 64 channels held in
 // registers until what was staged before has left 159, and the long window
-// 1.50; stages that no row of the second tile sees left out by it, in a kernel
-// of its own, 142 where this took 147, and grouped heads 201 instead of 197.
+// 1.50.
 #pragma once
 
 #include "prompt_attn.cuh"
@@ -50,6 +49,7 @@ struct __align__(16) StayBars {
   uint32_t tmem;
   uint32_t bad[2];          // a masked stage of the item held a non-finite value
   volatile uint32_t stop;
+  int first1[2];            // AHEAD: the item's first stage with keys that the second tile sees
 };
 static_assert(sizeof(StayBars) <= 1024, "barriers outgrow their place");
 
@@ -69,7 +69,11 @@ __device__ __forceinline__ void tmem_get16(uint32_t addr, float* r) {
                : "memory");
 }
 
-template <int KIND>
+// AHEAD: the second tile may have stages in front that none of its rows sees; it
+// leaves them out (17216 packed tokens of 32 ungrouped heads, window 128, whose
+// items have six blocks for tiles that see four: 147 to 142 us, window 1024 279
+// to 273; in the kernel of all calls grouped heads lose 2 to 4%).
+template <int KIND, bool AHEAD>
 __global__ void __launch_bounds__(Shape<2>::kThreads, 1)
 stay_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_constant__ PromptArgs a) {
   using H = Shape<2>;
@@ -161,6 +165,10 @@ stay_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_con
         const int n = have ? w.hi - w.lo : 0;
         if (lane == 0) {
           bars.item[it & 1] = w;
+          if constexpr (AHEAD) {
+            const int low = w.tok0 + a.tile_tokens + w.lk - w.lq + 1 - a.window;  // where its first row's window begins
+            bars.first1[it & 1] = n > 1 && w.two ? clampi((low - w.key1) / H::kKeys, 0, n - 1) : 0;
+          }
           bars.bad[it & 1] = 0;
           mbar_arrive(&bars.item_full[it & 1]);
           const auto load_kv = [&](bool values, int j) {
@@ -223,12 +231,12 @@ stay_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_con
         if (!ok) break;
         const PromptItem& w = bars.item[it & 1];
         if (__shfl_sync(0xFFFFFFFFu, w.s, 0) < 0) break;
-        const int stages = __shfl_sync(0xFFFFFFFFu, w.hi - w.lo, 0);
+        int stages = __shfl_sync(0xFFFFFFFFu, w.hi - w.lo, 0);
         const bool here = __shfl_sync(0xFFFFFFFFu, (int)(t == 0 || w.two), 0) != 0;
-        const int blocks = here && stages > 0 ? __shfl_sync(0xFFFFFFFFu, w.blocks[t], 0) : 0;
-        const int from_a = __shfl_sync(0xFFFFFFFFu, w.ma / H::kPerStage - w.lo, 0);
-        const int to_a = __shfl_sync(0xFFFFFFFFu, (w.mb + H::kPerStage - 1) / H::kPerStage - w.lo, 0);
-        const int from_c = __shfl_sync(0xFFFFFFFFu, w.mc / H::kPerStage - w.lo, 0);
+        int blocks = here && stages > 0 ? __shfl_sync(0xFFFFFFFFu, w.blocks[t], 0) : 0;
+        int from_a = __shfl_sync(0xFFFFFFFFu, w.ma / H::kPerStage - w.lo, 0);
+        int to_a = __shfl_sync(0xFFFFFFFFu, (w.mb + H::kPerStage - 1) / H::kPerStage - w.lo, 0);
+        int from_c = __shfl_sync(0xFFFFFFFFu, w.mc / H::kPerStage - w.lo, 0);
         const auto scanned = [&](int j) { return (j >= from_a && j < to_a) || j >= from_c; };
         const auto request = [&]() {
           if (t == 0 && lead) mbar_arrive(&bars.v_scan[requests & 1u]);
@@ -239,6 +247,19 @@ stay_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_con
         if (stages == 0) {
           leave(it);
           continue;
+        }
+        if constexpr (AHEAD) {
+          const int first = t == 1 && here ? __shfl_sync(0xFFFFFFFFu, bars.first1[it & 1], 0) : 0;
+          for (int j = 0; j < 2 * first && ok; ++j, ++x) {  // (the other tile frees what it uses, and what is looked through)
+            ok = mbar_wait_warp(bars, &bars.kv_full[x % kStages], (x / kStages) & 1);
+            if (ok && lead) mbar_arrive(&bars.kv_free[x % kStages]);
+            if (j % 2 == 1 && scanned(j / 2)) clean ^= 1u << (x % kStages);
+          }
+          stages -= first;
+          from_a -= first;
+          to_a -= first;
+          from_c -= first;
+          blocks -= H::kPerStage * first;
         }
         const int xk0 = x++, s0 = xk0 % kStages;
         ok = mbar_wait_warp(bars, &bars.kv_full[s0], (xk0 / kStages) & 1);
@@ -359,7 +380,12 @@ stay_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_con
       const int tok = w.tok0 + t * a.tile_tokens + r / a.G, head = w.hkv * a.G + r % a.G;
       const bool row = r < a.tile_tokens * a.G && tok < w.lq;
       const int seen = row ? clampi(tok + w.lk - w.lq + 1, 0, w.lk) : w.lk;
-      const int blocks = w.blocks[t], g0 = H::kPerStage * w.lo;
+      int blocks = w.blocks[t], g0 = H::kPerStage * w.lo, first = 0;
+      if constexpr (AHEAD) {
+        first = t == 1 ? bars.first1[it & 1] : 0;
+        blocks -= H::kPerStage * first;
+        g0 += H::kPerStage * first;
+      }
       const int from_a = w.ma - g0, to_a = w.mb - g0, from_c = w.mc - g0;
       const int low = KIND == kWindow ? max(0, seen - a.window) : 0;
       const auto visible = [&](int g) {
@@ -451,8 +477,8 @@ stay_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_con
             for (int i = 0; i < 32; ++i) y[i] = 0.f;
           }
           if (bad && row) {
-            for (int j = 0; j < walk; ++j) {
-              if (!partly(w, j)) continue;
+            for (int j = 0; j < walk - first; ++j) {
+              if (!partly(w, j + first)) continue;
               for (int g = g0 + j * H::kPerStage; g < g0 + (j + 1) * H::kPerStage && g < g0 + blocks; ++g) {
                 const uint64_t vis = visible(g);
                 const uint16_t* vr = a.v + w.s * a.v_b + (int64_t)(w.kb + block_key(w, g)) * a.v_t + w.hkv * a.v_h;
@@ -527,11 +553,13 @@ stay_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_con
 
 template <int KIND>
 cudaError_t launch_stay(const PromptMaps<KIND>& maps, const PromptArgs& a, cudaStream_t stream) {
-  static unsigned long long configured = 0ull;
-  const cudaError_t e = spc_host::ensure_smem_limit(configured, stay_attn_kernel<KIND>, kStaySmemBytes);
+  // tiles of as many tokens as a stage has keys, one head a KV head: such stages there may be (first tokens are seen by all)
+  const auto kernel = KIND == kWindow && a.sinks == 0 && a.tile_tokens >= Shape<2>::kKeys ? stay_attn_kernel<KIND, true>
+                                                                                        : stay_attn_kernel<KIND, false>;
+  static unsigned long long configured[2] = {0ull, 0ull};
+  const cudaError_t e = spc_host::ensure_smem_limit(configured[kernel == stay_attn_kernel<KIND, true>], kernel, kStaySmemBytes);
   if (e != cudaSuccess) return e;
-  stay_attn_kernel<KIND><<<std::min<unsigned>(a.items, (unsigned)spc_host::sm_count()), Shape<2>::kThreads, kStaySmemBytes,
-                           stream>>>(maps, a);
+  kernel<<<std::min<unsigned>(a.items, (unsigned)spc_host::sm_count()), Shape<2>::kThreads, kStaySmemBytes, stream>>>(maps, a);
   return cudaGetLastError();
 }
 

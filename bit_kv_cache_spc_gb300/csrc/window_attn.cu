@@ -9,7 +9,7 @@
 // burst rate; 0.73 us per 64 keys and two tiles, where the products take 0.68,
 // and 5 us of start and output for every 66 such blocks).  Short windows by
 // starts and outputs, of which CTAs that stay hide a part (prompt_stay.cuh):
-// 17216 packed tokens of 32 ungrouped heads, window 128, 147 us (564 MB, 84 us
+// 17216 packed tokens of 32 ungrouped heads, window 128, 142 us (564 MB, 84 us
 // at the copy rate).
 #include "few_attn.cuh"
 #include "prompt_stay.cuh"
