@@ -485,6 +485,19 @@ def spc_rope_axes(sections, rot=128, order="sections"):
     return list(buf[:int(rot) // 2])
 
 
+def _axis_table(fn, axis, rot, axes):
+    """The bytes of a table of axes: a sequence of any whole numbers is taken entry by entry (bytes() of an array would be
+    its memory, several bytes an entry)."""
+    if axis is None:
+        if axes != 1:
+            raise ValueError(f"{fn}: positions of {axes} axes need axis")
+        return b""
+    axis = list(axis)
+    if len(axis) != rot // 2:
+        raise ValueError(f"{fn}: axis must be {rot // 2} numbers from 0 to {axes - 1}")
+    return bytes(axis)
+
+
 def spc_norm_rope(q, k, pos, turns, q_weight=None, k_weight=None, eps=1e-6, axis=None, rot=128, interleaved=False,
                   mscale=1.0, v=None, q_out=None, k_out=None, v_out=None, stream=None, _later=None):
     """spc_rope with a norm of each query and key row before it.  q_weight, k_weight: fp32 [D] on the device, or None
@@ -493,18 +506,13 @@ def spc_norm_rope(q, k, pos, turns, q_weight=None, k_weight=None, eps=1e-6, axis
     fn = "spc_norm_rope"
     dev, (B, T, Hq, Hkv, D), layouts, rows = _rope_rows(fn, q, k, v, q_out, k_out, v_out)
     axes = pos.shape[0] if pos.dim() == 3 else 1
-    if axis is None:
-        if axes != 1:
-            raise ValueError(f"{fn}: positions of {axes} axes need axis")
-        axis = b""
-    elif len(axis) != rot // 2:
-        raise ValueError(f"{fn}: axis must be {rot // 2} numbers from 0 to {axes - 1}")
+    axis = _axis_table(fn, axis, rot, axes)
     pos = _words(fn, "pos", pos, torch.int32, axes * B * T, dev)
     turns = _words(fn, "turns", turns, torch.int64, rot // 2, dev)
     wq, wk = _words(fn, "q_weight", q_weight, torch.float32, D, dev), _words(fn, "k_weight", k_weight, torch.float32, D, dev)
     if T == 0:
         return
-    d = _NORM_ROPE.pack(B, T, Hq, Hkv, D, rot, 1 if interleaved else 0, mscale, *layouts, axes, eps, bytes(axis))
+    d = _NORM_ROPE.pack(B, T, Hq, Hkv, D, rot, 1 if interleaved else 0, mscale, *layouts, axes, eps, axis)
     args = (d, pos, turns, wq, wk, *rows, _raw_stream(stream, dev))
     if _later is not None:
         _later.append((fn, args, None))
