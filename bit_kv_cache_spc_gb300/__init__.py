@@ -506,6 +506,8 @@ def spc_norm_rope(q, k, pos, turns, q_weight=None, k_weight=None, eps=1e-6, axis
     fn = "spc_norm_rope"
     dev, (B, T, Hq, Hkv, D), layouts, rows = _rope_rows(fn, q, k, v, q_out, k_out, v_out)
     axes = pos.shape[0] if pos.dim() == 3 else 1
+    if pos.dim() == 3 and pos.shape[1:] != (B, T):  # [B][T][axes], with as many axes as sequences, has as many elements
+        raise ValueError(f"{fn}: pos has shape {tuple(pos.shape)}, expected [axes][{B}][{T}]")
     axis = _axis_table(fn, axis, rot, axes)
     pos = _words(fn, "pos", pos, torch.int32, axes * B * T, dev)
     turns = _words(fn, "turns", turns, torch.int64, rot // 2, dev)

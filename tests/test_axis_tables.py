@@ -51,3 +51,18 @@ def test_other_numbers_are_refused(packed, bad):
 def test_what_holds_no_whole_numbers_is_refused(packed, bad):
     with pytest.raises(TypeError):
         packed(bad)
+
+
+@pytest.mark.parametrize("shape", [(1, 2, AXES), (AXES, 2, 1), (AXES, 1, 3), (AXES, 2, 2)])
+def test_positions_of_another_order_are_refused(packed, shape):
+    """One sequence of two tokens: [axes][1][2] alone."""
+    with pytest.raises(ValueError):
+        packed(TABLE, torch.zeros(shape, dtype=torch.int32))
+
+
+def test_as_many_axes_as_sequences(monkeypatch, packed):
+    """[B][T][axes] has then the shape's first number and its count of elements right."""
+    monkeypatch.setattr(spc, "_rope_rows", lambda *_: (0, (AXES, 7, 4, 2, 128), (0,) * 18, (None,) * 6))
+    with pytest.raises(ValueError):
+        packed(TABLE, torch.zeros((AXES, 7, AXES), dtype=torch.int32))
+    assert packed(TABLE, torch.zeros((AXES, AXES, 7), dtype=torch.int32))[:3] == TABLE[:3]
