@@ -28,7 +28,7 @@ __all__ = [
     "spc_rope_axes", "spc_norm_rope",
     "spc_prompt_attn", "spc_prompt_attn_workspace_bytes", "spc_prompt_attn_status",
     "spc_prompt_attn_wait_limit", "spc_window_attn", "spc_window_attn_workspace_bytes", "spc_prefix_attn",
-    "spc_prefix_attn_workspace_bytes", "spc_extend_kv", "spc_dequantize_kv", "lib_path",
+    "spc_prefix_attn_workspace_bytes", "spc_prefix_attn_together", "spc_extend_kv", "spc_dequantize_kv", "lib_path",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -147,6 +147,7 @@ _sig = {
     "spc_window_attn_workspace_bytes": (C.c_size_t, [_P, C.c_int32, C.c_int32]),
     "spc_window_attn": (C.c_int, [_P, C.c_int32, C.c_int32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, C.c_size_t, _P]),
     "spc_prefix_attn_workspace_bytes": (C.c_size_t, [_P, _P]),
+    "spc_prefix_attn_together": (C.c_int32, [_P, _P, C.c_int32]),
     "spc_prefix_attn": (C.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, C.c_size_t, _P]),
     "spc_extend_kv": (C.c_int, [_D, C.c_int32, _P, _P, _P, _P, _P, _P, _P, C.c_int64, _P]),
     "spc_dequantize_kv": (C.c_int, [_D, _P, _P, C.c_int32, C.c_int32, _P, _P, _P, _P, _P]),
@@ -643,6 +644,15 @@ def spc_prefix_attn_workspace_bytes(q, pk, pv, k, v, o, S=None, q_max=None, k_ma
     dev = _device(fn, q)
     d = _prompt_dims(fn, q, k, v, o, _sequences(q, k) if S is None else S, q_max, k_max, None, dev)
     return int(_lib.spc_prefix_attn_workspace_bytes(d, _prefix(fn, pk, pv, k, dev)))
+
+
+def spc_prefix_attn_together(q, pk, pv, k, v, o, S=None, q_max=None, k_max=None, placed=False) -> int:
+    """Whether spc_prefix_attn over these tensors (placed: with a q_begin) walks over the prefix once for all sequences' rows
+    (2: with their own keys in the same walk, 1: these in a launch of their own) or for each sequence (0)."""
+    fn = "spc_prefix_attn_together"
+    dev = _device(fn, q)
+    d = _prompt_dims(fn, q, k, v, o, _sequences(q, k) if S is None else S, q_max, k_max, None, dev)
+    return int(_lib.spc_prefix_attn_together(d, _prefix(fn, pk, pv, k, dev), 1 if placed else 0))
 
 
 def spc_prefix_attn(q, pk, pv, k, v, o, lse=None, p_len=None, q_begin=None, q_len=None, k_begin=None, k_len=None,

@@ -22,6 +22,13 @@ size_t prefix_workspace_bytes(const spc_prompt_dims* d, const spc_prefix* p) {
   return prompt_bytes(d, rule);
 }
 
+int32_t prefix_together(const spc_prompt_dims* d, const spc_prefix* p, bool placed) {
+  PromptRule rule;
+  rule.prefix = p->tokens;
+  const PromptGrid g = together_grid(d, rule);
+  return !taken_together(d, g, placed) ? 0 : g.mixed ? 2 : 1;
+}
+
 spc_status launch_prefix_attn(const spc_prompt_dims* d, const spc_prefix* p, const uint16_t* q, const uint16_t* pk,
                               const uint16_t* pv, const int32_t* p_len, const uint16_t* k, const uint16_t* v,
                               const int32_t* q_begin, const int32_t* q_len, const int32_t* k_begin,

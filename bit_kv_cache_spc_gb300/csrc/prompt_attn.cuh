@@ -1823,6 +1823,11 @@ PromptGrid together_grid(const spc_prompt_dims* d, const PromptRule& rule) {
   return g;
 }
 
+// Whether a call takes that grid (placed: with a q_begin).
+bool taken_together(const spc_prompt_dims* d, const PromptGrid& g, bool placed) {
+  return g.p_items > 0 && !(d->q.b != 0 && placed);
+}
+
 constexpr size_t kPromptHead = 256;  // the fault word
 
 int64_t part_rows(const spc_prompt_dims* d, const PromptGrid& g) {
@@ -1953,7 +1958,7 @@ spc_status launch_prompt(const spc_prompt_dims* d, const PromptRule& rule, const
   PromptGrid g = prompt_grid(d, rule);
   if constexpr (KIND == kPrefix) {
     const PromptGrid all = together_grid(d, rule);
-    a.together = all.p_items > 0 && !(d->q.b != 0 && x.q_begin != nullptr);
+    a.together = taken_together(d, all, x.q_begin != nullptr);
     if (a.together) g = all;
     a.p_items = (int32_t)g.p_items;
     a.p_tiles = g.p_tiles;

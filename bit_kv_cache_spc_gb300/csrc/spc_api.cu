@@ -31,6 +31,7 @@ spc_status launch_norm_rope(const spc_norm_rope_dims*, const int32_t*, const uin
 size_t prompt_workspace_bytes(const spc_prompt_dims*);
 size_t window_workspace_bytes(const spc_prompt_dims*, int32_t, int32_t);
 size_t prefix_workspace_bytes(const spc_prompt_dims*, const spc_prefix*);
+int32_t prefix_together(const spc_prompt_dims*, const spc_prefix*, bool);
 cudaError_t window_fault_word(void**);
 cudaError_t prefix_fault_word(void**);
 spc_status launch_window_attn(const spc_prompt_dims*, int32_t, int32_t, const uint16_t*, const uint16_t*,
@@ -969,6 +970,10 @@ static spc_status check_prefix(const spc_prompt_dims* d, const spc_prefix* p) {
 size_t spc_prefix_attn_workspace_bytes(const spc_prompt_dims* d, const spc_prefix* p) {
   if (check_prefix(d, p) != SPC_OK) return 0;
   return p->tokens == 0 ? spc::prompt_workspace_bytes(d) : spc::prefix_workspace_bytes(d, p);
+}
+
+int32_t spc_prefix_attn_together(const spc_prompt_dims* d, const spc_prefix* p, int32_t placed) {
+  return check_prefix(d, p) != SPC_OK ? 0 : spc::prefix_together(d, p, placed != 0);
 }
 
 static spc_status check_prefix_attn(const spc_prompt_dims* d, const spc_prefix* p, const uint16_t* q,

@@ -581,6 +581,15 @@ typedef struct spc_prefix {
  */
 size_t spc_prefix_attn_workspace_bytes(const spc_prompt_dims* d, const spc_prefix* p);
 
+/* How a call of this shape on the current device walks over the prefix: once
+ * for the rows of all sequences together, with their own keys in the same walk
+ * (2) or in a launch of their own (1); or for each sequence by itself (0, and
+ * for an invalid shape), where that takes no longer or tiles would hold few
+ * rows: batched queries of which no two sequences fit into a tile of 128 G-head
+ * rows (2 * q_max > 128 / G), or with a q_begin (placed != 0); packed ones on an
+ * axis of more than 4 * S * q_max tokens. */
+int32_t spc_prefix_attn_together(const spc_prompt_dims* d, const spc_prefix* p, int32_t placed);
+
 spc_status spc_prefix_attn(const spc_prompt_dims* d, const spc_prefix* p, const uint16_t* q, const uint16_t* pk,
                            const uint16_t* pv, const int32_t* p_len, const uint16_t* k, const uint16_t* v,
                            const int32_t* q_begin, const int32_t* q_len, const int32_t* k_begin,
