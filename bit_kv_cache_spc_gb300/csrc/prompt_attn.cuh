@@ -258,7 +258,7 @@ __device__ __forceinline__ bool mbar_try(uint64_t* b, uint32_t parity) {
 // The softmax warps take UNROLL = 1: with 64 tries written out at each of their
 // waits, their code and the other warps' come late from the instruction cache
 // (prefix attention of 8192 queries 676 to 665 us, of 17 turns 109.4 to
-// 106.6; 17216 packed tokens, window 128, 164 to 147).  For the warps of the
+// 106.6; 17216 packed tokens, window 128, 160 to 147).  For the warps of the
 // products they are written out: rolled, a 32768-token prompt takes 5.73 ms
 // instead of 5.59.
 template <int UNROLL = 64, class Bars>
@@ -540,13 +540,6 @@ __device__ __forceinline__ bool dense_item(const PromptArgs& a, int k, PromptIte
   return true;
 }
 
-// Item i of all (a whole warp): split fastest (slowest where the last one is
-// shorter than the others, and so taken last), then KV head, then sequence,
-// then pair, later pairs (more keys) first.  CTAs that run together then read
-// different heads' keys at the same depth, and several pairs of a head share
-// them in L2.  Up to kDense sequences of different lengths are numbered over
-// the pairs that exist, so that long and short prompts packed together leave
-// no empty CTAs; more, or equal ones, over all pairs.  False for none.
 // Item i of the prefix's, rows of all sequences together: the cluster's split fastest, then tile of rows, so that CTAs that
 // run together share keys, then KV head, then the other splits.  False where no sequence has a row in the tile.
 template <int TILES>
@@ -623,6 +616,13 @@ __device__ __forceinline__ bool shared_item(const PromptArgs& a, uint32_t i, Pro
   return true;
 }
 
+// Item i of all (a whole warp): split fastest (slowest where the last one is
+// shorter than the others, and so taken last), then KV head, then sequence,
+// then pair, later pairs (more keys) first.  CTAs that run together then read
+// different heads' keys at the same depth, and several pairs of a head share
+// them in L2.  Up to kDense sequences of different lengths are numbered over
+// the pairs that exist, so that long and short prompts packed together leave
+// no empty CTAs; more, or equal ones, over all pairs.  False for none.
 template <int TILES, int KIND>
 __device__ __forceinline__ bool prompt_item(const PromptArgs& a, uint32_t i, PromptItem& w, MixedSeq* table) {
   constexpr int kKeys = Shape<TILES>::kKeys;
