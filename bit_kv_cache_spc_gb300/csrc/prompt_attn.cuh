@@ -1740,7 +1740,7 @@ PromptGrid together_grid(const spc_prompt_dims* d, const PromptRule& rule) {
   int64_t tokens = (int64_t)d->S * d->q_max, own_tiles = (int64_t)d->S * g.pairs, tiles;
   if (batched) {
     g.p_bt = d->q_max;
-    g.p_bs = std::min(g.tile_tokens / d->q_max, 256);
+    g.p_bs = g.tile_tokens / d->q_max;
     tiles = ceil_div(d->S, g.p_bs);
   } else {
     tokens = std::min<int64_t>(tokens, d->q_tokens);

@@ -73,9 +73,9 @@ __device__ __forceinline__ void tmem_get16(uint32_t addr, float* r) {
 // leaves them out (17216 packed tokens of 32 ungrouped heads, window 128, whose
 // items have six blocks for tiles that see four: 147 to 142 us, window 1024 279
 // to 273; in the kernel of all calls grouped heads lose 2 to 4%).
-template <int KIND, bool AHEAD>
+template <bool AHEAD>
 __global__ void __launch_bounds__(Shape<2>::kThreads, 1)
-stay_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_constant__ PromptArgs a) {
+stay_attn_kernel(const __grid_constant__ PromptMaps<kWindow> maps, const __grid_constant__ PromptArgs a) {
   using H = Shape<2>;
   constexpr int kStages = kStayStages;
   constexpr int kScanWarps = H::kThreads / 32 - H::kScanWarp;
@@ -156,7 +156,7 @@ stay_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_con
         PromptItem w;
         bool have = false;
         while (!have && next < a.items) {  // items without rows are left out
-          have = prompt_item<2, KIND>(a, next, w, nullptr);
+          have = prompt_item<2, kWindow>(a, next, w, nullptr);
           next += gridDim.x;
         }
         if (!have) w.s = -1;
@@ -387,12 +387,11 @@ stay_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_con
         g0 += H::kPerStage * first;
       }
       const int from_a = w.ma - g0, to_a = w.mb - g0, from_c = w.mc - g0;
-      const int low = KIND == kWindow ? max(0, seen - a.window) : 0;
+      const int low = max(0, seen - a.window);
       const auto visible = [&](int g) {
         const auto first = [](int k) { return k <= 0 ? 0ull : k >= 64 ? ~0ull : (1ull << k) - 1ull; };
         const int key = block_key(w, g);
-        const uint64_t m = first(seen - key);
-        return KIND == kWindow ? m & (~first(low - key) | first(a.sinks - key)) : m;
+        return first(seen - key) & (~first(low - key) | first(a.sinks - key));
       };
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < blocks; ++i) {
@@ -456,7 +455,7 @@ stay_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_con
       }
       tc_fence_after();
       const bool bad = *(volatile uint32_t*)&bars.bad[it & 1] != 0u;
-      const bool any = blocks > 0 && (seen > 0 || (KIND == kPrefix && w.prefix > 0));
+      const bool any = blocks > 0 && seen > 0;
       const float inv = any ? 1.f / l : 0.f;
       const uint64_t out =
           row ? (uint64_t)(a.o + w.s * a.o_b + (int64_t)(w.qb + tok) * a.o_t + head * a.o_h) : 0;  // where the row goes
@@ -551,13 +550,11 @@ stay_attn_kernel(const __grid_constant__ PromptMaps<KIND> maps, const __grid_con
   }
 }
 
-template <int KIND>
-cudaError_t launch_stay(const PromptMaps<KIND>& maps, const PromptArgs& a, cudaStream_t stream) {
+cudaError_t launch_stay(const PromptMaps<kWindow>& maps, const PromptArgs& a, cudaStream_t stream) {
   // tiles of as many tokens as a stage has keys, one head a KV head: such stages there may be (first tokens are seen by all)
-  const auto kernel = KIND == kWindow && a.sinks == 0 && a.tile_tokens >= Shape<2>::kKeys ? stay_attn_kernel<KIND, true>
-                                                                                        : stay_attn_kernel<KIND, false>;
+  const auto kernel = a.sinks == 0 && a.tile_tokens >= Shape<2>::kKeys ? stay_attn_kernel<true> : stay_attn_kernel<false>;
   static unsigned long long configured[2] = {0ull, 0ull};
-  const cudaError_t e = spc_host::ensure_smem_limit(configured[kernel == stay_attn_kernel<KIND, true>], kernel, kStaySmemBytes);
+  const cudaError_t e = spc_host::ensure_smem_limit(configured[kernel == stay_attn_kernel<true>], kernel, kStaySmemBytes);
   if (e != cudaSuccess) return e;
   kernel<<<std::min<unsigned>(a.items, (unsigned)spc_host::sm_count()), Shape<2>::kThreads, kStaySmemBytes, stream>>>(maps, a);
   return cudaGetLastError();

@@ -38,7 +38,7 @@ spc_status launch_window_attn(const spc_prompt_dims* d, int32_t window, int32_t 
     PromptArgs a = prompt_args(d, rule, x);
     return launch_few<false>(a, d, stream);
   }
-  return launch_prompt<kWindow>(d, rule, x, stream, nullptr, launch_stay<kWindow>);
+  return launch_prompt<kWindow>(d, rule, x, stream, nullptr, launch_stay);
 }
 
 }  // namespace spc
