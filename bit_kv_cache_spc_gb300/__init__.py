@@ -551,10 +551,10 @@ def spc_prompt_attn_workspace_bytes(q, k, v, o, S=None, q_max=None, k_max=None) 
     return int(_lib.spc_prompt_attn_workspace_bytes(d))
 
 
-def _attend(fn, rule, prefix, q, k, v, o, lse, q_begin, q_len, k_begin, k_len, q_max, k_max, scale, ws, ws_bytes, stream,
+def _attend(fn, call, size, rule, prefix, q, k, v, o, lse, q_begin, q_len, k_begin, k_len, q_max, k_max, scale, ws, ws_bytes, stream,
             later):
-    """A call of spc_prompt_attn or one of its siblings: rule, its arguments behind the dims, and prefix, those between
-    the queries and the keys."""
+    """A call of spc_prompt_attn or one of its siblings: call and size, the library's functions; rule, its arguments behind
+    the dims, and prefix, those between the queries and the keys."""
     dev = _device(fn, q)
     S = _sequences(q, k, q_len, k_len, q_begin, k_begin)
     d = _prompt_dims(fn, q, k, v, o, S, q_max, k_max, scale, dev)
@@ -567,7 +567,7 @@ def _attend(fn, rule, prefix, q, k, v, o, lse, q_begin, q_len, k_begin, k_len, q
     if ws is None:
         if stream is not None and s != _raw_stream(None, dev):
             raise ValueError(f"{fn}: a call on another stream than the current one needs ws")
-        w, ws_bytes = None, getattr(_lib, fn + "_workspace_bytes")(d, *rule)
+        w, ws_bytes = None, size(d, *rule)
         if ws_bytes > 256:  # the keys are split; else the call needs none
             w = own = torch._C._cuda_cudaCachingAllocator_raw_alloc(ws_bytes, s)  # a tensor's allocation takes 3 us more
         else:
@@ -586,7 +586,7 @@ def _attend(fn, rule, prefix, q, k, v, o, lse, q_begin, q_len, k_begin, k_len, q
         later.append((fn, args, own))
         return
     try:
-        st = getattr(_lib, fn)(*args)
+        st = call(*args)
     finally:
         if own is not None:
             torch._C._cuda_cudaCachingAllocator_raw_delete(own)
@@ -603,8 +603,8 @@ def spc_prompt_attn(q, k, v, o, lse=None, q_begin=None, q_len=None, k_begin=None
     workspace, where one is needed, is taken from torch's allocator for the
     call, which needs the call to be on the current stream; a wait that ran
     out is then found by spc_prompt_attn_status() of the device."""
-    _attend("spc_prompt_attn", (), (), q, k, v, o, lse, q_begin, q_len, k_begin, k_len, q_max, k_max, scale, ws, ws_bytes,
-            stream, _later)
+    _attend("spc_prompt_attn", _lib.spc_prompt_attn, _lib.spc_prompt_attn_workspace_bytes, (), (), q, k, v, o, lse, q_begin,
+            q_len, k_begin, k_len, q_max, k_max, scale, ws, ws_bytes, stream, _later)
 
 
 def _window(fn, window, sinks):
@@ -626,8 +626,8 @@ def spc_window_attn(q, k, v, o, window, sinks=0, lse=None, q_begin=None, q_len=N
     and the first `sinks` keys of its sequence; the other arguments are
     spc_prompt_attn's."""
     fn = "spc_window_attn"
-    _attend(fn, _window(fn, window, sinks), (), q, k, v, o, lse, q_begin, q_len, k_begin, k_len, q_max, k_max, scale, ws,
-            ws_bytes, stream, _later)
+    _attend(fn, _lib.spc_window_attn, _lib.spc_window_attn_workspace_bytes, _window(fn, window, sinks), (), q, k, v, o, lse,
+            q_begin, q_len, k_begin, k_len, q_max, k_max, scale, ws, ws_bytes, stream, _later)
 
 
 def _prefix(fn, pk, pv, k, dev):
@@ -665,8 +665,8 @@ def spc_prefix_attn(q, pk, pv, k, v, o, lse=None, p_len=None, q_begin=None, q_le
     dev = _device(fn, q)
     p = _prefix(fn, pk, pv, k, dev)
     n = _words(fn, "p_len", p_len, torch.int32, 1, dev)
-    _attend(fn, (p,), (pk.data_ptr(), pv.data_ptr(), n), q, k, v, o, lse, q_begin, q_len, k_begin, k_len, q_max, k_max,
-            scale, ws, ws_bytes, stream, _later)
+    _attend(fn, _lib.spc_prefix_attn, _lib.spc_prefix_attn_workspace_bytes, (p,), (pk.data_ptr(), pv.data_ptr(), n), q, k, v, o,
+            lse, q_begin, q_len, k_begin, k_len, q_max, k_max, scale, ws, ws_bytes, stream, _later)
 
 
 def spc_prompt_attn_status(ws=None, stream=None) -> int:
