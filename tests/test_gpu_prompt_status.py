@@ -74,8 +74,11 @@ def test_many_threads():
 
 
 def test_beside_a_capture():
-    """A first call of another thread takes its words while a stream is being captured: the capture goes on."""
+    """A first call of another thread takes its words while a stream is being captured: the capture goes on.  (torch deals
+    32 streams out by turns: 21 in a row are different ones.)"""
     import bit_kv_cache_spc_gb300 as spc
+    captured, *streams = [torch.cuda.Stream() for _ in range(21)]
+    assert len({s.cuda_stream for s in (captured, *streams)}) == 21
     ws, x = [torch.zeros(256, dtype=torch.uint8, device="cuda") for _ in range(20)], torch.zeros(64, device="cuda")
     torch.cuda.synchronize()
     got, go = [], threading.Barrier(len(ws))
@@ -84,9 +87,9 @@ def test_beside_a_capture():
         go.wait()
         got.append(spc.spc_prompt_attn_status(w, stream=st))
 
-    threads = [threading.Thread(target=ask, args=(w, torch.cuda.Stream())) for w in ws]
+    threads = [threading.Thread(target=ask, args=a) for a in zip(ws, streams)]
     g = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(g, capture_error_mode="thread_local"):
+    with torch.cuda.graph(g, stream=captured, capture_error_mode="thread_local"):
         x.add_(1)
         for t in threads:
             t.start()
