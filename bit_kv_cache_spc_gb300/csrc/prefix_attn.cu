@@ -5,11 +5,13 @@
 // rows, over the prefix with the rows of all of them together, and then over
 // each one's own keys (single tokens with few_attn.cuh's kernel).
 // 64 single tokens of 32 and 8 heads behind 32768 keys, up to 1024 of their own
-// (276 MB, 41 us at the copy rate): 62 to 63 us, against 1035 with the prefix
+// (276 MB, 41 us at the copy rate): 62 to 65 us, against 1035 with the prefix
 // walked for each.  17 prompts of up to 77 tokens, 32 ungrouped heads, behind
-// 8011 keys (81 GFLOP, 43 us at the burst rate): 104 us, against 315.  Four of
-// up to 2048 tokens behind 16384 keys, one by one (1.02 TFLOP, 537 us): 658 to
-// 673 us.
+// 8011 keys (81 GFLOP, 43 us at the burst rate): 104 to 108 us, against 315.
+// Four of up to 2048 tokens behind 16384 keys, one by one (1.02 TFLOP, 537 us):
+// 624 to 676 us.  64 batched prompts of 17 tokens, 32 and 8 heads, behind 8192
+// keys, each of which walks over these: 274 us, packed 107 (of 16 tokens 106 and
+// 106).
 #include "few_attn.cuh"
 
 namespace spc {

@@ -5,11 +5,11 @@
 // windows of an item's rows: what lies between is not read.  Single tokens take
 // few_attn.cuh's.
 // Long windows are bound by the tensor cores: a 32768-token prompt of 32 and 8
-// heads, window 4096, takes 1.45 to 1.49 ms (2.06 TFLOP: 74% of the measured
+// heads, window 4096, takes 1.46 to 1.50 ms (2.06 TFLOP: 74% of the measured
 // burst rate; 0.73 us per 64 keys and two tiles, where the products take 0.68,
 // and 5 us of start and output for every 66 such blocks).  Short windows by
 // starts and outputs, of which CTAs that stay hide a part (prompt_stay.cuh):
-// 17216 packed tokens of 32 ungrouped heads, window 128, 142 us (564 MB, 84 us
+// 17216 packed tokens of 32 ungrouped heads, window 128, 142 to 145 us (564 MB, 84 us
 // at the copy rate).
 #include "few_attn.cuh"
 #include "prompt_stay.cuh"

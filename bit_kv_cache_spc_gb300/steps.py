@@ -74,12 +74,16 @@ def prompt_layer(d, q, k, v, pos, turns, o, records, resid, host_kv=None, n_cap=
     by the axis axis[i].
     window (and sinks): a query sees the last `window` keys and the first
     `sinks`; of a history only what some query sees is read back, and the rows
-    between hold what they held.
+    between hold what they held.  Such a layer's single tokens come here too:
+    predecode_layer and decode_layer have no window and attend over the whole
+    cache.
     prefix: a pair of 16-bit [P][Hkv][D] views (keys, values), rotated, of the
     first P tokens, which all sequences' caches share and hold already (P <=
     d.N): they are attended to there, and the history is read back from token P
     on.  Row i of the history buffers is then token P + i, and they need
-    d.N - P + n rows.  Not together with a window."""
+    d.N - P + n rows.  One walk over the prefix can serve all sequences while
+    two of them fit into a tile, 2 n <= 128 / G for G query heads to a KV head
+    (spc_prefix_attn_together); for longer prompts each has its own.  Not together with a window."""
     n, N = k.shape[1], d.N
     P = 0 if prefix is None else prefix[0].shape[0]
     if prefix is not None and (window is not None or P > N):

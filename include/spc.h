@@ -470,7 +470,9 @@ typedef struct spc_norm_rope_dims {
  *   k_weight : the same of the key rows.
  * The values' rows are copied as they are.  Everything else as spc_rope.  The
  * mean, the norm and the rotation are binary32, rounded once to bf16; squares
- * that overflow binary32 are formed of scaled elements.
+ * that overflow binary32 are formed of scaled elements.  x_j * w_j is formed
+ * before the division: beyond 2^127 it overflows, and below 2^-126 it loses bits
+ * (rows whose squares overflow are multiplied by 2^-70 first).
  */
 spc_status spc_norm_rope(const spc_norm_rope_dims* d, const int32_t* pos, const uint64_t* turns, const float* q_weight,
                          const float* k_weight, const uint16_t* q, const uint16_t* k, const uint16_t* v,
